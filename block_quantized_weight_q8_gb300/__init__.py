@@ -22,7 +22,7 @@ STATUS = {0: "QMM_OK", 1: "QMM_E_NULL", 2: "QMM_E_SHAPE", 3: "QMM_E_TYPE", 4: "Q
           5: "QMM_E_SCRATCH", 6: "QMM_E_CUDA", 7: "QMM_E_TIMEOUT", 8: "QMM_E_BOUNDS"}
 
 # every entry point the header declares, with its argument kinds
-# p: pointer, i: int64, s: size_t, t: int (type code), c: int, q: stream
+# p: pointer, i: int64, s: size_t, t: int (type code), c: int, f: float, d: double, q: stream
 SIGNATURES = {
     "qmm_block_bytes": ("t", ctypes.c_size_t),
     "qmm_block_values": ("t", ctypes.c_int),
@@ -71,6 +71,13 @@ SIGNATURES = {
     "qmm_kv_scores": ("pppiiiifq", ctypes.c_int),
     "qmm_kv_wsum_scratch_bytes": ("iii", ctypes.c_size_t),
     "qmm_kv_wsum": ("pppps" + "iiiiq", ctypes.c_int),
+    "qmm_rope_freqs": ("pidtddddq", ctypes.c_int),
+    "qmm_rope": ("ppipipiiicq", ctypes.c_int),
+    "qmm_kv_page_bytes": ("tiii", ctypes.c_size_t),
+    "qmm_kv_store": ("ppipippippipiiq", ctypes.c_int),
+    "qmm_kv_load": ("pppipipiq", ctypes.c_int),
+    "qmm_kv_attend_scratch_bytes": ("iii", ctypes.c_size_t),
+    "qmm_kv_attend": ("ppipppippsiifiq", ctypes.c_int),
     "qmm_matmul_q4_K": ("pppiiiq", ctypes.c_int),
     "qmm_matmul_q6_K": ("pppiiiq", ctypes.c_int),
     "qmm_matmul_q5_K": ("pppiiiq", ctypes.c_int),
@@ -82,7 +89,7 @@ SIGNATURES = {
     "qmm_device_status": ("c", ctypes.c_int),
 }
 _CT = {"p": ctypes.c_void_p, "i": ctypes.c_int64, "s": ctypes.c_size_t, "t": ctypes.c_int, "c": ctypes.c_int,
-       "q": ctypes.c_void_p, "f": ctypes.c_float, "u": ctypes.c_uint64}
+       "q": ctypes.c_void_p, "f": ctypes.c_float, "d": ctypes.c_double, "u": ctypes.c_uint64}
 
 _lib = None
 
@@ -324,6 +331,145 @@ def qmm_kv_wsum(w, vc, out, scratch, scratch_bytes, Hq, Hkv, P, hd, stream=None)
     """out[h] = sum_p w[h][p] * (dequantized V row of position p, KV head h / (Hq/Hkv))."""
     _call("qmm_kv_wsum", ptr(w), ptr(vc), ptr(out), ptr(scratch), int(scratch_bytes), int(Hq), int(Hkv), int(P),
           int(hd), stream_handle(stream))
+
+
+# ---- rotary positions and the paged KV cache
+QMM_KV_Q8, QMM_KV_F16 = 0, 1
+KV_TYPES = {"q8": QMM_KV_Q8, "f16": QMM_KV_F16}
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "bands": 2, "yarn": 3}
+
+
+def _on_device(name, t, dtype, ndim):
+    """Checks a tensor that a kernel reads or writes by its shape."""
+    import torch
+    if not (t.is_cuda and t.dtype == getattr(torch, dtype) and t.dim() == ndim):
+        raise ValueError("%s: a %d-dimensional CUDA tensor of %s is needed" % (name, ndim, dtype))
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError("%s lies on %s, the current device is cuda:%d" % (name, t.device, torch.cuda.current_device()))
+
+
+def _heads(name, t, like=None):
+    """(address, token stride) of head rows [T][H][hd]: heads side by side, tokens any stride apart."""
+    _on_device(name, t, "float32", 3)
+    T, H, hd = t.shape
+    s = t.stride()
+    if like is not None and tuple(t.shape) != tuple(like):
+        raise ValueError("%s: shape %s is needed, got %s" % (name, tuple(like), tuple(t.shape)))
+    if s[2] != 1 or (H > 1 and s[1] != hd):
+        raise ValueError("%s: the heads of a token must be contiguous" % name)
+    return t.data_ptr(), (s[0] if T > 1 else H * hd)
+
+
+def _ints(name, t, n):
+    if t is None:
+        return None
+    _on_device(name, t, "int32", 1)
+    if t.shape[0] != n or not t.is_contiguous():
+        raise ValueError("%s: %d contiguous values are needed" % (name, n))
+    return t.data_ptr()
+
+
+class RopeSpec(ctypes.Structure):
+    """qmm_rope_spec: a frequency table (int64 CUDA tensor [n_rot / 2], filled by qmm_rope_freqs), how values are
+    paired ("half" or "interleaved") and the factor of the result.  Keeps the table alive."""
+    _fields_ = [("freqs", ctypes.c_void_p), ("n_rot", ctypes.c_int64), ("layout", ctypes.c_int32),
+                ("mscale", ctypes.c_float)]
+
+    def __init__(self, freqs, layout="half", mscale=1.0):
+        _on_device("freqs", freqs, "int64", 1)
+        if not freqs.is_contiguous():
+            raise ValueError("freqs: contiguous values are needed")
+        super().__init__(freqs.data_ptr(), 2 * freqs.shape[0], ROPE_LAYOUTS[layout], mscale)
+        self.tensor, self.ref = freqs, ctypes.addressof(self)
+
+
+class KvPages(ctypes.Structure):
+    """qmm_kv_pages: pools k and v (uint8 CUDA tensors [num_pages][at least qmm_kv_page_bytes], pages a multiple of
+    16 bytes apart), a page table (int32 CUDA tensor [num_seqs][max_pages]) and the shape.  Keeps the tensors alive."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64), ("num_seqs", ctypes.c_int64),
+                ("max_pages", ctypes.c_int64), ("Hkv", ctypes.c_int64), ("hd", ctypes.c_int64),
+                ("type", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+
+    def __init__(self, type, k, v, table, page_size, Hkv, hd):
+        _on_device("k", k, "uint8", 2)
+        _on_device("v", v, "uint8", 2)
+        _on_device("table", table, "int32", 2)
+        need = qmm_kv_page_bytes(type, Hkv, page_size, hd)
+        if need == 0:
+            raise ValueError("no cache of type %r has %r heads of %r in pages of %r" % (type, Hkv, hd, page_size))
+        if k.shape != v.shape or k.stride() != v.stride() or k.stride(1) != 1 or k.shape[1] < need:
+            raise ValueError("k and v: pools of one shape and stride are needed, %d bytes a page at least" % need)
+        if not table.is_contiguous():
+            raise ValueError("table: contiguous rows are needed")
+        stride = k.stride(0) if k.shape[0] > 1 else -(-k.shape[1] // 16) * 16
+        super().__init__(k.data_ptr(), v.data_ptr(), table.data_ptr(), k.shape[0], stride, table.shape[0],
+                         table.shape[1], Hkv, hd, KV_TYPES[type], page_size)
+        self.tensors, self.ref = (k, v, table), ctypes.addressof(self)
+
+
+def qmm_rope_freqs(freqs, base=10000.0, scaling="plain", factor=1.0, orig_len=0.0, lo=0.0, hi=0.0, stream=None):
+    """Fills the frequency table freqs (int64 CUDA tensor [n_rot / 2])."""
+    _on_device("freqs", freqs, "int64", 1)
+    _call("qmm_rope_freqs", freqs.data_ptr(), 2 * freqs.shape[0], float(base), ROPE_SCALINGS[scaling], float(factor),
+          float(orig_len), float(lo), float(hi), stream_handle(stream))
+
+
+def qmm_rope(rope, x, y, pos, inverse=False, stream=None):
+    """y = x ([T][H][hd] f32) rotated to the positions pos; y may be x."""
+    px, ldx = _heads("x", x)
+    py, ldy = _heads("y", y, x.shape)
+    T, H, hd = x.shape
+    _call("qmm_rope", rope.ref, px, ldx, py, ldy, _ints("pos", pos, T), T, H, hd, 1 if inverse else 0,
+          stream_handle(stream))
+
+
+def qmm_kv_page_bytes(type, Hkv, page_size, hd):
+    return int(load().qmm_kv_page_bytes(KV_TYPES[type], int(Hkv), int(page_size), int(hd)))
+
+
+def qmm_kv_store(pages, k, v, pos, seq=None, rope=None, q=None, q_out=None, stream=None):
+    """Stores keys k and values v ([T][Hkv][hd] f32) at positions pos of the sequences seq; with rope, keys are rotated
+    first, and queries q ([T][Hq][hd]) into q_out."""
+    T = k.shape[0]
+    pk, ldk = _heads("k", k, (T, pages.Hkv, pages.hd))
+    pv, ldv = _heads("v", v, k.shape)
+    pq = ldq = po = ldo = Hq = 0
+    if q is not None:
+        Hq = q.shape[1]
+        pq, ldq = _heads("q", q, (T, Hq, pages.hd))
+        po, ldo = _heads("q_out", q_out, q.shape)
+    _call("qmm_kv_store", pages.ref, pk, ldk, pv, ldv, _ints("pos", pos, T), _ints("seq", seq, T), T,
+          rope.ref if rope is not None else None, pq, ldq, po, ldo, Hq, stream_handle(stream))
+
+
+def qmm_kv_load(pages, pos, k_out=None, v_out=None, seq=None, stream=None):
+    """The rows at positions pos of the sequences seq as f32 ([T][Hkv][hd]); either output may be None."""
+    T = pos.shape[0]
+    pk, ldk = _heads("k_out", k_out, (T, pages.Hkv, pages.hd)) if k_out is not None else (None, 0)
+    pv, ldv = _heads("v_out", v_out, (T, pages.Hkv, pages.hd)) if v_out is not None else (None, 0)
+    _call("qmm_kv_load", pages.ref, _ints("pos", pos, T), _ints("seq", seq, T), T, pk, ldk, pv, ldv,
+          stream_handle(stream))
+
+
+def qmm_kv_attend_scratch_bytes(Hq, Hkv, hd):
+    return int(load().qmm_kv_attend_scratch_bytes(int(Hq), int(Hkv), int(hd)))
+
+
+def qmm_kv_attend(pages, q, lens, out, scratch, scratch_bytes, scale, lse=None, seq=None, window=0, stream=None):
+    """out[r] = the attention of query heads q[r] ([R][Hq][hd] f32) over the first lens[r] positions (the last window
+    of them) of their sequences; lse ([R][Hq] f32) the log of the softmax's sum."""
+    R, Hq, _ = q.shape
+    pq, ldq = _heads("q", q, (R, Hq, pages.hd))
+    po, ldo = _heads("out", out, q.shape)
+    if lse is not None:
+        _on_device("lse", lse, "float32", 2)
+        if tuple(lse.shape) != (R, Hq) or not lse.is_contiguous():
+            raise ValueError("lse: contiguous [R][Hq] is needed")
+    _call("qmm_kv_attend", pages.ref, pq, ldq, _ints("lens", lens, R), _ints("seq", seq, R), po, ldo,
+          lse.data_ptr() if lse is not None else None, ptr(scratch), int(scratch_bytes), R, Hq, float(scale), int(window),
+          stream_handle(stream))
 
 
 def qmm_blocksums(wtype, W, xq, s, M, N, K, stream=None):

@@ -192,6 +192,9 @@ unsigned qmm_internal_matmul_kq_error(int clear);
 unsigned qmm_internal_getrows_error(int clear);
 unsigned qmm_internal_kv_error(int clear);
 unsigned qmm_internal_quantize_error(int clear);
+unsigned qmm_internal_rope_error(int clear);
+unsigned qmm_internal_pages_error(int clear);
+unsigned qmm_internal_attend_error(int clear);
 
 qmm_status qmm_linear_group(int wtype, int G, const void* const* W, const int64_t* N, const float* x, void* xq_scratch,
                             size_t scratch_bytes, float* const* y, int64_t M, int64_t K, qmm_stream_t stream) {
@@ -316,7 +319,8 @@ qmm_status qmm_device_status(int clear) {
     if (cudaDeviceSynchronize() != cudaSuccess) return QMM_E_CUDA;
     unsigned e = qmm_internal_matvec_error(clear) | qmm_internal_matmul_error(clear) |
                  qmm_internal_matmul_kq_error(clear) | qmm_internal_getrows_error(clear) |
-                 qmm_internal_kv_error(clear) | qmm_internal_quantize_error(clear);
+                 qmm_internal_kv_error(clear) | qmm_internal_quantize_error(clear) | qmm_internal_rope_error(clear) |
+                 qmm_internal_pages_error(clear) | qmm_internal_attend_error(clear);
     {
         unsigned v = 0;
         if (cudaMemcpyFromSymbol(&v, g_test_error, sizeof(v)) != cudaSuccess) return QMM_E_CUDA;
@@ -327,7 +331,7 @@ qmm_status qmm_device_status(int clear) {
     if (cudaGetLastError() != cudaSuccess) return QMM_E_CUDA;
     if (e & kErrTimeout) return QMM_E_TIMEOUT;  // a device wait ran out of time
     if (e & kErrBounds) return QMM_E_BOUNDS;    // an index check of a bounds-checked build failed
-    if (e & 2u) return QMM_E_SHAPE;             // qmm_get_rows met an index outside [0, N)
+    if (e & 2u) return QMM_E_SHAPE;  // qmm_get_rows met an index outside [0, N), a cache call a position without a page
     return QMM_OK;
 }
 

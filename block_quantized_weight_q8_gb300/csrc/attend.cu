@@ -1,0 +1,667 @@
+// attend.cu -- attention of one new token per sequence over a paged key-value
+// cache: out[h] = sum_p w_p v_p, w = softmax_p(scale * q_h . k_p), p over the
+// sequence's positions (or the last `window` of them), h's KV head shared by the
+// G = Hq / Hkv query heads of its group.
+//
+// Bound by the cache's bytes, each read once: 2 (hd + 4) per position and KV head
+// (8-bit rows), against 4 G hd operations, which is more than the f32 units do at
+// the memory's rate for G = 8 -- so both products run on the tensor cores, as
+// m16n8k16 f16 products with f32 sums (mma.sync: eight query heads fill a
+// sixteen-row tile; a tcgen05 tile has 64 rows at least, and its operands would
+// have to be stored to shared memory again after their conversion).
+//   codes   int8 is exact in f16; the row's scale multiplies the f32 sum (keys) or
+//           the softmax weight (values)
+//   f32     a query, and the weights times the value scales, are split into two
+//           f16 (hi + lo, 22 bits) and take two rows of the tile: rows 0-7 are
+//           the heads' hi, rows 8-15 their lo, and one thread holds both sums.
+//           Each is first brought near 2^14 by a power of two (per head; per tile
+//           of positions), so that lo does not fall below f16's range
+//   layout  the order of the 16 values within a step is free as long as both
+//           operands share it, so a lane takes its operand straight from 16-byte
+//           loads of natural rows, and a tile's scores are in the registers where
+//           the second product wants its weights: nothing is shuffled but the
+//           row maximum
+// Running maximum and sum of a softmax (in base 2) per warp: one pass.
+//
+// Split.  The work is the list of (row, unit, tile): a unit is a KV head and up to
+// eight of its query heads, a tile 32 (16) positions.  A fixed number of CTAs each
+// take an equal run of the list, found by a scan of the lengths on the device: a
+// captured launch serves any lengths, ragged batches are balanced to a tile, and a
+// long sequence is spread over the whole GPU.  Within a run a CTA's four warps
+// take the tiles of a unit in turn, each through its own ring of asynchronous
+// copies, and meet in shared memory.  A unit that one CTA finishes is written at
+// once; else its parts go to the workspace (at most two per CTA), and the second
+// kernel joins them in order.  Nothing is added by atomics: results do not vary.
+#include <type_traits>
+
+#include "kvpages.cuh"
+
+namespace qmm {
+
+static __device__ unsigned int g_attend_error = 0;
+
+constexpr int kAttendWarps = 4;
+constexpr int kAttendThreads = 32 * kAttendWarps;
+constexpr int kAttendSms = 152;
+constexpr int kAttendHeads = 8;  // query heads per unit
+constexpr int kAttendMaxCtas = 3 * kAttendSms;
+constexpr int kJoinWarps = 8;
+
+template <int TYPE, int HDT>
+struct AttendShape {
+    static constexpr int kRow = HDT * (TYPE == QMM_KV_F16 ? 2 : 1);  // bytes of a row
+    static constexpr int kTile = kRow <= 128 ? 32 : 16;              // positions
+    static constexpr int kStages = kRow <= 64 ? 4 : 3;
+    static constexpr int kCtas = kRow <= 64 ? 3 : kRow <= 256 ? 2 : 1;  // per SM
+    static constexpr int kStage = 2 * kTile * kRow + 8 * kTile + 16;    // keys, values, their scales, the mask
+    static constexpr int kRing = kStages * kStage;                      // of a warp
+    static constexpr int kSmem = kAttendWarps * kRing;
+};
+
+struct AttendArgs {
+    const float* q;
+    const int32_t* lens;
+    const int32_t* seq;  // may be null: row r reads sequence r
+    float* out;
+    float* lse;  // may be null
+    float* parts;
+    int64_t R, ldq, ldo, window;
+    int G, blocks;  // query heads per KV head, units per KV head
+    float scale;
+};
+
+// What row r reads: positions first .. len - 1 of sequence seq.
+struct RowRange {
+    int64_t seq, first, len;
+};
+__device__ __forceinline__ RowRange attend_row(const KvPages& c, const AttendArgs& a, int64_t r) {
+    RowRange x;
+    x.len = __ldg(a.lens + r);
+    x.seq = a.seq ? (int64_t)__ldg(a.seq + r) : r;
+    x.first = 0;
+    if (x.len > 0) {
+        const int64_t room = c.max_pages << c.page_shift;
+        if (x.seq < 0 || x.seq >= c.num_seqs) {
+            atomicOr(&g_attend_error, kErrPlace);
+            x.len = 0;
+        } else if (x.len > room) {
+            atomicOr(&g_attend_error, kErrPlace);
+            x.len = room;
+        }
+        if (a.window > 0 && x.len > a.window) x.first = x.len - a.window;
+    }
+    return x;
+}
+template <int TILE>
+__device__ __forceinline__ int64_t row_tiles(const RowRange& x) {
+    return x.len > 0 ? (x.len + TILE - 1) / TILE - x.first / TILE : 0;
+}
+
+// The run of CTA c out of `ctas` is [run_begin(c), run_begin(c + 1)) of `work`
+// tiles; no more CTAs than leave each a tile per warp.
+__device__ __forceinline__ int64_t run_ctas(int64_t work, int ctas) {
+    const int64_t most = work / kAttendWarps;
+    return most < 1 ? 1 : (most < ctas ? most : ctas);
+}
+__device__ __forceinline__ int64_t run_begin(int64_t c, int64_t work, int64_t ctas) { return c * work / ctas; }
+__device__ __forceinline__ int64_t run_of(int64_t g, int64_t work, int64_t ctas) { return ((g + 1) * ctas - 1) / work; }
+
+// Sum over the block of each thread's v; *before: over the threads before this one.
+template <int THREADS>
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* before, int64_t* sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t incl = v;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const int64_t o = __shfl_up_sync(0xFFFFFFFFu, incl, m);
+        if (lane >= m) incl += o;
+    }
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    int64_t base = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; w++) {
+        if (w < warp) base += sums[w];
+        total += sums[w];
+    }
+    __syncthreads();  // sums may be used again
+    *before = base + incl - v;
+    return total;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4z(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float exp2_approx(float x) {  // within 2 units in the last place; 0 at -inf
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void mma_f16(float d[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// (lo, hi) to two f16, the first in the low half
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// the two f16 of hi, and of what they leave of (x, y)
+__device__ __forceinline__ void split_h2(float x, float y, uint32_t* hi, uint32_t* lo) {
+    const __half2 h = __floats2half2_rn(x, y);
+    const float2 f = __half22float2(h);
+    *hi = *reinterpret_cast<const uint32_t*>(&h);
+    *lo = pack_h2(x - f.x, y - f.y);
+}
+// biased bytes (code + 128) sel of w as two f16: 1024 + byte, less 1152
+__device__ __forceinline__ uint32_t codes_h2(uint32_t w, uint32_t sel) {
+    const uint32_t b = __byte_perm(w, 0x64646464u, sel);
+    const uint32_t bias = 0x64806480u;
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&b), *reinterpret_cast<const __half2*>(&bias));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+// 2^e
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+// e with 2^e <= |x| < 2^(e + 1), held where 2^(14 - e) and 2^(e - 14) are normal
+__device__ __forceinline__ int exponent_of(uint32_t bits) {
+    const int e = (int)((bits & 0x7FFFFFFFu) >> 23);
+    return (e < 20 ? 20 : e) - 127;
+}
+
+template <int TYPE, int HDT>
+__global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
+    attend_kernel(KvPages c, AttendArgs a) {
+    using S = AttendShape<TYPE, HDT>;
+    constexpr int TILE = S::kTile, ROW = S::kRow;
+    constexpr int kChunks = ROW / 16;                    // 16-byte chunks of a row
+    constexpr int kSize = TYPE == QMM_KV_F16 ? 2 : 1;    // bytes of a value
+    constexpr int kPer = 16 / kSize;                     // values of a chunk
+    constexpr int kGroups = kChunks / 4, kSteps = HDT / 16;
+    constexpr int kVB = ROW >= 128 ? 16 : 8;             // bytes of a value row that a lane takes at once
+    constexpr int kSets = ROW / (8 * kVB), kVD = kVB / kSize;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ int64_t scan[kAttendWarps];
+    __shared__ int64_t where[2];  // the run's first row, and the tiles before it
+    __shared__ float part_m[kAttendWarps][kAttendHeads], part_l[kAttendWarps][kAttendHeads];
+    __shared__ float part_f[kAttendWarps][kAttendHeads], unit_l[kAttendHeads];
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = lane >> 2, j = lane & 3;
+    const int units = c.Hkv * a.blocks;
+
+    // the run: total work, then the row in which it begins
+    int64_t mine = 0, before, total;
+    for (int64_t r = threadIdx.x; r < a.R; r += kAttendThreads) mine += row_tiles<TILE>(attend_row(c, a, r));
+    total = block_scan<kAttendThreads>(mine, &before, scan);
+    const int64_t work = total * units, ctas = run_ctas(work, gridDim.x);
+    if (work == 0 || blockIdx.x >= ctas) return;
+    const int64_t begin = run_begin(blockIdx.x, work, ctas), end = run_begin(blockIdx.x + 1, work, ctas);
+    int64_t base = 0;
+    for (int64_t r0 = 0; r0 < a.R; r0 += kAttendThreads) {
+        const int64_t r = r0 + threadIdx.x;
+        const int64_t t = r < a.R ? row_tiles<TILE>(attend_row(c, a, r)) : 0;
+        const int64_t sum = block_scan<kAttendThreads>(t, &before, scan);
+        const int64_t at = begin / units;
+        if (base + before <= at && at < base + before + t) where[0] = r, where[1] = base + before;
+        base += sum;
+        if (at < base) break;
+    }
+    __syncthreads();
+    int64_t r = where[0], g = begin, row_start = where[1] * units;  // the row's first tile in the list
+
+    uint8_t* ring = smem + warp * S::kRing;
+    const uint32_t ring_u = smem_u32(ring);
+    while (g < end) {
+        const RowRange x = attend_row(c, a, r);
+        const int64_t tiles = row_tiles<TILE>(x);
+        if (tiles == 0 || g >= row_start + tiles * units) {
+            row_start += tiles * units;
+            r++;
+            continue;
+        }
+        const int u = (int)((g - row_start) / tiles);
+        const int64_t ta = g - row_start - u * tiles;
+        const int64_t tb = tiles - ta < end - g ? tiles : ta + (end - g);
+        g += tb - ta;
+        const int kvh = u / a.blocks, hb = u - kvh * a.blocks;
+        const int head0 = kvh * a.G + hb * kAttendHeads;
+        const int heads = a.G - hb * kAttendHeads < kAttendHeads ? a.G - hb * kAttendHeads : kAttendHeads;
+        const int64_t tile0 = x.first / TILE;
+
+        // the pages of this lane's position in the warp's i-th tile
+        const int mask_o = (1 << c.page_shift) - 1;
+        auto page_at = [&](int64_t t) -> int {
+            const int64_t p = (tile0 + t) * TILE + lane;
+            if (lane >= TILE || t >= tb || p < x.first || p >= x.len) return -1;
+            const int id = kv_page_of(c, x.seq, p);
+            if (id < 0) atomicOr(&g_attend_error, kErrPlace);
+            return id;
+        };
+        auto issue = [&](int64_t t, int id, int slot) {
+            if (t < tb) {
+                const uint32_t dst = ring_u + slot * S::kStage;
+                const int p0 = (int)((tile0 + t) * TILE) & mask_o;  // TILE and the page size are powers of two
+                const uint32_t live = __ballot_sync(0xFFFFFFFFu, id >= 0);
+                if (lane == 0) *reinterpret_cast<uint32_t*>(ring + slot * S::kStage + 2 * TILE * ROW + 8 * TILE) = live;
+#pragma unroll
+                for (int it = 0; it < TILE * kChunks / 32; it++) {
+                    const int i = it * 32 + lane, row = i / kChunks, ch = i % kChunks;
+                    const int pid = __shfl_sync(0xFFFFFFFFu, id, row);
+                    int bytes = (pid >= 0 && ch * 16 < c.row_bytes) ? 16 : 0;
+                    int64_t at = bytes ? kv_row_at(c, pid, kvh, (p0 + row) & mask_o) + ch * 16 : 0;
+                    if (!QMM_IN_BOUNDS(g_attend_error, at + 15, c.num_pages * c.stride)) at = 0, bytes = 0;
+                    const int ck = ROW >= 128 ? ch ^ ((row >> 2 & 1) << 2) : ch;
+                    const int cv = ROW >= 128 ? ch ^ ((row & 3) << 1) : ch ^ ((row >> 1 & 1) << 1);
+                    cp_async16(dst + row * ROW + ck * 16, c.k + at, bytes);
+                    cp_async16(dst + (TILE + row) * ROW + cv * 16, c.v + at, bytes);
+                }
+                if (TYPE == QMM_KV_Q8 && lane < TILE) {
+                    int bytes = id >= 0 ? 4 : 0;
+                    int64_t at = bytes ? kv_scale_at(c, id, kvh, (p0 + lane) & mask_o) : 0;
+                    if (!QMM_IN_BOUNDS(g_attend_error, at + 3, c.num_pages * c.stride)) at = 0, bytes = 0;
+                    cp_async4z(dst + 2 * TILE * ROW + 4 * lane, c.k + at, bytes);
+                    cp_async4z(dst + 2 * TILE * ROW + 4 * TILE + 4 * lane, c.v + at, bytes);
+                }
+            }
+            cp_async_commit();  // an empty group where there is no tile: the wait counts groups
+        };
+
+        // fill the ring, then fetch the queries under its copies
+        int64_t next = ta + warp;
+        int id = page_at(next);
+#pragma unroll
+        for (int s = 0; s < S::kStages - 1; s++) {
+            const int id1 = page_at(next + kAttendWarps);
+            issue(next, id, s);
+            id = id1;
+            next += kAttendWarps;
+        }
+
+        // A operand of the first product: step s of lane j holds values
+        // kPer * (j + 4 * (s / (kPer / 4))) + 4 * (s % (kPer / 4)) .. + 3 of head n
+        uint32_t qf[kSteps][4];
+        float q_scale;
+        {
+            float4 qv[kSteps];
+            float amax = 0.0f;
+            const float* qh = a.q + r * a.ldq + (int64_t)(head0 + n) * c.hd;
+#pragma unroll
+            for (int s = 0; s < kSteps; s++) {
+                const int d = kPer * (j + 4 * (s / (kPer / 4))) + 4 * (s % (kPer / 4));
+                qv[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (n < heads && d < c.hd &&
+                    QMM_IN_BOUNDS(g_attend_error, r * a.ldq + (int64_t)(head0 + n) * c.hd + d + 3, a.R * a.ldq))
+                    qv[s] = __ldg(reinterpret_cast<const float4*>(qh + d));
+                amax = fmaxf(amax, fmaxf(fmaxf(fabsf(qv[s].x), fabsf(qv[s].y)), fmaxf(fabsf(qv[s].z), fabsf(qv[s].w))));
+            }
+            amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+            const int e = exponent_of(__float_as_uint(amax));
+            const float up = pow2i(14 - e);
+            q_scale = a.scale * 1.44269504088896341f * pow2i(e - 14);  // scores in base 2
+#pragma unroll
+            for (int s = 0; s < kSteps; s++) {
+                split_h2(qv[s].x * up, qv[s].y * up, &qf[s][0], &qf[s][1]);
+                split_h2(qv[s].z * up, qv[s].w * up, &qf[s][2], &qf[s][3]);
+            }
+        }
+
+        float m_run = -INFINITY, l_run = 0.0f;  // of head n; l_run of this lane's positions
+        float o[kSets][kVD][2];
+#pragma unroll
+        for (int s = 0; s < kSets; s++)
+#pragma unroll
+            for (int t = 0; t < kVD; t++) o[s][t][0] = o[s][t][1] = 0.0f;
+
+        int slot = 0;
+        for (int64_t t = ta + warp; t < tb; t += kAttendWarps) {
+            cp_async_wait<S::kStages - 2>();
+            __syncwarp();  // the tile is here for every lane, and the slot before it is read out
+            {
+                const int id1 = page_at(next + kAttendWarps);
+                issue(next, id, slot == 0 ? S::kStages - 1 : slot - 1);
+                id = id1;
+                next += kAttendWarps;
+            }
+            const uint32_t st = ring_u + slot * S::kStage;
+            const float* scales = reinterpret_cast<const float*>(ring + slot * S::kStage + 2 * TILE * ROW);
+            const uint32_t live = *reinterpret_cast<const uint32_t*>(scales + 2 * TILE);
+
+            // scores: column i of n-tile m is position 16 (m / 2) + 8 (m % 2) + i / 2 + 4 (i % 2)
+            float sc[TILE / 8][4];
+#pragma unroll
+            for (int m = 0; m < TILE / 8; m++) sc[m][0] = sc[m][1] = sc[m][2] = sc[m][3] = 0.0f;
+#pragma unroll
+            for (int cg = 0; cg < kGroups; cg++) {
+                uint4 kw[TILE / 8];
+#pragma unroll
+                for (int m = 0; m < TILE / 8; m++) {
+                    const int row = 8 * m + (n >> 1) + 4 * (n & 1);
+                    const int ch = ROW >= 128 ? (4 * cg + j) ^ ((n & 1) << 2) : 4 * cg + j;
+                    kw[m] = lds128(st + row * ROW + ch * 16);
+                }
+#pragma unroll
+                for (int w = 0; w < kPer / 4; w++) {
+#pragma unroll
+                    for (int m = 0; m < TILE / 8; m++) {
+                        const uint32_t* f = reinterpret_cast<const uint32_t*>(&kw[m]);
+                        uint32_t b0, b1;
+                        if (TYPE == QMM_KV_Q8) {
+                            const uint32_t y = f[w] ^ 0x80808080u;
+                            b0 = codes_h2(y, 0x4140u), b1 = codes_h2(y, 0x4342u);
+                        } else {
+                            b0 = f[2 * w], b1 = f[2 * w + 1];
+                        }
+                        mma_f16(sc[m], qf[cg * (kPer / 4) + w], b0, b1);
+                    }
+                }
+            }
+            // weights: this lane has positions 8 m + j and 8 m + j + 4 of head n
+            float wt[TILE / 8][2], top = -INFINITY;
+#pragma unroll
+            for (int m = 0; m < TILE / 8; m++)
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    const int p = 8 * m + j + 4 * i;
+                    const float ks = TYPE == QMM_KV_Q8 ? scales[p] * q_scale : q_scale;
+                    wt[m][i] = (live >> p & 1u) ? (sc[m][i] + sc[m][i + 2]) * ks : -INFINITY;
+                    top = fmaxf(top, wt[m][i]);
+                }
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+            const float m_new = fmaxf(m_run, top);
+            const float m_at = m_new == -INFINITY ? 0.0f : m_new;  // nothing seen yet: every weight is 0
+            const float keep = exp2_approx(m_run - m_at);
+            m_run = m_new;
+            l_run *= keep;
+            float up = 16384.0f, down = 1.0f / 16384.0f;
+            if (TYPE == QMM_KV_Q8) {
+                const uint32_t bits = lane < TILE ? __float_as_uint(scales[TILE + lane]) & 0x7FFFFFFFu : 0u;
+                const int e = exponent_of(__reduce_max_sync(0xFFFFFFFFu, bits));
+                up = pow2i(14 - e), down = pow2i(e - 14);
+            }
+            uint32_t pf[TILE / 16][4];
+#pragma unroll
+            for (int m = 0; m < TILE / 8; m++) {
+                float cv[2];
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    const int p = 8 * m + j + 4 * i;
+                    const float w = exp2_approx(wt[m][i] - m_at);
+                    l_run += w;
+                    cv[i] = (TYPE == QMM_KV_Q8 ? w * scales[TILE + p] : w) * up;
+                }
+                split_h2(cv[0], cv[1], &pf[m >> 1][2 * (m & 1)], &pf[m >> 1][2 * (m & 1) + 1]);
+            }
+            // values: column n of n-tile (set, t) is value 8 kVD set + kVD n + t; fresh
+            // sums per tile, added to the running ones by f32 FMAs (the tensor core's own
+            // additions cut off instead of rounding: over a long cache that would add up)
+#pragma unroll
+            for (int s = 0; s < kSets; s++) {
+                float acc[kVD][4];
+#pragma unroll
+                for (int t2 = 0; t2 < kVD; t2++) acc[t2][0] = acc[t2][1] = acc[t2][2] = acc[t2][3] = 0.0f;
+#pragma unroll
+                for (int b = 0; b < TILE / 16; b++) {
+                    uint32_t vw[4][kVB / 4];
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const uint32_t vr = st + (TILE + 16 * b + j + 4 * i) * ROW;
+                        if (kVB == 16) {
+                            const uint4 y = lds128(vr + (((8 * s + n) ^ (j << 1)) << 4));
+                            vw[i][0] = y.x, vw[i][1] = y.y, vw[i][kVB / 4 - 2] = y.z, vw[i][kVB / 4 - 1] = y.w;
+                        } else {
+                            const uint32_t at = vr + (((n >> 1) ^ (j & 2)) << 4) + ((n & 1) << 3);
+                            vw[i][0] = lds32(at), vw[i][1] = lds32(at + 4);
+                        }
+                    }
+#pragma unroll
+                    for (int w = 0; w < kVB / 4; w++) {
+                        if (TYPE == QMM_KV_Q8) {
+                            const uint32_t w0 = vw[0][w] ^ 0x80808080u, w1 = vw[1][w] ^ 0x80808080u;
+                            const uint32_t w2 = vw[2][w] ^ 0x80808080u, w3 = vw[3][w] ^ 0x80808080u;
+                            const uint32_t al = __byte_perm(w0, w1, 0x5140u), ah = __byte_perm(w0, w1, 0x7362u);
+                            const uint32_t bl = __byte_perm(w2, w3, 0x5140u), bh = __byte_perm(w2, w3, 0x7362u);
+                            mma_f16(acc[(4 * w) % kVD], pf[b], codes_h2(al, 0x4140u), codes_h2(bl, 0x4140u));
+                            mma_f16(acc[(4 * w + 1) % kVD], pf[b], codes_h2(al, 0x4342u), codes_h2(bl, 0x4342u));
+                            mma_f16(acc[(4 * w + 2) % kVD], pf[b], codes_h2(ah, 0x4140u), codes_h2(bh, 0x4140u));
+                            mma_f16(acc[(4 * w + 3) % kVD], pf[b], codes_h2(ah, 0x4342u), codes_h2(bh, 0x4342u));
+                        } else {
+                            mma_f16(acc[2 * w], pf[b], __byte_perm(vw[0][w], vw[1][w], 0x5410u),
+                                    __byte_perm(vw[2][w], vw[3][w], 0x5410u));
+                            mma_f16(acc[2 * w + 1], pf[b], __byte_perm(vw[0][w], vw[1][w], 0x7632u),
+                                    __byte_perm(vw[2][w], vw[3][w], 0x7632u));
+                        }
+                    }
+                }
+#pragma unroll
+                for (int t2 = 0; t2 < kVD; t2++)
+#pragma unroll
+                    for (int i = 0; i < 2; i++)
+                        o[s][t2][i] = __fmaf_rn(o[s][t2][i], keep, down * (acc[t2][i] + acc[t2][i + 2]));
+            }
+            slot = slot == S::kStages - 1 ? 0 : slot + 1;
+        }
+
+        // the warps meet: running maxima and sums, then the values through shared memory
+        l_run += __shfl_xor_sync(0xFFFFFFFFu, l_run, 1);
+        l_run += __shfl_xor_sync(0xFFFFFFFFu, l_run, 2);
+        if (j == 0) part_m[warp][n] = m_run, part_l[warp][n] = l_run;
+        cp_async_wait<0>();
+        __syncthreads();  // every ring is read out: its memory is the exchange now
+        float* xo = reinterpret_cast<float*>(smem) + warp * kAttendHeads * HDT;
+#pragma unroll
+        for (int s = 0; s < kSets; s++)
+#pragma unroll
+            for (int i = 0; i < 2; i++)
+#pragma unroll
+                for (int t = 0; t < kVD; t += 4)
+                    *reinterpret_cast<float4*>(xo + n * HDT + 8 * kVD * s + kVD * (2 * j + i) + t) =
+                        make_float4(o[s][t][i], o[s][t + 1][i], o[s][t + 2][i], o[s][t + 3][i]);
+        const bool whole = ta == 0 && tb == tiles;
+        float* part = a.parts + (2 * (int64_t)blockIdx.x + (ta == 0 ? 1 : 0)) * (kAttendHeads * (c.hd + 2));
+        if (threadIdx.x < heads) {
+            const int h = threadIdx.x;
+            float m = -INFINITY, l = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kAttendWarps; w++) m = fmaxf(m, part_m[w][h]);
+            const float at = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+            for (int w = 0; w < kAttendWarps; w++) {
+                part_f[w][h] = exp2_approx(part_m[w][h] - at);
+                l += part_l[w][h] * part_f[w][h];
+            }
+            unit_l[h] = l;
+            if (!whole) {
+                part[kAttendHeads * c.hd + h] = m;
+                part[kAttendHeads * c.hd + kAttendHeads + h] = l;
+            } else if (a.lse && QMM_IN_BOUNDS(g_attend_error, r * (a.G * c.Hkv) + head0 + h, a.R * a.G * c.Hkv)) {
+                a.lse[r * (a.G * c.Hkv) + head0 + h] = (m + log2f(l)) * 0.693147180559945309f;
+            }
+        }
+        __syncthreads();
+        const int quads = c.hd >> 2;
+        for (int i = threadIdx.x; i < heads * quads; i += kAttendThreads) {
+            const int h = i / quads, d = 4 * (i - h * quads);
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kAttendWarps; w++) {
+                const float4 z = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(smem) +
+                                                                  (w * kAttendHeads + h) * HDT + d);
+                const float f = part_f[w][h];
+                y.x = __fmaf_rn(z.x, f, y.x), y.y = __fmaf_rn(z.y, f, y.y);
+                y.z = __fmaf_rn(z.z, f, y.z), y.w = __fmaf_rn(z.w, f, y.w);
+            }
+            if (whole) {
+                const float l = unit_l[h], inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+                y.x *= inv, y.y *= inv, y.z *= inv, y.w *= inv;
+                if (QMM_IN_BOUNDS(g_attend_error, r * a.ldo + (int64_t)(head0 + h) * c.hd + d + 3, a.R * a.ldo))
+                    *reinterpret_cast<float4*>(a.out + r * a.ldo + (int64_t)(head0 + h) * c.hd + d) = y;
+            } else {
+                *reinterpret_cast<float4*>(part + h * c.hd + d) = y;
+            }
+        }
+        __syncthreads();  // the exchange is read out
+    }
+    pdl_launch_dependents();
+}
+
+// One CTA per (row, query head): where the head's unit lies in several runs, their
+// parts are joined; a row without positions gets zeros and -inf.  Warp w adds parts
+// w, w + kJoinWarps, ... in order, then the warps' sums in order.
+__global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(KvPages c, AttendArgs a, int tile, int grid) {
+    __shared__ int64_t scan[kJoinWarps];
+    __shared__ float factor[kAttendMaxCtas], red[kJoinWarps], sum[kJoinWarps][kHeadMax];
+    pdl_wait();
+    constexpr int kThreads = 32 * kJoinWarps;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int Hq = a.G * c.Hkv, units = c.Hkv * a.blocks;
+    const int64_t r = blockIdx.x / Hq;
+    const int head = (int)(blockIdx.x - r * Hq), kvh = head / a.G, in = head - kvh * a.G;
+    const int u = kvh * a.blocks + in / kAttendHeads, hl = in % kAttendHeads;
+    if (__ldg(a.lens + r) < 0) return;  // a padding row: left as it was
+    auto tiles_of = [&](int64_t row) {
+        const RowRange x = attend_row(c, a, row);
+        return tile == 32 ? row_tiles<32>(x) : row_tiles<16>(x);
+    };
+    int64_t mine = 0, mine_before = 0, before;
+    for (int64_t i = threadIdx.x; i < a.R; i += kThreads) {
+        const int64_t t = tiles_of(i);
+        mine += t;
+        if (i < r) mine_before += t;
+    }
+    const int64_t total = block_scan<kThreads>(mine, &before, scan);
+    const int64_t ahead = block_scan<kThreads>(mine_before, &before, scan);
+    const int64_t tiles = tiles_of(r), work = total * units;
+    float* out = a.out + r * a.ldo + (int64_t)head * c.hd;
+    if (tiles == 0) {
+        for (int d = threadIdx.x; d < c.hd; d += kThreads) out[d] = 0.0f;
+        if (a.lse && threadIdx.x == 0) a.lse[r * Hq + head] = -INFINITY;
+        return;
+    }
+    const int64_t ctas = run_ctas(work, grid), g0 = ahead * units + u * tiles;
+    const int64_t c0 = run_of(g0, work, ctas), c1 = run_of(g0 + tiles - 1, work, ctas);
+    if (c0 == c1) return;  // written by that run's CTA
+    const int n = (int)(c1 - c0 + 1);
+    const int64_t size = kAttendHeads * (c.hd + 2);
+    auto part = [&](int i) -> const float* {  // the unit begins in run c0, the others continue it
+        return a.parts + (2 * (c0 + i) + (i == 0 ? 1 : 0)) * size;
+    };
+    float m = -INFINITY;
+    for (int i = threadIdx.x; i < n; i += kThreads) m = fmaxf(m, part(i)[kAttendHeads * c.hd + hl]);
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
+    if (lane == 0) red[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; w++) m = fmaxf(m, red[w]);
+    const float at = m == -INFINITY ? 0.0f : m;
+    for (int i = threadIdx.x; i < n; i += kThreads)
+        if (QMM_IN_BOUNDS(g_attend_error, i, kAttendMaxCtas))
+            factor[i] = exp2_approx(part(i)[kAttendHeads * c.hd + hl] - at);
+    __syncthreads();
+    float l = 0.0f;
+    for (int i = 0; i < n; i++) l = __fmaf_rn(part(i)[kAttendHeads * c.hd + kAttendHeads + hl], factor[i], l);
+    for (int d0 = 4 * lane; d0 < c.hd; d0 += 128) {
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int i = warp; i < n; i += kJoinWarps) {
+            const float4 z = *reinterpret_cast<const float4*>(part(i) + hl * c.hd + d0);
+            const float f = factor[i];
+            y.x = __fmaf_rn(z.x, f, y.x), y.y = __fmaf_rn(z.y, f, y.y);
+            y.z = __fmaf_rn(z.z, f, y.z), y.w = __fmaf_rn(z.w, f, y.w);
+        }
+        *reinterpret_cast<float4*>(&sum[warp][d0]) = y;
+    }
+    __syncthreads();
+    const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+    for (int d = threadIdx.x; d < c.hd; d += kThreads) {
+        float y = sum[0][d];
+#pragma unroll
+        for (int w = 1; w < kJoinWarps; w++) y += sum[w][d];
+        out[d] = y * inv;
+    }
+    if (a.lse && threadIdx.x == 0) a.lse[r * Hq + head] = (m + log2f(l)) * 0.693147180559945309f;
+    pdl_launch_dependents();
+}
+
+}  // namespace qmm
+
+using namespace qmm;
+
+extern "C" {
+
+unsigned qmm_internal_attend_error(int clear) {
+    unsigned v = 0;
+    cudaMemcpyFromSymbol(&v, g_attend_error, sizeof(v));
+    if (clear) {
+        const unsigned z = 0;
+        cudaMemcpyToSymbol(g_attend_error, &z, sizeof(z));
+    }
+    return v;
+}
+
+size_t qmm_kv_attend_scratch_bytes(int64_t Hq, int64_t Hkv, int64_t hd) {
+    if (!head_dim_ok(hd) || Hkv < 1 || Hkv > 1024 || Hq < 1 || Hq % Hkv || Hq / Hkv > 64) return 0;
+    return (size_t)kAttendMaxCtas * 2 * kAttendHeads * (size_t)(hd + 2) * sizeof(float);
+}
+
+qmm_status qmm_kv_attend(const qmm_kv_pages* cache, const float* q, int64_t ldq, const int32_t* lens,
+                         const int32_t* seq, float* out, int64_t ldo, float* lse, void* scratch, size_t scratch_bytes,
+                         int64_t R, int64_t Hq, float scale, int64_t window, qmm_stream_t stream) {
+    if (!q || !lens || !out || !scratch) return QMM_E_NULL;
+    KvPages c;
+    qmm_status st = kv_pages_check(cache, &c);
+    if (st != QMM_OK) return st;
+    const size_t need = qmm_kv_attend_scratch_bytes(Hq, c.Hkv, c.hd);
+    if (need == 0 || R < 1 || R * Hq > kMaxDim || R > kMaxDim || (!seq && R > c.num_seqs) || window < 0 ||
+        !row_stride_ok(ldq, Hq * c.hd) || !row_stride_ok(ldo, Hq * c.hd))
+        return QMM_E_SHAPE;
+    if (!aligned16(q) || !aligned16(out) || !aligned4(lens) || !aligned4(seq) || !aligned4(lse) || !aligned16(scratch))
+        return QMM_E_ALIGN;
+    if (scratch_bytes < need) return QMM_E_SCRATCH;
+    AttendArgs a;
+    a.q = q, a.lens = lens, a.seq = seq, a.out = out, a.lse = lse, a.parts = (float*)scratch;
+    a.R = R, a.ldq = ldq, a.ldo = ldo, a.window = window;
+    a.G = (int)(Hq / c.Hkv);
+    a.blocks = (a.G + kAttendHeads - 1) / kAttendHeads;
+    a.scale = scale;
+    DeviceInfo dev;
+    st = current_device(&dev);
+    if (st != QMM_OK) return st;
+    const cudaStream_t cs = (cudaStream_t)stream;
+    int tile = 0, grid = 0;
+    auto go = [&](auto type, auto hdt) -> qmm_status {
+        constexpr int TYPE = decltype(type)::value, HDT = decltype(hdt)::value;
+        using S = AttendShape<TYPE, HDT>;
+        static PerDeviceOnce once;
+        const qmm_status set = once.run(dev.device, [&] {
+            return cudaFuncSetAttribute(attend_kernel<TYPE, HDT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        S::kSmem) == cudaSuccess ? QMM_OK : QMM_E_CUDA;
+        });
+        if (set != QMM_OK) return set;
+        tile = S::kTile, grid = S::kCtas * kAttendSms;
+        return launch_pdl(attend_kernel<TYPE, HDT>, dim3((unsigned)grid), kAttendThreads, S::kSmem, cs, c, a);
+    };
+    using std::integral_constant;
+    auto by_width = [&](auto type) -> qmm_status {
+        if (c.hd <= 64) return go(type, integral_constant<int, 64>());
+        if (c.hd <= 128) return go(type, integral_constant<int, 128>());
+        return go(type, integral_constant<int, 256>());
+    };
+    st = cache->type == QMM_KV_Q8 ? by_width(integral_constant<int, QMM_KV_Q8>())
+                                  : by_width(integral_constant<int, QMM_KV_F16>());
+    if (st != QMM_OK) return st;
+    return launch_pdl(attend_join_kernel, dim3((unsigned)(R * Hq)), 32 * kJoinWarps, 0, cs, c, a, tile, grid);
+}
+
+}  // extern "C"

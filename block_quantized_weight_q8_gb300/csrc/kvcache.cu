@@ -334,27 +334,6 @@ static qmm_status kv_heads_ok(int64_t Hq, int64_t Hkv, int64_t P) {
     return QMM_OK;
 }
 
-static bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
-
-// A programmatic dependent launch: the kernel waits for its predecessor's
-// memory before it reads anything, and lets its successor launch when its own
-// work is done.
-template <typename... KArgs, typename... Args>
-static qmm_status launch_pdl(void (*kern)(KArgs...), dim3 grid, int block, size_t smem, cudaStream_t stream,
-                             Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)block);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...) == cudaSuccess ? QMM_OK : QMM_E_CUDA;
-}
-
 }  // namespace qmm
 
 using namespace qmm;

@@ -17,6 +17,7 @@ constexpr int64_t kMaxK = 65536;
 constexpr int64_t kMaxDim = 2147483647LL;
 
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+inline bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
 inline int block_values_of(int t) {
     switch (t) {
@@ -119,6 +120,32 @@ struct NoWorkspaceAllocScope {
     NoWorkspaceAllocScope() : prev(tl_no_workspace_alloc) { tl_no_workspace_alloc = true; }
     ~NoWorkspaceAllocScope() { tl_no_workspace_alloc = prev; }
 };
+
+// Heads: their width, their number, and the stride (in values) of token rows of
+// `values` values that are read and written 16 bytes at a time.
+constexpr int kHeadMax = 256;
+constexpr int64_t kHeadsMax = 65536;
+inline bool head_dim_ok(int64_t hd) { return hd >= 16 && hd <= kHeadMax && hd % 16 == 0; }
+inline bool row_stride_ok(int64_t ld, int64_t values) { return ld >= values && ld % 4 == 0 && ld <= ((int64_t)1 << 32); }
+
+// A programmatic dependent launch: the kernel waits for its predecessor's
+// memory before it reads anything, and lets its successor launch when its own
+// work is done.
+template <typename... KArgs, typename... Args>
+static inline qmm_status launch_pdl(void (*kern)(KArgs...), dim3 grid, int block, size_t smem, cudaStream_t stream,
+                                    Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...) == cudaSuccess ? QMM_OK : QMM_E_CUDA;
+}
 
 inline qmm_status launch_status() {
     return cudaGetLastError() == cudaSuccess ? QMM_OK : QMM_E_CUDA;

@@ -431,6 +431,128 @@ QMM_API size_t qmm_kv_wsum_scratch_bytes(int64_t Hq, int64_t P, int64_t hd);
 QMM_API qmm_status qmm_kv_wsum(const float* w, const void* vc, float* out, void* scratch, size_t scratch_bytes,
                                int64_t Hq, int64_t Hkv, int64_t P, int64_t hd, qmm_stream_t stream);
 
+/* ---- rotary positions ----------------------------------------------------- */
+/* No counterpart on the pages beyond their naming it ([krafla] "Architecture",
+ * "Data flow for one token": q, k = rope(...) between the projections and the
+ * cache).  A position turns each pair (a, b) of a head's first n_rot values:
+ *   a' = m (a cos t - b sin t),  b' = m (a sin t + b cos t),  t = 2 pi p F[i] / 2^64
+ * for pair i = 0 .. n_rot/2 - 1 at position p; the values behind n_rot are copied.
+ *   freqs   F: uint64 [n_rot/2], device, 16-byte aligned: the fraction of a turn
+ *           that a pair advances per position.  qmm_rope_freqs fills it; a caller
+ *           with other frequencies f (radians per position) stores
+ *           round(2^64 * frac(f / 2 pi)).  p F[i] is taken modulo 2^64, so far
+ *           positions cost no accuracy
+ *   layout  QMM_ROPE_HALF pairs value i with i + n_rot/2, QMM_ROPE_INTERLEAVED 2i
+ *           with 2i + 1
+ *   mscale  m (1 for none; the attention factor of QMM_ROPE_YARN)
+ * Each result is the exact value rounded once to f32, but where that lies within
+ * 2^-42 of a rounding border. */
+typedef enum { QMM_ROPE_HALF = 0, QMM_ROPE_INTERLEAVED = 1 } qmm_rope_layout;
+typedef enum { QMM_ROPE_PLAIN = 0, QMM_ROPE_LINEAR = 1, QMM_ROPE_BANDS = 2, QMM_ROPE_YARN = 3 } qmm_rope_scaling;
+typedef struct {
+    const void* freqs;
+    int64_t n_rot;  /* even, 2..hd */
+    int32_t layout;
+    float mscale;
+} qmm_rope_spec;
+
+/* The table of f_i = base^(-2i / n_rot), i < n_rot/2 (n_rot even, at most 256),
+ * computed in binary64 and stretched for a longer context:
+ *   PLAIN   f
+ *   LINEAR  f / factor
+ *   BANDS   (1 - g) f / factor + g f, g = (turns - lo) / (hi - lo) held in 0..1,
+ *           turns = orig_len f / 2 pi the pair's turns in the original context
+ *   YARN    the same blend with g = 1 - (i - first) / (last - first) held in 0..1,
+ *           first and last the pair indices (floor, at least 0, and ceil, at most
+ *           n_rot - 1) that turn hi and lo times in orig_len positions
+ * factor, orig_len, lo < hi are positive and unused where not named. */
+QMM_API qmm_status qmm_rope_freqs(void* freqs, int64_t n_rot, double base, int scaling, double factor, double orig_len,
+                                  double lo, double hi, qmm_stream_t stream);
+
+/* y = x rotated: f32 [T][H][hd], token t at position pos[t] (int32, device; may be
+ * negative).  ldx, ldy: values from one token to the next, multiples of 4, at least
+ * H * hd (a part of a fused projection's row is x with its row's ldx).  y may be x
+ * (then ldy = ldx); otherwise they do not overlap.  inverse != 0 turns by -t: with
+ * the same m that is the transposed map, the gradient of the rotation.
+ * hd: a multiple of 16 in 16..256; H <= 65536. */
+QMM_API qmm_status qmm_rope(const qmm_rope_spec* rope, const float* x, int64_t ldx, float* y, int64_t ldy,
+                            const int32_t* pos, int64_t T, int64_t H, int64_t hd, int inverse, qmm_stream_t stream);
+
+/* ---- the paged KV cache ---------------------------------------------------- */
+/* Additions for serving: a cache in pages that sequences take as they grow, and
+ * the attention over it in one call.  (qmm_kv_quantize, qmm_kv_scores and
+ * qmm_kv_wsum work on one sequence's contiguous rows.)
+ *   pages   pools k and v of num_pages pages, page_stride bytes apart (a multiple of
+ *           16, at least qmm_kv_page_bytes; the two may interleave, or be a slice of
+ *           pages that hold several layers)
+ *   table   int32 [num_seqs][max_pages], device: position p of sequence s lies in
+ *           page table[s][p / page_size] at p % page_size.  Entries behind a
+ *           sequence's last position are not read.
+ *   rows    QMM_KV_Q8: the codes and f32 scale of qmm_kv_quantize, bit for bit;
+ *           QMM_KV_F16: binary16, rounded to nearest even
+ *   a page  row (KV head h, position o) at byte (h * page_size + o) * row, row = hd
+ *           (Q8) or 2 hd (F16); Q8 scales follow all codes: f32 (h, o) at
+ *           Hkv * page_size * hd + 4 * (h * page_size + o)
+ * hd: a multiple of 16 in 16..256; Hkv 1..1024; page_size a power of two up to 4096.
+ * The struct is read by the call; its device pointers stay valid until the stream
+ * has passed it.  k, v 16-byte aligned, int32 arrays and lse 4-byte, every other
+ * device pointer 16-byte.  Token and row strides (ld*) are in values, multiples of
+ * 4, at least heads * hd.
+ * seq: int32, device: the table row of each token (or attention row); NULL: token t
+ * reads row t.  A position or sequence without a place in the table (a page id
+ * outside 0..num_pages - 1 included) makes qmm_device_status() return QMM_E_SHAPE;
+ * such a row is not stored, loads as zeros, and counts as absent in the attention. */
+typedef enum { QMM_KV_Q8 = 0, QMM_KV_F16 = 1 } qmm_kv_type;
+typedef struct {
+    void* k;
+    void* v;
+    const int32_t* table;
+    int64_t num_pages, page_stride;
+    int64_t num_seqs, max_pages;
+    int64_t Hkv, hd;
+    int32_t type, page_size;
+} qmm_kv_pages;
+
+/* Bytes of one pool's page: page_size * Hkv * (hd + 4) or * 2 hd; 0 for a bad argument. */
+QMM_API size_t qmm_kv_page_bytes(int type, int64_t Hkv, int64_t page_size, int64_t hd);
+
+/* Stores the keys and values (f32 [T][Hkv][hd]) of T tokens at positions pos[t] of
+ * their sequences.  With rope, keys are rotated first; with q (which needs rope)
+ * the tokens' query heads (f32 [T][Hq][hd]) are rotated into q_out (which may be q,
+ * ldqo = ldq) by the same launch -- both equal to qmm_rope's result bit for bit.  A
+ * token with pos < 0 is padding: nothing of it is stored or written.  The places of
+ * one call's tokens are distinct: where two name the same one, what that row holds
+ * afterwards is unspecified. */
+QMM_API qmm_status qmm_kv_store(const qmm_kv_pages* cache, const float* k, int64_t ldk, const float* v, int64_t ldv,
+                                const int32_t* pos, const int32_t* seq, int64_t T, const qmm_rope_spec* rope,
+                                const float* q, int64_t ldq, float* q_out, int64_t ldqo, int64_t Hq,
+                                qmm_stream_t stream);
+
+/* The rows at (seq[t], pos[t]) as f32 (d * code, one rounding) into k_out and v_out
+ * ([T][Hkv][hd] each; either may be NULL).  A token with pos < 0 leaves its rows as
+ * they were. */
+QMM_API qmm_status qmm_kv_load(const qmm_kv_pages* cache, const int32_t* pos, const int32_t* seq, int64_t T,
+                               float* k_out, int64_t ldk, float* v_out, int64_t ldv, qmm_stream_t stream);
+
+/* out[r][h] = sum_p w_p v_p, w = softmax over p of scale * (q[r][h] . k_p), p the
+ * positions 0..lens[r] - 1 of row r's sequence (its last `window` of them where
+ * window > 0), the KV head h / (Hq / Hkv); lse[r][h] (f32, may be NULL) the log of
+ * the softmax's sum, natural, with its maximum.  q and out f32 [R][Hq][hd], lens
+ * int32 [R], device.  lens[r] = 0 gives zeros and -inf; lens[r] < 0 is a padding
+ * row, which is left as it was; a length beyond max_pages * page_size is cut there
+ * (status as above).  Several rows may read one sequence (tokens of one step
+ * checked at their own lengths).  Hq a multiple of Hkv, Hq / Hkv <= 64.
+ * q is taken in f32 (split into two f16, 22 bits), sums and the softmax in f32.
+ * The launch does not depend on the lengths, so a captured call serves any; the
+ * order of the sums depends on lens, window and the shapes alone.  scratch: at
+ * least qmm_kv_attend_scratch_bytes(Hq, Hkv, hd) bytes, written before it is read;
+ * calls that may overlap on the GPU take one each. */
+QMM_API size_t qmm_kv_attend_scratch_bytes(int64_t Hq, int64_t Hkv, int64_t hd);
+QMM_API qmm_status qmm_kv_attend(const qmm_kv_pages* cache, const float* q, int64_t ldq, const int32_t* lens,
+                                 const int32_t* seq, float* out, int64_t ldo, float* lse, void* scratch,
+                                 size_t scratch_bytes, int64_t R, int64_t Hq, float scale, int64_t window,
+                                 qmm_stream_t stream);
+
 /* ---- verification hooks (not on the hot path) --------------------------- */
 /* The exact int32 block sums the kernels fold, for bit-exact checking:
  * s[t][o][b] for every token t, row o and block b; Q4_0/Q8_0 give one int32 per
@@ -458,7 +580,8 @@ QMM_API qmm_status qmm_blocksums(int wtype, const void* W, const void* xq, int32
 QMM_API qmm_status qmm_test_wait_timeout(uint64_t limit_ns, qmm_stream_t stream);
 
 /* Reads (and with clear != 0 resets) the device error words that bounded waits
- * (QMM_E_TIMEOUT), qmm_get_rows (QMM_E_SHAPE for an id outside [0, N)) and, in a
+ * (QMM_E_TIMEOUT), qmm_get_rows (QMM_E_SHAPE for an id outside [0, N)), the paged
+ * cache's calls (QMM_E_SHAPE for a position without a page) and, in a
  * bounds-checked build, the kernels' index checks (QMM_E_BOUNDS) set; a timeout
  * is reported first, then a bounds record.  Synchronizes the device.  QMM_OK
  * when nothing was recorded. */
