@@ -137,7 +137,8 @@ def ptr(t) -> int:
 def stream_handle(stream=None) -> int:
     if stream is None:
         import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the handle without a Stream object around it
+        return raw(torch.cuda.current_device()) if raw else int(torch.cuda.current_stream().cuda_stream)
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
@@ -341,31 +342,28 @@ ROPE_SCALINGS = {"plain": 0, "linear": 1, "bands": 2, "yarn": 3}
 
 
 def _on_device(name, t, dtype, ndim):
-    """Checks a tensor that a kernel reads or writes by its shape."""
+    """Checks a tensor that a kernel reads or writes by its shape: type, dimensions, and the current device."""
     import torch
-    if not (t.is_cuda and t.dtype == getattr(torch, dtype) and t.dim() == ndim):
-        raise ValueError("%s: a %d-dimensional CUDA tensor of %s is needed" % (name, ndim, dtype))
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError("%s lies on %s, the current device is cuda:%d" % (name, t.device, torch.cuda.current_device()))
+    if t.dtype is not getattr(torch, dtype) or t.dim() != ndim or t.get_device() != torch.cuda.current_device():
+        raise ValueError("%s: a %d-dimensional tensor of %s on the current device (cuda:%d) is needed, got %d dimensions "
+                         "of %s on %s" % (name, ndim, dtype, torch.cuda.current_device(), t.dim(), t.dtype, t.device))
 
 
-def _heads(name, t, like=None):
+def _heads(name, t, T, H, hd):
     """(address, token stride) of head rows [T][H][hd]: heads side by side, tokens any stride apart."""
     _on_device(name, t, "float32", 3)
-    T, H, hd = t.shape
-    s = t.stride()
-    if like is not None and tuple(t.shape) != tuple(like):
-        raise ValueError("%s: shape %s is needed, got %s" % (name, tuple(like), tuple(t.shape)))
-    if s[2] != 1 or (H > 1 and s[1] != hd):
-        raise ValueError("%s: the heads of a token must be contiguous" % name)
-    return t.data_ptr(), (s[0] if T > 1 else H * hd)
+    s0, s1, s2 = t.stride()
+    if t.shape != (T, H, hd) or s2 != 1 or (s1 != hd and H > 1):
+        raise ValueError("%s: shape %s with the heads of a token contiguous is needed, got %s (strides %s)" % (
+            name, (T, H, hd), tuple(t.shape), (s0, s1, s2)))
+    return t.data_ptr(), (s0 if T > 1 else H * hd)
 
 
 def _ints(name, t, n):
     if t is None:
         return None
     _on_device(name, t, "int32", 1)
-    if t.shape[0] != n or not t.is_contiguous():
+    if t.numel() != n or not t.is_contiguous():
         raise ValueError("%s: %d contiguous values are needed" % (name, n))
     return t.data_ptr()
 
@@ -418,9 +416,10 @@ def qmm_rope_freqs(freqs, base=10000.0, scaling="plain", factor=1.0, orig_len=0.
 
 def qmm_rope(rope, x, y, pos, inverse=False, stream=None):
     """y = x ([T][H][hd] f32) rotated to the positions pos; y may be x."""
-    px, ldx = _heads("x", x)
-    py, ldy = _heads("y", y, x.shape)
+    _on_device("x", x, "float32", 3)
     T, H, hd = x.shape
+    px, ldx = _heads("x", x, T, H, hd)
+    py, ldy = _heads("y", y, T, H, hd)
     _call("qmm_rope", rope.ref, px, ldx, py, ldy, _ints("pos", pos, T), T, H, hd, 1 if inverse else 0,
           stream_handle(stream))
 
@@ -432,23 +431,23 @@ def qmm_kv_page_bytes(type, Hkv, page_size, hd):
 def qmm_kv_store(pages, k, v, pos, seq=None, rope=None, q=None, q_out=None, stream=None):
     """Stores keys k and values v ([T][Hkv][hd] f32) at positions pos of the sequences seq; with rope, keys are rotated
     first, and queries q ([T][Hq][hd]) into q_out."""
-    T = k.shape[0]
-    pk, ldk = _heads("k", k, (T, pages.Hkv, pages.hd))
-    pv, ldv = _heads("v", v, k.shape)
+    T, Hkv, hd = k.shape[0], pages.Hkv, pages.hd
+    pk, ldk = _heads("k", k, T, Hkv, hd)
+    pv, ldv = _heads("v", v, T, Hkv, hd)
     pq = ldq = po = ldo = Hq = 0
     if q is not None:
         Hq = q.shape[1]
-        pq, ldq = _heads("q", q, (T, Hq, pages.hd))
-        po, ldo = _heads("q_out", q_out, q.shape)
+        pq, ldq = _heads("q", q, T, Hq, hd)
+        po, ldo = _heads("q_out", q_out, T, Hq, hd)
     _call("qmm_kv_store", pages.ref, pk, ldk, pv, ldv, _ints("pos", pos, T), _ints("seq", seq, T), T,
           rope.ref if rope is not None else None, pq, ldq, po, ldo, Hq, stream_handle(stream))
 
 
 def qmm_kv_load(pages, pos, k_out=None, v_out=None, seq=None, stream=None):
     """The rows at positions pos of the sequences seq as f32 ([T][Hkv][hd]); either output may be None."""
-    T = pos.shape[0]
-    pk, ldk = _heads("k_out", k_out, (T, pages.Hkv, pages.hd)) if k_out is not None else (None, 0)
-    pv, ldv = _heads("v_out", v_out, (T, pages.Hkv, pages.hd)) if v_out is not None else (None, 0)
+    T, Hkv, hd = pos.shape[0], pages.Hkv, pages.hd
+    pk, ldk = _heads("k_out", k_out, T, Hkv, hd) if k_out is not None else (None, 0)
+    pv, ldv = _heads("v_out", v_out, T, Hkv, hd) if v_out is not None else (None, 0)
     _call("qmm_kv_load", pages.ref, _ints("pos", pos, T), _ints("seq", seq, T), T, pk, ldk, pv, ldv,
           stream_handle(stream))
 
@@ -460,12 +459,12 @@ def qmm_kv_attend_scratch_bytes(Hq, Hkv, hd):
 def qmm_kv_attend(pages, q, lens, out, scratch, scratch_bytes, scale, lse=None, seq=None, window=0, stream=None):
     """out[r] = the attention of query heads q[r] ([R][Hq][hd] f32) over the first lens[r] positions (the last window
     of them) of their sequences; lse ([R][Hq] f32) the log of the softmax's sum."""
-    R, Hq, _ = q.shape
-    pq, ldq = _heads("q", q, (R, Hq, pages.hd))
-    po, ldo = _heads("out", out, q.shape)
+    R, Hq, hd = q.shape[0], q.shape[1], pages.hd
+    pq, ldq = _heads("q", q, R, Hq, hd)
+    po, ldo = _heads("out", out, R, Hq, hd)
     if lse is not None:
         _on_device("lse", lse, "float32", 2)
-        if tuple(lse.shape) != (R, Hq) or not lse.is_contiguous():
+        if lse.shape != (R, Hq) or not lse.is_contiguous():
             raise ValueError("lse: contiguous [R][Hq] is needed")
     _call("qmm_kv_attend", pages.ref, pq, ldq, _ints("lens", lens, R), _ints("seq", seq, R), po, ldo,
           lse.data_ptr() if lse is not None else None, ptr(scratch), int(scratch_bytes), R, Hq, float(scale), int(window),
