@@ -21,13 +21,15 @@
 //           loads of natural rows, and a tile's scores are in the registers where
 //           the second product wants its weights: nothing is shuffled but the
 //           row maximum
-// Running maximum and sum of a softmax (in base 2) per warp: one pass.
+// Running maximum and sum of a softmax (in base 2) per warp: one pass.  The reference
+// is the maximum rounded up to a whole number, so rescaling by it is exact and rare.
 //
 // Split.  The work is the list of (row, unit, tile): a unit is a KV head and up to
-// eight of its query heads, a tile 32 (16) positions.  A fixed number of CTAs each
-// take an equal run of the list, found by a scan of the lengths on the device: a
-// captured launch serves any lengths, ragged batches are balanced to a tile, and a
-// long sequence is spread over the whole GPU.  Within a run a CTA's four warps
+// eight of its query heads, a tile 32 (16) positions; each unit counts as
+// kUnitCost tiles more than it has, which is what starting and finishing one takes.
+// A fixed number of CTAs each take an equal run of the list, found by a scan of the
+// lengths on the device: a captured launch serves any lengths, ragged batches are
+// balanced to a tile, and a long sequence is spread over the whole GPU.  Within a run a CTA's four warps
 // take the tiles of a unit in turn, each through its own ring of asynchronous
 // copies, and meet in shared memory.  A unit that one CTA finishes is written at
 // once; else its parts go to the workspace (at most two per CTA), and the second
@@ -46,6 +48,8 @@ constexpr int kAttendSms = 152;
 constexpr int kAttendHeads = 8;  // query heads per unit
 constexpr int kAttendMaxCtas = 3 * kAttendSms;
 constexpr int kJoinWarps = 8;
+constexpr uint32_t kUnitCost = 8;  // of a unit besides its tiles, in tiles
+constexpr int kFold = 4;           // tiles between two folds of the tensor cores' sums
 
 template <int TYPE, int HDT>
 struct AttendShape {
@@ -72,7 +76,8 @@ struct AttendArgs {
 
 // What row r reads: positions first .. len - 1 of sequence seq.
 struct RowRange {
-    int64_t seq, first, len;
+    int64_t seq;
+    int first, len;
 };
 __device__ __forceinline__ RowRange attend_row(const KvPages& c, const AttendArgs& a, int64_t r) {
     RowRange x;
@@ -86,45 +91,55 @@ __device__ __forceinline__ RowRange attend_row(const KvPages& c, const AttendArg
             x.len = 0;
         } else if (x.len > room) {
             atomicOr(&g_attend_error, kErrPlace);
-            x.len = room;
+            x.len = (int)room;
         }
-        if (a.window > 0 && x.len > a.window) x.first = x.len - a.window;
+        if (a.window > 0 && x.len > a.window) x.first = x.len - (int)a.window;
     }
     return x;
 }
 template <int TILE>
-__device__ __forceinline__ int64_t row_tiles(const RowRange& x) {
-    return x.len > 0 ? (x.len + TILE - 1) / TILE - x.first / TILE : 0;
+__device__ __forceinline__ uint32_t row_tiles(const RowRange& x) {
+    return x.len > 0 ? (uint32_t)(x.len - 1) / TILE + 1u - (uint32_t)x.first / TILE : 0u;
 }
+// A unit's share of the list: its cost, then its tiles.
+__device__ __forceinline__ uint32_t unit_weight(uint32_t tiles) { return tiles ? tiles + kUnitCost : 0u; }
 
-// The run of CTA c out of `ctas` is [run_begin(c), run_begin(c + 1)) of `work`
-// tiles; no more CTAs than leave each a tile per warp.
-__device__ __forceinline__ int64_t run_ctas(int64_t work, int ctas) {
-    const int64_t most = work / kAttendWarps;
-    return most < 1 ? 1 : (most < ctas ? most : ctas);
-}
-__device__ __forceinline__ int64_t run_begin(int64_t c, int64_t work, int64_t ctas) { return c * work / ctas; }
-__device__ __forceinline__ int64_t run_of(int64_t g, int64_t work, int64_t ctas) { return ((g + 1) * ctas - 1) / work; }
+// The list cut into `ctas` runs whose lengths differ by one at most; no more runs
+// than leave each a tile per warp.
+struct Runs {
+    uint32_t ctas, q, rem;
+    __device__ __forceinline__ Runs(uint32_t work, uint32_t most) {
+        const uint32_t fill = work / kAttendWarps;
+        ctas = fill < 1 ? 1 : (fill < most ? fill : most);
+        q = work / ctas;
+        rem = work - q * ctas;
+    }
+    __device__ __forceinline__ uint32_t begin(uint32_t c) const { return c * q + (c < rem ? c : rem); }
+    __device__ __forceinline__ uint32_t of(uint32_t g) const {  // the run that holds position g
+        const uint32_t cut = rem * (q + 1);
+        return g < cut ? g / (q + 1) : rem + (g - cut) / q;
+    }
+};
 
 // Sum over the block of each thread's v; *before: over the threads before this one.
 template <int THREADS>
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* before, int64_t* sums) {
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* before, uint32_t* sums) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t incl = v;
+    uint32_t incl = v;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
-        const int64_t o = __shfl_up_sync(0xFFFFFFFFu, incl, m);
+        const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, incl, m);
         if (lane >= m) incl += o;
     }
+    __syncthreads();  // sums may still be read from the scan before
     if (lane == 31) sums[warp] = incl;
     __syncthreads();
-    int64_t base = 0, total = 0;
+    uint32_t base = 0, total = 0;
 #pragma unroll
     for (int w = 0; w < THREADS / 32; w++) {
         if (w < warp) base += sums[w];
         total += sums[w];
     }
-    __syncthreads();  // sums may be used again
     *before = base + incl - v;
     return total;
 }
@@ -144,6 +159,12 @@ __device__ __forceinline__ float exp2_approx(float x) {  // within 2 units in th
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// the same from a zero sum
+__device__ __forceinline__ void mma_f16_first(float d[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 __device__ __forceinline__ void mma_f16(float d[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
     asm(
@@ -172,11 +193,16 @@ __device__ __forceinline__ uint32_t codes_h2(uint32_t w, uint32_t sel) {
 }
 // 2^e
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
-// e with 2^e <= |x| < 2^(e + 1), held where 2^(14 - e) and 2^(e - 14) are normal
-__device__ __forceinline__ int exponent_of(uint32_t bits) {
-    const int e = (int)((bits & 0x7FFFFFFFu) >> 23);
-    return (e < 20 ? 20 : e) - 127;
+// |x|'s exponent field (e + 127 with 2^e <= |x| < 2^(e + 1)), at least kExpLow so that
+// 2^(14 - e) and 2^(e - 14) are normal
+constexpr int kExpLow = 20;
+__device__ __forceinline__ int exponent_of(float x) {
+    const int e = (int)((__float_as_uint(x) & 0x7FFFFFFFu) >> 23);
+    return e < kExpLow ? kExpLow : e;
 }
+// Where an exchanged value quad q of head h lies in its head's row: quads a lane
+// holds in turn (q / 8 apart) and neighbouring heads in different banks.
+__device__ __forceinline__ int exchange_quad(int h, int q) { return q ^ ((q >> 3) & 7) ^ ((h & 1) << 2); }
 
 template <int TYPE, int HDT>
 __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
@@ -189,94 +215,134 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
     constexpr int kGroups = kChunks / 4, kSteps = HDT / 16;
     constexpr int kVB = ROW >= 128 ? 16 : 8;             // bytes of a value row that a lane takes at once
     constexpr int kSets = ROW / (8 * kVB), kVD = kVB / kSize;
+    constexpr int kChains = TILE == 16 ? 2 : 1;  // sums of the first product that run side by side
+    constexpr bool kKeep = HDT <= 128;           // the second product's sums stay in registers between tiles
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ int64_t scan[kAttendWarps];
-    __shared__ int64_t where[2];  // the run's first row, and the tiles before it
+    __shared__ uint32_t scan[kAttendWarps], where[2];  // the run's first row, and the list's length before it
     __shared__ float part_m[kAttendWarps][kAttendHeads], part_l[kAttendWarps][kAttendHeads];
     __shared__ float part_f[kAttendWarps][kAttendHeads], unit_l[kAttendHeads];
     pdl_wait();
+    pdl_launch_dependents();  // the join is launched now and waits for this grid
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = lane >> 2, j = lane & 3;
-    const int units = c.Hkv * a.blocks;
+    const uint32_t units = c.Hkv * a.blocks;
 
     // the run: total work, then the row in which it begins
-    int64_t mine = 0, before, total;
-    for (int64_t r = threadIdx.x; r < a.R; r += kAttendThreads) mine += row_tiles<TILE>(attend_row(c, a, r));
+    const uint32_t R = (uint32_t)a.R;
+    uint32_t mine = 0, before, total;
+    for (uint32_t r = threadIdx.x; r < R; r += kAttendThreads)
+        mine += unit_weight(row_tiles<TILE>(attend_row(c, a, r)));
     total = block_scan<kAttendThreads>(mine, &before, scan);
-    const int64_t work = total * units, ctas = run_ctas(work, gridDim.x);
-    if (work == 0 || blockIdx.x >= ctas) return;
-    const int64_t begin = run_begin(blockIdx.x, work, ctas), end = run_begin(blockIdx.x + 1, work, ctas);
-    int64_t base = 0;
-    for (int64_t r0 = 0; r0 < a.R; r0 += kAttendThreads) {
-        const int64_t r = r0 + threadIdx.x;
-        const int64_t t = r < a.R ? row_tiles<TILE>(attend_row(c, a, r)) : 0;
-        const int64_t sum = block_scan<kAttendThreads>(t, &before, scan);
-        const int64_t at = begin / units;
-        if (base + before <= at && at < base + before + t) where[0] = r, where[1] = base + before;
-        base += sum;
-        if (at < base) break;
+    if (total == 0) return;
+    const Runs runs(total * units, gridDim.x);
+    if (blockIdx.x >= runs.ctas) return;
+    const uint32_t begin = runs.begin(blockIdx.x), end = runs.begin(blockIdx.x + 1), at = begin / units;
+    if (R <= kAttendThreads) {
+        if (before <= at && at < before + mine) where[0] = threadIdx.x, where[1] = before;
+    } else {
+        uint32_t base = 0;
+        for (uint32_t r0 = 0; r0 < R && base <= at; r0 += kAttendThreads) {
+            const uint32_t r = r0 + threadIdx.x;
+            const uint32_t t = r < R ? unit_weight(row_tiles<TILE>(attend_row(c, a, r))) : 0;
+            const uint32_t sum = block_scan<kAttendThreads>(t, &before, scan);
+            if (base + before <= at && at < base + before + t) where[0] = r, where[1] = base + before;
+            base += sum;
+        }
     }
     __syncthreads();
-    int64_t r = where[0], g = begin, row_start = where[1] * units;  // the row's first tile in the list
+    uint32_t r = where[0], g = begin, row_start = where[1] * units;
 
     uint8_t* ring = smem + warp * S::kRing;
     const uint32_t ring_u = smem_u32(ring);
+    // where this lane's chunk of the it-th copy goes in a tile (swizzled so that both
+    // products' 16-byte loads are free of bank conflicts), but for the part of the
+    // swizzle that depends on `it`
+    constexpr int kRowsPer = 32 / kChunks > 0 ? 32 / kChunks : 1;  // rows of one copy instruction
+    const int c_row = lane / kChunks, c_ch = lane % kChunks;
+    auto put_k = [&](int it) {
+        const int row = it * kRowsPer + c_row;
+        return row * ROW + (ROW >= 128 ? c_ch ^ ((row >> 2 & 1) << 2) : c_ch) * 16;
+    };
+    auto put_v = [&](int it) {
+        const int row = it * kRowsPer + c_row;
+        return row * ROW + (ROW >= 128 ? c_ch ^ ((row & 3) << 1) : c_ch ^ ((row >> 1 & 1) << 1)) * 16;
+    };
+    const bool wide = c.hd == HDT && c.page_shift >= 4;  // rows fill their tile's, sixteen of them share a page
+    const int mask_o = (1 << c.page_shift) - 1;
     while (g < end) {
         const RowRange x = attend_row(c, a, r);
-        const int64_t tiles = row_tiles<TILE>(x);
-        if (tiles == 0 || g >= row_start + tiles * units) {
-            row_start += tiles * units;
+        const uint32_t tiles = row_tiles<TILE>(x), weight = unit_weight(tiles);
+        if (tiles == 0 || g >= row_start + weight * units) {
+            row_start += weight * units;
             r++;
             continue;
         }
-        const int u = (int)((g - row_start) / tiles);
-        const int64_t ta = g - row_start - u * tiles;
-        const int64_t tb = tiles - ta < end - g ? tiles : ta + (end - g);
-        g += tb - ta;
-        const int kvh = u / a.blocks, hb = u - kvh * a.blocks;
+        const uint32_t u = (g - row_start) / weight, off = g - row_start - u * weight;
+        const uint32_t take = weight - off < end - g ? weight - off : end - g;
+        const int ta = off > kUnitCost ? (int)(off - kUnitCost) : 0;
+        const int tb = off + take > kUnitCost ? (int)(off + take - kUnitCost) : 0;
+        g += take;
+        if (ta == tb) continue;
+        const int kvh = (int)u / a.blocks, hb = (int)u - kvh * a.blocks;
         const int head0 = kvh * a.G + hb * kAttendHeads;
         const int heads = a.G - hb * kAttendHeads < kAttendHeads ? a.G - hb * kAttendHeads : kAttendHeads;
-        const int64_t tile0 = x.first / TILE;
+        const int tile0 = x.first / TILE;
+        const int32_t* pages = c.table + x.seq * c.max_pages;
 
-        // the pages of this lane's position in the warp's i-th tile
-        const int mask_o = (1 << c.page_shift) - 1;
-        auto page_at = [&](int64_t t) -> int {
-            const int64_t p = (tile0 + t) * TILE + lane;
+        // the page of this lane's position in tile t
+        auto page_at = [&](int t) -> int {
+            const int p = (tile0 + t) * TILE + lane;
             if (lane >= TILE || t >= tb || p < x.first || p >= x.len) return -1;
-            const int id = kv_page_of(c, x.seq, p);
-            if (id < 0) atomicOr(&g_attend_error, kErrPlace);
+            const int id = __ldg(pages + (p >> c.page_shift));
+            if ((unsigned)id >= (unsigned)c.num_pages) {
+                atomicOr(&g_attend_error, kErrPlace);
+                return -1;
+            }
             return id;
         };
-        auto issue = [&](int64_t t, int id, int slot) {
+        auto issue = [&](int t, int id, int slot) {
             if (t < tb) {
                 const uint32_t dst = ring_u + slot * S::kStage;
-                const int p0 = (int)((tile0 + t) * TILE) & mask_o;  // TILE and the page size are powers of two
+                const int p0 = ((tile0 + t) * TILE) & mask_o;  // TILE and the page size are powers of two
                 const uint32_t live = __ballot_sync(0xFFFFFFFFu, id >= 0);
                 if (lane == 0) *reinterpret_cast<uint32_t*>(ring + slot * S::kStage + 2 * TILE * ROW + 8 * TILE) = live;
+                if (wide && live == (TILE == 32 ? 0xFFFFFFFFu : 0xFFFFu)) {
 #pragma unroll
-                for (int it = 0; it < TILE * kChunks / 32; it++) {
-                    const int i = it * 32 + lane, row = i / kChunks, ch = i % kChunks;
-                    const int pid = __shfl_sync(0xFFFFFFFFu, id, row);
-                    int bytes = (pid >= 0 && ch * 16 < c.row_bytes) ? 16 : 0;
-                    int64_t at = bytes ? kv_row_at(c, pid, kvh, (p0 + row) & mask_o) + ch * 16 : 0;
-                    if (!QMM_IN_BOUNDS(g_attend_error, at + 15, c.num_pages * c.stride)) at = 0, bytes = 0;
-                    const int ck = ROW >= 128 ? ch ^ ((row >> 2 & 1) << 2) : ch;
-                    const int cv = ROW >= 128 ? ch ^ ((row & 3) << 1) : ch ^ ((row >> 1 & 1) << 1);
-                    cp_async16(dst + row * ROW + ck * 16, c.k + at, bytes);
-                    cp_async16(dst + (TILE + row) * ROW + cv * 16, c.v + at, bytes);
+                    for (int b = 0; b < TILE / 16; b++) {
+                        const int pid = __shfl_sync(0xFFFFFFFFu, id, 16 * b);
+                        const int64_t from = kv_row_at(c, pid, kvh, (p0 + 16 * b) & mask_o) + c_row * ROW + c_ch * 16;
+                        constexpr int kN = kChunks / 2;  // copies of sixteen rows
+#pragma unroll
+                        for (int i = 0; i < kN; i++) {
+                            if (!QMM_IN_BOUNDS(g_attend_error, from + i * 512 + 15, c.num_pages * c.stride)) continue;
+                            cp_async16(dst + put_k(b * kN + i), c.k + from + i * 512, 16);
+                            cp_async16(dst + TILE * ROW + put_v(b * kN + i), c.v + from + i * 512, 16);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int it = 0; it < TILE * kChunks / 32; it++) {
+                        const int row = it * kRowsPer + c_row, pid = __shfl_sync(0xFFFFFFFFu, id, row);
+                        int bytes = (pid >= 0 && c_ch * 16 < c.row_bytes) ? 16 : 0;
+                        int64_t from = bytes ? kv_row_at(c, pid, kvh, (p0 + row) & mask_o) + c_ch * 16 : 0;
+                        if (!QMM_IN_BOUNDS(g_attend_error, from + 15, c.num_pages * c.stride)) from = 0, bytes = 0;
+                        cp_async16(dst + put_k(it), c.k + from, bytes);
+                        cp_async16(dst + TILE * ROW + put_v(it), c.v + from, bytes);
+                    }
                 }
-                if (TYPE == QMM_KV_Q8 && lane < TILE) {
+                if (TYPE == QMM_KV_Q8 && lane < TILE) {  // position p's scale at (p % 4) (TILE / 4) + p / 4
                     int bytes = id >= 0 ? 4 : 0;
-                    int64_t at = bytes ? kv_scale_at(c, id, kvh, (p0 + lane) & mask_o) : 0;
-                    if (!QMM_IN_BOUNDS(g_attend_error, at + 3, c.num_pages * c.stride)) at = 0, bytes = 0;
-                    cp_async4z(dst + 2 * TILE * ROW + 4 * lane, c.k + at, bytes);
-                    cp_async4z(dst + 2 * TILE * ROW + 4 * TILE + 4 * lane, c.v + at, bytes);
+                    int64_t from = bytes ? kv_scale_at(c, id, kvh, (p0 + lane) & mask_o) : 0;
+                    if (!QMM_IN_BOUNDS(g_attend_error, from + 3, c.num_pages * c.stride)) from = 0, bytes = 0;
+                    const uint32_t to = dst + 2 * TILE * ROW + 4 * ((lane & 3) * (TILE / 4) + (lane >> 2));
+                    cp_async4z(to, c.k + from, bytes);
+                    cp_async4z(to + 4 * TILE, c.v + from, bytes);
                 }
             }
             cp_async_commit();  // an empty group where there is no tile: the wait counts groups
         };
 
         // fill the ring, then fetch the queries under its copies
-        int64_t next = ta + warp;
+        int next = ta + warp;
         int id = page_at(next);
 #pragma unroll
         for (int s = 0; s < S::kStages - 1; s++) {
@@ -305,7 +371,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
             }
             amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-            const int e = exponent_of(__float_as_uint(amax));
+            const int e = exponent_of(amax) - 127;
             const float up = pow2i(14 - e);
             q_scale = a.scale * 1.44269504088896341f * pow2i(e - 14);  // scores in base 2
 #pragma unroll
@@ -315,15 +381,43 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
             }
         }
 
-        float m_run = -INFINITY, l_run = 0.0f;  // of head n; l_run of this lane's positions
-        float o[kSets][kVD][2];
+        // Of head n: m_run, a whole number at or above every score so far, and the sum of
+        // weights 2^(score - m_run) of this lane's positions.  The weighted values: o, and
+        // in acc what the tensor cores have summed since the last fold, of weights times
+        // 2^(14 - e_run) times value scales below 2^(e_run + 1).
+        float m_run = -INFINITY, l_run = 0.0f, up = 16384.0f, down = 1.0f / 16384.0f;
+        int e_run = kExpLow, since = 0;  // e_run: an exponent field
+        if (TYPE == QMM_KV_Q8) up = pow2i(14 + 127 - e_run), down = pow2i(e_run - 127 - 14);
+        float o[kSets][kVD][2], acc[kKeep ? kSets : 1][kVD][4];
 #pragma unroll
         for (int s = 0; s < kSets; s++)
 #pragma unroll
             for (int t = 0; t < kVD; t++) o[s][t][0] = o[s][t][1] = 0.0f;
+        if (kKeep) {
+#pragma unroll
+            for (int s = 0; s < kSets; s++)
+#pragma unroll
+                for (int t = 0; t < kVD; t++)
+                    acc[kKeep ? s : 0][t][0] = acc[kKeep ? s : 0][t][1] = acc[kKeep ? s : 0][t][2] =
+                        acc[kKeep ? s : 0][t][3] = 0.0f;
+        }
+        // o = (o + acc) keep by f32 operations: the tensor core's own additions cut off
+        // instead of rounding, which over a long cache would add up
+        auto fold = [&](float keep) {
+#pragma unroll
+            for (int s = 0; s < kSets; s++)
+#pragma unroll
+                for (int t = 0; t < kVD; t++) {
+                    float* y = acc[kKeep ? s : 0][t];
+#pragma unroll
+                    for (int i = 0; i < 2; i++) o[s][t][i] = __fmaf_rn(y[i] + y[i + 2], down, o[s][t][i]) * keep;
+                    y[0] = y[1] = y[2] = y[3] = 0.0f;
+                }
+            since = 0;
+        };
 
         int slot = 0;
-        for (int64_t t = ta + warp; t < tb; t += kAttendWarps) {
+        for (int t = ta + warp; t < tb; t += kAttendWarps) {
             cp_async_wait<S::kStages - 2>();
             __syncwarp();  // the tile is here for every lane, and the slot before it is read out
             {
@@ -333,13 +427,11 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
                 next += kAttendWarps;
             }
             const uint32_t st = ring_u + slot * S::kStage;
-            const float* scales = reinterpret_cast<const float*>(ring + slot * S::kStage + 2 * TILE * ROW);
-            const uint32_t live = *reinterpret_cast<const uint32_t*>(scales + 2 * TILE);
+            const uint8_t* tail = ring + slot * S::kStage + 2 * TILE * ROW;  // scales, then the mask
+            const uint32_t live = *reinterpret_cast<const uint32_t*>(tail + 8 * TILE);
 
-            // scores: column i of n-tile m is position 16 (m / 2) + 8 (m % 2) + i / 2 + 4 (i % 2)
-            float sc[TILE / 8][4];
-#pragma unroll
-            for (int m = 0; m < TILE / 8; m++) sc[m][0] = sc[m][1] = sc[m][2] = sc[m][3] = 0.0f;
+            // scores: column i of n-tile m is position 8 m + i / 2 + 4 (i % 2)
+            float sc[TILE / 8][kChains][4];
 #pragma unroll
             for (int cg = 0; cg < kGroups; cg++) {
                 uint4 kw[TILE / 8];
@@ -351,6 +443,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
                 }
 #pragma unroll
                 for (int w = 0; w < kPer / 4; w++) {
+                    const int step = cg * (kPer / 4) + w;
 #pragma unroll
                     for (int m = 0; m < TILE / 8; m++) {
                         const uint32_t* f = reinterpret_cast<const uint32_t*>(&kw[m]);
@@ -361,55 +454,76 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
                         } else {
                             b0 = f[2 * w], b1 = f[2 * w + 1];
                         }
-                        mma_f16(sc[m], qf[cg * (kPer / 4) + w], b0, b1);
+                        if (step < kChains) mma_f16_first(sc[m][step % kChains], qf[step], b0, b1);
+                        else mma_f16(sc[m][step % kChains], qf[step], b0, b1);
                     }
                 }
             }
-            // weights: this lane has positions 8 m + j and 8 m + j + 4 of head n
-            float wt[TILE / 8][2], top = -INFINITY;
+            // this lane's positions of head n: 4 i + j
+            constexpr int kMine = TILE / 4;
+            float wt[kMine], vs[kMine], top = -INFINITY;
 #pragma unroll
-            for (int m = 0; m < TILE / 8; m++)
-#pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    const int p = 8 * m + j + 4 * i;
-                    const float ks = TYPE == QMM_KV_Q8 ? scales[p] * q_scale : q_scale;
-                    wt[m][i] = (live >> p & 1u) ? (sc[m][i] + sc[m][i + 2]) * ks : -INFINITY;
-                    top = fmaxf(top, wt[m][i]);
+            for (int i = 0; i < kMine; i += 4) {
+                const float* y0 = sc[i >> 1][0];
+                const float* y1 = sc[(i >> 1) + 1][0];
+                wt[i] = y0[0] + y0[2], wt[i + 1] = y0[1] + y0[3];
+                wt[i + 2] = y1[0] + y1[2], wt[i + 3] = y1[1] + y1[3];
+                if (kChains == 2) {
+                    const float* z0 = sc[i >> 1][kChains - 1];
+                    const float* z1 = sc[(i >> 1) + 1][kChains - 1];
+                    wt[i] += z0[0] + z0[2], wt[i + 1] += z0[1] + z0[3];
+                    wt[i + 2] += z1[0] + z1[2], wt[i + 3] += z1[1] + z1[3];
                 }
+                if (TYPE == QMM_KV_Q8) {
+                    const float4 ks = *reinterpret_cast<const float4*>(tail + 4 * (j * kMine + i));
+                    const float4 v4 = *reinterpret_cast<const float4*>(tail + 4 * TILE + 4 * (j * kMine + i));
+                    wt[i] *= ks.x * q_scale, wt[i + 1] *= ks.y * q_scale;
+                    wt[i + 2] *= ks.z * q_scale, wt[i + 3] *= ks.w * q_scale;
+                    vs[i] = v4.x, vs[i + 1] = v4.y, vs[i + 2] = v4.z, vs[i + 3] = v4.w;
+                } else {
+                    wt[i] *= q_scale, wt[i + 1] *= q_scale, wt[i + 2] *= q_scale, wt[i + 3] *= q_scale;
+                }
+            }
+            if (live != (TILE == 32 ? 0xFFFFFFFFu : 0xFFFFu)) {
+#pragma unroll
+                for (int i = 0; i < kMine; i++)
+                    if (!(live >> (4 * i + j) & 1u)) wt[i] = -INFINITY;
+            }
+#pragma unroll
+            for (int i = 0; i < kMine; i++) top = fmaxf(top, wt[i]);
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-            const float m_new = fmaxf(m_run, top);
-            const float m_at = m_new == -INFINITY ? 0.0f : m_new;  // nothing seen yet: every weight is 0
-            const float keep = exp2_approx(m_run - m_at);
-            m_run = m_new;
-            l_run *= keep;
-            float up = 16384.0f, down = 1.0f / 16384.0f;
-            if (TYPE == QMM_KV_Q8) {
-                const uint32_t bits = lane < TILE ? __float_as_uint(scales[TILE + lane]) & 0x7FFFFFFFu : 0u;
-                const int e = exponent_of(__reduce_max_sync(0xFFFFFFFFu, bits));
-                up = pow2i(14 - e), down = pow2i(e - 14);
+            float keep = 1.0f;
+            const int e_lane = TYPE == QMM_KV_Q8 && lane < TILE
+                                   ? exponent_of(*reinterpret_cast<const float*>(tail + 4 * TILE + 4 * lane)) : 0;
+            if (__any_sync(0xFFFFFFFFu, top > m_run || (TYPE == QMM_KV_Q8 && e_lane > e_run))) {
+                const float m_new = fmaxf(m_run, ceilf(top));
+                keep = exp2_approx(m_run - (m_new == -INFINITY ? 0.0f : m_new));
+                m_run = m_new;
+                l_run *= keep;
+                if (kKeep) fold(keep);
+                if (TYPE == QMM_KV_Q8) {
+                    const int e = (int)__reduce_max_sync(0xFFFFFFFFu, (unsigned)e_lane);
+                    e_run = e > e_run ? e : e_run;
+                    up = pow2i(14 + 127 - e_run), down = pow2i(e_run - 127 - 14);
+                }
+            } else if (kKeep && since == kFold) {
+                fold(1.0f);
             }
+            since++;
+            const float m_at = m_run == -INFINITY ? 0.0f : m_run;  // nothing seen yet: every weight is 0
             uint32_t pf[TILE / 16][4];
 #pragma unroll
-            for (int m = 0; m < TILE / 8; m++) {
-                float cv[2];
-#pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    const int p = 8 * m + j + 4 * i;
-                    const float w = exp2_approx(wt[m][i] - m_at);
-                    l_run += w;
-                    cv[i] = (TYPE == QMM_KV_Q8 ? w * scales[TILE + p] : w) * up;
-                }
-                split_h2(cv[0], cv[1], &pf[m >> 1][2 * (m & 1)], &pf[m >> 1][2 * (m & 1) + 1]);
+            for (int i = 0; i < kMine; i += 2) {
+                const float w0 = exp2_approx(wt[i] - m_at), w1 = exp2_approx(wt[i + 1] - m_at);
+                l_run += w0 + w1;
+                const float s0 = TYPE == QMM_KV_Q8 ? vs[i] * up : up, s1 = TYPE == QMM_KV_Q8 ? vs[i + 1] * up : up;
+                split_h2(w0 * s0, w1 * s1, &pf[i >> 2][i & 2], &pf[i >> 2][(i & 2) + 1]);
             }
-            // values: column n of n-tile (set, t) is value 8 kVD set + kVD n + t; fresh
-            // sums per tile, added to the running ones by f32 FMAs (the tensor core's own
-            // additions cut off instead of rounding: over a long cache that would add up)
+            // values: column n of n-tile (set, t) is value 8 kVD set + kVD n + t
 #pragma unroll
             for (int s = 0; s < kSets; s++) {
-                float acc[kVD][4];
-#pragma unroll
-                for (int t2 = 0; t2 < kVD; t2++) acc[t2][0] = acc[t2][1] = acc[t2][2] = acc[t2][3] = 0.0f;
+                float(*ac)[4] = acc[kKeep ? s : 0];
 #pragma unroll
                 for (int b = 0; b < TILE / 16; b++) {
                     uint32_t vw[4][kVB / 4];
@@ -424,6 +538,10 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
                             vw[i][0] = lds32(at), vw[i][1] = lds32(at + 4);
                         }
                     }
+                    auto mma = [&](int t, uint32_t b0, uint32_t b1) {
+                        if (!kKeep && b == 0) mma_f16_first(ac[t % kVD], pf[b], b0, b1);
+                        else mma_f16(ac[t % kVD], pf[b], b0, b1);
+                    };
 #pragma unroll
                     for (int w = 0; w < kVB / 4; w++) {
                         if (TYPE == QMM_KV_Q8) {
@@ -431,26 +549,28 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
                             const uint32_t w2 = vw[2][w] ^ 0x80808080u, w3 = vw[3][w] ^ 0x80808080u;
                             const uint32_t al = __byte_perm(w0, w1, 0x5140u), ah = __byte_perm(w0, w1, 0x7362u);
                             const uint32_t bl = __byte_perm(w2, w3, 0x5140u), bh = __byte_perm(w2, w3, 0x7362u);
-                            mma_f16(acc[(4 * w) % kVD], pf[b], codes_h2(al, 0x4140u), codes_h2(bl, 0x4140u));
-                            mma_f16(acc[(4 * w + 1) % kVD], pf[b], codes_h2(al, 0x4342u), codes_h2(bl, 0x4342u));
-                            mma_f16(acc[(4 * w + 2) % kVD], pf[b], codes_h2(ah, 0x4140u), codes_h2(bh, 0x4140u));
-                            mma_f16(acc[(4 * w + 3) % kVD], pf[b], codes_h2(ah, 0x4342u), codes_h2(bh, 0x4342u));
+                            mma(4 * w, codes_h2(al, 0x4140u), codes_h2(bl, 0x4140u));
+                            mma(4 * w + 1, codes_h2(al, 0x4342u), codes_h2(bl, 0x4342u));
+                            mma(4 * w + 2, codes_h2(ah, 0x4140u), codes_h2(bh, 0x4140u));
+                            mma(4 * w + 3, codes_h2(ah, 0x4342u), codes_h2(bh, 0x4342u));
                         } else {
-                            mma_f16(acc[2 * w], pf[b], __byte_perm(vw[0][w], vw[1][w], 0x5410u),
-                                    __byte_perm(vw[2][w], vw[3][w], 0x5410u));
-                            mma_f16(acc[2 * w + 1], pf[b], __byte_perm(vw[0][w], vw[1][w], 0x7632u),
-                                    __byte_perm(vw[2][w], vw[3][w], 0x7632u));
+                            mma(2 * w, __byte_perm(vw[0][w], vw[1][w], 0x5410u), __byte_perm(vw[2][w], vw[3][w], 0x5410u));
+                            mma(2 * w + 1, __byte_perm(vw[0][w], vw[1][w], 0x7632u),
+                                __byte_perm(vw[2][w], vw[3][w], 0x7632u));
                         }
                     }
                 }
+                if (!kKeep) {
 #pragma unroll
-                for (int t2 = 0; t2 < kVD; t2++)
+                    for (int t2 = 0; t2 < kVD; t2++)
 #pragma unroll
-                    for (int i = 0; i < 2; i++)
-                        o[s][t2][i] = __fmaf_rn(o[s][t2][i], keep, down * (acc[t2][i] + acc[t2][i + 2]));
+                        for (int i = 0; i < 2; i++)
+                            o[s][t2][i] = __fmaf_rn(o[s][t2][i], keep, down * (ac[t2][i] + ac[t2][i + 2]));
+                }
             }
             slot = slot == S::kStages - 1 ? 0 : slot + 1;
         }
+        if (kKeep) fold(1.0f);
 
         // the warps meet: running maxima and sums, then the values through shared memory
         l_run += __shfl_xor_sync(0xFFFFFFFFu, l_run, 1);
@@ -458,26 +578,26 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
         if (j == 0) part_m[warp][n] = m_run, part_l[warp][n] = l_run;
         cp_async_wait<0>();
         __syncthreads();  // every ring is read out: its memory is the exchange now
-        float* xo = reinterpret_cast<float*>(smem) + warp * kAttendHeads * HDT;
+        float* xo = reinterpret_cast<float*>(smem) + (warp * kAttendHeads + n) * HDT;
 #pragma unroll
         for (int s = 0; s < kSets; s++)
 #pragma unroll
             for (int i = 0; i < 2; i++)
 #pragma unroll
                 for (int t = 0; t < kVD; t += 4)
-                    *reinterpret_cast<float4*>(xo + n * HDT + 8 * kVD * s + kVD * (2 * j + i) + t) =
+                    *reinterpret_cast<float4*>(xo + 4 * exchange_quad(n, (8 * kVD * s + kVD * (2 * j + i) + t) / 4)) =
                         make_float4(o[s][t][i], o[s][t + 1][i], o[s][t + 2][i], o[s][t + 3][i]);
-        const bool whole = ta == 0 && tb == tiles;
+        const bool whole = ta == 0 && tb == (int)tiles;
         float* part = a.parts + (2 * (int64_t)blockIdx.x + (ta == 0 ? 1 : 0)) * (kAttendHeads * (c.hd + 2));
         if (threadIdx.x < heads) {
             const int h = threadIdx.x;
             float m = -INFINITY, l = 0.0f;
 #pragma unroll
             for (int w = 0; w < kAttendWarps; w++) m = fmaxf(m, part_m[w][h]);
-            const float at = m == -INFINITY ? 0.0f : m;
+            const float ref = m == -INFINITY ? 0.0f : m;
 #pragma unroll
             for (int w = 0; w < kAttendWarps; w++) {
-                part_f[w][h] = exp2_approx(part_m[w][h] - at);
+                part_f[w][h] = exp2_approx(part_m[w][h] - ref);
                 l += part_l[w][h] * part_f[w][h];
             }
             unit_l[h] = l;
@@ -485,18 +605,18 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
                 part[kAttendHeads * c.hd + h] = m;
                 part[kAttendHeads * c.hd + kAttendHeads + h] = l;
             } else if (a.lse && QMM_IN_BOUNDS(g_attend_error, r * (a.G * c.Hkv) + head0 + h, a.R * a.G * c.Hkv)) {
-                a.lse[r * (a.G * c.Hkv) + head0 + h] = (m + log2f(l)) * 0.693147180559945309f;
+                a.lse[(int64_t)r * (a.G * c.Hkv) + head0 + h] = (m + log2f(l)) * 0.693147180559945309f;
             }
         }
         __syncthreads();
         const int quads = c.hd >> 2;
         for (int i = threadIdx.x; i < heads * quads; i += kAttendThreads) {
-            const int h = i / quads, d = 4 * (i - h * quads);
+            const int h = i / quads, q = i - h * quads, d = 4 * q;
             float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kAttendWarps; w++) {
                 const float4 z = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(smem) +
-                                                                  (w * kAttendHeads + h) * HDT + d);
+                                                                  (w * kAttendHeads + h) * HDT + 4 * exchange_quad(h, q));
                 const float f = part_f[w][h];
                 y.x = __fmaf_rn(z.x, f, y.x), y.y = __fmaf_rn(z.y, f, y.y);
                 y.z = __fmaf_rn(z.z, f, y.z), y.w = __fmaf_rn(z.w, f, y.w);
@@ -512,71 +632,74 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
         }
         __syncthreads();  // the exchange is read out
     }
-    pdl_launch_dependents();
 }
 
 // One CTA per (row, query head): where the head's unit lies in several runs, their
 // parts are joined; a row without positions gets zeros and -inf.  Warp w adds parts
 // w, w + kJoinWarps, ... in order, then the warps' sums in order.
 __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(KvPages c, AttendArgs a, int tile, int grid) {
-    __shared__ int64_t scan[kJoinWarps];
-    __shared__ float factor[kAttendMaxCtas], red[kJoinWarps], sum[kJoinWarps][kHeadMax];
+    __shared__ uint2 sums[kJoinWarps];
+    __shared__ float2 ml[kAttendMaxCtas];
+    __shared__ float sum[kJoinWarps][kHeadMax];
     pdl_wait();
-    constexpr int kThreads = 32 * kJoinWarps;
+    constexpr uint32_t kThreads = 32 * kJoinWarps;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int Hq = a.G * c.Hkv, units = c.Hkv * a.blocks;
-    const int64_t r = blockIdx.x / Hq;
-    const int head = (int)(blockIdx.x - r * Hq), kvh = head / a.G, in = head - kvh * a.G;
-    const int u = kvh * a.blocks + in / kAttendHeads, hl = in % kAttendHeads;
+    const uint32_t Hq = a.G * c.Hkv, units = c.Hkv * a.blocks;
+    const uint32_t r = blockIdx.x / Hq, head = blockIdx.x - r * Hq, kvh = head / a.G, in = head - kvh * a.G;
+    const uint32_t u = kvh * a.blocks + in / kAttendHeads, hl = in % kAttendHeads;
     if (__ldg(a.lens + r) < 0) return;  // a padding row: left as it was
-    auto tiles_of = [&](int64_t row) {
+    auto tiles_of = [&](uint32_t row) {
         const RowRange x = attend_row(c, a, row);
         return tile == 32 ? row_tiles<32>(x) : row_tiles<16>(x);
     };
-    int64_t mine = 0, mine_before = 0, before;
-    for (int64_t i = threadIdx.x; i < a.R; i += kThreads) {
-        const int64_t t = tiles_of(i);
-        mine += t;
-        if (i < r) mine_before += t;
+    uint2 mine = make_uint2(0u, 0u);  // of all rows, of the rows ahead
+    for (uint32_t i = threadIdx.x; i < (uint32_t)a.R; i += kThreads) {
+        const uint32_t t = unit_weight(tiles_of(i));
+        mine.x += t;
+        if (i < r) mine.y += t;
     }
-    const int64_t total = block_scan<kThreads>(mine, &before, scan);
-    const int64_t ahead = block_scan<kThreads>(mine_before, &before, scan);
-    const int64_t tiles = tiles_of(r), work = total * units;
+    mine.x = __reduce_add_sync(0xFFFFFFFFu, mine.x), mine.y = __reduce_add_sync(0xFFFFFFFFu, mine.y);
+    if (lane == 0) sums[warp] = mine;
+    __syncthreads();
+    uint32_t total = 0, ahead = 0;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; w++) total += sums[w].x, ahead += sums[w].y;
+    const uint32_t tiles = tiles_of(r);
     float* out = a.out + r * a.ldo + (int64_t)head * c.hd;
     if (tiles == 0) {
         for (int d = threadIdx.x; d < c.hd; d += kThreads) out[d] = 0.0f;
-        if (a.lse && threadIdx.x == 0) a.lse[r * Hq + head] = -INFINITY;
+        if (a.lse && threadIdx.x == 0) a.lse[(int64_t)r * Hq + head] = -INFINITY;
         return;
     }
-    const int64_t ctas = run_ctas(work, grid), g0 = ahead * units + u * tiles;
-    const int64_t c0 = run_of(g0, work, ctas), c1 = run_of(g0 + tiles - 1, work, ctas);
+    const Runs runs(total * units, grid);
+    const uint32_t g0 = ahead * units + u * unit_weight(tiles) + kUnitCost;  // the unit's first tile
+    const uint32_t c0 = runs.of(g0), c1 = runs.of(g0 + tiles - 1);
     if (c0 == c1) return;  // written by that run's CTA
     const int n = (int)(c1 - c0 + 1);
     const int64_t size = kAttendHeads * (c.hd + 2);
     auto part = [&](int i) -> const float* {  // the unit begins in run c0, the others continue it
-        return a.parts + (2 * (c0 + i) + (i == 0 ? 1 : 0)) * size;
+        return a.parts + (2 * (int64_t)(c0 + i) + (i == 0 ? 1 : 0)) * size;
     };
-    float m = -INFINITY;
-    for (int i = threadIdx.x; i < n; i += kThreads) m = fmaxf(m, part(i)[kAttendHeads * c.hd + hl]);
+    for (int i = threadIdx.x; i < n; i += kThreads)
+        if (QMM_IN_BOUNDS(g_attend_error, i, kAttendMaxCtas)) {
+            const float* p = part(i) + kAttendHeads * c.hd + hl;
+            ml[i] = make_float2(p[0], p[kAttendHeads]);
+        }
+    __syncthreads();
+    float m = -INFINITY, l = 0.0f;  // every warp for itself: n is a few hundred at most
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, ml[i].x);
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
-    if (lane == 0) red[warp] = m;
-    __syncthreads();
+    const float ref = m == -INFINITY ? 0.0f : m;
+    for (int i = lane; i < n; i += 32) l = __fmaf_rn(ml[i].y, exp2_approx(ml[i].x - ref), l);
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; w++) m = fmaxf(m, red[w]);
-    const float at = m == -INFINITY ? 0.0f : m;
-    for (int i = threadIdx.x; i < n; i += kThreads)
-        if (QMM_IN_BOUNDS(g_attend_error, i, kAttendMaxCtas))
-            factor[i] = exp2_approx(part(i)[kAttendHeads * c.hd + hl] - at);
-    __syncthreads();
-    float l = 0.0f;
-    for (int i = 0; i < n; i++) l = __fmaf_rn(part(i)[kAttendHeads * c.hd + kAttendHeads + hl], factor[i], l);
+    for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, s);
     for (int d0 = 4 * lane; d0 < c.hd; d0 += 128) {
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
         for (int i = warp; i < n; i += kJoinWarps) {
             const float4 z = *reinterpret_cast<const float4*>(part(i) + hl * c.hd + d0);
-            const float f = factor[i];
+            const float f = exp2_approx(ml[i].x - ref);
             y.x = __fmaf_rn(z.x, f, y.x), y.y = __fmaf_rn(z.y, f, y.y);
             y.z = __fmaf_rn(z.z, f, y.z), y.w = __fmaf_rn(z.w, f, y.w);
         }
@@ -590,7 +713,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(KvPages c,
         for (int w = 1; w < kJoinWarps; w++) y += sum[w][d];
         out[d] = y * inv;
     }
-    if (a.lse && threadIdx.x == 0) a.lse[r * Hq + head] = (m + log2f(l)) * 0.693147180559945309f;
+    if (a.lse && threadIdx.x == 0) a.lse[(int64_t)r * Hq + head] = (m + log2f(l)) * 0.693147180559945309f;
     pdl_launch_dependents();
 }
 
@@ -626,6 +749,10 @@ qmm_status qmm_kv_attend(const qmm_kv_pages* cache, const float* q, int64_t ldq,
     if (need == 0 || R < 1 || R * Hq > kMaxDim || R > kMaxDim || (!seq && R > c.num_seqs) || window < 0 ||
         !row_stride_ok(ldq, Hq * c.hd) || !row_stride_ok(ldo, Hq * c.hd))
         return QMM_E_SHAPE;
+    // the list of tiles is counted in 32 bits
+    const int64_t room = c.max_pages << c.page_shift, seen = window > 0 && window < room ? window + 16 : room;
+    const int64_t blocks = (Hq / c.Hkv + kAttendHeads - 1) / kAttendHeads;
+    if (room > kMaxDim || R * c.Hkv * blocks > kMaxDim / (seen / 16 + 2 + kUnitCost)) return QMM_E_SHAPE;
     if (!aligned16(q) || !aligned16(out) || !aligned4(lens) || !aligned4(seq) || !aligned4(lse) || !aligned16(scratch))
         return QMM_E_ALIGN;
     if (scratch_bytes < need) return QMM_E_SCRATCH;
@@ -633,7 +760,7 @@ qmm_status qmm_kv_attend(const qmm_kv_pages* cache, const float* q, int64_t ldq,
     a.q = q, a.lens = lens, a.seq = seq, a.out = out, a.lse = lse, a.parts = (float*)scratch;
     a.R = R, a.ldq = ldq, a.ldo = ldo, a.window = window;
     a.G = (int)(Hq / c.Hkv);
-    a.blocks = (a.G + kAttendHeads - 1) / kAttendHeads;
+    a.blocks = (int)blocks;
     a.scale = scale;
     DeviceInfo dev;
     st = current_device(&dev);
