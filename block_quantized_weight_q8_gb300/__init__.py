@@ -134,18 +134,20 @@ def ptr(t) -> int:
     return int(t.data_ptr())
 
 
-def stream_handle(stream=None) -> int:
+def stream_handle(stream=None, dev=None) -> int:
     if stream is None:
         import torch
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the handle without a Stream object around it
-        return raw(torch.cuda.current_device()) if raw else int(torch.cuda.current_stream().cuda_stream)
+        if raw is None:
+            return int(torch.cuda.current_stream().cuda_stream)
+        return raw(torch.cuda.current_device() if dev is None else dev)
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
 
 
 def _call(name, *args):
-    r = getattr(load(), name)(*args)
+    r = getattr(_lib or load(), name)(*args)
     if r != 0:
         raise QmmError(name, r)
 
@@ -341,30 +343,49 @@ ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ROPE_SCALINGS = {"plain": 0, "linear": 1, "bands": 2, "yarn": 3}
 
 
-def _on_device(name, t, dtype, ndim):
-    """Checks a tensor that a kernel reads or writes by its shape: type, dimensions, and the current device."""
-    import torch
-    if t.dtype is not getattr(torch, dtype) or t.dim() != ndim or t.get_device() != torch.cuda.current_device():
-        raise ValueError("%s: a %d-dimensional tensor of %s on the current device (cuda:%d) is needed, got %d dimensions "
-                         "of %s on %s" % (name, ndim, dtype, torch.cuda.current_device(), t.dim(), t.dtype, t.device))
+_torch = None
 
 
-def _heads(name, t, T, H, hd):
-    """(address, token stride) of head rows [T][H][hd]: heads side by side, tokens any stride apart."""
-    _on_device(name, t, "float32", 3)
+def _device() -> int:
+    """The current device; imports torch on first use."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch.cuda.current_device()
+
+
+def _refuse(name, t, dtype, shape, dev):
+    raise ValueError("%s: %s of shape %s on the current device (cuda:%d) with contiguous heads or values is needed, got %s "
+                     "of shape %s (strides %s) on %s" % (name, dtype, shape, dev, t.dtype, tuple(t.shape), t.stride(),
+                                                        t.device))
+
+
+def _heads(name, t, dev, T, H, hd):
+    """(address, token stride) of f32 head rows [T][H][hd]: heads side by side, tokens any stride apart."""
+    if t.dtype is not _torch.float32 or t.get_device() != dev or t.shape != (T, H, hd):
+        _refuse(name, t, "float32", (T, H, hd), dev)
     s0, s1, s2 = t.stride()
-    if t.shape != (T, H, hd) or s2 != 1 or (s1 != hd and H > 1):
-        raise ValueError("%s: shape %s with the heads of a token contiguous is needed, got %s (strides %s)" % (
-            name, (T, H, hd), tuple(t.shape), (s0, s1, s2)))
+    if s2 != 1 or (s1 != hd and H > 1):
+        _refuse(name, t, "float32", (T, H, hd), dev)
     return t.data_ptr(), (s0 if T > 1 else H * hd)
 
 
-def _ints(name, t, n):
+def _plain(name, t, dev, dtype, shape):
+    """The address of a contiguous tensor of this type and shape (None as an extent: any); None for None."""
     if t is None:
         return None
-    _on_device(name, t, "int32", 1)
-    if t.numel() != n or not t.is_contiguous():
-        raise ValueError("%s: %d contiguous values are needed" % (name, n))
+    if t.dtype is not getattr(_torch, dtype) or t.get_device() != dev or not t.is_contiguous() or (
+            t.shape != shape if None not in shape else t.dim() != len(shape)):
+        _refuse(name, t, dtype, shape, dev)
+    return t.data_ptr()
+
+
+def _ints(name, t, dev, n):
+    if t is None:
+        return None
+    if t.dtype is not _torch.int32 or t.get_device() != dev or t.shape != (n,) or not t.is_contiguous():
+        _refuse(name, t, "int32", (n,), dev)
     return t.data_ptr()
 
 
@@ -375,10 +396,7 @@ class RopeSpec(ctypes.Structure):
                 ("mscale", ctypes.c_float)]
 
     def __init__(self, freqs, layout="half", mscale=1.0):
-        _on_device("freqs", freqs, "int64", 1)
-        if not freqs.is_contiguous():
-            raise ValueError("freqs: contiguous values are needed")
-        super().__init__(freqs.data_ptr(), 2 * freqs.shape[0], ROPE_LAYOUTS[layout], mscale)
+        super().__init__(_plain("freqs", freqs, _device(), "int64", (None,)), 2 * freqs.shape[0], ROPE_LAYOUTS[layout], mscale)
         self.tensor, self.ref = freqs, ctypes.addressof(self)
 
 
@@ -391,37 +409,38 @@ class KvPages(ctypes.Structure):
                 ("type", ctypes.c_int32), ("page_size", ctypes.c_int32)]
 
     def __init__(self, type, k, v, table, page_size, Hkv, hd):
-        _on_device("k", k, "uint8", 2)
-        _on_device("v", v, "uint8", 2)
-        _on_device("table", table, "int32", 2)
+        dev = _device()
+        for name, t in (("k", k), ("v", v)):
+            if t.dtype is not _torch.uint8 or t.get_device() != dev or t.dim() != 2:
+                _refuse(name, t, "uint8", ("pages", "bytes"), dev)
+        rows = _plain("table", table, dev, "int32", (None, None))
         need = qmm_kv_page_bytes(type, Hkv, page_size, hd)
         if need == 0:
             raise ValueError("no cache of type %r has %r heads of %r in pages of %r" % (type, Hkv, hd, page_size))
         if k.shape != v.shape or k.stride() != v.stride() or k.stride(1) != 1 or k.shape[1] < need:
             raise ValueError("k and v: pools of one shape and stride are needed, %d bytes a page at least" % need)
-        if not table.is_contiguous():
-            raise ValueError("table: contiguous rows are needed")
         stride = k.stride(0) if k.shape[0] > 1 else -(-k.shape[1] // 16) * 16
-        super().__init__(k.data_ptr(), v.data_ptr(), table.data_ptr(), k.shape[0], stride, table.shape[0],
+        super().__init__(k.data_ptr(), v.data_ptr(), rows, k.shape[0], stride, table.shape[0],
                          table.shape[1], Hkv, hd, KV_TYPES[type], page_size)
         self.tensors, self.ref = (k, v, table), ctypes.addressof(self)
 
 
 def qmm_rope_freqs(freqs, base=10000.0, scaling="plain", factor=1.0, orig_len=0.0, lo=0.0, hi=0.0, stream=None):
     """Fills the frequency table freqs (int64 CUDA tensor [n_rot / 2])."""
-    _on_device("freqs", freqs, "int64", 1)
-    _call("qmm_rope_freqs", freqs.data_ptr(), 2 * freqs.shape[0], float(base), ROPE_SCALINGS[scaling], float(factor),
+    _call("qmm_rope_freqs", _plain("freqs", freqs, _device(), "int64", (None,)), 2 * freqs.shape[0], float(base), ROPE_SCALINGS[scaling], float(factor),
           float(orig_len), float(lo), float(hi), stream_handle(stream))
 
 
 def qmm_rope(rope, x, y, pos, inverse=False, stream=None):
     """y = x ([T][H][hd] f32) rotated to the positions pos; y may be x."""
-    _on_device("x", x, "float32", 3)
+    dev = _device()
+    if x.dim() != 3:
+        _refuse("x", x, "float32", ("T", "H", "hd"), dev)
     T, H, hd = x.shape
-    px, ldx = _heads("x", x, T, H, hd)
-    py, ldy = _heads("y", y, T, H, hd)
-    _call("qmm_rope", rope.ref, px, ldx, py, ldy, _ints("pos", pos, T), T, H, hd, 1 if inverse else 0,
-          stream_handle(stream))
+    px, ldx = _heads("x", x, dev, T, H, hd)
+    py, ldy = _heads("y", y, dev, T, H, hd)
+    _call("qmm_rope", rope.ref, px, ldx, py, ldy, _ints("pos", pos, dev, T), T, H, hd, 1 if inverse else 0,
+          stream_handle(stream, dev))
 
 
 def qmm_kv_page_bytes(type, Hkv, page_size, hd):
@@ -431,25 +450,25 @@ def qmm_kv_page_bytes(type, Hkv, page_size, hd):
 def qmm_kv_store(pages, k, v, pos, seq=None, rope=None, q=None, q_out=None, stream=None):
     """Stores keys k and values v ([T][Hkv][hd] f32) at positions pos of the sequences seq; with rope, keys are rotated
     first, and queries q ([T][Hq][hd]) into q_out."""
-    T, Hkv, hd = k.shape[0], pages.Hkv, pages.hd
-    pk, ldk = _heads("k", k, T, Hkv, hd)
-    pv, ldv = _heads("v", v, T, Hkv, hd)
+    dev, T, Hkv, hd = _device(), k.shape[0], pages.Hkv, pages.hd
+    pk, ldk = _heads("k", k, dev, T, Hkv, hd)
+    pv, ldv = _heads("v", v, dev, T, Hkv, hd)
     pq = ldq = po = ldo = Hq = 0
     if q is not None:
         Hq = q.shape[1]
-        pq, ldq = _heads("q", q, T, Hq, hd)
-        po, ldo = _heads("q_out", q_out, T, Hq, hd)
-    _call("qmm_kv_store", pages.ref, pk, ldk, pv, ldv, _ints("pos", pos, T), _ints("seq", seq, T), T,
-          rope.ref if rope is not None else None, pq, ldq, po, ldo, Hq, stream_handle(stream))
+        pq, ldq = _heads("q", q, dev, T, Hq, hd)
+        po, ldo = _heads("q_out", q_out, dev, T, Hq, hd)
+    _call("qmm_kv_store", pages.ref, pk, ldk, pv, ldv, _ints("pos", pos, dev, T), _ints("seq", seq, dev, T), T,
+          rope.ref if rope is not None else None, pq, ldq, po, ldo, Hq, stream_handle(stream, dev))
 
 
 def qmm_kv_load(pages, pos, k_out=None, v_out=None, seq=None, stream=None):
     """The rows at positions pos of the sequences seq as f32 ([T][Hkv][hd]); either output may be None."""
-    T, Hkv, hd = pos.shape[0], pages.Hkv, pages.hd
-    pk, ldk = _heads("k_out", k_out, T, Hkv, hd) if k_out is not None else (None, 0)
-    pv, ldv = _heads("v_out", v_out, T, Hkv, hd) if v_out is not None else (None, 0)
-    _call("qmm_kv_load", pages.ref, _ints("pos", pos, T), _ints("seq", seq, T), T, pk, ldk, pv, ldv,
-          stream_handle(stream))
+    dev, T, Hkv, hd = _device(), pos.shape[0], pages.Hkv, pages.hd
+    pk, ldk = _heads("k_out", k_out, dev, T, Hkv, hd) if k_out is not None else (None, 0)
+    pv, ldv = _heads("v_out", v_out, dev, T, Hkv, hd) if v_out is not None else (None, 0)
+    _call("qmm_kv_load", pages.ref, _ints("pos", pos, dev, T), _ints("seq", seq, dev, T), T, pk, ldk, pv, ldv,
+          stream_handle(stream, dev))
 
 
 def qmm_kv_attend_scratch_bytes(Hq, Hkv, hd):
@@ -459,16 +478,12 @@ def qmm_kv_attend_scratch_bytes(Hq, Hkv, hd):
 def qmm_kv_attend(pages, q, lens, out, scratch, scratch_bytes, scale, lse=None, seq=None, window=0, stream=None):
     """out[r] = the attention of query heads q[r] ([R][Hq][hd] f32) over the first lens[r] positions (the last window
     of them) of their sequences; lse ([R][Hq] f32) the log of the softmax's sum."""
-    R, Hq, hd = q.shape[0], q.shape[1], pages.hd
-    pq, ldq = _heads("q", q, R, Hq, hd)
-    po, ldo = _heads("out", out, R, Hq, hd)
-    if lse is not None:
-        _on_device("lse", lse, "float32", 2)
-        if lse.shape != (R, Hq) or not lse.is_contiguous():
-            raise ValueError("lse: contiguous [R][Hq] is needed")
-    _call("qmm_kv_attend", pages.ref, pq, ldq, _ints("lens", lens, R), _ints("seq", seq, R), po, ldo,
-          lse.data_ptr() if lse is not None else None, ptr(scratch), int(scratch_bytes), R, Hq, float(scale), int(window),
-          stream_handle(stream))
+    dev, R, Hq, hd = _device(), q.shape[0], q.shape[1], pages.hd
+    pq, ldq = _heads("q", q, dev, R, Hq, hd)
+    po, ldo = _heads("out", out, dev, R, Hq, hd)
+    _call("qmm_kv_attend", pages.ref, pq, ldq, _ints("lens", lens, dev, R), _ints("seq", seq, dev, R), po, ldo,
+          _plain("lse", lse, dev, "float32", (R, Hq)), ptr(scratch), scratch_bytes, R, Hq, scale, window,
+          stream_handle(stream, dev))
 
 
 def qmm_blocksums(wtype, W, xq, s, M, N, K, stream=None):

@@ -192,7 +192,6 @@ unsigned qmm_internal_matmul_kq_error(int clear);
 unsigned qmm_internal_getrows_error(int clear);
 unsigned qmm_internal_kv_error(int clear);
 unsigned qmm_internal_quantize_error(int clear);
-unsigned qmm_internal_rope_error(int clear);
 unsigned qmm_internal_pages_error(int clear);
 unsigned qmm_internal_attend_error(int clear);
 
@@ -319,8 +318,8 @@ qmm_status qmm_device_status(int clear) {
     if (cudaDeviceSynchronize() != cudaSuccess) return QMM_E_CUDA;
     unsigned e = qmm_internal_matvec_error(clear) | qmm_internal_matmul_error(clear) |
                  qmm_internal_matmul_kq_error(clear) | qmm_internal_getrows_error(clear) |
-                 qmm_internal_kv_error(clear) | qmm_internal_quantize_error(clear) | qmm_internal_rope_error(clear) |
-                 qmm_internal_pages_error(clear) | qmm_internal_attend_error(clear);
+                 qmm_internal_kv_error(clear) | qmm_internal_quantize_error(clear) | qmm_internal_pages_error(clear) |
+                 qmm_internal_attend_error(clear);
     {
         unsigned v = 0;
         if (cudaMemcpyFromSymbol(&v, g_test_error, sizeof(v)) != cudaSuccess) return QMM_E_CUDA;

@@ -3,17 +3,11 @@
 //
 //   rope_freqs  one thread per pair, in f64 (once per model): turns per position
 //               as 64-bit fractions
-//   rope        a CTA per ~512 shares of eight values of neighbouring tokens: the
-//               tokens' tables of (cos, sin) pairs into shared memory, then two
-//               shares per thread, whose loads are issued before the tables are
-//               computed
-// Bound by memory: 8 bytes moved per value.
-#include "qmm_host.h"
+//   rope        the row kernel of the cache's store (kvpages.cu) with query rows only
+#include "kvpages.cuh"
 #include "rope_device.cuh"
 
 namespace qmm {
-
-static __device__ unsigned int g_rope_error = 0;
 
 // keep, the share of the unscaled frequency: QMM_ROPE_BANDS, a ramp over the turns
 // in orig_len positions, from lo to hi; QMM_ROPE_YARN, a ramp over the pair index,
@@ -48,67 +42,17 @@ __global__ void rope_freqs_kernel(uint64_t* __restrict__ freqs, int n_rot, doubl
     pdl_launch_dependents();
 }
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeShares = 2 * kRopeThreads;  // shares of eight values per CTA
-constexpr int kRopeTable = 1024;               // (cos, sin) entries in shared memory
+qmm_status rows_launch(int type, const KvPages& c, const RowArgs& a, int hd, cudaStream_t stream);
 
-// grid (groups of tpb tokens, groups of kRopeShares shares of one token when tpb
-// is 1); shares: of one token, H * hd / 8
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const float* x, float* y, const int32_t* __restrict__ pos,
-                                                            const uint64_t* __restrict__ freqs, int64_t T, int shares,
-                                                            int hd, int64_t ldx, int64_t ldy, int tpb, RopeLayout L,
-                                                            float mscale, int inverse) {
-    __shared__ float4 cs[kRopeTable];
-    pdl_wait();
-    const int64_t t0 = (int64_t)blockIdx.x * tpb;
-    const int nt = T - t0 < tpb ? (int)(T - t0) : tpb;
-    const int per_head = hd >> 3, half = L.n_rot >> 1;
-    const int s0 = blockIdx.y * kRopeShares;
-    const int n = tpb > 1 ? nt * shares : (shares - s0 < kRopeShares ? shares - s0 : kRopeShares);
-    float v[2][8];
-    int token[2], share[2];
-    int64_t at[2];
-#pragma unroll
-    for (int k = 0; k < 2; k++) {
-        const int i = threadIdx.x + k * kRopeThreads;
-        if (i < n) {
-            token[k] = tpb > 1 ? i / shares : 0;
-            const int s = s0 + i - token[k] * shares;
-            const int head = s / per_head;
-            share[k] = s - head * per_head;
-            at[k] = (int64_t)head * hd;
-            if (QMM_IN_BOUNDS(g_rope_error, (t0 + token[k]) * ldx + at[k] + hd - 1, T * ldx))
-                rope_load8(L, share[k], x + (t0 + token[k]) * ldx + at[k], v[k]);
-        }
-    }
-    for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
-        const int t = i / half;
-        const uint64_t f = freqs[i - t * half];
-        float4 c = turn_cos_sin((uint64_t)(int64_t)pos[t0 + t] * f, mscale);
-        if (inverse) c.z = -c.z, c.w = -c.w;
-        if (QMM_IN_BOUNDS(g_rope_error, i, kRopeTable)) cs[i] = c;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 2; k++) {
-        const int i = threadIdx.x + k * kRopeThreads;
-        if (i < n) {
-            rope_turn8(L, share[k], v[k], cs + token[k] * half);
-            if (QMM_IN_BOUNDS(g_rope_error, (t0 + token[k]) * ldy + at[k] + hd - 1, T * ldy))
-                rope_store8(L, share[k], y + (t0 + token[k]) * ldy + at[k], v[k]);
-        }
-    }
-    pdl_launch_dependents();
-}
-
-qmm_status rope_check(const qmm_rope_spec* r, int64_t hd, RopeLayout* L) {
+qmm_status rope_check(const qmm_rope_spec* r, int64_t hd, RowArgs* a) {
     if (!r || !r->freqs) return QMM_E_NULL;
     if (r->layout != QMM_ROPE_HALF && r->layout != QMM_ROPE_INTERLEAVED) return QMM_E_TYPE;
     if (r->n_rot < 2 || r->n_rot > hd || r->n_rot % 2) return QMM_E_SHAPE;
     if (!aligned16(r->freqs)) return QMM_E_ALIGN;
-    L->n_rot = (int)r->n_rot;
-    L->halves = r->layout == QMM_ROPE_HALF;
-    L->scattered = L->halves && r->n_rot % 8 != 0;
+    a->freqs = (const uint64_t*)r->freqs;
+    a->mscale = r->mscale;
+    a->n_rot = (int)r->n_rot;
+    a->pairs = r->layout == QMM_ROPE_INTERLEAVED ? kPairsNext : (r->n_rot % 8 ? kPairsScattered : kPairsHalf);
     return QMM_OK;
 }
 
@@ -117,16 +61,6 @@ qmm_status rope_check(const qmm_rope_spec* r, int64_t hd, RopeLayout* L) {
 using namespace qmm;
 
 extern "C" {
-
-unsigned qmm_internal_rope_error(int clear) {
-    unsigned v = 0;
-    cudaMemcpyFromSymbol(&v, g_rope_error, sizeof(v));
-    if (clear) {
-        const unsigned z = 0;
-        cudaMemcpyToSymbol(g_rope_error, &z, sizeof(z));
-    }
-    return v;
-}
 
 qmm_status qmm_rope_freqs(void* freqs, int64_t n_rot, double base, int scaling, double factor, double orig_len,
                           double lo, double hi, qmm_stream_t stream) {
@@ -146,17 +80,15 @@ qmm_status qmm_rope(const qmm_rope_spec* rope, const float* x, int64_t ldx, floa
     if (!x || !y || !pos) return QMM_E_NULL;
     if (!head_dim_ok(hd) || T < 1 || T > kMaxDim || H < 1 || H > kHeadsMax) return QMM_E_SHAPE;
     if (!row_stride_ok(ldx, H * hd) || !row_stride_ok(ldy, H * hd) || (x == y && ldx != ldy)) return QMM_E_SHAPE;
-    RopeLayout L;
-    const qmm_status st = rope_check(rope, hd, &L);
+    RowArgs a = {};
+    const qmm_status st = rope_check(rope, hd, &a);
     if (st != QMM_OK) return st;
-    if (!aligned16(x) || !aligned16(y) || ((uintptr_t)pos & 3u)) return QMM_E_ALIGN;
-    const int shares = (int)(H * hd / 8), half = L.n_rot / 2;
-    int tpb = kRopeShares / shares;  // tokens per CTA
-    if (tpb > kRopeTable / half) tpb = kRopeTable / half;
-    if (tpb < 1) tpb = 1;
-    const dim3 grid((unsigned)((T + tpb - 1) / tpb), tpb > 1 ? 1u : (unsigned)((shares + kRopeShares - 1) / kRopeShares));
-    return launch_pdl(rope_kernel, grid, kRopeThreads, 0, (cudaStream_t)stream, x, y, pos, (const uint64_t*)rope->freqs,
-                      T, shares, (int)hd, ldx, ldy, tpb, L, rope->mscale, inverse);
+    if (!aligned16(x) || !aligned16(y) || !aligned4(pos)) return QMM_E_ALIGN;
+    a.q = x, a.q_out = y, a.pos = pos;
+    a.T = T, a.ldq = ldx, a.ldqo = ldy, a.Hq = (int)H;
+    a.inverse = inverse;
+    const KvPages none = {};
+    return rows_launch(kNoPages, none, a, (int)hd, (cudaStream_t)stream);
 }
 
 }  // extern "C"

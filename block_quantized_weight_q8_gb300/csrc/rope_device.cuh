@@ -19,8 +19,8 @@
 // the exact value rounded once to f32 except where that lies within 2^-42 of a
 // rounding border.  That is what makes a rotated key's 8-bit codes reproducible by
 // any implementation that computes in 64 bits and rounds once.
-// About 40 f32 operations per pair's angle (once for every head of a token) and 28
-// per rotated pair, a third of the f32 rate at the speed the values arrive in.
+// About 90 operations per pair's angle (once for a token's heads) and 38 per rotated
+// pair: less than half of the issue slots in the time the values take to arrive.
 #pragma once
 
 #include "qmm_device.cuh"
@@ -76,13 +76,14 @@ __device__ __forceinline__ float4 turn_cos_sin(uint64_t phase, float m) {
     const int k = (int)(near >> 56);
     const int64_t rest = (int64_t)(near & ((1ull << 56) - 1)) - (1ll << 55);
     const float4 t = *reinterpret_cast<const float4*>(g_turn_table.v[k]);
-    // r = rest * 2 pi / 2^64
+    // r = rest * 2 pi / 2^64, rest as 2^32 times its upper half (24 bits: exact) and the lower
     constexpr double kStep = 2.0 * kPi / 18446744073709551616.0;
     constexpr float kHi = (float)kStep, kLo = (float)(kStep - (double)(float)kStep);
-    const float nh = __ll2float_rn(rest), nl = __ll2float_rn(rest - __float2ll_rn(nh));
+    const float nh = 4294967296.0f * (float)(int)(rest >> 32), nl = (float)(uint32_t)rest;
     const float p = __fmul_rn(nh, kHi);
     const float pe = __fmaf_rn(nl, kHi, __fmaf_rn(nh, kLo, __fmaf_rn(nh, kHi, -p)));
-    const float rh = __fadd_rn(p, pe), rl = __fsub_rn(pe, __fsub_rn(rh, p));
+    float rl;
+    const float rh = two_sum(p, pe, &rl);
     const float zh = __fmul_rn(rh, rh), zl = __fmaf_rn(2.0f * rh, rl, __fmaf_rn(rh, rh, -zh));
     // sin r = rh + sl, cos r - 1 = dh + dl
     const float sl = __fmaf_rn(rh * zh, __fmaf_rn(zh, 1.0f / 120.0f, -1.0f / 6.0f), rl);
@@ -125,70 +126,98 @@ __device__ __forceinline__ void turn_pair(float& a, float& b, float4 cs) {
     a = y;
 }
 
-// One thread's share of a head: eight values, the four pairs 4o .. 4o + 3 (pair p
-// < n_rot / 2 is rotated, the values behind n_rot are pairs of neighbours that are
-// not).  They are two float4: at 4o and n_rot/2 + 4o where halves are paired, else
-// eight neighbours -- or, where halves are paired and n_rot is no multiple of 8,
-// single values.
-struct RopeLayout {
-    int n_rot;     // 0: nothing is rotated
-    int halves;    // pairs (i, i + n_rot/2) instead of (2i, 2i + 1)
-    int scattered; // halves, and n_rot % 8 != 0
-};
-__device__ __forceinline__ bool rope_split(const RopeLayout& L, int o) { return L.halves && 8 * o < L.n_rot; }
-__device__ __forceinline__ int rope_first(const RopeLayout& L, int o) { return rope_split(L, o) ? 4 * o : 8 * o; }
-__device__ __forceinline__ int rope_second(const RopeLayout& L, int o) {
-    return rope_split(L, o) ? (L.n_rot >> 1) + 4 * o : 8 * o + 4;
-}
-// indices of pair p's two values in a head
-__device__ __forceinline__ int2 rope_pair(const RopeLayout& L, int p) {
-    const int half = L.n_rot >> 1;
-    return L.halves && p < half ? make_int2(p, p + half) : make_int2(2 * p, 2 * p + 1);
-}
+// Rows for the row kernel (kvpages.cu): f32 heads of T tokens, keys and values into a
+// cache's pages, queries rotated.
+constexpr int kNoPages = -1;  // in the place of a cache type: query rows only
 
-// v: the eight values as loaded (pair i of the share in v[i], v[i + 4] where halves
-// are paired or scattered, else in v[2i], v[2i + 1]); cs: the token's table
-__device__ __forceinline__ void rope_turn8(const RopeLayout& L, int o, float v[8], const float4* cs) {
-    if (L.scattered) {
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-            if (2 * (4 * o + i) < L.n_rot) turn_pair(v[i], v[i + 4], cs[4 * o + i]);
-    } else if (rope_split(L, o)) {
-#pragma unroll
-        for (int i = 0; i < 4; i++) turn_pair(v[i], v[i + 4], cs[4 * o + i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-            if (2 * (4 * o + i) < L.n_rot) turn_pair(v[2 * i], v[2 * i + 1], cs[4 * o + i]);
-    }
+// One thread's share of a head: eight values, of the four pairs 4o .. 4o + 3 (pair p
+// < n_rot / 2 is rotated; the values behind n_rot are taken as pairs of neighbours).
+// How the pairs lie:
+enum RowPairs {
+    kPairsNone = 0,       // nothing is rotated
+    kPairsHalf = 1,       // (i, i + n_rot/2), n_rot a multiple of 8: a float4 of each half
+    kPairsNext = 2,       // (2i, 2i + 1): eight neighbours
+    kPairsScattered = 3,  // (i, i + n_rot/2), any even n_rot: single values
+};
+struct RowArgs {
+    const float* k;
+    const float* v;
+    const float* q;  // null: no queries
+    float* q_out;
+    const int32_t* pos;
+    const int32_t* seq;  // null: token t belongs to sequence t
+    const uint64_t* freqs;
+    int64_t T, ldk, ldv, ldq, ldqo;
+    int Hq, inverse;
+    int n_rot, pairs;  // pairs: a RowPairs
+    float mscale;
+};
+// Where pair p's entry of a token's table lies: the four of a share in four runs, so
+// that a warp's lanes read neighbouring entries.
+__host__ __device__ __forceinline__ int turn_run(int half) { return (half + 3) >> 2; }
+__device__ __forceinline__ int turn_at(int half, int p) { return (p & 3) * turn_run(half) + (p >> 2); }
+
+// The places of a share's values in its head: two float4 at first and second, or (for
+// kPairsScattered) value i at a[i], value i + 4 at b[i].
+struct Share {
+    int first, second, turned;  // turned: pairs of the share that are rotated
+};
+template <int PAIRS>
+__device__ __forceinline__ Share row_share(int n_rot, int o) {
+    const int half = n_rot >> 1;
+    Share s;
+    s.turned = PAIRS == kPairsNone ? 0 : half - 4 * o;
+    s.turned = s.turned < 0 ? 0 : (s.turned > 4 ? 4 : s.turned);
+    const bool split = PAIRS == kPairsHalf && s.turned > 0;
+    s.first = split ? 4 * o : 8 * o;
+    s.second = split ? half + 4 * o : 8 * o + 4;
+    return s;
 }
-__device__ __forceinline__ void rope_load8(const RopeLayout& L, int o, const float* x, float v[8]) {
-    if (L.scattered) {
+__device__ __forceinline__ int2 scattered_at(int n_rot, int p) {
+    const int half = n_rot >> 1;
+    return p < half ? make_int2(p, p + half) : make_int2(2 * p, 2 * p + 1);
+}
+template <int PAIRS>
+__device__ __forceinline__ void row_load8(const Share& s, int n_rot, int o, const float* x, float v[8]) {
+    if (PAIRS == kPairsScattered) {
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            const int2 at = rope_pair(L, 4 * o + i);
+            const int2 at = scattered_at(n_rot, 4 * o + i);
             v[i] = x[at.x];
             v[i + 4] = x[at.y];
         }
         return;
     }
-    const float4 a = *reinterpret_cast<const float4*>(x + rope_first(L, o));
-    const float4 b = *reinterpret_cast<const float4*>(x + rope_second(L, o));
+    const float4 a = *reinterpret_cast<const float4*>(x + s.first);
+    const float4 b = *reinterpret_cast<const float4*>(x + s.second);
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
     v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
-__device__ __forceinline__ void rope_store8(const RopeLayout& L, int o, float* y, const float v[8]) {
-    if (L.scattered) {
+template <int PAIRS>
+__device__ __forceinline__ void row_store8(const Share& s, int n_rot, int o, float* y, const float v[8]) {
+    if (PAIRS == kPairsScattered) {
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            const int2 at = rope_pair(L, 4 * o + i);
+            const int2 at = scattered_at(n_rot, 4 * o + i);
             y[at.x] = v[i];
             y[at.y] = v[i + 4];
         }
         return;
     }
-    *reinterpret_cast<float4*>(y + rope_first(L, o)) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4*>(y + rope_second(L, o)) = make_float4(v[4], v[5], v[6], v[7]);
+    *reinterpret_cast<float4*>(y + s.first) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(y + s.second) = make_float4(v[4], v[5], v[6], v[7]);
+}
+// table: the token's, at this share's first pair (entry i is i * turn_run on)
+template <int PAIRS>
+__device__ __forceinline__ void row_turn8(const Share& s, float v[8], const float4* table, int run) {
+    if (PAIRS == kPairsNone) return;
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+        if (i < s.turned) {
+            const float4 cs = table[i * run];
+            if (PAIRS == kPairsNext) turn_pair(v[2 * i], v[2 * i + 1], cs);
+            else turn_pair(v[i], v[i + 4], cs);
+        }
 }
 
 }  // namespace qmm
