@@ -46,19 +46,22 @@ constexpr int kAttendWarps = 4;
 constexpr int kAttendThreads = 32 * kAttendWarps;
 constexpr int kAttendSms = 152;
 constexpr int kAttendHeads = 8;  // query heads per unit
-constexpr int kAttendMaxCtas = 3 * kAttendSms;
+constexpr int kAttendMaxCtas = 4 * kAttendSms;
 constexpr int kJoinWarps = 8;
 constexpr uint32_t kUnitCost = 8;  // of a unit besides its tiles, in tiles
-constexpr int kFold = 4;           // tiles between two folds of the tensor cores' sums
 
 template <int TYPE, int HDT>
 struct AttendShape {
     static constexpr int kRow = HDT * (TYPE == QMM_KV_F16 ? 2 : 1);  // bytes of a row
     static constexpr int kTile = kRow <= 128 ? 32 : 16;              // positions
-    static constexpr int kStages = kRow <= 64 ? 4 : 3;
-    static constexpr int kCtas = kRow <= 64 ? 3 : kRow <= 256 ? 2 : 1;  // per SM
-    static constexpr int kStage = 2 * kTile * kRow + 8 * kTile + 16;    // keys, values, their scales, the mask
-    static constexpr int kRing = kStages * kStage;                      // of a warp
+    // A warp's ring has slots of one tile's keys or values, with their scales and the
+    // mask.  Four, or three where rows are wide, and as many CTAs per SM as the
+    // registers allow (12 warps at HDT = 128: 8 with a deeper ring left the SM's issue
+    // slots half empty, as a warp waits about four cycles from one instruction to the next)
+    static constexpr int kSlots = kRow <= 256 ? 4 : 3;
+    static constexpr int kCtas = kRow <= 64 ? 4 : HDT <= 128 ? 3 : 2;  // per SM
+    static constexpr int kSlot = kTile * kRow + 4 * kTile + 16;
+    static constexpr int kRing = kSlots * kSlot;  // of a warp
     static constexpr int kSmem = kAttendWarps * kRing;
 };
 
@@ -155,6 +158,11 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
 __device__ __forceinline__ float exp2_approx(float x) {  // within 2 units in the last place; 0 at -inf
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -200,9 +208,9 @@ __device__ __forceinline__ int exponent_of(float x) {
     const int e = (int)((__float_as_uint(x) & 0x7FFFFFFFu) >> 23);
     return e < kExpLow ? kExpLow : e;
 }
-// Where an exchanged value quad q of head h lies in its head's row: quads a lane
-// holds in turn (q / 8 apart) and neighbouring heads in different banks.
-__device__ __forceinline__ int exchange_quad(int h, int q) { return q ^ ((q >> 3) & 7) ^ ((h & 1) << 2); }
+// Where an exchanged value quad q of head h lies in its head's row: what the eight
+// lanes of two heads write at once (quads 4 apart) goes to different banks.
+__device__ __forceinline__ int exchange_quad(int h, int q) { return q ^ ((q >> 3) & 1) ^ ((h & 1) << 1); }
 
 template <int TYPE, int HDT>
 __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
@@ -213,10 +221,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
     constexpr int kSize = TYPE == QMM_KV_F16 ? 2 : 1;    // bytes of a value
     constexpr int kPer = 16 / kSize;                     // values of a chunk
     constexpr int kGroups = kChunks / 4, kSteps = HDT / 16;
-    constexpr int kVB = ROW >= 128 ? 16 : 8;             // bytes of a value row that a lane takes at once
-    constexpr int kSets = ROW / (8 * kVB), kVD = kVB / kSize;
+    constexpr int kVB = 8 * kSize, kSets = ROW / (8 * kVB);  // a lane takes eight values of a row at once
     constexpr int kChains = TILE == 16 ? 2 : 1;  // sums of the first product that run side by side
-    constexpr bool kKeep = HDT <= 128;           // the second product's sums stay in registers between tiles
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ uint32_t scan[kAttendWarps], where[2];  // the run's first row, and the list's length before it
     __shared__ float part_m[kAttendWarps][kAttendHeads], part_l[kAttendWarps][kAttendHeads];
@@ -299,12 +305,14 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
             }
             return id;
         };
-        auto issue = [&](int t, int id, int slot) {
+        // one half of tile t, its keys or its values, into a slot of the ring
+        auto issue = [&](int t, int id, bool values, int slot) {
             if (t < tb) {
-                const uint32_t dst = ring_u + slot * S::kStage;
+                const uint8_t* pool = values ? c.v : c.k;
+                const uint32_t dst = ring_u + slot * S::kSlot;
                 const int p0 = ((tile0 + t) * TILE) & mask_o;  // TILE and the page size are powers of two
                 const uint32_t live = __ballot_sync(0xFFFFFFFFu, id >= 0);
-                if (lane == 0) *reinterpret_cast<uint32_t*>(ring + slot * S::kStage + 2 * TILE * ROW + 8 * TILE) = live;
+                if (lane == 0) *reinterpret_cast<uint32_t*>(ring + slot * S::kSlot + TILE * ROW + 4 * TILE) = live;
                 if (wide && live == (TILE == 32 ? 0xFFFFFFFFu : 0xFFFFu)) {
 #pragma unroll
                     for (int b = 0; b < TILE / 16; b++) {
@@ -314,8 +322,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
 #pragma unroll
                         for (int i = 0; i < kN; i++) {
                             if (!QMM_IN_BOUNDS(g_attend_error, from + i * 512 + 15, c.num_pages * c.stride)) continue;
-                            cp_async16(dst + put_k(b * kN + i), c.k + from + i * 512, 16);
-                            cp_async16(dst + TILE * ROW + put_v(b * kN + i), c.v + from + i * 512, 16);
+                            cp_async16(dst + (values ? put_v(b * kN + i) : put_k(b * kN + i)), pool + from + i * 512, 16);
                         }
                     }
                 } else {
@@ -325,31 +332,29 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
                         int bytes = (pid >= 0 && c_ch * 16 < c.row_bytes) ? 16 : 0;
                         int64_t from = bytes ? kv_row_at(c, pid, kvh, (p0 + row) & mask_o) + c_ch * 16 : 0;
                         if (!QMM_IN_BOUNDS(g_attend_error, from + 15, c.num_pages * c.stride)) from = 0, bytes = 0;
-                        cp_async16(dst + put_k(it), c.k + from, bytes);
-                        cp_async16(dst + TILE * ROW + put_v(it), c.v + from, bytes);
+                        cp_async16(dst + (values ? put_v(it) : put_k(it)), pool + from, bytes);
                     }
                 }
                 if (TYPE == QMM_KV_Q8 && lane < TILE) {  // position p's scale at (p % 4) (TILE / 4) + p / 4
                     int bytes = id >= 0 ? 4 : 0;
                     int64_t from = bytes ? kv_scale_at(c, id, kvh, (p0 + lane) & mask_o) : 0;
                     if (!QMM_IN_BOUNDS(g_attend_error, from + 3, c.num_pages * c.stride)) from = 0, bytes = 0;
-                    const uint32_t to = dst + 2 * TILE * ROW + 4 * ((lane & 3) * (TILE / 4) + (lane >> 2));
-                    cp_async4z(to, c.k + from, bytes);
-                    cp_async4z(to + 4 * TILE, c.v + from, bytes);
+                    cp_async4z(dst + TILE * ROW + 4 * ((lane & 3) * (TILE / 4) + (lane >> 2)), pool + from, bytes);
                 }
             }
             cp_async_commit();  // an empty group where there is no tile: the wait counts groups
         };
 
-        // fill the ring, then fetch the queries under its copies
-        int next = ta + warp;
-        int id = page_at(next);
-#pragma unroll
-        for (int s = 0; s < S::kStages - 1; s++) {
-            const int id1 = page_at(next + kAttendWarps);
-            issue(next, id, s);
-            id = id1;
-            next += kAttendWarps;
+        // Fill the ring but for one slot, then fetch the queries under its copies.  While
+        // half q is read, half q + kSlots - 1 is on its way into the slot of half q - 1.
+        const int ahead = kAttendWarps;  // from a warp's tile to its next
+        int next = ta + warp, id1, id2;  // the pages of the tiles one and two ahead
+        {
+            const int id0 = page_at(next);
+            id1 = page_at(next + ahead), id2 = page_at(next + 2 * ahead);
+            issue(next, id0, false, 0);
+            issue(next, id0, true, 1);
+            if (S::kSlots == 4) issue(next + ahead, id1, false, 2);
         }
 
         // A operand of the first product: step s of lane j holds values
@@ -381,54 +386,28 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
             }
         }
 
-        // Of head n: m_run, a whole number at or above every score so far, and the sum of
-        // weights 2^(score - m_run) of this lane's positions.  The weighted values: o, and
-        // in acc what the tensor cores have summed since the last fold, of weights times
-        // 2^(14 - e_run) times value scales below 2^(e_run + 1).
+        // Of head n: m_run, a whole number at or above every score so far, the sum of
+        // weights 2^(score - m_run) of this lane's positions, and the weighted values.  In
+        // the tensor cores weights are times 2^(14 - e_run), value scales below
+        // 2^(e_run + 1).
         float m_run = -INFINITY, l_run = 0.0f, up = 16384.0f, down = 1.0f / 16384.0f;
-        int e_run = kExpLow, since = 0;  // e_run: an exponent field
+        int e_run = kExpLow;  // an exponent field
         if (TYPE == QMM_KV_Q8) up = pow2i(14 + 127 - e_run), down = pow2i(e_run - 127 - 14);
-        float o[kSets][kVD][2], acc[kKeep ? kSets : 1][kVD][4];
+        float o[kSets][8][2];
 #pragma unroll
         for (int s = 0; s < kSets; s++)
 #pragma unroll
-            for (int t = 0; t < kVD; t++) o[s][t][0] = o[s][t][1] = 0.0f;
-        if (kKeep) {
-#pragma unroll
-            for (int s = 0; s < kSets; s++)
-#pragma unroll
-                for (int t = 0; t < kVD; t++)
-                    acc[kKeep ? s : 0][t][0] = acc[kKeep ? s : 0][t][1] = acc[kKeep ? s : 0][t][2] =
-                        acc[kKeep ? s : 0][t][3] = 0.0f;
-        }
-        // o = (o + acc) keep by f32 operations: the tensor core's own additions cut off
-        // instead of rounding, which over a long cache would add up
-        auto fold = [&](float keep) {
-#pragma unroll
-            for (int s = 0; s < kSets; s++)
-#pragma unroll
-                for (int t = 0; t < kVD; t++) {
-                    float* y = acc[kKeep ? s : 0][t];
-#pragma unroll
-                    for (int i = 0; i < 2; i++) o[s][t][i] = __fmaf_rn(y[i] + y[i + 2], down, o[s][t][i]) * keep;
-                    y[0] = y[1] = y[2] = y[3] = 0.0f;
-                }
-            since = 0;
-        };
+            for (int t = 0; t < 8; t++) o[s][t][0] = o[s][t][1] = 0.0f;
 
         int slot = 0;
-        for (int t = ta + warp; t < tb; t += kAttendWarps) {
-            cp_async_wait<S::kStages - 2>();
-            __syncwarp();  // the tile is here for every lane, and the slot before it is read out
-            {
-                const int id1 = page_at(next + kAttendWarps);
-                issue(next, id, slot == 0 ? S::kStages - 1 : slot - 1);
-                id = id1;
-                next += kAttendWarps;
-            }
-            const uint32_t st = ring_u + slot * S::kStage;
-            const uint8_t* tail = ring + slot * S::kStage + 2 * TILE * ROW;  // scales, then the mask
-            const uint32_t live = *reinterpret_cast<const uint32_t*>(tail + 8 * TILE);
+        auto turn = [&](int by) { return slot + by >= S::kSlots ? slot + by - S::kSlots : slot + by; };
+        for (int t = ta + warp; t < tb; t += ahead) {
+            cp_async_wait<S::kSlots - 2>();
+            __syncwarp();  // the keys are here for every lane, and the slot before is read out
+            issue(t + ahead, id1, S::kSlots == 4, turn(S::kSlots - 1));
+            const uint32_t st = ring_u + slot * S::kSlot;
+            const uint8_t* tail = ring + slot * S::kSlot + TILE * ROW;  // scales, then the mask
+            const uint32_t live = *reinterpret_cast<const uint32_t*>(tail + 4 * TILE);
 
             // scores: column i of n-tile m is position 8 m + i / 2 + 4 (i % 2)
             float sc[TILE / 8][kChains][4];
@@ -461,7 +440,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
             }
             // this lane's positions of head n: 4 i + j
             constexpr int kMine = TILE / 4;
-            float wt[kMine], vs[kMine], top = -INFINITY;
+            float wt[kMine], top = -INFINITY;
 #pragma unroll
             for (int i = 0; i < kMine; i += 4) {
                 const float* y0 = sc[i >> 1][0];
@@ -476,10 +455,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
                 }
                 if (TYPE == QMM_KV_Q8) {
                     const float4 ks = *reinterpret_cast<const float4*>(tail + 4 * (j * kMine + i));
-                    const float4 v4 = *reinterpret_cast<const float4*>(tail + 4 * TILE + 4 * (j * kMine + i));
                     wt[i] *= ks.x * q_scale, wt[i + 1] *= ks.y * q_scale;
                     wt[i + 2] *= ks.z * q_scale, wt[i + 3] *= ks.w * q_scale;
-                    vs[i] = v4.x, vs[i + 1] = v4.y, vs[i + 2] = v4.z, vs[i + 3] = v4.w;
                 } else {
                     wt[i] *= q_scale, wt[i + 1] *= q_scale, wt[i + 2] *= q_scale, wt[i + 3] *= q_scale;
                 }
@@ -493,54 +470,66 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
             for (int i = 0; i < kMine; i++) top = fmaxf(top, wt[i]);
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-            float keep = 1.0f;
-            const int e_lane = TYPE == QMM_KV_Q8 && lane < TILE
-                                   ? exponent_of(*reinterpret_cast<const float*>(tail + 4 * TILE + 4 * lane)) : 0;
+            slot = turn(1);
+            cp_async_wait<S::kSlots - 2>();
+            __syncwarp();  // the values are here, the keys are read out
+            if (S::kSlots == 4) issue(t + 2 * ahead, id2, false, turn(S::kSlots - 1));
+            else issue(t + ahead, id1, true, turn(S::kSlots - 1));
+            id1 = id2, id2 = page_at(t + 3 * ahead);
+            const uint32_t sv = ring_u + slot * S::kSlot;
+            const float* vs = reinterpret_cast<const float*>(ring + slot * S::kSlot + TILE * ROW);
+            const int e_lane = TYPE == QMM_KV_Q8 && lane < TILE ? exponent_of(vs[lane]) : 0;
             if (__any_sync(0xFFFFFFFFu, top > m_run || (TYPE == QMM_KV_Q8 && e_lane > e_run))) {
                 const float m_new = fmaxf(m_run, ceilf(top));
-                keep = exp2_approx(m_run - (m_new == -INFINITY ? 0.0f : m_new));
+                const float keep = exp2_approx(m_run - (m_new == -INFINITY ? 0.0f : m_new));
                 m_run = m_new;
                 l_run *= keep;
-                if (kKeep) fold(keep);
+#pragma unroll
+                for (int s = 0; s < kSets; s++)
+#pragma unroll
+                    for (int t2 = 0; t2 < 8; t2++) o[s][t2][0] *= keep, o[s][t2][1] *= keep;
                 if (TYPE == QMM_KV_Q8) {
                     const int e = (int)__reduce_max_sync(0xFFFFFFFFu, (unsigned)e_lane);
                     e_run = e > e_run ? e : e_run;
                     up = pow2i(14 + 127 - e_run), down = pow2i(e_run - 127 - 14);
                 }
-            } else if (kKeep && since == kFold) {
-                fold(1.0f);
             }
-            since++;
             const float m_at = m_run == -INFINITY ? 0.0f : m_run;  // nothing seen yet: every weight is 0
             uint32_t pf[TILE / 16][4];
 #pragma unroll
-            for (int i = 0; i < kMine; i += 2) {
+            for (int i = 0; i < kMine; i += 4) {
+                float4 v4 = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+                if (TYPE == QMM_KV_Q8) v4 = *reinterpret_cast<const float4*>(vs + j * kMine + i);
                 const float w0 = exp2_approx(wt[i] - m_at), w1 = exp2_approx(wt[i + 1] - m_at);
-                l_run += w0 + w1;
-                const float s0 = TYPE == QMM_KV_Q8 ? vs[i] * up : up, s1 = TYPE == QMM_KV_Q8 ? vs[i + 1] * up : up;
-                split_h2(w0 * s0, w1 * s1, &pf[i >> 2][i & 2], &pf[i >> 2][(i & 2) + 1]);
+                const float w2 = exp2_approx(wt[i + 2] - m_at), w3 = exp2_approx(wt[i + 3] - m_at);
+                l_run += (w0 + w1) + (w2 + w3);
+                split_h2(w0 * (v4.x * up), w1 * (v4.y * up), &pf[i >> 2][0], &pf[i >> 2][1]);
+                split_h2(w2 * (v4.z * up), w3 * (v4.w * up), &pf[i >> 2][2], &pf[i >> 2][3]);
             }
-            // values: column n of n-tile (set, t) is value 8 kVD set + kVD n + t
+            // Values: column n of n-tile (set, t) is value 64 set + 8 n + t.  Fresh sums per
+            // tile, added to the running ones by f32 FMAs: the tensor core's own additions cut
+            // off instead of rounding, which over a long cache would add up.
 #pragma unroll
             for (int s = 0; s < kSets; s++) {
-                float(*ac)[4] = acc[kKeep ? s : 0];
+                float acc[8][4];
 #pragma unroll
                 for (int b = 0; b < TILE / 16; b++) {
                     uint32_t vw[4][kVB / 4];
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
-                        const uint32_t vr = st + (TILE + 16 * b + j + 4 * i) * ROW;
+                        const uint32_t vr = sv + (16 * b + j + 4 * i) * ROW;
                         if (kVB == 16) {
                             const uint4 y = lds128(vr + (((8 * s + n) ^ (j << 1)) << 4));
                             vw[i][0] = y.x, vw[i][1] = y.y, vw[i][kVB / 4 - 2] = y.z, vw[i][kVB / 4 - 1] = y.w;
                         } else {
-                            const uint32_t at = vr + (((n >> 1) ^ (j & 2)) << 4) + ((n & 1) << 3);
-                            vw[i][0] = lds32(at), vw[i][1] = lds32(at + 4);
+                            const int ch = (4 * s + (n >> 1)) ^ (ROW >= 128 ? j << 1 : j & 2);
+                            const uint2 y = lds64(vr + (ch << 4) + ((n & 1) << 3));
+                            vw[i][0] = y.x, vw[i][1] = y.y;
                         }
                     }
-                    auto mma = [&](int t, uint32_t b0, uint32_t b1) {
-                        if (!kKeep && b == 0) mma_f16_first(ac[t % kVD], pf[b], b0, b1);
-                        else mma_f16(ac[t % kVD], pf[b], b0, b1);
+                    auto mma = [&](int t2, uint32_t b0, uint32_t b1) {
+                        if (b == 0) mma_f16_first(acc[t2 & 7], pf[b], b0, b1);
+                        else mma_f16(acc[t2 & 7], pf[b], b0, b1);
                     };
 #pragma unroll
                     for (int w = 0; w < kVB / 4; w++) {
@@ -560,17 +549,14 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
                         }
                     }
                 }
-                if (!kKeep) {
 #pragma unroll
-                    for (int t2 = 0; t2 < kVD; t2++)
+                for (int t2 = 0; t2 < 8; t2++)
 #pragma unroll
-                        for (int i = 0; i < 2; i++)
-                            o[s][t2][i] = __fmaf_rn(o[s][t2][i], keep, down * (ac[t2][i] + ac[t2][i + 2]));
-                }
+                    for (int i = 0; i < 2; i++)
+                        o[s][t2][i] = __fmaf_rn(acc[t2][i] + acc[t2][i + 2], down, o[s][t2][i]);
             }
-            slot = slot == S::kStages - 1 ? 0 : slot + 1;
+            slot = turn(1);
         }
-        if (kKeep) fold(1.0f);
 
         // the warps meet: running maxima and sums, then the values through shared memory
         l_run += __shfl_xor_sync(0xFFFFFFFFu, l_run, 1);
@@ -584,8 +570,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
 #pragma unroll
             for (int i = 0; i < 2; i++)
 #pragma unroll
-                for (int t = 0; t < kVD; t += 4)
-                    *reinterpret_cast<float4*>(xo + 4 * exchange_quad(n, (8 * kVD * s + kVD * (2 * j + i) + t) / 4)) =
+                for (int t = 0; t < 8; t += 4)
+                    *reinterpret_cast<float4*>(xo + 4 * exchange_quad(n, (64 * s + 8 * (2 * j + i) + t) / 4)) =
                         make_float4(o[s][t][i], o[s][t + 1][i], o[s][t + 2][i], o[s][t + 3][i]);
         const bool whole = ta == 0 && tb == (int)tiles;
         float* part = a.parts + (2 * (int64_t)blockIdx.x + (ta == 0 ? 1 : 0)) * (kAttendHeads * (c.hd + 2));
