@@ -54,15 +54,16 @@ template <int TYPE, int HDT>
 struct AttendShape {
     static constexpr int kRow = HDT * (TYPE == QMM_KV_F16 ? 2 : 1);  // bytes of a row
     static constexpr int kTile = kRow <= 128 ? 32 : 16;              // positions
-    // A warp's ring has slots of one tile's keys or values, with their scales and the
-    // mask.  Four, or three where rows are wide, and as many CTAs per SM as the
-    // registers allow (12 warps at HDT = 128: 8 with a deeper ring left the SM's issue
-    // slots half empty, as a warp waits about four cycles from one instruction to the next)
-    static constexpr int kSlots = kRow <= 256 ? 4 : 3;
-    static constexpr int kCtas = kRow <= 64 ? 4 : HDT <= 128 ? 3 : 2;  // per SM
+    // A warp's ring has three slots of one tile's keys or values, with their scales and
+    // the mask: two are on their way while one is read.
+    static constexpr int kSlots = 3;
     static constexpr int kSlot = kTile * kRow + 4 * kTile + 16;
     static constexpr int kRing = kSlots * kSlot;  // of a warp
-    static constexpr int kSmem = kAttendWarps * kRing;
+    static constexpr int kQuery = HDT / 16 * 512;  // the unit's queries, as the first product takes them
+    static constexpr int kSmem = kAttendWarps * kRing + kQuery;
+    // CTAs per SM, as many as registers and shared memory allow: a warp waits about four
+    // cycles from one instruction to the next, so 8 warps leave half the issue slots empty
+    static constexpr int kCtas = HDT <= 128 ? (kRow == 128 && HDT == 64 ? 3 : 4) : kRow <= 256 ? 3 : 2;
 };
 
 struct AttendArgs {
@@ -257,6 +258,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
     __syncthreads();
     uint32_t r = where[0], g = begin, row_start = where[1] * units;
 
+    constexpr uint32_t kFull = TILE == 32 ? 0xFFFFFFFFu : 0xFFFFu;
+    uint4* query = reinterpret_cast<uint4*>(smem + kAttendWarps * S::kRing);
     uint8_t* ring = smem + warp * S::kRing;
     const uint32_t ring_u = smem_u32(ring);
     // where this lane's chunk of the it-th copy goes in a tile (swizzled so that both
@@ -305,19 +308,22 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
             }
             return id;
         };
-        // one half of tile t, its keys or its values, into a slot of the ring
-        auto issue = [&](int t, int id, bool values, int slot) {
+        // its row in the pools, from their start; -1: none
+        auto row_at = [&](int t, int id) -> int64_t {
+            return id < 0 ? -1 : kv_row_at(c, id, kvh, ((tile0 + t) * TILE + lane) & mask_o);
+        };
+        // one half of tile t, its keys or its values, into a slot of the ring; at: this
+        // lane's position's row, live: the positions that have one
+        auto issue = [&](int t, int64_t at, uint32_t live, bool values, int slot) {
             if (t < tb) {
                 const uint8_t* pool = values ? c.v : c.k;
                 const uint32_t dst = ring_u + slot * S::kSlot;
-                const int p0 = ((tile0 + t) * TILE) & mask_o;  // TILE and the page size are powers of two
-                const uint32_t live = __ballot_sync(0xFFFFFFFFu, id >= 0);
-                if (lane == 0) *reinterpret_cast<uint32_t*>(ring + slot * S::kSlot + TILE * ROW + 4 * TILE) = live;
-                if (wide && live == (TILE == 32 ? 0xFFFFFFFFu : 0xFFFFu)) {
+                if (!values && lane == 0)
+                    *reinterpret_cast<uint32_t*>(ring + slot * S::kSlot + TILE * ROW + 4 * TILE) = live;
+                if (wide && live == kFull) {
 #pragma unroll
                     for (int b = 0; b < TILE / 16; b++) {
-                        const int pid = __shfl_sync(0xFFFFFFFFu, id, 16 * b);
-                        const int64_t from = kv_row_at(c, pid, kvh, (p0 + 16 * b) & mask_o) + c_row * ROW + c_ch * 16;
+                        const int64_t from = __shfl_sync(0xFFFFFFFFu, at, 16 * b) + c_row * ROW + c_ch * 16;
                         constexpr int kN = kChunks / 2;  // copies of sixteen rows
 #pragma unroll
                         for (int i = 0; i < kN; i++) {
@@ -328,16 +334,18 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
                 } else {
 #pragma unroll
                     for (int it = 0; it < TILE * kChunks / 32; it++) {
-                        const int row = it * kRowsPer + c_row, pid = __shfl_sync(0xFFFFFFFFu, id, row);
-                        int bytes = (pid >= 0 && c_ch * 16 < c.row_bytes) ? 16 : 0;
-                        int64_t from = bytes ? kv_row_at(c, pid, kvh, (p0 + row) & mask_o) + c_ch * 16 : 0;
+                        int64_t from = __shfl_sync(0xFFFFFFFFu, at, it * kRowsPer + c_row);
+                        int bytes = (from >= 0 && c_ch * 16 < c.row_bytes) ? 16 : 0;
+                        from = bytes ? from + c_ch * 16 : 0;
                         if (!QMM_IN_BOUNDS(g_attend_error, from + 15, c.num_pages * c.stride)) from = 0, bytes = 0;
                         cp_async16(dst + (values ? put_v(it) : put_k(it)), pool + from, bytes);
                     }
                 }
                 if (TYPE == QMM_KV_Q8 && lane < TILE) {  // position p's scale at (p % 4) (TILE / 4) + p / 4
-                    int bytes = id >= 0 ? 4 : 0;
-                    int64_t from = bytes ? kv_scale_at(c, id, kvh, (p0 + lane) & mask_o) : 0;
+                    // its scale lies as far behind its page's scales as its row behind the page
+                    const int row = (kvh << c.page_shift) + (((tile0 + t) * TILE + lane) & mask_o);
+                    int bytes = at >= 0 ? 4 : 0;
+                    int64_t from = bytes ? at + (c.scales - (int64_t)row * (c.row_bytes - 4)) : 0;
                     if (!QMM_IN_BOUNDS(g_attend_error, from + 3, c.num_pages * c.stride)) from = 0, bytes = 0;
                     cp_async4z(dst + TILE * ROW + 4 * ((lane & 3) * (TILE / 4) + (lane >> 2)), pool + from, bytes);
                 }
@@ -345,21 +353,19 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
             cp_async_commit();  // an empty group where there is no tile: the wait counts groups
         };
 
-        // Fill the ring but for one slot, then fetch the queries under its copies.  While
-        // half q is read, half q + kSlots - 1 is on its way into the slot of half q - 1.
-        const int ahead = kAttendWarps;  // from a warp's tile to its next
-        int next = ta + warp, id1, id2;  // the pages of the tiles one and two ahead
-        {
-            const int id0 = page_at(next);
-            id1 = page_at(next + ahead), id2 = page_at(next + 2 * ahead);
-            issue(next, id0, false, 0);
-            issue(next, id0, true, 1);
-            if (S::kSlots == 4) issue(next + ahead, id1, false, 2);
-        }
+        // Fill two slots, then fetch the queries under their copies.  While half q of the
+        // tiles' halves is read, q + 1 and q + 2 are on their way.
+        constexpr int ahead = kAttendWarps;  // from a warp's tile to its next
+        int id1 = page_at(ta + warp);        // the page of the tile after
+        int64_t at1 = row_at(ta + warp, id1);
+        uint32_t live1 = __ballot_sync(0xFFFFFFFFu, id1 >= 0);
+        issue(ta + warp, at1, live1, false, 0);
+        issue(ta + warp, at1, live1, true, 1);
+        id1 = page_at(ta + warp + ahead);
 
         // A operand of the first product: step s of lane j holds values
-        // kPer * (j + 4 * (s / (kPer / 4))) + 4 * (s % (kPer / 4)) .. + 3 of head n
-        uint32_t qf[kSteps][4];
+        // kPer * (j + 4 * (s / (kPer / 4))) + 4 * (s % (kPer / 4)) .. + 3 of head n.  Every
+        // warp reads them all for their largest, and writes its share of the steps.
         float q_scale;
         {
             float4 qv[kSteps];
@@ -377,14 +383,18 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
             amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
             const int e = exponent_of(amax) - 127;
-            const float up = pow2i(14 - e);
+            const float by = pow2i(14 - e);
             q_scale = a.scale * 1.44269504088896341f * pow2i(e - 14);  // scores in base 2
 #pragma unroll
             for (int s = 0; s < kSteps; s++) {
-                split_h2(qv[s].x * up, qv[s].y * up, &qf[s][0], &qf[s][1]);
-                split_h2(qv[s].z * up, qv[s].w * up, &qf[s][2], &qf[s][3]);
+                if (s % kAttendWarps != warp) continue;
+                uint4 f;
+                split_h2(qv[s].x * by, qv[s].y * by, &f.x, &f.y);
+                split_h2(qv[s].z * by, qv[s].w * by, &f.z, &f.w);
+                query[s * 32 + lane] = f;
             }
         }
+        __syncthreads();
 
         // Of head n: m_run, a whole number at or above every score so far, the sum of
         // weights 2^(score - m_run) of this lane's positions, and the weighted values.  In
@@ -404,7 +414,9 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
         for (int t = ta + warp; t < tb; t += ahead) {
             cp_async_wait<S::kSlots - 2>();
             __syncwarp();  // the keys are here for every lane, and the slot before is read out
-            issue(t + ahead, id1, S::kSlots == 4, turn(S::kSlots - 1));
+            at1 = row_at(t + ahead, id1);
+            live1 = __ballot_sync(0xFFFFFFFFu, id1 >= 0);
+            issue(t + ahead, at1, live1, false, turn(2));
             const uint32_t st = ring_u + slot * S::kSlot;
             const uint8_t* tail = ring + slot * S::kSlot + TILE * ROW;  // scales, then the mask
             const uint32_t live = *reinterpret_cast<const uint32_t*>(tail + 4 * TILE);
@@ -423,6 +435,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
 #pragma unroll
                 for (int w = 0; w < kPer / 4; w++) {
                     const int step = cg * (kPer / 4) + w;
+                    const uint4 qf = query[step * 32 + lane];
 #pragma unroll
                     for (int m = 0; m < TILE / 8; m++) {
                         const uint32_t* f = reinterpret_cast<const uint32_t*>(&kw[m]);
@@ -433,8 +446,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
                         } else {
                             b0 = f[2 * w], b1 = f[2 * w + 1];
                         }
-                        if (step < kChains) mma_f16_first(sc[m][step % kChains], qf[step], b0, b1);
-                        else mma_f16(sc[m][step % kChains], qf[step], b0, b1);
+                        if (step < kChains) mma_f16_first(sc[m][step % kChains], &qf.x, b0, b1);
+                        else mma_f16(sc[m][step % kChains], &qf.x, b0, b1);
                     }
                 }
             }
@@ -461,7 +474,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
                     wt[i] *= q_scale, wt[i + 1] *= q_scale, wt[i + 2] *= q_scale, wt[i + 3] *= q_scale;
                 }
             }
-            if (live != (TILE == 32 ? 0xFFFFFFFFu : 0xFFFFu)) {
+            if (live != kFull) {
 #pragma unroll
                 for (int i = 0; i < kMine; i++)
                     if (!(live >> (4 * i + j) & 1u)) wt[i] = -INFINITY;
@@ -473,9 +486,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
             slot = turn(1);
             cp_async_wait<S::kSlots - 2>();
             __syncwarp();  // the values are here, the keys are read out
-            if (S::kSlots == 4) issue(t + 2 * ahead, id2, false, turn(S::kSlots - 1));
-            else issue(t + ahead, id1, true, turn(S::kSlots - 1));
-            id1 = id2, id2 = page_at(t + 3 * ahead);
+            issue(t + ahead, at1, live1, true, turn(2));
+            id1 = page_at(t + 2 * ahead);
             const uint32_t sv = ring_u + slot * S::kSlot;
             const float* vs = reinterpret_cast<const float*>(ring + slot * S::kSlot + TILE * ROW);
             const int e_lane = TYPE == QMM_KV_Q8 && lane < TILE ? exponent_of(vs[lane]) : 0;
