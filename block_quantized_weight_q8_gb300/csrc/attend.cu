@@ -14,7 +14,7 @@
 //   f32     a query, and the weights times the value scales, are split into two
 //           f16 (hi + lo, 22 bits) and take two rows of the tile: rows 0-7 are
 //           the heads' hi, rows 8-15 their lo, and one thread holds both sums.
-//           Each is first brought near 2^14 by a power of two (per head; per tile
+//           Each is first brought near f16's upper end by a power of two (per head; per tile
 //           of positions), so that lo does not fall below f16's range
 //   layout  the order of the 16 values within a step is free as long as both
 //           operands share it, so a lane takes its operand straight from 16-byte
@@ -22,7 +22,7 @@
 //           the second product wants its weights: nothing is shuffled but the
 //           row maximum
 // Running maximum and sum of a softmax (in base 2) per warp: one pass.  The reference
-// is the maximum rounded up to a whole number, so rescaling by it is exact and rare.
+// is a whole number near the maximum, so rescaling by it is exact and rare.
 //
 // Split.  The work is the list of (row, unit, tile): a unit is a KV head and up to
 // eight of its query heads, a tile 32 (16) positions; each unit counts as
@@ -49,6 +49,7 @@ constexpr int kAttendHeads = 8;  // query heads per unit
 constexpr int kAttendMaxCtas = 4 * kAttendSms;
 constexpr int kJoinWarps = 8;
 constexpr uint32_t kUnitCost = 8;  // of a unit besides its tiles, in tiles
+constexpr float kSlack = 4.0f;     // what scores may be over the running reference, in powers of two
 
 template <int TYPE, int HDT>
 struct AttendShape {
@@ -83,10 +84,11 @@ struct RowRange {
     int64_t seq;
     int first, len;
 };
+template <bool L2 = false>
 __device__ __forceinline__ RowRange attend_row(const KvPages& c, const AttendArgs& a, int64_t r) {
     RowRange x;
-    x.len = __ldg(a.lens + r);
-    x.seq = a.seq ? (int64_t)__ldg(a.seq + r) : r;
+    x.len = L2 ? __ldcg(a.lens + r) : __ldg(a.lens + r);
+    x.seq = a.seq ? (int64_t)(L2 ? __ldcg(a.seq + r) : __ldg(a.seq + r)) : r;
     x.first = 0;
     if (x.len > 0) {
         const int64_t room = c.max_pages << c.page_shift;
@@ -233,30 +235,55 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = lane >> 2, j = lane & 3;
     const uint32_t units = c.Hkv * a.blocks;
 
-    // the run: total work, then the row in which it begins
+    // The run: total work, then the row r in which it begins.  Up to 32 rows are held by
+    // each warp's lanes; more are scanned by the block.
     const uint32_t R = (uint32_t)a.R;
-    uint32_t mine = 0, before, total;
-    for (uint32_t r = threadIdx.x; r < R; r += kAttendThreads)
-        mine += unit_weight(row_tiles<TILE>(attend_row(c, a, r)));
-    total = block_scan<kAttendThreads>(mine, &before, scan);
+    const bool few = R <= 32;
+    RowRange mine;
+    mine.len = mine.first = 0, mine.seq = 0;
+    if (few && lane < R) mine = attend_row(c, a, lane);
+    uint32_t total, before, weight1 = few ? unit_weight(row_tiles<TILE>(mine)) : 0;
+    if (few) {
+        before = weight1;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, before, m);
+            if (lane >= m) before += v;
+        }
+        total = __shfl_sync(0xFFFFFFFFu, before, 31);
+        before -= weight1;
+    } else {
+        for (uint32_t i = threadIdx.x; i < R; i += kAttendThreads)
+            weight1 += unit_weight(row_tiles<TILE>(attend_row(c, a, i)));
+        total = block_scan<kAttendThreads>(weight1, &before, scan);
+    }
     if (total == 0) return;
     const Runs runs(total * units, gridDim.x);
     if (blockIdx.x >= runs.ctas) return;
-    const uint32_t begin = runs.begin(blockIdx.x), end = runs.begin(blockIdx.x + 1), at = begin / units;
-    if (R <= kAttendThreads) {
-        if (before <= at && at < before + mine) where[0] = threadIdx.x, where[1] = before;
+    const uint32_t begin = runs.begin(blockIdx.x), end = runs.begin(blockIdx.x + 1);
+    uint32_t r, g = begin, row_start;  // row_start: the row's first position in the list
+    if (few) {
+        r = __ffs(__ballot_sync(0xFFFFFFFFu, before * units <= begin && begin < (before + weight1) * units)) - 1;
+        row_start = __shfl_sync(0xFFFFFFFFu, before, r) * units;
     } else {
         uint32_t base = 0;
-        for (uint32_t r0 = 0; r0 < R && base <= at; r0 += kAttendThreads) {
-            const uint32_t r = r0 + threadIdx.x;
-            const uint32_t t = r < R ? unit_weight(row_tiles<TILE>(attend_row(c, a, r))) : 0;
-            const uint32_t sum = block_scan<kAttendThreads>(t, &before, scan);
-            if (base + before <= at && at < base + before + t) where[0] = r, where[1] = base + before;
+        for (uint32_t r0 = 0; r0 < R && base * units <= begin; r0 += kAttendThreads) {
+            const uint32_t i = r0 + threadIdx.x, w = i < R ? unit_weight(row_tiles<TILE>(attend_row(c, a, i))) : 0;
+            const uint32_t sum = block_scan<kAttendThreads>(w, &before, scan);
+            if ((base + before) * units <= begin && begin < (base + before + w) * units)
+                where[0] = i, where[1] = base + before;
             base += sum;
         }
+        __syncthreads();
+        r = where[0], row_start = where[1] * units;
     }
-    __syncthreads();
-    uint32_t r = where[0], g = begin, row_start = where[1] * units;
+    auto row_of = [&](uint32_t i) {
+        if (!few) return attend_row(c, a, i);
+        RowRange x;
+        x.len = __shfl_sync(0xFFFFFFFFu, mine.len, i), x.first = __shfl_sync(0xFFFFFFFFu, mine.first, i);
+        x.seq = __shfl_sync(0xFFFFFFFFu, mine.seq, i);
+        return x;
+    };
 
     constexpr uint32_t kFull = TILE == 32 ? 0xFFFFFFFFu : 0xFFFFu;
     uint4* query = reinterpret_cast<uint4*>(smem + kAttendWarps * S::kRing);
@@ -278,7 +305,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
     const bool wide = c.hd == HDT && c.page_shift >= 4;  // rows fill their tile's, sixteen of them share a page
     const int mask_o = (1 << c.page_shift) - 1;
     while (g < end) {
-        const RowRange x = attend_row(c, a, r);
+        const RowRange x = row_of(r);
         const uint32_t tiles = row_tiles<TILE>(x), weight = unit_weight(tiles);
         if (tiles == 0 || g >= row_start + weight * units) {
             row_start += weight * units;
@@ -291,7 +318,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
         const int tb = off + take > kUnitCost ? (int)(off + take - kUnitCost) : 0;
         g += take;
         if (ta == tb) continue;
-        const int kvh = (int)u / a.blocks, hb = (int)u - kvh * a.blocks;
+        const int kvh = a.blocks == 1 ? (int)u : (int)u / a.blocks, hb = (int)u - kvh * a.blocks;
         const int head0 = kvh * a.G + hb * kAttendHeads;
         const int heads = a.G - hb * kAttendHeads < kAttendHeads ? a.G - hb * kAttendHeads : kAttendHeads;
         const int tile0 = x.first / TILE;
@@ -332,7 +359,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
                         }
                     }
                 } else {
-#pragma unroll
+#pragma unroll 1
                     for (int it = 0; it < TILE * kChunks / 32; it++) {
                         int64_t from = __shfl_sync(0xFFFFFFFFu, at, it * kRowsPer + c_row);
                         int bytes = (from >= 0 && c_ch * 16 < c.row_bytes) ? 16 : 0;
@@ -353,23 +380,14 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
             cp_async_commit();  // an empty group where there is no tile: the wait counts groups
         };
 
-        // Fill two slots, then fetch the queries under their copies.  While half q of the
-        // tiles' halves is read, q + 1 and q + 2 are on their way.
         constexpr int ahead = kAttendWarps;  // from a warp's tile to its next
-        int id1 = page_at(ta + warp);        // the page of the tile after
-        int64_t at1 = row_at(ta + warp, id1);
-        uint32_t live1 = __ballot_sync(0xFFFFFFFFu, id1 >= 0);
-        issue(ta + warp, at1, live1, false, 0);
-        issue(ta + warp, at1, live1, true, 1);
-        id1 = page_at(ta + warp + ahead);
-
+        const int id0 = page_at(ta + warp);
+        int id1 = page_at(ta + warp + ahead);  // the page of the tile after
         // A operand of the first product: step s of lane j holds values
         // kPer * (j + 4 * (s / (kPer / 4))) + 4 * (s % (kPer / 4)) .. + 3 of head n.  Every
         // warp reads them all for their largest, and writes its share of the steps.
-        float q_scale;
+        float4 qv[kSteps];
         {
-            float4 qv[kSteps];
-            float amax = 0.0f;
             const float* qh = a.q + r * a.ldq + (int64_t)(head0 + n) * c.hd;
 #pragma unroll
             for (int s = 0; s < kSteps; s++) {
@@ -378,8 +396,21 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
                 if (n < heads && d < c.hd &&
                     QMM_IN_BOUNDS(g_attend_error, r * a.ldq + (int64_t)(head0 + n) * c.hd + d + 3, a.R * a.ldq))
                     qv[s] = __ldg(reinterpret_cast<const float4*>(qh + d));
-                amax = fmaxf(amax, fmaxf(fmaxf(fabsf(qv[s].x), fabsf(qv[s].y)), fmaxf(fabsf(qv[s].z), fabsf(qv[s].w))));
             }
+        }
+        // Fill two slots.  While half q of the tiles' halves is read, q + 1 and q + 2 are on
+        // their way.
+        int64_t at1 = row_at(ta + warp, id0);
+        uint32_t live1 = __ballot_sync(0xFFFFFFFFu, id0 >= 0);
+        issue(ta + warp, at1, live1, false, 0);
+        issue(ta + warp, at1, live1, true, 1);
+
+        float q_scale;
+        {
+            float amax = 0.0f;
+#pragma unroll
+            for (int s = 0; s < kSteps; s++)
+                amax = fmaxf(amax, fmaxf(fmaxf(fabsf(qv[s].x), fabsf(qv[s].y)), fmaxf(fabsf(qv[s].z), fabsf(qv[s].w))));
             amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
             const int e = exponent_of(amax) - 127;
@@ -396,13 +427,13 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
         }
         __syncthreads();
 
-        // Of head n: m_run, a whole number at or above every score so far, the sum of
-        // weights 2^(score - m_run) of this lane's positions, and the weighted values.  In
-        // the tensor cores weights are times 2^(14 - e_run), value scales below
-        // 2^(e_run + 1).
-        float m_run = -INFINITY, l_run = 0.0f, up = 16384.0f, down = 1.0f / 16384.0f;
-        int e_run = kExpLow;  // an exponent field
-        if (TYPE == QMM_KV_Q8) up = pow2i(14 + 127 - e_run), down = pow2i(e_run - 127 - 14);
+        // Of head n: m_run, a whole number that no score so far is over by more than kSlack,
+        // the sum of weights 2^(score - m_run) of this lane's positions, and the weighted
+        // values.  The slack makes raising m_run rare; as it is whole, rescaling is exact.
+        // In the tensor cores weights up to 2^kSlack stand times 2^(10 - e_run), value scales
+        // are at most 2^(e_run + 1) = most: their product stays in f16.
+        float m_run = -INFINITY, l_run = 0.0f, up = 1024.0f, down = 1.0f / 1024.0f, most = INFINITY;
+        if (TYPE == QMM_KV_Q8) most = 0.0f;  // set by the first tile
         float o[kSets][8][2];
 #pragma unroll
         for (int s = 0; s < kSets; s++)
@@ -490,9 +521,9 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
             id1 = page_at(t + 2 * ahead);
             const uint32_t sv = ring_u + slot * S::kSlot;
             const float* vs = reinterpret_cast<const float*>(ring + slot * S::kSlot + TILE * ROW);
-            const int e_lane = TYPE == QMM_KV_Q8 && lane < TILE ? exponent_of(vs[lane]) : 0;
-            if (__any_sync(0xFFFFFFFFu, top > m_run || (TYPE == QMM_KV_Q8 && e_lane > e_run))) {
-                const float m_new = fmaxf(m_run, ceilf(top));
+            const float v_lane = TYPE == QMM_KV_Q8 && lane < TILE ? fabsf(vs[lane]) : 0.0f;
+            if (__any_sync(0xFFFFFFFFu, top > m_run + kSlack || v_lane > most)) {
+                const float m_new = top > m_run + kSlack ? ceilf(top) : m_run;
                 const float keep = exp2_approx(m_run - (m_new == -INFINITY ? 0.0f : m_new));
                 m_run = m_new;
                 l_run *= keep;
@@ -500,10 +531,11 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
                 for (int s = 0; s < kSets; s++)
 #pragma unroll
                     for (int t2 = 0; t2 < 8; t2++) o[s][t2][0] *= keep, o[s][t2][1] *= keep;
-                if (TYPE == QMM_KV_Q8) {
-                    const int e = (int)__reduce_max_sync(0xFFFFFFFFu, (unsigned)e_lane);
-                    e_run = e > e_run ? e : e_run;
-                    up = pow2i(14 + 127 - e_run), down = pow2i(e_run - 127 - 14);
+                const float v_max = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v_lane)));
+                if (TYPE == QMM_KV_Q8 && v_max > most) {
+                    const int e = exponent_of(v_max) - 127;
+                    up = pow2i(10 - e), down = pow2i(e - 10);
+                    most = e == 128 ? INFINITY : 2.0f * pow2i(e);
                 }
             }
             const float m_at = m_run == -INFINITY ? 0.0f : m_run;  // nothing seen yet: every weight is 0
@@ -635,21 +667,24 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
 // One CTA per (row, query head): where the head's unit lies in several runs, their
 // parts are joined; a row without positions gets zeros and -inf.  Warp w adds parts
 // w, w + kJoinWarps, ... in order, then the warps' sums in order.
+//
+// Which parts there are follows from the lengths alone, and is worked out before the
+// wait for the grid ahead: that grid lets this one start only after its own wait, so
+// whatever wrote lens and seq has finished (they are read from the L2, past an L1 that
+// may be older).  What the grid ahead writes, and what is written here, waits.
 __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(KvPages c, AttendArgs a, int tile, int grid) {
     __shared__ uint2 sums[kJoinWarps];
     __shared__ float2 ml[kAttendMaxCtas];
     __shared__ float sum[kJoinWarps][kHeadMax];
-    pdl_wait();
     constexpr uint32_t kThreads = 32 * kJoinWarps;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t Hq = a.G * c.Hkv, units = c.Hkv * a.blocks;
-    const uint32_t r = blockIdx.x / Hq, head = blockIdx.x - r * Hq, kvh = head / a.G, in = head - kvh * a.G;
-    const uint32_t u = kvh * a.blocks + in / kAttendHeads, hl = in % kAttendHeads;
-    if (__ldg(a.lens + r) < 0) return;  // a padding row: left as it was
+    const uint32_t units = c.Hkv * a.blocks, r = blockIdx.x, head = blockIdx.y;
     auto tiles_of = [&](uint32_t row) {
-        const RowRange x = attend_row(c, a, row);
+        const RowRange x = attend_row<true>(c, a, row);
         return tile == 32 ? row_tiles<32>(x) : row_tiles<16>(x);
     };
+    const int len = __ldcg(a.lens + r);
+    const uint32_t tiles = tiles_of(r);
     uint2 mine = make_uint2(0u, 0u);  // of all rows, of the rows ahead
     for (uint32_t i = threadIdx.x; i < (uint32_t)a.R; i += kThreads) {
         const uint32_t t = unit_weight(tiles_of(i));
@@ -659,25 +694,41 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(KvPages c,
     mine.x = __reduce_add_sync(0xFFFFFFFFu, mine.x), mine.y = __reduce_add_sync(0xFFFFFFFFu, mine.y);
     if (lane == 0) sums[warp] = mine;
     __syncthreads();
-    uint32_t total = 0, ahead = 0;
+    uint32_t total = 0, before = 0;
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; w++) total += sums[w].x, ahead += sums[w].y;
-    const uint32_t tiles = tiles_of(r);
+    for (int w = 0; w < kJoinWarps; w++) total += sums[w].x, before += sums[w].y;
+    uint32_t c0 = 0, c1 = 0;
+    const uint32_t kvh = head / a.G, in = head - kvh * a.G, hl = in % kAttendHeads;
+    if (tiles) {
+        const Runs runs(total * units, grid);
+        const uint32_t u = kvh * a.blocks + in / kAttendHeads;
+        const uint32_t g0 = before * units + u * unit_weight(tiles) + kUnitCost;  // the unit's first tile
+        c0 = runs.of(g0), c1 = runs.of(g0 + tiles - 1);
+    }
+    pdl_wait();
+    if (len < 0) return;  // a padding row: left as it was
     float* out = a.out + r * a.ldo + (int64_t)head * c.hd;
+    float* lse = a.lse ? a.lse + (int64_t)r * gridDim.y + head : nullptr;
     if (tiles == 0) {
         for (int d = threadIdx.x; d < c.hd; d += kThreads) out[d] = 0.0f;
-        if (a.lse && threadIdx.x == 0) a.lse[(int64_t)r * Hq + head] = -INFINITY;
+        if (lse && threadIdx.x == 0) *lse = -INFINITY;
         return;
     }
-    const Runs runs(total * units, grid);
-    const uint32_t g0 = ahead * units + u * unit_weight(tiles) + kUnitCost;  // the unit's first tile
-    const uint32_t c0 = runs.of(g0), c1 = runs.of(g0 + tiles - 1);
     if (c0 == c1) return;  // written by that run's CTA
-    const int n = (int)(c1 - c0 + 1);
-    const int64_t size = kAttendHeads * (c.hd + 2);
-    auto part = [&](int i) -> const float* {  // the unit begins in run c0, the others continue it
-        return a.parts + (2 * (int64_t)(c0 + i) + (i == 0 ? 1 : 0)) * size;
-    };
+    const int n = (int)(c1 - c0 + 1), size = kAttendHeads * (c.hd + 2);
+    const float* parts = a.parts + 2 * (int64_t)c0 * size;
+    // the unit begins in run c0, the others continue it
+    auto part = [&](int i) -> const float* { return parts + (2 * i + (i == 0 ? 1 : 0)) * size; };
+    // the first parts' values are fetched along with all parts' maxima and sums
+    constexpr int kFirst = 4;
+    float4 z[kFirst];
+    const int d0 = 4 * lane;
+#pragma unroll
+    for (int k = 0; k < kFirst; k++) {
+        const int i = warp + k * kJoinWarps;
+        z[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < n && d0 < c.hd) z[k] = *reinterpret_cast<const float4*>(part(i) + hl * c.hd + d0);
+    }
     for (int i = threadIdx.x; i < n; i += kThreads)
         if (QMM_IN_BOUNDS(g_attend_error, i, kAttendMaxCtas)) {
             const float* p = part(i) + kAttendHeads * c.hd + hl;
@@ -692,16 +743,22 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(KvPages c,
     for (int i = lane; i < n; i += 32) l = __fmaf_rn(ml[i].y, exp2_approx(ml[i].x - ref), l);
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, s);
-    for (int d0 = 4 * lane; d0 < c.hd; d0 += 128) {
+    auto add = [&](float4& y, const float4& v, int i) {
+        const float f = exp2_approx(ml[i].x - ref);
+        y.x = __fmaf_rn(v.x, f, y.x), y.y = __fmaf_rn(v.y, f, y.y);
+        y.z = __fmaf_rn(v.z, f, y.z), y.w = __fmaf_rn(v.w, f, y.w);
+    };
+    for (int d = d0, first = 1; d < c.hd; d += 128, first = 0) {
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int i = warp; i < n; i += kJoinWarps) {
-            const float4 z = *reinterpret_cast<const float4*>(part(i) + hl * c.hd + d0);
-            const float f = exp2_approx(ml[i].x - ref);
-            y.x = __fmaf_rn(z.x, f, y.x), y.y = __fmaf_rn(z.y, f, y.y);
-            y.z = __fmaf_rn(z.z, f, y.z), y.w = __fmaf_rn(z.w, f, y.w);
+        int i = warp;
+        if (first) {
+#pragma unroll
+            for (int k = 0; k < kFirst; k++, i += kJoinWarps)
+                if (i < n) add(y, z[k], i);
         }
-        *reinterpret_cast<float4*>(&sum[warp][d0]) = y;
+#pragma unroll 8
+        for (; i < n; i += kJoinWarps) add(y, *reinterpret_cast<const float4*>(part(i) + hl * c.hd + d), i);
+        *reinterpret_cast<float4*>(&sum[warp][d]) = y;
     }
     __syncthreads();
     const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
@@ -711,7 +768,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(KvPages c,
         for (int w = 1; w < kJoinWarps; w++) y += sum[w][d];
         out[d] = y * inv;
     }
-    if (a.lse && threadIdx.x == 0) a.lse[(int64_t)r * Hq + head] = (m + log2f(l)) * 0.693147180559945309f;
+    if (lse && threadIdx.x == 0) *lse = (m + log2f(l)) * 0.693147180559945309f;
     pdl_launch_dependents();
 }
 
@@ -744,7 +801,7 @@ qmm_status qmm_kv_attend(const qmm_kv_pages* cache, const float* q, int64_t ldq,
     qmm_status st = kv_pages_check(cache, &c);
     if (st != QMM_OK) return st;
     const size_t need = qmm_kv_attend_scratch_bytes(Hq, c.Hkv, c.hd);
-    if (need == 0 || R < 1 || R * Hq > kMaxDim || R > kMaxDim || (!seq && R > c.num_seqs) || window < 0 ||
+    if (need == 0 || R < 1 || R > kMaxDim || Hq > 65535 || (!seq && R > c.num_seqs) || window < 0 ||
         !row_stride_ok(ldq, Hq * c.hd) || !row_stride_ok(ldo, Hq * c.hd))
         return QMM_E_SHAPE;
     // the list of tiles is counted in 32 bits
@@ -786,7 +843,7 @@ qmm_status qmm_kv_attend(const qmm_kv_pages* cache, const float* q, int64_t ldq,
     st = cache->type == QMM_KV_Q8 ? by_width(integral_constant<int, QMM_KV_Q8>())
                                   : by_width(integral_constant<int, QMM_KV_F16>());
     if (st != QMM_OK) return st;
-    return launch_pdl(attend_join_kernel, dim3((unsigned)(R * Hq)), 32 * kJoinWarps, 0, cs, c, a, tile, grid);
+    return launch_pdl(attend_join_kernel, dim3((unsigned)R, (unsigned)Hq), 32 * kJoinWarps, 0, cs, c, a, tile, grid);
 }
 
 }  // extern "C"
