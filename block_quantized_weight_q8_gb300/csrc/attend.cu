@@ -227,7 +227,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
     constexpr int kVB = 8 * kSize, kSets = ROW / (8 * kVB);  // a lane takes eight values of a row at once
     constexpr int kChains = TILE == 16 ? 2 : 1;  // sums of the first product that run side by side
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ uint32_t scan[kAttendWarps], where[2];  // the run's first row, and the list's length before it
+    __shared__ uint32_t scan[kAttendWarps], ends[32];  // ends: the list's length up to and with each row
+    __shared__ RowRange rows[32];
     __shared__ float part_m[kAttendWarps][kAttendHeads], part_l[kAttendWarps][kAttendHeads];
     __shared__ float part_f[kAttendWarps][kAttendHeads], unit_l[kAttendHeads];
     pdl_wait();
@@ -235,23 +236,28 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = lane >> 2, j = lane & 3;
     const uint32_t units = c.Hkv * a.blocks;
 
-    // The run: total work, then the row r in which it begins.  Up to 32 rows are held by
-    // each warp's lanes; more are scanned by the block.
+    // The run: total work, then the row r in which it begins.  Up to 32 rows are read and
+    // scanned by the first warp, for the whole block: a load of lens by every warp of the
+    // grid meets in one line of the L2 (1.5 us of a single row's 10).
     const uint32_t R = (uint32_t)a.R;
     const bool few = R <= 32;
-    RowRange mine;
-    mine.len = mine.first = 0, mine.seq = 0;
-    if (few && lane < R) mine = attend_row(c, a, lane);
-    uint32_t total, before, weight1 = few ? unit_weight(row_tiles<TILE>(mine)) : 0;
+    uint32_t before, total, weight1 = 0;
     if (few) {
-        before = weight1;
+        if (warp == 0) {
+            RowRange mine;
+            mine.len = mine.first = 0, mine.seq = 0;
+            if (lane < R) mine = attend_row(c, a, lane);
+            rows[lane] = mine;
+            weight1 = before = unit_weight(row_tiles<TILE>(mine));
 #pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-            const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, before, m);
-            if (lane >= m) before += v;
+            for (int m = 1; m < 32; m <<= 1) {
+                const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, before, m);
+                if (lane >= m) before += v;
+            }
+            ends[lane] = before;
         }
-        total = __shfl_sync(0xFFFFFFFFu, before, 31);
-        before -= weight1;
+        __syncthreads();
+        total = ends[31];
     } else {
         for (uint32_t i = threadIdx.x; i < R; i += kAttendThreads)
             weight1 += unit_weight(row_tiles<TILE>(attend_row(c, a, i)));
@@ -263,27 +269,21 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
     const uint32_t begin = runs.begin(blockIdx.x), end = runs.begin(blockIdx.x + 1);
     uint32_t r, g = begin, row_start;  // row_start: the row's first position in the list
     if (few) {
-        r = __ffs(__ballot_sync(0xFFFFFFFFu, before * units <= begin && begin < (before + weight1) * units)) - 1;
-        row_start = __shfl_sync(0xFFFFFFFFu, before, r) * units;
+        r = __ffs(__ballot_sync(0xFFFFFFFFu, begin < ends[lane] * units)) - 1;
+        row_start = r ? ends[r - 1] * units : 0;
     } else {
         uint32_t base = 0;
         for (uint32_t r0 = 0; r0 < R && base * units <= begin; r0 += kAttendThreads) {
             const uint32_t i = r0 + threadIdx.x, w = i < R ? unit_weight(row_tiles<TILE>(attend_row(c, a, i))) : 0;
             const uint32_t sum = block_scan<kAttendThreads>(w, &before, scan);
             if ((base + before) * units <= begin && begin < (base + before + w) * units)
-                where[0] = i, where[1] = base + before;
+                ends[0] = i, ends[1] = base + before;
             base += sum;
         }
         __syncthreads();
-        r = where[0], row_start = where[1] * units;
+        r = ends[0], row_start = ends[1] * units;
     }
-    auto row_of = [&](uint32_t i) {
-        if (!few) return attend_row(c, a, i);
-        RowRange x;
-        x.len = __shfl_sync(0xFFFFFFFFu, mine.len, i), x.first = __shfl_sync(0xFFFFFFFFu, mine.first, i);
-        x.seq = __shfl_sync(0xFFFFFFFFu, mine.seq, i);
-        return x;
-    };
+    auto row_of = [&](uint32_t i) { return few ? rows[i] : attend_row(c, a, i); };
 
     constexpr uint32_t kFull = TILE == 32 ? 0xFFFFFFFFu : 0xFFFFu;
     uint4* query = reinterpret_cast<uint4*>(smem + kAttendWarps * S::kRing);
@@ -324,20 +324,17 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
         const int tile0 = x.first / TILE;
         const int32_t* pages = c.table + x.seq * c.max_pages;
 
-        // the page of this lane's position in tile t
+        // the page of this lane's position in tile t, as the table has it; -1: no position
         auto page_at = [&](int t) -> int {
             const int p = (tile0 + t) * TILE + lane;
-            if (lane >= TILE || t >= tb || p < x.first || p >= x.len) return -1;
-            const int id = __ldg(pages + (p >> c.page_shift));
-            if ((unsigned)id >= (unsigned)c.num_pages) {
-                atomicOr(&g_attend_error, kErrPlace);
-                return -1;
-            }
-            return id;
+            return lane >= TILE || t >= tb || p < x.first || p >= x.len ? -1 : __ldg(pages + (p >> c.page_shift));
         };
         // its row in the pools, from their start; -1: none
         auto row_at = [&](int t, int id) -> int64_t {
-            return id < 0 ? -1 : kv_row_at(c, id, kvh, ((tile0 + t) * TILE + lane) & mask_o);
+            const int p = (tile0 + t) * TILE + lane;
+            if ((unsigned)id < (unsigned)c.num_pages) return kv_row_at(c, id, kvh, p & mask_o);
+            if (lane < TILE && t < tb && p >= x.first && p < x.len) atomicOr(&g_attend_error, kErrPlace);
+            return -1;
         };
         // one half of tile t, its keys or its values, into a slot of the ring; at: this
         // lane's position's row, live: the positions that have one
@@ -401,7 +398,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
         // Fill two slots.  While half q of the tiles' halves is read, q + 1 and q + 2 are on
         // their way.
         int64_t at1 = row_at(ta + warp, id0);
-        uint32_t live1 = __ballot_sync(0xFFFFFFFFu, id0 >= 0);
+        uint32_t live1 = __ballot_sync(0xFFFFFFFFu, at1 >= 0);
         issue(ta + warp, at1, live1, false, 0);
         issue(ta + warp, at1, live1, true, 1);
 
@@ -446,7 +443,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
             cp_async_wait<S::kSlots - 2>();
             __syncwarp();  // the keys are here for every lane, and the slot before is read out
             at1 = row_at(t + ahead, id1);
-            live1 = __ballot_sync(0xFFFFFFFFu, id1 >= 0);
+            live1 = __ballot_sync(0xFFFFFFFFu, at1 >= 0);
             issue(t + ahead, at1, live1, false, turn(2));
             const uint32_t st = ring_u + slot * S::kSlot;
             const uint8_t* tail = ring + slot * S::kSlot + TILE * ROW;  // scales, then the mask
@@ -674,26 +671,26 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
 // may be older).  What the grid ahead writes, and what is written here, waits.
 __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(KvPages c, AttendArgs a, int tile, int grid) {
     __shared__ uint2 sums[kJoinWarps];
+    __shared__ int row_len;
+    __shared__ uint32_t row_t;
     __shared__ float2 ml[kAttendMaxCtas];
-    __shared__ float sum[kJoinWarps][kHeadMax];
+    __shared__ __align__(16) float sum[kJoinWarps][kHeadMax];
     constexpr uint32_t kThreads = 32 * kJoinWarps;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t units = c.Hkv * a.blocks, r = blockIdx.x, head = blockIdx.y;
-    auto tiles_of = [&](uint32_t row) {
-        const RowRange x = attend_row<true>(c, a, row);
-        return tile == 32 ? row_tiles<32>(x) : row_tiles<16>(x);
-    };
-    const int len = __ldcg(a.lens + r);
-    const uint32_t tiles = tiles_of(r);
     uint2 mine = make_uint2(0u, 0u);  // of all rows, of the rows ahead
     for (uint32_t i = threadIdx.x; i < (uint32_t)a.R; i += kThreads) {
-        const uint32_t t = unit_weight(tiles_of(i));
-        mine.x += t;
-        if (i < r) mine.y += t;
+        const RowRange x = attend_row<true>(c, a, i);
+        const uint32_t t = tile == 32 ? row_tiles<32>(x) : row_tiles<16>(x), w = unit_weight(t);
+        mine.x += w;
+        if (i < r) mine.y += w;
+        if (i == r) row_len = x.len, row_t = t;
     }
     mine.x = __reduce_add_sync(0xFFFFFFFFu, mine.x), mine.y = __reduce_add_sync(0xFFFFFFFFu, mine.y);
     if (lane == 0) sums[warp] = mine;
     __syncthreads();
+    const int len = row_len;
+    const uint32_t tiles = row_t;
     uint32_t total = 0, before = 0;
 #pragma unroll
     for (int w = 0; w < kJoinWarps; w++) total += sums[w].x, before += sums[w].y;
