@@ -324,22 +324,31 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
         const int tile0 = x.first / TILE;
         const int32_t* pages = c.table + x.seq * c.max_pages;
 
-        // the page of this lane's position in tile t, as the table has it; -1: no position
-        auto page_at = [&](int t) -> int {
-            const int p = (tile0 + t) * TILE + lane;
-            return lane >= TILE || t >= tb || p < x.first || p >= x.len ? -1 : __ldg(pages + (p >> c.page_shift));
+        // This lane's position in the warp's next tile to look up, less x.first; positions
+        // of this piece are those below `span`.
+        const int last_p = (tile0 + tb) * TILE < x.len ? (tile0 + tb) * TILE : x.len;
+        const unsigned span = (unsigned)(last_p - x.first);
+        int look = lane < TILE ? (tile0 + ta + warp) * TILE + lane - x.first : -(1 << 30);
+        // the page there as the table has it; -1: no position
+        auto page_at = [&](int at) -> int {
+            return (unsigned)at < span ? __ldg(pages + ((at + x.first) >> c.page_shift)) : -1;
         };
         // its row in the pools, from their start; -1: none
-        auto row_at = [&](int t, int id) -> int64_t {
-            const int p = (tile0 + t) * TILE + lane;
-            if ((unsigned)id < (unsigned)c.num_pages) return kv_row_at(c, id, kvh, p & mask_o);
-            if (lane < TILE && t < tb && p >= x.first && p < x.len) atomicOr(&g_attend_error, kErrPlace);
+        const int64_t head_at = (int64_t)(kvh << c.page_shift) * c.row_bytes;
+        auto row_at = [&](int at, int id) -> int64_t {
+            if ((unsigned)id < (unsigned)c.num_pages)
+                return id * c.stride + head_at + (int64_t)((at + x.first) & mask_o) * c.row_bytes;
+            if ((unsigned)at < span) atomicOr(&g_attend_error, kErrPlace);
             return -1;
         };
-        // one half of tile t, its keys or its values, into a slot of the ring; at: this
-        // lane's position's row, live: the positions that have one
-        auto issue = [&](int t, int64_t at, uint32_t live, bool values, int slot) {
-            if (t < tb) {
+        // from there to its scale: as far behind the page's scales as the row behind the page
+        auto scale_by = [&](int at) -> uint32_t {
+            return (uint32_t)(c.scales - (int64_t)((kvh << c.page_shift) + ((at + x.first) & mask_o)) * (c.row_bytes - 4));
+        };
+        // one half of a tile, its keys or its values, into a slot of the ring; at: this
+        // lane's position's row, by: from there to its scale, live: the positions that have one
+        auto issue = [&](bool there, int64_t at, uint32_t by, uint32_t live, bool values, int slot) {
+            if (there) {
                 const uint8_t* pool = values ? c.v : c.k;
                 const uint32_t dst = ring_u + slot * S::kSlot;
                 if (!values && lane == 0)
@@ -366,10 +375,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
                     }
                 }
                 if (TYPE == QMM_KV_Q8 && lane < TILE) {  // position p's scale at (p % 4) (TILE / 4) + p / 4
-                    // its scale lies as far behind its page's scales as its row behind the page
-                    const int row = (kvh << c.page_shift) + (((tile0 + t) * TILE + lane) & mask_o);
                     int bytes = at >= 0 ? 4 : 0;
-                    int64_t from = bytes ? at + (c.scales - (int64_t)row * (c.row_bytes - 4)) : 0;
+                    int64_t from = bytes ? at + by : 0;
                     if (!QMM_IN_BOUNDS(g_attend_error, from + 3, c.num_pages * c.stride)) from = 0, bytes = 0;
                     cp_async4z(dst + TILE * ROW + 4 * ((lane & 3) * (TILE / 4) + (lane >> 2)), pool + from, bytes);
                 }
@@ -378,8 +385,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
         };
 
         constexpr int ahead = kAttendWarps;  // from a warp's tile to its next
-        const int id0 = page_at(ta + warp);
-        int id1 = page_at(ta + warp + ahead);  // the page of the tile after
+        const int id0 = page_at(look);
+        int id1 = page_at(look + ahead * TILE);  // the page of the tile after
         // A operand of the first product: step s of lane j holds values
         // kPer * (j + 4 * (s / (kPer / 4))) + 4 * (s % (kPer / 4)) .. + 3 of head n.  Every
         // warp reads them all for their largest, and writes its share of the steps.
@@ -397,10 +404,11 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
         }
         // Fill two slots.  While half q of the tiles' halves is read, q + 1 and q + 2 are on
         // their way.
-        int64_t at1 = row_at(ta + warp, id0);
-        uint32_t live1 = __ballot_sync(0xFFFFFFFFu, at1 >= 0);
-        issue(ta + warp, at1, live1, false, 0);
-        issue(ta + warp, at1, live1, true, 1);
+        int64_t at1 = row_at(look, id0);
+        uint32_t live1 = __ballot_sync(0xFFFFFFFFu, at1 >= 0), by1 = scale_by(look);
+        issue(ta + warp < tb, at1, by1, live1, false, 0);
+        issue(ta + warp < tb, at1, by1, live1, true, 1);
+        look += ahead * TILE;  // the tile whose page is in id1
 
         float q_scale;
         {
@@ -442,9 +450,9 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
         for (int t = ta + warp; t < tb; t += ahead) {
             cp_async_wait<S::kSlots - 2>();
             __syncwarp();  // the keys are here for every lane, and the slot before is read out
-            at1 = row_at(t + ahead, id1);
+            at1 = row_at(look, id1), by1 = scale_by(look);
             live1 = __ballot_sync(0xFFFFFFFFu, at1 >= 0);
-            issue(t + ahead, at1, live1, false, turn(2));
+            issue(t + ahead < tb, at1, by1, live1, false, turn(2));
             const uint32_t st = ring_u + slot * S::kSlot;
             const uint8_t* tail = ring + slot * S::kSlot + TILE * ROW;  // scales, then the mask
             const uint32_t live = *reinterpret_cast<const uint32_t*>(tail + 4 * TILE);
@@ -514,8 +522,9 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
             slot = turn(1);
             cp_async_wait<S::kSlots - 2>();
             __syncwarp();  // the values are here, the keys are read out
-            issue(t + ahead, at1, live1, true, turn(2));
-            id1 = page_at(t + 2 * ahead);
+            issue(t + ahead < tb, at1, by1, live1, true, turn(2));
+            look += ahead * TILE;
+            id1 = page_at(look);
             const uint32_t sv = ring_u + slot * S::kSlot;
             const float* vs = reinterpret_cast<const float*>(ring + slot * S::kSlot + TILE * ROW);
             const float v_lane = TYPE == QMM_KV_Q8 && lane < TILE ? fabsf(vs[lane]) : 0.0f;
