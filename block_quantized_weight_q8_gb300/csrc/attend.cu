@@ -712,6 +712,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(KvPages c,
         c0 = runs.of(g0), c1 = runs.of(g0 + tiles - 1);
     }
     pdl_wait();
+    pdl_launch_dependents();
     if (len < 0) return;  // a padding row: left as it was
     float* out = a.out + r * a.ldo + (int64_t)head * c.hd;
     float* lse = a.lse ? a.lse + (int64_t)r * gridDim.y + head : nullptr;
@@ -775,7 +776,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(KvPages c,
         out[d] = y * inv;
     }
     if (lse && threadIdx.x == 0) *lse = (m + log2f(l)) * 0.693147180559945309f;
-    pdl_launch_dependents();
 }
 
 }  // namespace qmm

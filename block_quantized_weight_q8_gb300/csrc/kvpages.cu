@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas) rows_kernel(KvPages c, 
     __shared__ float4 tables[2][kRowTable];
     __shared__ Place places[2][TYPE == kNoPages ? 1 : kRowTokens];
     pdl_wait();
+    pdl_launch_dependents();  // every kernel here waits before it touches memory: the next may be placed now
     const CtaTokens own(a.T, par);
     const int nt = own.count;
     const int Hkv = TYPE == kNoPages ? 0 : c.Hkv, rows = 2 * Hkv + a.Hq;
@@ -190,7 +191,6 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas) rows_kernel(KvPages c, 
         for (int i = 0; i < 8; i++) v[i] = ahead[i];
       }
     }
-    pdl_launch_dependents();
 }
 
 // CTAs that share T tokens, `par` at a time: one wave of `ctas` per SM at most.
@@ -258,6 +258,7 @@ __global__ void __launch_bounds__(kLoadThreads, kLoadCtas)
                    float* v_out, int64_t ldv, int64_t T, int par, int block) {
     __shared__ Place places[2][kLoadTokens];
     pdl_wait();
+    pdl_launch_dependents();  // every kernel here waits before it touches memory: the next may be placed now
     const CtaTokens own(T, par);
     const int nt = own.count;
     const int quads = c.hd >> 2, side = c.Hkv * quads, columns = (k_out ? side : 0) + (v_out ? side : 0);
@@ -322,7 +323,6 @@ __global__ void __launch_bounds__(kLoadThreads, kLoadCtas)
             }
         }
     }
-    pdl_launch_dependents();
 }
 
 qmm_status rope_check(const qmm_rope_spec* r, int64_t hd, RowArgs* a);
