@@ -25,15 +25,15 @@
 // is a whole number near the maximum, so rescaling by it is exact and rare.
 //
 // Split.  The work is the list of (row, unit, tile): a unit is a KV head and up to
-// eight of its query heads, a tile 32 (16) positions; each unit counts as
-// kUnitCost tiles more than it has, which is what starting and finishing one takes.
-// A fixed number of CTAs each take an equal run of the list, found by a scan of the
-// lengths on the device: a captured launch serves any lengths, ragged batches are
-// balanced to a tile, and a long sequence is spread over the whole GPU.  Within a run a CTA's four warps
-// take the tiles of a unit in turn, each through its own ring of asynchronous
-// copies, and meet in shared memory.  A unit that one CTA finishes is written at
-// once; else its parts go to the workspace (at most two per CTA), and the second
-// kernel joins them in order.  Nothing is added by atomics: results do not vary.
+// eight of its query heads, a tile 32 (16) positions; each unit counts as unit_cost
+// tiles more than it has, which is what starting and finishing one takes.  A fixed
+// number of teams each take an equal run of the list, found by a scan of the lengths on
+// the device: a captured launch serves any lengths, ragged batches are balanced to a
+// tile, and a long sequence is spread over the whole GPU.  A unit inside one run is
+// written at once; else its parts go to the workspace (at most two per run), and the
+// second kernel joins them in order.  Nothing is added by atomics: results do not vary.
+// A team is a CTA whose four warps take tiles in turn and meet in shared memory, or,
+// where there are many units, a single warp, which meets nobody (kTeamUnits).
 #include <type_traits>
 
 #include "kvpages.cuh"
@@ -46,25 +46,31 @@ constexpr int kAttendWarps = 4;
 constexpr int kAttendThreads = 32 * kAttendWarps;
 constexpr int kAttendSms = 152;
 constexpr int kAttendHeads = 8;  // query heads per unit
-constexpr int kAttendMaxCtas = 4 * kAttendSms;
-constexpr int kJoinWarps = 8;
-constexpr uint32_t kUnitCost = 8;  // of a unit besides its tiles, in tiles
+constexpr int kAttendMaxRuns = 4 * kAttendSms * kAttendWarps;
+constexpr int kJoinThreads = 128;
+constexpr int kJoinFew = 8;  // parts that one CTA joins for all heads
+// Up to so many units, a team is a CTA (the first tokens of one request: 4.8 us, a single
+// warp per unit 7.2; a row of 4096 positions 8.6 and 12.3); with more, a warp (1000 rows
+// of 40 positions, 8 units each: 220 us by CTAs, 49 by warps; 256 of 300: 70 and 48).
+// They are equal at 512 units (64 ragged rows: 84 and 86 us).
+constexpr int64_t kTeamUnits = 608;
+// what a unit costs a team besides its tiles, in tiles
+__host__ __device__ constexpr uint32_t unit_cost(int team) { return team == 1 ? 4 : 8; }
 constexpr float kSlack = 4.0f;     // what scores may be over the running reference, in powers of two
 
 template <int TYPE, int HDT>
 struct AttendShape {
     static constexpr int kRow = HDT * (TYPE == QMM_KV_F16 ? 2 : 1);  // bytes of a row
     static constexpr int kTile = kRow <= 128 ? 32 : 16;              // positions
-    // A warp's ring has three slots of one tile's keys or values, with their scales and
-    // the mask: two are on their way while one is read.
-    static constexpr int kSlots = 3;
+    // A warp's ring has slots of one tile's keys or values, with their scales and the
+    // mask: all but one are on their way while it is read.
+    static constexpr int kSlots = kRow <= 256 ? 4 : 3;
     static constexpr int kSlot = kTile * kRow + 4 * kTile + 16;
     static constexpr int kRing = kSlots * kSlot;  // of a warp
-    static constexpr int kQuery = HDT / 16 * 512;  // the unit's queries, as the first product takes them
-    static constexpr int kSmem = kAttendWarps * kRing + kQuery;
+    static constexpr int kSmem = kAttendWarps * kRing;
     // CTAs per SM, as many as registers and shared memory allow: a warp waits about four
-    // cycles from one instruction to the next, so 8 warps leave half the issue slots empty
-    static constexpr int kCtas = HDT <= 128 ? (kRow == 128 && HDT == 64 ? 3 : 4) : kRow <= 256 ? 3 : 2;
+    // cycles from one instruction to the next
+    static constexpr int kCtas = kRow <= 64 ? 4 : HDT <= 128 ? 3 : 2;
 };
 
 struct AttendArgs {
@@ -74,6 +80,7 @@ struct AttendArgs {
     float* out;
     float* lse;  // may be null
     float* parts;
+    int4* joins;
     int64_t R, ldq, ldo, window;
     int G, blocks;  // query heads per KV head, units per KV head
     float scale;
@@ -84,11 +91,10 @@ struct RowRange {
     int64_t seq;
     int first, len;
 };
-template <bool L2 = false>
 __device__ __forceinline__ RowRange attend_row(const KvPages& c, const AttendArgs& a, int64_t r) {
     RowRange x;
-    x.len = L2 ? __ldcg(a.lens + r) : __ldg(a.lens + r);
-    x.seq = a.seq ? (int64_t)(L2 ? __ldcg(a.seq + r) : __ldg(a.seq + r)) : r;
+    x.len = __ldg(a.lens + r);
+    x.seq = a.seq ? (int64_t)__ldg(a.seq + r) : r;
     x.first = 0;
     if (x.len > 0) {
         const int64_t room = c.max_pages << c.page_shift;
@@ -108,17 +114,21 @@ __device__ __forceinline__ uint32_t row_tiles(const RowRange& x) {
     return x.len > 0 ? (uint32_t)(x.len - 1) / TILE + 1u - (uint32_t)x.first / TILE : 0u;
 }
 // A unit's share of the list: its cost, then its tiles.
-__device__ __forceinline__ uint32_t unit_weight(uint32_t tiles) { return tiles ? tiles + kUnitCost : 0u; }
+template <int TEAM>
+__device__ __forceinline__ uint32_t unit_weight(uint32_t tiles) {
+    return tiles ? tiles + unit_cost(TEAM) : 0u;
+}
 
-// The list cut into `ctas` runs whose lengths differ by one at most; no more runs
-// than leave each a tile per warp.
+// The list cut into `count` runs whose lengths differ by one at most; no more runs than
+// leave each a tile per warp.
+template <int TEAM>
 struct Runs {
-    uint32_t ctas, q, rem;
+    uint32_t count, q, rem;
     __device__ __forceinline__ Runs(uint32_t work, uint32_t most) {
-        const uint32_t fill = work / kAttendWarps;
-        ctas = fill < 1 ? 1 : (fill < most ? fill : most);
-        q = work / ctas;
-        rem = work - q * ctas;
+        const uint32_t fill = work / TEAM;
+        count = fill < 1 ? 1 : (fill < most ? fill : most);
+        q = work / count;
+        rem = work - q * count;
     }
     __device__ __forceinline__ uint32_t begin(uint32_t c) const { return c * q + (c < rem ? c : rem); }
     __device__ __forceinline__ uint32_t of(uint32_t g) const {  // the run that holds position g
@@ -215,7 +225,7 @@ __device__ __forceinline__ int exponent_of(float x) {
 // lanes of two heads write at once (quads 4 apart) goes to different banks.
 __device__ __forceinline__ int exchange_quad(int h, int q) { return q ^ ((q >> 3) & 1) ^ ((h & 1) << 1); }
 
-template <int TYPE, int HDT>
+template <int TYPE, int HDT, int TEAM>
 __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
     attend_kernel(KvPages c, AttendArgs a) {
     using S = AttendShape<TYPE, HDT>;
@@ -227,8 +237,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
     constexpr int kVB = 8 * kSize, kSets = ROW / (8 * kVB);  // a lane takes eight values of a row at once
     constexpr int kChains = TILE == 16 ? 2 : 1;  // sums of the first product that run side by side
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ uint32_t scan[kAttendWarps], ends[32];  // ends: the list's length up to and with each row
-    __shared__ RowRange rows[32];
+    __shared__ uint32_t scan[kAttendWarps], ends[kAttendThreads];
+    __shared__ RowRange rows[kAttendThreads];
     __shared__ float part_m[kAttendWarps][kAttendHeads], part_l[kAttendWarps][kAttendHeads];
     __shared__ float part_f[kAttendWarps][kAttendHeads], unit_l[kAttendHeads];
     pdl_wait();
@@ -236,19 +246,20 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = lane >> 2, j = lane & 3;
     const uint32_t units = c.Hkv * a.blocks;
 
-    // The run: total work, then the row r in which it begins.  Up to 32 rows are read and
-    // scanned by the first warp, for the whole block: a load of lens by every warp of the
-    // grid meets in one line of the L2 (1.5 us of a single row's 10).
-    const uint32_t R = (uint32_t)a.R;
-    const bool few = R <= 32;
-    uint32_t before, total, weight1 = 0;
-    if (few) {
+    // The list's length up to each of (at most) 128 chunks of rows, read once per block:
+    // a load of lens by every warp of the grid meets in one line of the L2 (1.5 us of a
+    // single row's 10).
+    const uint32_t R = (uint32_t)a.R, chunk = (R + kAttendThreads - 1) / kAttendThreads, chunks = (R + chunk - 1) / chunk;
+    const bool held = chunk == 1;  // every row's range fits in shared memory
+    uint32_t total, before, mine = 0;
+    for (uint32_t i = threadIdx.x * chunk; i < R && i < (threadIdx.x + 1) * chunk; i++) {
+        const RowRange x = attend_row(c, a, i);
+        if (held) rows[i] = x;
+        mine += unit_weight<TEAM>(row_tiles<TILE>(x));
+    }
+    if (R <= 32) {
         if (warp == 0) {
-            RowRange mine;
-            mine.len = mine.first = 0, mine.seq = 0;
-            if (lane < R) mine = attend_row(c, a, lane);
-            rows[lane] = mine;
-            weight1 = before = unit_weight(row_tiles<TILE>(mine));
+            before = mine;
 #pragma unroll
             for (int m = 1; m < 32; m <<= 1) {
                 const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, before, m);
@@ -259,34 +270,47 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
         __syncthreads();
         total = ends[31];
     } else {
-        for (uint32_t i = threadIdx.x; i < R; i += kAttendThreads)
-            weight1 += unit_weight(row_tiles<TILE>(attend_row(c, a, i)));
-        total = block_scan<kAttendThreads>(weight1, &before, scan);
-    }
-    if (total == 0) return;
-    const Runs runs(total * units, gridDim.x);
-    if (blockIdx.x >= runs.ctas) return;
-    const uint32_t begin = runs.begin(blockIdx.x), end = runs.begin(blockIdx.x + 1);
-    uint32_t r, g = begin, row_start;  // row_start: the row's first position in the list
-    if (few) {
-        r = __ffs(__ballot_sync(0xFFFFFFFFu, begin < ends[lane] * units)) - 1;
-        row_start = r ? ends[r - 1] * units : 0;
-    } else {
-        uint32_t base = 0;
-        for (uint32_t r0 = 0; r0 < R && base * units <= begin; r0 += kAttendThreads) {
-            const uint32_t i = r0 + threadIdx.x, w = i < R ? unit_weight(row_tiles<TILE>(attend_row(c, a, i))) : 0;
-            const uint32_t sum = block_scan<kAttendThreads>(w, &before, scan);
-            if ((base + before) * units <= begin && begin < (base + before + w) * units)
-                ends[0] = i, ends[1] = base + before;
-            base += sum;
-        }
+        total = block_scan<kAttendThreads>(mine, &before, scan);
+        ends[threadIdx.x] = before + mine;
         __syncthreads();
-        r = ends[0], row_start = ends[1] * units;
     }
-    auto row_of = [&](uint32_t i) { return few ? rows[i] : attend_row(c, a, i); };
+    auto row_of = [&](uint32_t i) { return held ? rows[i] : attend_row(c, a, i); };
+
+    // rows without positions, shared out among all warps
+    const int Hq = a.G * c.Hkv;
+    for (uint32_t i = blockIdx.x * kAttendWarps + warp; i < R; i += gridDim.x * kAttendWarps)
+        if (row_of(i).len == 0) {
+            for (int d = lane; d < Hq * (c.hd >> 2); d += 32)
+                reinterpret_cast<float4*>(a.out + i * a.ldo)[d] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (a.lse)
+                for (int h = lane; h < Hq; h += 32) a.lse[(int64_t)i * Hq + h] = -INFINITY;
+        }
+
+    // The team's run, and the row r in which it begins.  joins: for the second kernel,
+    // the unit that the run continues and the one that it leaves unfinished.
+    const uint32_t run = TEAM == 1 ? blockIdx.x * kAttendWarps + warp : blockIdx.x;
+    const int member = TEAM == 1 ? 0 : warp;
+    if (member == 0 && lane < 2) a.joins[2 * run + lane] = make_int4(0, 0, 0, 0);
+    __syncwarp();
+    if (total == 0) return;
+    const Runs<TEAM> runs(total * units, gridDim.x * (kAttendWarps / TEAM));
+    if (run >= runs.count) return;
+    const uint32_t begin = runs.begin(run), end = runs.begin(run + 1);
+    uint32_t r = 0, g = begin, row_start;  // row_start: the row's first position in the list
+    {
+        uint32_t at = 0;
+        for (uint32_t k = 0; k < chunks; k += 32) {
+            const uint32_t found = __ballot_sync(0xFFFFFFFFu, k + lane < chunks && begin < ends[k + lane] * units);
+            if (found) {
+                at = k + __ffs(found) - 1;
+                break;
+            }
+        }
+        r = at * chunk;
+        row_start = at ? ends[at - 1] * units : 0;
+    }
 
     constexpr uint32_t kFull = TILE == 32 ? 0xFFFFFFFFu : 0xFFFFu;
-    uint4* query = reinterpret_cast<uint4*>(smem + kAttendWarps * S::kRing);
     uint8_t* ring = smem + warp * S::kRing;
     const uint32_t ring_u = smem_u32(ring);
     // where this lane's chunk of the it-th copy goes in a tile (swizzled so that both
@@ -306,7 +330,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
     const int mask_o = (1 << c.page_shift) - 1;
     while (g < end) {
         const RowRange x = row_of(r);
-        const uint32_t tiles = row_tiles<TILE>(x), weight = unit_weight(tiles);
+        const uint32_t tiles = row_tiles<TILE>(x), weight = unit_weight<TEAM>(tiles);
         if (tiles == 0 || g >= row_start + weight * units) {
             row_start += weight * units;
             r++;
@@ -314,8 +338,9 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
         }
         const uint32_t u = (g - row_start) / weight, off = g - row_start - u * weight;
         const uint32_t take = weight - off < end - g ? weight - off : end - g;
-        const int ta = off > kUnitCost ? (int)(off - kUnitCost) : 0;
-        const int tb = off + take > kUnitCost ? (int)(off + take - kUnitCost) : 0;
+        constexpr uint32_t kCost = unit_cost(TEAM);
+        const int ta = off > kCost ? (int)(off - kCost) : 0;
+        const int tb = off + take > kCost ? (int)(off + take - kCost) : 0;
         g += take;
         if (ta == tb) continue;
         const int kvh = a.blocks == 1 ? (int)u : (int)u / a.blocks, hb = (int)u - kvh * a.blocks;
@@ -324,11 +349,11 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
         const int tile0 = x.first / TILE;
         const int32_t* pages = c.table + x.seq * c.max_pages;
 
-        // This lane's position in the warp's next tile to look up, less x.first; positions
+        // This lane's position in the next tile to look up, less x.first; positions
         // of this piece are those below `span`.
         const int last_p = (tile0 + tb) * TILE < x.len ? (tile0 + tb) * TILE : x.len;
         const unsigned span = (unsigned)(last_p - x.first);
-        int look = lane < TILE ? (tile0 + ta + warp) * TILE + lane - x.first : -(1 << 30);
+        int look = lane < TILE ? (tile0 + ta + member) * TILE + lane - x.first : -(1 << 30);
         // the page there as the table has it; -1: no position
         auto page_at = [&](int at) -> int {
             return (unsigned)at < span ? __ldg(pages + ((at + x.first) >> c.page_shift)) : -1;
@@ -384,12 +409,10 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
             cp_async_commit();  // an empty group where there is no tile: the wait counts groups
         };
 
-        constexpr int ahead = kAttendWarps;  // from a warp's tile to its next
         const int id0 = page_at(look);
-        int id1 = page_at(look + ahead * TILE);  // the page of the tile after
+        int id1 = page_at(look + TEAM * TILE);  // the page of the tile after
         // A operand of the first product: step s of lane j holds values
-        // kPer * (j + 4 * (s / (kPer / 4))) + 4 * (s % (kPer / 4)) .. + 3 of head n.  Every
-        // warp reads them all for their largest, and writes its share of the steps.
+        // kPer * (j + 4 * (s / (kPer / 4))) + 4 * (s % (kPer / 4)) .. + 3 of head n
         float4 qv[kSteps];
         {
             const float* qh = a.q + r * a.ldq + (int64_t)(head0 + n) * c.hd;
@@ -402,14 +425,24 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
                     qv[s] = __ldg(reinterpret_cast<const float4*>(qh + d));
             }
         }
-        // Fill two slots.  While half q of the tiles' halves is read, q + 1 and q + 2 are on
-        // their way.
+        // Fill all slots but one.  While half q of the tiles' halves is read, the following
+        // kSlots - 1 are on their way.
         int64_t at1 = row_at(look, id0);
         uint32_t live1 = __ballot_sync(0xFFFFFFFFu, at1 >= 0), by1 = scale_by(look);
-        issue(ta + warp < tb, at1, by1, live1, false, 0);
-        issue(ta + warp < tb, at1, by1, live1, true, 1);
-        look += ahead * TILE;  // the tile whose page is in id1
+        auto next_tile = [&]() {  // at1, by1 and live1 to the tile after, whose page is in id1
+            look += TEAM * TILE;
+            at1 = row_at(look, id1), by1 = scale_by(look);
+            live1 = __ballot_sync(0xFFFFFFFFu, at1 >= 0);
+            id1 = page_at(look + TEAM * TILE);
+        };
+        issue(ta + member < tb, at1, by1, live1, false, 0);
+        issue(ta + member < tb, at1, by1, live1, true, 1);
+        if (S::kSlots == 4) {
+            next_tile();
+            issue(ta + member + TEAM < tb, at1, by1, live1, false, 2);
+        }
 
+        uint32_t qf[kSteps][4];
         float q_scale;
         {
             float amax = 0.0f;
@@ -423,14 +456,10 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
             q_scale = a.scale * 1.44269504088896341f * pow2i(e - 14);  // scores in base 2
 #pragma unroll
             for (int s = 0; s < kSteps; s++) {
-                if (s % kAttendWarps != warp) continue;
-                uint4 f;
-                split_h2(qv[s].x * by, qv[s].y * by, &f.x, &f.y);
-                split_h2(qv[s].z * by, qv[s].w * by, &f.z, &f.w);
-                query[s * 32 + lane] = f;
+                split_h2(qv[s].x * by, qv[s].y * by, &qf[s][0], &qf[s][1]);
+                split_h2(qv[s].z * by, qv[s].w * by, &qf[s][2], &qf[s][3]);
             }
         }
-        __syncthreads();
 
         // Of head n: m_run, a whole number that no score so far is over by more than kSlack,
         // the sum of weights 2^(score - m_run) of this lane's positions, and the weighted
@@ -447,12 +476,11 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
 
         int slot = 0;
         auto turn = [&](int by) { return slot + by >= S::kSlots ? slot + by - S::kSlots : slot + by; };
-        for (int t = ta + warp; t < tb; t += ahead) {
+        for (int t = ta + member; t < tb; t += TEAM) {
             cp_async_wait<S::kSlots - 2>();
             __syncwarp();  // the keys are here for every lane, and the slot before is read out
-            at1 = row_at(look, id1), by1 = scale_by(look);
-            live1 = __ballot_sync(0xFFFFFFFFu, at1 >= 0);
-            issue(t + ahead < tb, at1, by1, live1, false, turn(2));
+            if (S::kSlots == 3) next_tile();
+            issue(t + TEAM < tb, at1, by1, live1, S::kSlots == 4, turn(S::kSlots - 1));
             const uint32_t st = ring_u + slot * S::kSlot;
             const uint8_t* tail = ring + slot * S::kSlot + TILE * ROW;  // scales, then the mask
             const uint32_t live = *reinterpret_cast<const uint32_t*>(tail + 4 * TILE);
@@ -471,7 +499,6 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
 #pragma unroll
                 for (int w = 0; w < kPer / 4; w++) {
                     const int step = cg * (kPer / 4) + w;
-                    const uint4 qf = query[step * 32 + lane];
 #pragma unroll
                     for (int m = 0; m < TILE / 8; m++) {
                         const uint32_t* f = reinterpret_cast<const uint32_t*>(&kw[m]);
@@ -482,8 +509,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
                         } else {
                             b0 = f[2 * w], b1 = f[2 * w + 1];
                         }
-                        if (step < kChains) mma_f16_first(sc[m][step % kChains], &qf.x, b0, b1);
-                        else mma_f16(sc[m][step % kChains], &qf.x, b0, b1);
+                        if (step < kChains) mma_f16_first(sc[m][step % kChains], qf[step], b0, b1);
+                        else mma_f16(sc[m][step % kChains], qf[step], b0, b1);
                     }
                 }
             }
@@ -522,9 +549,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
             slot = turn(1);
             cp_async_wait<S::kSlots - 2>();
             __syncwarp();  // the values are here, the keys are read out
-            issue(t + ahead < tb, at1, by1, live1, true, turn(2));
-            look += ahead * TILE;
-            id1 = page_at(look);
+            if (S::kSlots == 4) next_tile();
+            issue(t + (S::kSlots - 2) * TEAM < tb, at1, by1, live1, S::kSlots == 3, turn(S::kSlots - 1));
             const uint32_t sv = ring_u + slot * S::kSlot;
             const float* vs = reinterpret_cast<const float*>(ring + slot * S::kSlot + TILE * ROW);
             const float v_lane = TYPE == QMM_KV_Q8 && lane < TILE ? fabsf(vs[lane]) : 0.0f;
@@ -608,11 +634,48 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
             slot = turn(1);
         }
 
-        // the warps meet: running maxima and sums, then the values through shared memory
+        cp_async_wait<0>();
         l_run += __shfl_xor_sync(0xFFFFFFFFu, l_run, 1);
         l_run += __shfl_xor_sync(0xFFFFFFFFu, l_run, 2);
+        const bool whole = ta == 0 && tb == (int)tiles;
+        float* part = a.parts + (2 * (int64_t)run + (ta == 0 ? 1 : 0)) * (kAttendHeads * (c.hd + 2));
+        float* out = a.out + r * a.ldo + (int64_t)head0 * c.hd;
+        if (!whole && member == 0 && lane == 0) {
+            const uint32_t g0 = row_start + u * weight + kCost;  // the unit's first tile
+            const uint32_t c0 = runs.of(g0);
+            a.joins[2 * run + (ta == 0 ? 1 : 0)] = make_int4((int)r, (int)u, (int)c0, (int)(runs.of(g0 + tiles - 1) - c0 + 1));
+        }
+        auto put_ml = [&](int h, float m, float l) {
+            if (!whole) {
+                part[kAttendHeads * c.hd + h] = m, part[kAttendHeads * (c.hd + 1) + h] = l;
+            } else if (a.lse && QMM_IN_BOUNDS(g_attend_error, r * Hq + head0 + h, a.R * Hq)) {
+                a.lse[(int64_t)r * Hq + head0 + h] = (m + log2f(l)) * 0.693147180559945309f;
+            }
+        };
+        auto put = [&](int h, int d, float4 y) {
+            if (!whole) *reinterpret_cast<float4*>(part + h * c.hd + d) = y;
+            else if (QMM_IN_BOUNDS(g_attend_error, r * a.ldo + (int64_t)(head0 + h) * c.hd + d + 3, a.R * a.ldo))
+                *reinterpret_cast<float4*>(out + h * c.hd + d) = y;
+        };
+        if (TEAM == 1) {
+            const float by = !whole ? 1.0f : (l_run == 0.0f ? 0.0f : __fdiv_rn(1.0f, l_run));
+#pragma unroll
+            for (int s = 0; s < kSets; s++)
+#pragma unroll
+                for (int i = 0; i < 2; i++)
+#pragma unroll
+                    for (int t = 0; t < 8; t += 4) {
+                        const int d = 64 * s + 8 * (2 * j + i) + t;
+                        if (n < heads && d < c.hd)
+                            put(n, d, make_float4(o[s][t][i] * by, o[s][t + 1][i] * by, o[s][t + 2][i] * by,
+                                                  o[s][t + 3][i] * by));
+                    }
+            if (j == 0 && n < heads) put_ml(n, m_run, l_run);
+            __syncwarp();  // the ring is free for the next unit
+            continue;
+        }
+        // the warps meet: running references and sums, then the values through shared memory
         if (j == 0) part_m[warp][n] = m_run, part_l[warp][n] = l_run;
-        cp_async_wait<0>();
         __syncthreads();  // every ring is read out: its memory is the exchange now
         float* xo = reinterpret_cast<float*>(smem) + (warp * kAttendHeads + n) * HDT;
 #pragma unroll
@@ -623,8 +686,6 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
                 for (int t = 0; t < 8; t += 4)
                     *reinterpret_cast<float4*>(xo + 4 * exchange_quad(n, (64 * s + 8 * (2 * j + i) + t) / 4)) =
                         make_float4(o[s][t][i], o[s][t + 1][i], o[s][t + 2][i], o[s][t + 3][i]);
-        const bool whole = ta == 0 && tb == (int)tiles;
-        float* part = a.parts + (2 * (int64_t)blockIdx.x + (ta == 0 ? 1 : 0)) * (kAttendHeads * (c.hd + 2));
         if (threadIdx.x < heads) {
             const int h = threadIdx.x;
             float m = -INFINITY, l = 0.0f;
@@ -637,17 +698,12 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
                 l += part_l[w][h] * part_f[w][h];
             }
             unit_l[h] = l;
-            if (!whole) {
-                part[kAttendHeads * c.hd + h] = m;
-                part[kAttendHeads * c.hd + kAttendHeads + h] = l;
-            } else if (a.lse && QMM_IN_BOUNDS(g_attend_error, r * (a.G * c.Hkv) + head0 + h, a.R * a.G * c.Hkv)) {
-                a.lse[(int64_t)r * (a.G * c.Hkv) + head0 + h] = (m + log2f(l)) * 0.693147180559945309f;
-            }
+            put_ml(h, m, l);
         }
         __syncthreads();
         const int quads = c.hd >> 2;
         for (int i = threadIdx.x; i < heads * quads; i += kAttendThreads) {
-            const int h = i / quads, q = i - h * quads, d = 4 * q;
+            const int h = i / quads, q = i - h * quads;
             float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kAttendWarps; w++) {
@@ -658,124 +714,129 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
                 y.z = __fmaf_rn(z.z, f, y.z), y.w = __fmaf_rn(z.w, f, y.w);
             }
             if (whole) {
-                const float l = unit_l[h], inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
-                y.x *= inv, y.y *= inv, y.z *= inv, y.w *= inv;
-                if (QMM_IN_BOUNDS(g_attend_error, r * a.ldo + (int64_t)(head0 + h) * c.hd + d + 3, a.R * a.ldo))
-                    *reinterpret_cast<float4*>(a.out + r * a.ldo + (int64_t)(head0 + h) * c.hd + d) = y;
-            } else {
-                *reinterpret_cast<float4*>(part + h * c.hd + d) = y;
+                const float by = unit_l[h] == 0.0f ? 0.0f : __fdiv_rn(1.0f, unit_l[h]);
+                y.x *= by, y.y *= by, y.z *= by, y.w *= by;
             }
+            put(h, 4 * q, y);
         }
         __syncthreads();  // the exchange is read out
     }
 }
 
-// One CTA per (row, query head): where the head's unit lies in several runs, their
-// parts are joined; a row without positions gets zeros and -inf.  Warp w adds parts
-// w, w + kJoinWarps, ... in order, then the warps' sums in order.
-//
-// Which parts there are follows from the lengths alone, and is worked out before the
-// wait for the grid ahead: that grid lets this one start only after its own wait, so
-// whatever wrote lens and seq has finished (they are read from the L2, past an L1 that
-// may be older).  What the grid ahead writes, and what is written here, waits.
-__global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(KvPages c, AttendArgs a, int tile, int grid) {
-    __shared__ uint2 sums[kJoinWarps];
-    __shared__ int row_len;
-    __shared__ uint32_t row_t;
-    __shared__ float2 ml[kAttendMaxCtas];
-    __shared__ __align__(16) float sum[kJoinWarps][kHeadMax];
-    constexpr uint32_t kThreads = 32 * kJoinWarps;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t units = c.Hkv * a.blocks, r = blockIdx.x, head = blockIdx.y;
-    uint2 mine = make_uint2(0u, 0u);  // of all rows, of the rows ahead
-    for (uint32_t i = threadIdx.x; i < (uint32_t)a.R; i += kThreads) {
-        const RowRange x = attend_row<true>(c, a, i);
-        const uint32_t t = tile == 32 ? row_tiles<32>(x) : row_tiles<16>(x), w = unit_weight(t);
-        mine.x += w;
-        if (i < r) mine.y += w;
-        if (i == r) row_len = x.len, row_t = t;
-    }
-    mine.x = __reduce_add_sync(0xFFFFFFFFu, mine.x), mine.y = __reduce_add_sync(0xFFFFFFFFu, mine.y);
-    if (lane == 0) sums[warp] = mine;
-    __syncthreads();
-    const int len = row_len;
-    const uint32_t tiles = row_t;
-    uint32_t total = 0, before = 0;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; w++) total += sums[w].x, before += sums[w].y;
-    uint32_t c0 = 0, c1 = 0;
-    const uint32_t kvh = head / a.G, in = head - kvh * a.G, hl = in % kAttendHeads;
-    if (tiles) {
-        const Runs runs(total * units, grid);
-        const uint32_t u = kvh * a.blocks + in / kAttendHeads;
-        const uint32_t g0 = before * units + u * unit_weight(tiles) + kUnitCost;  // the unit's first tile
-        c0 = runs.of(g0), c1 = runs.of(g0 + tiles - 1);
-    }
+// One CTA per run, for the unit that its team continued and the one that it began and
+// left unfinished (a.joins: row, unit, first run, number of runs).  Up to kJoinFew parts
+// are joined by the first run's CTA, a thread per four values; the values of a unit in
+// more parts are shared out among its runs' CTAs, 32 values at a time, sixteen threads
+// side by side over the parts.  Either way in an order that the number of parts fixes.
+__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(KvPages c, AttendArgs a) {
+    constexpr int kSide = kJoinThreads / 8;  // threads side by side over the parts
+    __shared__ __align__(16) float4 sum[kSide][8];
+    __shared__ float fold_m[kSide], fold_l[kSide];
     pdl_wait();
     pdl_launch_dependents();
-    if (len < 0) return;  // a padding row: left as it was
-    float* out = a.out + r * a.ldo + (int64_t)head * c.hd;
-    float* lse = a.lse ? a.lse + (int64_t)r * gridDim.y + head : nullptr;
-    if (tiles == 0) {
-        for (int d = threadIdx.x; d < c.hd; d += kThreads) out[d] = 0.0f;
-        if (lse && threadIdx.x == 0) *lse = -INFINITY;
-        return;
-    }
-    if (c0 == c1) return;  // written by that run's CTA
-    const int n = (int)(c1 - c0 + 1), size = kAttendHeads * (c.hd + 2);
-    const float* parts = a.parts + 2 * (int64_t)c0 * size;
-    // the unit begins in run c0, the others continue it
-    auto part = [&](int i) -> const float* { return parts + (2 * i + (i == 0 ? 1 : 0)) * size; };
-    // the first parts' values are fetched along with all parts' maxima and sums
-    constexpr int kFirst = 4;
-    float4 z[kFirst];
-    const int d0 = 4 * lane;
+    const int Hq = a.G * c.Hkv, size = kAttendHeads * (c.hd + 2);
+    const int4 jobs[2] = {a.joins[2 * blockIdx.x], a.joins[2 * blockIdx.x + 1]};
+    for (int side = 0; side < 2; side++) {
+        const int4 job = side ? jobs[1] : jobs[0];
+        const int n = job.w;
+        if (n == 0) continue;
+        const int kvh = job.y / a.blocks, hb = job.y - kvh * a.blocks, head0 = kvh * a.G + hb * kAttendHeads;
+        const int heads = a.G - hb * kAttendHeads < kAttendHeads ? a.G - hb * kAttendHeads : kAttendHeads;
+        const float* parts = a.parts + 2 * (int64_t)job.z * size;
+        // the unit begins in its first run, the others continue it
+        auto part = [&](int i) -> const float* { return parts + (2 * (int64_t)i + (i == 0 ? 1 : 0)) * size; };
+        float* out = a.out + job.x * a.ldo + (int64_t)head0 * c.hd;
+        float* lse = a.lse ? a.lse + (int64_t)job.x * Hq + head0 : nullptr;
+        if (n <= kJoinFew) {
+            if (side == 0) continue;  // the first run's
+            const int quads = c.hd >> 2;
+            for (int e = threadIdx.x; e < heads * quads; e += kJoinThreads) {
+                const int h = e / quads, d = 4 * (e - h * quads);
+                float4 z[kJoinFew];
+                float pm[kJoinFew], pl[kJoinFew], m = -INFINITY, l = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kFirst; k++) {
-        const int i = warp + k * kJoinWarps;
-        z[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i < n && d0 < c.hd) z[k] = *reinterpret_cast<const float4*>(part(i) + hl * c.hd + d0);
-    }
-    for (int i = threadIdx.x; i < n; i += kThreads)
-        if (QMM_IN_BOUNDS(g_attend_error, i, kAttendMaxCtas)) {
-            const float* p = part(i) + kAttendHeads * c.hd + hl;
-            ml[i] = make_float2(p[0], p[kAttendHeads]);
+                for (int i = 0; i < kJoinFew; i++) {
+                    const float* p = part(i < n ? i : 0);
+                    z[i] = *reinterpret_cast<const float4*>(p + h * c.hd + d);
+                    pm[i] = p[kAttendHeads * c.hd + h], pl[i] = p[kAttendHeads * c.hd + kAttendHeads + h];
+                }
+#pragma unroll
+                for (int i = 0; i < kJoinFew; i++)
+                    if (i < n) m = fmaxf(m, pm[i]);
+                const float ref = m == -INFINITY ? 0.0f : m;
+                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < kJoinFew; i++)
+                    if (i < n) {
+                        const float f = exp2_approx(pm[i] - ref);
+                        l = __fmaf_rn(pl[i], f, l);
+                        y.x = __fmaf_rn(z[i].x, f, y.x), y.y = __fmaf_rn(z[i].y, f, y.y);
+                        y.z = __fmaf_rn(z[i].z, f, y.z), y.w = __fmaf_rn(z[i].w, f, y.w);
+                    }
+                const float by = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+                *reinterpret_cast<float4*>(out + h * c.hd + d) = make_float4(y.x * by, y.y * by, y.z * by, y.w * by);
+                if (lse && d == 0) lse[h] = (m + log2f(l)) * 0.693147180559945309f;
+            }
+            continue;
         }
-    __syncthreads();
-    float m = -INFINITY, l = 0.0f;  // every warp for itself: n is a few hundred at most
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, ml[i].x);
+        // pieces of 32 values of a head (the last one of a head may be 16)
+        const int per_head = (c.hd + 31) >> 5, s = threadIdx.x >> 3, q = threadIdx.x & 7;
+        for (int e = blockIdx.x - job.z; e < heads * per_head; e += n) {
+            const int h = e / per_head, d = 32 * (e - h * per_head) + 4 * q;
+            const bool there = d < c.hd;
+            // each thread's parts about their own maximum, then the threads' about theirs
+            float m = -INFINITY, l = 0.0f;
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i0 = s; i0 < n; i0 += 8 * kSide) {
+                float4 z[8];
+                float pm[8], pl[8], top = m;
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
-    const float ref = m == -INFINITY ? 0.0f : m;
-    for (int i = lane; i < n; i += 32) l = __fmaf_rn(ml[i].y, exp2_approx(ml[i].x - ref), l);
+                for (int k = 0; k < 8; k++) {
+                    const int i = i0 + k * kSide;
+                    const float* p = part(i < n ? i : s);
+                    z[k] = *reinterpret_cast<const float4*>(p + h * c.hd + (there ? d : 0));
+                    pm[k] = p[kAttendHeads * c.hd + h], pl[k] = p[kAttendHeads * c.hd + kAttendHeads + h];
+                }
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, s);
-    auto add = [&](float4& y, const float4& v, int i) {
-        const float f = exp2_approx(ml[i].x - ref);
-        y.x = __fmaf_rn(v.x, f, y.x), y.y = __fmaf_rn(v.y, f, y.y);
-        y.z = __fmaf_rn(v.z, f, y.z), y.w = __fmaf_rn(v.w, f, y.w);
-    };
-    for (int d = d0, first = 1; d < c.hd; d += 128, first = 0) {
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        int i = warp;
-        if (first) {
+                for (int k = 0; k < 8; k++)
+                    if (i0 + k * kSide < n) top = fmaxf(top, pm[k]);
+                const float ref = top == -INFINITY ? 0.0f : top, keep = exp2_approx(m - ref);
+                m = top;
+                l *= keep, y.x *= keep, y.y *= keep, y.z *= keep, y.w *= keep;
 #pragma unroll
-            for (int k = 0; k < kFirst; k++, i += kJoinWarps)
-                if (i < n) add(y, z[k], i);
+                for (int k = 0; k < 8; k++)
+                    if (i0 + k * kSide < n) {
+                        const float f = exp2_approx(pm[k] - ref);
+                        l = __fmaf_rn(pl[k], f, l);
+                        y.x = __fmaf_rn(z[k].x, f, y.x), y.y = __fmaf_rn(z[k].y, f, y.y);
+                        y.z = __fmaf_rn(z[k].z, f, y.z), y.w = __fmaf_rn(z[k].w, f, y.w);
+                    }
+            }
+            sum[s][q] = y;
+            if (q == 0) fold_m[s] = m, fold_l[s] = l;
+            __syncthreads();
+            if (s == 0) {
+                float top = -INFINITY, all = 0.0f;
+#pragma unroll
+                for (int k = 0; k < kSide; k++) top = fmaxf(top, fold_m[k]);
+                const float ref = top == -INFINITY ? 0.0f : top;
+                y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < kSide; k++) {
+                    const float f = exp2_approx(fold_m[k] - ref);
+                    const float4 z = sum[k][q];
+                    all = __fmaf_rn(fold_l[k], f, all);
+                    y.x = __fmaf_rn(z.x, f, y.x), y.y = __fmaf_rn(z.y, f, y.y);
+                    y.z = __fmaf_rn(z.z, f, y.z), y.w = __fmaf_rn(z.w, f, y.w);
+                }
+                const float by = all == 0.0f ? 0.0f : __fdiv_rn(1.0f, all);
+                if (there)
+                    *reinterpret_cast<float4*>(out + h * c.hd + d) = make_float4(y.x * by, y.y * by, y.z * by, y.w * by);
+                if (lse && d == 0) lse[h] = (top + log2f(all)) * 0.693147180559945309f;
+            }
+            __syncthreads();
         }
-#pragma unroll 8
-        for (; i < n; i += kJoinWarps) add(y, *reinterpret_cast<const float4*>(part(i) + hl * c.hd + d), i);
-        *reinterpret_cast<float4*>(&sum[warp][d]) = y;
     }
-    __syncthreads();
-    const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
-    for (int d = threadIdx.x; d < c.hd; d += kThreads) {
-        float y = sum[0][d];
-#pragma unroll
-        for (int w = 1; w < kJoinWarps; w++) y += sum[w][d];
-        out[d] = y * inv;
-    }
-    if (lse && threadIdx.x == 0) *lse = (m + log2f(l)) * 0.693147180559945309f;
 }
 
 }  // namespace qmm
@@ -796,7 +857,7 @@ unsigned qmm_internal_attend_error(int clear) {
 
 size_t qmm_kv_attend_scratch_bytes(int64_t Hq, int64_t Hkv, int64_t hd) {
     if (!head_dim_ok(hd) || Hkv < 1 || Hkv > 1024 || Hq < 1 || Hq % Hkv || Hq / Hkv > 64) return 0;
-    return (size_t)kAttendMaxCtas * 2 * kAttendHeads * (size_t)(hd + 2) * sizeof(float);
+    return (size_t)kAttendMaxRuns * 2 * (kAttendHeads * (size_t)(hd + 2) * sizeof(float) + sizeof(int4));
 }
 
 qmm_status qmm_kv_attend(const qmm_kv_pages* cache, const float* q, int64_t ldq, const int32_t* lens,
@@ -807,18 +868,20 @@ qmm_status qmm_kv_attend(const qmm_kv_pages* cache, const float* q, int64_t ldq,
     qmm_status st = kv_pages_check(cache, &c);
     if (st != QMM_OK) return st;
     const size_t need = qmm_kv_attend_scratch_bytes(Hq, c.Hkv, c.hd);
-    if (need == 0 || R < 1 || R > kMaxDim || Hq > 65535 || (!seq && R > c.num_seqs) || window < 0 ||
+    if (need == 0 || R < 1 || R > kMaxDim || R * Hq > kMaxDim || (!seq && R > c.num_seqs) || window < 0 ||
         !row_stride_ok(ldq, Hq * c.hd) || !row_stride_ok(ldo, Hq * c.hd))
         return QMM_E_SHAPE;
     // the list of tiles is counted in 32 bits
     const int64_t room = c.max_pages << c.page_shift, seen = window > 0 && window < room ? window + 16 : room;
     const int64_t blocks = (Hq / c.Hkv + kAttendHeads - 1) / kAttendHeads;
-    if (room > kMaxDim || R * c.Hkv * blocks > kMaxDim / (seen / 16 + 2 + kUnitCost)) return QMM_E_SHAPE;
+    if (room > kMaxDim || R * c.Hkv * blocks > kMaxDim / (seen / 16 + 2 + unit_cost(kAttendWarps))) return QMM_E_SHAPE;
     if (!aligned16(q) || !aligned16(out) || !aligned4(lens) || !aligned4(seq) || !aligned4(lse) || !aligned16(scratch))
         return QMM_E_ALIGN;
     if (scratch_bytes < need) return QMM_E_SCRATCH;
     AttendArgs a;
-    a.q = q, a.lens = lens, a.seq = seq, a.out = out, a.lse = lse, a.parts = (float*)scratch;
+    a.q = q, a.lens = lens, a.seq = seq, a.out = out, a.lse = lse;
+    a.joins = (int4*)scratch;
+    a.parts = (float*)(a.joins + 2 * kAttendMaxRuns);
     a.R = R, a.ldq = ldq, a.ldo = ldo, a.window = window;
     a.G = (int)(Hq / c.Hkv);
     a.blocks = (int)blocks;
@@ -827,29 +890,34 @@ qmm_status qmm_kv_attend(const qmm_kv_pages* cache, const float* q, int64_t ldq,
     st = current_device(&dev);
     if (st != QMM_OK) return st;
     const cudaStream_t cs = (cudaStream_t)stream;
-    int tile = 0, grid = 0;
-    auto go = [&](auto type, auto hdt) -> qmm_status {
-        constexpr int TYPE = decltype(type)::value, HDT = decltype(hdt)::value;
+    const bool ctas = R * c.Hkv * blocks <= kTeamUnits;
+    int runs = 0;
+    auto go = [&](auto type, auto hdt, auto team) -> qmm_status {
+        constexpr int TYPE = decltype(type)::value, HDT = decltype(hdt)::value, TEAM = decltype(team)::value;
         using S = AttendShape<TYPE, HDT>;
         static PerDeviceOnce once;
         const qmm_status set = once.run(dev.device, [&] {
-            return cudaFuncSetAttribute(attend_kernel<TYPE, HDT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            return cudaFuncSetAttribute(attend_kernel<TYPE, HDT, TEAM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         S::kSmem) == cudaSuccess ? QMM_OK : QMM_E_CUDA;
         });
         if (set != QMM_OK) return set;
-        tile = S::kTile, grid = S::kCtas * kAttendSms;
-        return launch_pdl(attend_kernel<TYPE, HDT>, dim3((unsigned)grid), kAttendThreads, S::kSmem, cs, c, a);
+        runs = S::kCtas * kAttendSms * (kAttendWarps / TEAM);
+        return launch_pdl(attend_kernel<TYPE, HDT, TEAM>, dim3((unsigned)(S::kCtas * kAttendSms)), kAttendThreads, S::kSmem,
+                          cs, c, a);
     };
     using std::integral_constant;
+    auto by_team = [&](auto type, auto hdt) -> qmm_status {
+        return ctas ? go(type, hdt, integral_constant<int, kAttendWarps>()) : go(type, hdt, integral_constant<int, 1>());
+    };
     auto by_width = [&](auto type) -> qmm_status {
-        if (c.hd <= 64) return go(type, integral_constant<int, 64>());
-        if (c.hd <= 128) return go(type, integral_constant<int, 128>());
-        return go(type, integral_constant<int, 256>());
+        if (c.hd <= 64) return by_team(type, integral_constant<int, 64>());
+        if (c.hd <= 128) return by_team(type, integral_constant<int, 128>());
+        return by_team(type, integral_constant<int, 256>());
     };
     st = cache->type == QMM_KV_Q8 ? by_width(integral_constant<int, QMM_KV_Q8>())
                                   : by_width(integral_constant<int, QMM_KV_F16>());
     if (st != QMM_OK) return st;
-    return launch_pdl(attend_join_kernel, dim3((unsigned)R, (unsigned)Hq), 32 * kJoinWarps, 0, cs, c, a, tile, grid);
+    return launch_pdl(attend_join_kernel, dim3((unsigned)runs), kJoinThreads, 0, cs, c, a);
 }
 
 }  // extern "C"

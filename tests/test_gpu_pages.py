@@ -184,6 +184,19 @@ def test_many_rows_and_shared_sequences():
     assert np.all(err <= bound[kept])
 
 
+@pytest.mark.parametrize("typ,Hq,Hkv,hd,page,lens,window", [
+    ("q8", 40, 40, 64, 16, [1, 33, 0, -1, 40, 32, 7, 64, 5, 31, 2, 50, 17, 48, 3, 65], 0),
+    ("q8", 120, 40, 128, 16, [700, 3, 0, 250, 64, 1, 300, 20, 9, 33, 128, 5, 77, 600, -1, 31, 450], 0),
+    ("q8", 80, 40, 256, 8, [90, 1, 15, 16, 17, 60, 0, 33, 5, 40, 2, 80, 64, 100, 9, 3], 0),
+    ("f16", 41, 41, 80, 32, [90, 1, 15, 16, 17, 60, 0, 33, 5, 40, 2, 80, 64, 100, 9, -1], 20),
+    ("f16", 160, 40, 128, 1, [70, 1, 15, 16, 17, 60, 0, 33, 5, 40, 2, 80, 64, 100, 9, 3], 0),
+    ("f16", 40, 40, 256, 16, [90, 1, 15, 16, 17, 60, 0, 33, 5, 40, 2, 80, 64, 100, 9, 3], 0),
+    ("q8", 50, 1, 48, 16, [20 + i % 40 for i in range(90)], 0)])
+def test_many_units(typ, Hq, Hkv, hd, page, lens, window):
+    """More units (KV heads, or eights of their query heads, of a row) than get a CTA each: a warp takes them alone."""
+    test_attend(typ, Hq, Hkv, hd, page, lens, window)
+
+
 @pytest.mark.parametrize("typ", ["q8", "f16"])
 def test_extreme_values(typ):
     """Very large and very small rows, zero rows, a zero query, a query whose scores dwarf the others."""
