@@ -134,13 +134,10 @@ def ptr(t) -> int:
     return int(t.data_ptr())
 
 
-def stream_handle(stream=None, dev=None) -> int:
+def stream_handle(stream=None) -> int:
     if stream is None:
-        import torch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the handle without a Stream object around it
-        if raw is None:
-            return int(torch.cuda.current_stream().cuda_stream)
-        return raw(torch.cuda.current_device() if dev is None else dev)
+        dev = _device()
+        return _raw_stream(dev)
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
@@ -343,14 +340,18 @@ ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ROPE_SCALINGS = {"plain": 0, "linear": 1, "bands": 2, "yarn": 3}
 
 
-_torch = None
+_torch = _raw_stream = None
 
 
 def _device() -> int:
     """The current device; imports torch on first use."""
-    global _torch
+    global _torch, _raw_stream
     if _torch is None:
         import torch
+        torch.cuda.current_device()  # initializes CUDA
+        # the stream's handle without a Stream object around it, where torch has that
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda dev: int(torch.cuda.current_stream(dev).cuda_stream))
         _torch = torch
     return _torch.cuda.current_device()
 
@@ -371,13 +372,10 @@ def _heads(name, t, dev, T, H, hd):
     return t.data_ptr(), (s0 if T > 1 else H * hd)
 
 
-def _plain(name, t, dev, dtype, shape):
-    """The address of a contiguous tensor of this type and shape (None as an extent: any); None for None."""
-    if t is None:
-        return None
-    if t.dtype is not getattr(_torch, dtype) or t.get_device() != dev or not t.is_contiguous() or (
-            t.shape != shape if None not in shape else t.dim() != len(shape)):
-        _refuse(name, t, dtype, shape, dev)
+def _plain(name, t, dev, dtype, dims):
+    """The address of a contiguous tensor of this type and number of dimensions."""
+    if t.dtype is not getattr(_torch, dtype) or t.get_device() != dev or not t.is_contiguous() or t.dim() != dims:
+        _refuse(name, t, dtype, "of %d dimensions" % dims, dev)
     return t.data_ptr()
 
 
@@ -396,7 +394,7 @@ class RopeSpec(ctypes.Structure):
                 ("mscale", ctypes.c_float)]
 
     def __init__(self, freqs, layout="half", mscale=1.0):
-        super().__init__(_plain("freqs", freqs, _device(), "int64", (None,)), 2 * freqs.shape[0], ROPE_LAYOUTS[layout], mscale)
+        super().__init__(_plain("freqs", freqs, _device(), "int64", 1), 2 * freqs.shape[0], ROPE_LAYOUTS[layout], mscale)
         self.tensor, self.ref = freqs, ctypes.addressof(self)
 
 
@@ -413,7 +411,7 @@ class KvPages(ctypes.Structure):
         for name, t in (("k", k), ("v", v)):
             if t.dtype is not _torch.uint8 or t.get_device() != dev or t.dim() != 2:
                 _refuse(name, t, "uint8", ("pages", "bytes"), dev)
-        rows = _plain("table", table, dev, "int32", (None, None))
+        rows = _plain("table", table, dev, "int32", 2)
         need = qmm_kv_page_bytes(type, Hkv, page_size, hd)
         if need == 0:
             raise ValueError("no cache of type %r has %r heads of %r in pages of %r" % (type, Hkv, hd, page_size))
@@ -427,7 +425,7 @@ class KvPages(ctypes.Structure):
 
 def qmm_rope_freqs(freqs, base=10000.0, scaling="plain", factor=1.0, orig_len=0.0, lo=0.0, hi=0.0, stream=None):
     """Fills the frequency table freqs (int64 CUDA tensor [n_rot / 2])."""
-    _call("qmm_rope_freqs", _plain("freqs", freqs, _device(), "int64", (None,)), 2 * freqs.shape[0], float(base), ROPE_SCALINGS[scaling], float(factor),
+    _call("qmm_rope_freqs", _plain("freqs", freqs, _device(), "int64", 1), 2 * freqs.shape[0], float(base), ROPE_SCALINGS[scaling], float(factor),
           float(orig_len), float(lo), float(hi), stream_handle(stream))
 
 
@@ -440,7 +438,7 @@ def qmm_rope(rope, x, y, pos, inverse=False, stream=None):
     px, ldx = _heads("x", x, dev, T, H, hd)
     py, ldy = _heads("y", y, dev, T, H, hd)
     _call("qmm_rope", rope.ref, px, ldx, py, ldy, _ints("pos", pos, dev, T), T, H, hd, 1 if inverse else 0,
-          stream_handle(stream, dev))
+          _raw_stream(dev) if stream is None else stream_handle(stream))
 
 
 def qmm_kv_page_bytes(type, Hkv, page_size, hd):
@@ -459,7 +457,7 @@ def qmm_kv_store(pages, k, v, pos, seq=None, rope=None, q=None, q_out=None, stre
         pq, ldq = _heads("q", q, dev, T, Hq, hd)
         po, ldo = _heads("q_out", q_out, dev, T, Hq, hd)
     _call("qmm_kv_store", pages.ref, pk, ldk, pv, ldv, _ints("pos", pos, dev, T), _ints("seq", seq, dev, T), T,
-          rope.ref if rope is not None else None, pq, ldq, po, ldo, Hq, stream_handle(stream, dev))
+          rope.ref if rope is not None else None, pq, ldq, po, ldo, Hq, _raw_stream(dev) if stream is None else stream_handle(stream))
 
 
 def qmm_kv_load(pages, pos, k_out=None, v_out=None, seq=None, stream=None):
@@ -468,7 +466,7 @@ def qmm_kv_load(pages, pos, k_out=None, v_out=None, seq=None, stream=None):
     pk, ldk = _heads("k_out", k_out, dev, T, Hkv, hd) if k_out is not None else (None, 0)
     pv, ldv = _heads("v_out", v_out, dev, T, Hkv, hd) if v_out is not None else (None, 0)
     _call("qmm_kv_load", pages.ref, _ints("pos", pos, dev, T), _ints("seq", seq, dev, T), T, pk, ldk, pv, ldv,
-          stream_handle(stream, dev))
+          _raw_stream(dev) if stream is None else stream_handle(stream))
 
 
 def qmm_kv_attend_scratch_bytes(Hq, Hkv, hd):
@@ -481,9 +479,14 @@ def qmm_kv_attend(pages, q, lens, out, scratch, scratch_bytes, scale, lse=None, 
     dev, R, Hq, hd = _device(), q.shape[0], q.shape[1], pages.hd
     pq, ldq = _heads("q", q, dev, R, Hq, hd)
     po, ldo = _heads("out", out, dev, R, Hq, hd)
-    _call("qmm_kv_attend", pages.ref, pq, ldq, _ints("lens", lens, dev, R), _ints("seq", seq, dev, R), po, ldo,
-          _plain("lse", lse, dev, "float32", (R, Hq)), ptr(scratch), scratch_bytes, R, Hq, scale, window,
-          stream_handle(stream, dev))
+    pl = None
+    if lse is not None:
+        if lse.dtype is not _torch.float32 or lse.get_device() != dev or lse.shape != (R, Hq) or not lse.is_contiguous():
+            _refuse("lse", lse, "float32", (R, Hq), dev)
+        pl = lse.data_ptr()
+    _call("qmm_kv_attend", pages.ref, pq, ldq, _ints("lens", lens, dev, R), _ints("seq", seq, dev, R) if seq is not None
+          else None, po, ldo, pl, scratch if type(scratch) is int else scratch.data_ptr(), scratch_bytes, R, Hq, scale, window,
+          _raw_stream(dev) if stream is None else stream_handle(stream))
 
 
 def qmm_blocksums(wtype, W, xq, s, M, N, K, stream=None):

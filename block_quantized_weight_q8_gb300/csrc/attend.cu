@@ -83,6 +83,7 @@ struct AttendArgs {
     int4* joins;
     int64_t R, ldq, ldo, window;
     int G, blocks;  // query heads per KV head, units per KV head
+    uint32_t chunk, chunks;  // rows per chunk, at most kAttendThreads chunks
     float scale;
 };
 
@@ -119,6 +120,18 @@ __device__ __forceinline__ uint32_t unit_weight(uint32_t tiles) {
     return tiles ? tiles + unit_cost(TEAM) : 0u;
 }
 
+// n / d for n < 2^31, d > 0, by the approximate reciprocal (relative error below 2^-21
+// with the conversions') and two corrections: the whole-number division takes twice as
+// long, and these stand one behind the other before the first byte is fetched.
+__device__ __forceinline__ uint32_t quick_div(uint32_t n, uint32_t d) {
+    const float by = __fdividef(1.0f, (float)d);
+    uint32_t q = (uint32_t)((float)n * by);
+    int rest = (int)(n - q * d);  // within 2^11 d of 0, modulo 2^32
+    q += (int)floorf((float)rest * by);
+    rest = (int)(n - q * d);
+    return rest < 0 ? q - 1 : (rest >= (int)d ? q + 1 : q);
+}
+
 // The list cut into `count` runs whose lengths differ by one at most; no more runs than
 // leave each a tile per warp.
 template <int TEAM>
@@ -127,13 +140,13 @@ struct Runs {
     __device__ __forceinline__ Runs(uint32_t work, uint32_t most) {
         const uint32_t fill = work / TEAM;
         count = fill < 1 ? 1 : (fill < most ? fill : most);
-        q = work / count;
+        q = quick_div(work, count);
         rem = work - q * count;
     }
     __device__ __forceinline__ uint32_t begin(uint32_t c) const { return c * q + (c < rem ? c : rem); }
     __device__ __forceinline__ uint32_t of(uint32_t g) const {  // the run that holds position g
         const uint32_t cut = rem * (q + 1);
-        return g < cut ? g / (q + 1) : rem + (g - cut) / q;
+        return g < cut ? quick_div(g, q + 1) : rem + quick_div(g - cut, q);
     }
 };
 
@@ -249,7 +262,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
     // The list's length up to each of (at most) 128 chunks of rows, read once per block:
     // a load of lens by every warp of the grid meets in one line of the L2 (1.5 us of a
     // single row's 10).
-    const uint32_t R = (uint32_t)a.R, chunk = (R + kAttendThreads - 1) / kAttendThreads, chunks = (R + chunk - 1) / chunk;
+    const uint32_t R = (uint32_t)a.R, chunk = a.chunk, chunks = a.chunks;
     const bool held = chunk == 1;  // every row's range fits in shared memory
     uint32_t total, before, mine = 0;
     for (uint32_t i = threadIdx.x * chunk; i < R && i < (threadIdx.x + 1) * chunk; i++) {
@@ -336,7 +349,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
             r++;
             continue;
         }
-        const uint32_t u = (g - row_start) / weight, off = g - row_start - u * weight;
+        const uint32_t u = quick_div(g - row_start, weight), off = g - row_start - u * weight;
         const uint32_t take = weight - off < end - g ? weight - off : end - g;
         constexpr uint32_t kCost = unit_cost(TEAM);
         const int ta = off > kCost ? (int)(off - kCost) : 0;
@@ -440,6 +453,13 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
         if (S::kSlots == 4) {
             next_tile();
             issue(ta + member + TEAM < tb, at1, by1, live1, false, 2);
+        }
+
+        const bool whole = ta == 0 && tb == (int)tiles;
+        if (!whole && member == 0 && lane == 0) {
+            const uint32_t g0 = row_start + u * weight + kCost;  // the unit's first tile
+            const uint32_t c0 = ta == 0 ? run : runs.of(g0), c1 = tb == (int)tiles ? run : runs.of(g0 + tiles - 1);
+            a.joins[2 * run + (ta == 0 ? 1 : 0)] = make_int4((int)r, (int)u, (int)c0, (int)(c1 - c0 + 1));
         }
 
         uint32_t qf[kSteps][4];
@@ -637,14 +657,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
         cp_async_wait<0>();
         l_run += __shfl_xor_sync(0xFFFFFFFFu, l_run, 1);
         l_run += __shfl_xor_sync(0xFFFFFFFFu, l_run, 2);
-        const bool whole = ta == 0 && tb == (int)tiles;
         float* part = a.parts + (2 * (int64_t)run + (ta == 0 ? 1 : 0)) * (kAttendHeads * (c.hd + 2));
         float* out = a.out + r * a.ldo + (int64_t)head0 * c.hd;
-        if (!whole && member == 0 && lane == 0) {
-            const uint32_t g0 = row_start + u * weight + kCost;  // the unit's first tile
-            const uint32_t c0 = runs.of(g0);
-            a.joins[2 * run + (ta == 0 ? 1 : 0)] = make_int4((int)r, (int)u, (int)c0, (int)(runs.of(g0 + tiles - 1) - c0 + 1));
-        }
         auto put_ml = [&](int h, float m, float l) {
             if (!whole) {
                 part[kAttendHeads * c.hd + h] = m, part[kAttendHeads * (c.hd + 1) + h] = l;
@@ -730,6 +744,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
 // side by side over the parts.  Either way in an order that the number of parts fixes.
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(KvPages c, AttendArgs a) {
     constexpr int kSide = kJoinThreads / 8;  // threads side by side over the parts
+    constexpr int kBatch = 4;                // parts that a thread fetches at once
     __shared__ __align__(16) float4 sum[kSide][8];
     __shared__ float fold_m[kSide], fold_l[kSide];
     pdl_wait();
@@ -787,24 +802,24 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(KvPages c, At
             // each thread's parts about their own maximum, then the threads' about theirs
             float m = -INFINITY, l = 0.0f;
             float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int i0 = s; i0 < n; i0 += 8 * kSide) {
-                float4 z[8];
-                float pm[8], pl[8], top = m;
+            for (int i0 = s; i0 < n; i0 += kBatch * kSide) {
+                float4 z[kBatch];
+                float pm[kBatch], pl[kBatch], top = m;
 #pragma unroll
-                for (int k = 0; k < 8; k++) {
+                for (int k = 0; k < kBatch; k++) {
                     const int i = i0 + k * kSide;
                     const float* p = part(i < n ? i : s);
                     z[k] = *reinterpret_cast<const float4*>(p + h * c.hd + (there ? d : 0));
                     pm[k] = p[kAttendHeads * c.hd + h], pl[k] = p[kAttendHeads * c.hd + kAttendHeads + h];
                 }
 #pragma unroll
-                for (int k = 0; k < 8; k++)
+                for (int k = 0; k < kBatch; k++)
                     if (i0 + k * kSide < n) top = fmaxf(top, pm[k]);
                 const float ref = top == -INFINITY ? 0.0f : top, keep = exp2_approx(m - ref);
                 m = top;
                 l *= keep, y.x *= keep, y.y *= keep, y.z *= keep, y.w *= keep;
 #pragma unroll
-                for (int k = 0; k < 8; k++)
+                for (int k = 0; k < kBatch; k++)
                     if (i0 + k * kSide < n) {
                         const float f = exp2_approx(pm[k] - ref);
                         l = __fmaf_rn(pl[k], f, l);
@@ -885,6 +900,8 @@ qmm_status qmm_kv_attend(const qmm_kv_pages* cache, const float* q, int64_t ldq,
     a.R = R, a.ldq = ldq, a.ldo = ldo, a.window = window;
     a.G = (int)(Hq / c.Hkv);
     a.blocks = (int)blocks;
+    a.chunk = (uint32_t)((R + kAttendThreads - 1) / kAttendThreads);
+    a.chunks = (uint32_t)((R + a.chunk - 1) / a.chunk);
     a.scale = scale;
     DeviceInfo dev;
     st = current_device(&dev);
