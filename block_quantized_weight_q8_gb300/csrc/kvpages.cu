@@ -25,18 +25,16 @@ constexpr int kRowCtas = 4;     // per SM
 constexpr int kRowTable = 512;  // (cos, sin) entries of one block of tokens
 constexpr int kRowTokens = 32;  // tokens of a block at most
 
-// What a token's rows need to know of its place: the page's offset in the pools (or
-// -1: nothing is stored) and the position in it.
-struct Place {
+// What a token's rows need to know of its place: the page's offset in the pools (-1:
+// it has none) and the position in it (-1: a padding token).
+struct __align__(16) Place {
     int64_t page;
     int o;
-    bool skip;  // a padding token
 };
 __device__ __forceinline__ Place place_of(const KvPages& c, const int32_t* pos, const int32_t* seq, int64_t t) {
     Place x;
     const int p = pos[t];
-    x.skip = p < 0;
-    x.o = p & ((1 << c.page_shift) - 1);
+    x.o = p < 0 ? -1 : p & ((1 << c.page_shift) - 1);
     x.page = -1;
     if (p >= 0) {
         const int id = kv_page_of(c, seq ? (int64_t)seq[t] : t, p);
@@ -87,16 +85,22 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas) rows_kernel(KvPages c, 
     if (value) share.turned = 0;
     const int side = TYPE == kNoPages ? 2 : (!live ? 0 : (query ? 2 : (value ? 1 : 0)));
     const int64_t ld = side == 2 ? a.ldq : (side == 1 ? a.ldv : a.ldk);
-    // Fetches are free of branches (a lane or token out of range reads the row's first
-    // share, or the last token's, again): a load inside a branch is waited for at its end.
-    const float* x = (side == 2 ? a.q : (side == 1 ? a.v : a.k)) + (live ? (int64_t)h * hd : 0);
+    // Fetches are free of branches (a lane out of range reads the row's first share, and
+    // the last token is read again): a load inside a branch is waited for at its end.
+    const int64_t step = (int64_t)gridDim.x * par;  // tokens from one of this thread's to its next
+    const int64_t first = own.at(tl < nt ? tl : nt - 1);
+    const float* x = (side == 2 ? a.q : (side == 1 ? a.v : a.k)) + first * ld + (live ? (int64_t)h * hd : 0);
+    [[maybe_unused]] const float* x_end = (side == 2 ? a.q : (side == 1 ? a.v : a.k)) + a.T * ld;
+    float* y = query ? a.q_out + first * a.ldqo + (int64_t)h * hd : nullptr;
     const int o_read = live ? o : 0;
     const Share from = live ? share : row_share<kPairsNone>(0, 0);
-    auto fetch = [&](int t, float v[8]) {
-        int64_t at = own.at(t < nt ? t : nt - 1) * ld;
-        if (!QMM_IN_BOUNDS(g_pages_error, at + (live ? (int64_t)h * hd : 0) + hd - 1, a.T * ld)) at = 0;
-        row_load8<PAIRS>(from, a.n_rot, o_read, x + at, v);
+    auto fetch = [&](float v[8]) {
+        if (!QMM_IN_BOUNDS(g_pages_error, hd - 1, x_end - x)) return;
+        row_load8<PAIRS>(from, a.n_rot, o_read, x, v);
     };
+    // where this thread's row lies in a page
+    uint8_t* pool = (value ? c.v : c.k) + (int64_t)(h << c.page_shift) * c.row_bytes;
+    uint8_t* pool_scale = (value ? c.v : c.k) + c.scales + 4 * (int64_t)(h << c.page_shift);
     auto prepare = [&](int b0, int buf) {  // places and tables of the block that begins at the CTA's token b0
         const int n = nt - b0 < block ? nt - b0 : block;
         if (TYPE != kNoPages && (int)threadIdx.x < n)
@@ -109,8 +113,8 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas) rows_kernel(KvPages c, 
             if (QMM_IN_BOUNDS(g_pages_error, to, kRowTable)) tables[buf][to] = e;
         }
     };
-    float v[8], ahead[8];
-    fetch(tl, v);
+    float v[8] = {}, ahead[8] = {};
+    fetch(v);
     prepare(0, 0);
     __syncthreads();
 
@@ -121,13 +125,17 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas) rows_kernel(KvPages c, 
       const int bn = nt - b0 < block ? nt - b0 : block;
       for (int i0 = 0; i0 < bn; i0 += par) {  // the same count for every lane: the shuffles need whole warps
         const int tb = i0 + tl, t = b0 + tb;  // of the block, of the CTA
-        fetch(t + par, ahead);
+        if (t + par < nt) x += step * ld;
+        fetch(ahead);
         const bool here = live && tb < bn;
+        Place p;
+        p.page = -1, p.o = 0;
+        if (TYPE != kNoPages) p = places[buf][here ? tb : 0];
         if (here) row_turn8<PAIRS>(share, v, tables[buf] + tb * 4 * run + o, run);
         if (query) {
-            if (here && (TYPE == kNoPages || !places[buf][TYPE == kNoPages ? 0 : tb].skip) &&
-                QMM_IN_BOUNDS(g_pages_error, own.at(t) * a.ldqo + (int64_t)h * hd + hd - 1, a.T * a.ldqo))
-                row_store8<PAIRS>(share, a.n_rot, o, a.q_out + own.at(t) * a.ldqo + (int64_t)h * hd, v);
+            if (here && p.o >= 0 && QMM_IN_BOUNDS(g_pages_error, (y - a.q_out) + hd - 1, a.T * a.ldqo))
+                row_store8<PAIRS>(share, a.n_rot, o, y, v);
+            y += step * a.ldqo;
         }
         if (TYPE != kNoPages) {
             float amax = 0.0f;
@@ -137,37 +145,33 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas) rows_kernel(KvPages c, 
                 amax = here ? amax : 0.0f;
                 for (int m = 1 << lw >> 1; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, m));
             }
-            const Place p = places[buf][here ? tb : 0];
             if (here && !query && p.page >= 0) {
-                uint8_t* pool = value ? c.v : c.k;
-                const int64_t at = p.page + (int64_t)((h << c.page_shift) + p.o) * c.row_bytes;
-                if (TYPE == QMM_KV_Q8) {
+                const int64_t at = p.page + (int64_t)p.o * c.row_bytes;
+                if (!QMM_IN_BOUNDS(g_pages_error, at + (int64_t)(h << c.page_shift) * c.row_bytes + c.row_bytes - 1,
+                                   c.num_pages * c.stride)) {
+                } else if (TYPE == QMM_KV_Q8) {
                     // |x * (127 / amax)| does not round beyond 127: no saturation is needed
                     const float inv = amax != 0.0f ? __fdiv_rn(127.0f, amax) : 0.0f;
                     uint32_t b[8];
 #pragma unroll
                     for (int i = 0; i < 8; i++) b[i] = (uint32_t)__float2int_rn(__fmul_rn(v[i], inv));
-                    const int64_t sat = p.page + c.scales + 4 * (int64_t)((h << c.page_shift) + p.o);
-                    if (QMM_IN_BOUNDS(g_pages_error, at + hd - 1, c.num_pages * c.stride) &&
-                        QMM_IN_BOUNDS(g_pages_error, sat + 3, c.num_pages * c.stride)) {
-                        if (PAIRS == kPairsScattered) {
+                    if (PAIRS == kPairsScattered) {
 #pragma unroll
-                            for (int i = 0; i < 4; i++) {
-                                const int2 e = scattered_at(a.n_rot, 4 * o + i);
-                                pool[at + e.x] = (uint8_t)b[i];
-                                pool[at + e.y] = (uint8_t)b[i + 4];
-                            }
-                        } else {
-                            const uint32_t w0 = __byte_perm(__byte_perm(b[0], b[1], 0x0040u),
-                                                            __byte_perm(b[2], b[3], 0x0040u), 0x5410u);
-                            const uint32_t w1 = __byte_perm(__byte_perm(b[4], b[5], 0x0040u),
-                                                            __byte_perm(b[6], b[7], 0x0040u), 0x5410u);
-                            *reinterpret_cast<uint32_t*>(pool + at + share.first) = w0;
-                            *reinterpret_cast<uint32_t*>(pool + at + share.second) = w1;
+                        for (int i = 0; i < 4; i++) {
+                            const int2 e = scattered_at(a.n_rot, 4 * o + i);
+                            pool[at + e.x] = (uint8_t)b[i];
+                            pool[at + e.y] = (uint8_t)b[i + 4];
                         }
-                        if (o == 0) *reinterpret_cast<float*>(pool + sat) = __fdiv_rn(amax, 127.0f);
+                    } else {
+                        const uint32_t w0 = __byte_perm(__byte_perm(b[0], b[1], 0x0040u),
+                                                        __byte_perm(b[2], b[3], 0x0040u), 0x5410u);
+                        const uint32_t w1 = __byte_perm(__byte_perm(b[4], b[5], 0x0040u),
+                                                        __byte_perm(b[6], b[7], 0x0040u), 0x5410u);
+                        *reinterpret_cast<uint32_t*>(pool + at + share.first) = w0;
+                        *reinterpret_cast<uint32_t*>(pool + at + share.second) = w1;
                     }
-                } else if (QMM_IN_BOUNDS(g_pages_error, at + 2 * hd - 1, c.num_pages * c.stride)) {
+                    if (o == 0) *reinterpret_cast<float*>(pool_scale + p.page + 4 * p.o) = __fdiv_rn(amax, 127.0f);
+                } else {
                     __half* to = reinterpret_cast<__half*>(pool + at);
                     if (PAIRS == kPairsScattered) {
 #pragma unroll
@@ -216,6 +220,7 @@ qmm_status rows_launch(int type, const KvPages& c, const RowArgs& a, int hd, cud
         switch (a.pairs) {
         case kPairsHalf: return go(rows_kernel<TYPE, kPairsHalf>);
         case kPairsNext: return go(rows_kernel<TYPE, kPairsNext>);
+        case kPairsNextAny: return go(rows_kernel<TYPE, kPairsNextAny>);
         case kPairsScattered: return go(rows_kernel<TYPE, kPairsScattered>);
         default: return TYPE == kNoPages ? QMM_E_TYPE : go(rows_kernel<TYPE == kNoPages ? QMM_KV_Q8 : TYPE, kPairsNone>);
         }
@@ -292,7 +297,7 @@ __global__ void __launch_bounds__(kLoadThreads, kLoadCtas)
                 const int t = ta + u * par;
                 const Place p = places[buf][t < n ? t : n - 1];
                 page[u] = p.page;
-                int64_t at = p.page < 0 ? 0 : p.page + p.o * c.row_bytes, sat = p.page < 0 ? 0 : p.page + 4 * p.o;
+                int64_t at = p.page < 0 ? 0 : p.page + (int64_t)p.o * c.row_bytes, sat = p.page < 0 ? 0 : p.page + 4 * p.o;
                 if (!QMM_IN_BOUNDS(g_pages_error, at + (int64_t)head * c.row_bytes + kQuad * quad + kQuad - 1,
                                    c.num_pages * c.stride))
                     at = 0;
@@ -306,7 +311,7 @@ __global__ void __launch_bounds__(kLoadThreads, kLoadCtas)
 #pragma unroll
             for (int u = 0; u < kLoadUnroll; u++) {
                 const int t = ta + u * par;
-                if (t >= n || places[buf][t].skip) continue;
+                if (t >= n || places[buf][t].o < 0) continue;
                 if (!QMM_IN_BOUNDS(g_pages_error, own.at(b0 + t) * ld + (int64_t)h * c.hd + 4 * quad + 3, T * ld)) continue;
                 float4 y;
                 if (TYPE == QMM_KV_Q8) {  // d * code, rounded once

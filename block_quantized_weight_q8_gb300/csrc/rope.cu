@@ -52,7 +52,9 @@ qmm_status rope_check(const qmm_rope_spec* r, int64_t hd, RowArgs* a) {
     a->freqs = (const uint64_t*)r->freqs;
     a->mscale = r->mscale;
     a->n_rot = (int)r->n_rot;
-    a->pairs = r->layout == QMM_ROPE_INTERLEAVED ? kPairsNext : (r->n_rot % 8 ? kPairsScattered : kPairsHalf);
+    const bool whole = r->n_rot % 8 == 0;
+    a->pairs = r->layout == QMM_ROPE_INTERLEAVED ? (whole ? kPairsNext : kPairsNextAny)
+                                                 : (whole ? kPairsHalf : kPairsScattered);
     return QMM_OK;
 }
 

@@ -136,8 +136,9 @@ constexpr int kNoPages = -1;  // in the place of a cache type: query rows only
 enum RowPairs {
     kPairsNone = 0,       // nothing is rotated
     kPairsHalf = 1,       // (i, i + n_rot/2), n_rot a multiple of 8: a float4 of each half
-    kPairsNext = 2,       // (2i, 2i + 1): eight neighbours
-    kPairsScattered = 3,  // (i, i + n_rot/2), any even n_rot: single values
+    kPairsNext = 2,       // (2i, 2i + 1), n_rot a multiple of 8: eight neighbours
+    kPairsNextAny = 3,    // the same, any even n_rot
+    kPairsScattered = 4,  // (i, i + n_rot/2), any even n_rot: single values
 };
 struct RowArgs {
     const float* k;
@@ -210,14 +211,17 @@ __device__ __forceinline__ void row_store8(const Share& s, int n_rot, int o, flo
 // table: the token's, at this share's first pair (entry i is i * turn_run on)
 template <int PAIRS>
 __device__ __forceinline__ void row_turn8(const Share& s, float v[8], const float4* table, int run) {
-    if (PAIRS == kPairsNone) return;
+    constexpr bool kWhole = PAIRS == kPairsHalf || PAIRS == kPairsNext;  // a share is rotated or it is not
+    if constexpr (PAIRS != kPairsNone) {
+        if (s.turned == 0) return;
 #pragma unroll
-    for (int i = 0; i < 4; i++)
-        if (i < s.turned) {
-            const float4 cs = table[i * run];
-            if (PAIRS == kPairsNext) turn_pair(v[2 * i], v[2 * i + 1], cs);
-            else turn_pair(v[i], v[i + 4], cs);
-        }
+        for (int i = 0; i < 4; i++)
+            if (kWhole || i < s.turned) {
+                const float4 cs = table[i * run];
+                if (PAIRS == kPairsNext || PAIRS == kPairsNextAny) turn_pair(v[2 * i], v[2 * i + 1], cs);
+                else turn_pair(v[i], v[i + 4], cs);
+            }
+    }
 }
 
 }  // namespace qmm
