@@ -49,28 +49,30 @@ constexpr int kAttendHeads = 8;  // query heads per unit
 constexpr int kAttendMaxRuns = 4 * kAttendSms * kAttendWarps;
 constexpr int kJoinThreads = 128;
 constexpr int kJoinFew = 8;  // parts that one CTA joins for all heads
-// Up to so many units, a team is a CTA (the first tokens of one request: 4.8 us, a single
-// warp per unit 7.2; a row of 4096 positions 8.6 and 12.3); with more, a warp (1000 rows
-// of 40 positions, 8 units each: 220 us by CTAs, 49 by warps; 256 of 300: 70 and 48).
-// They are equal at 512 units (64 ragged rows: 84 and 86 us).
-constexpr int64_t kTeamUnits = 608;
+// Up to so many units, a team is a CTA (the first tokens of one request: 5.7 us, a single
+// warp per unit 7.2; a row of 4096 positions 8.7 and 9.7); with more, a warp (1000 rows
+// of 40 positions, 8 units each: 220 us by CTAs, 47 by warps; 64 ragged rows, 512 units:
+// 74 and 71).
+constexpr int64_t kTeamUnits = 152;
 // what a unit costs a team besides its tiles, in tiles
-__host__ __device__ constexpr uint32_t unit_cost(int team) { return team == 1 ? 4 : 8; }
+__host__ __device__ constexpr uint32_t unit_cost(int team) { return team == 1 ? 2 : 12; }
 constexpr float kSlack = 4.0f;     // what scores may be over the running reference, in powers of two
 
 template <int TYPE, int HDT>
 struct AttendShape {
     static constexpr int kRow = HDT * (TYPE == QMM_KV_F16 ? 2 : 1);  // bytes of a row
     static constexpr int kTile = kRow <= 128 ? 32 : 16;              // positions
-    // A warp's ring has slots of one tile's keys or values, with their scales and the
-    // mask: all but one are on their way while it is read.
-    static constexpr int kSlots = kRow <= 256 ? 4 : 3;
+    // A warp's ring has three slots of one tile's keys or values, with their scales and the
+    // mask: two are on their way while one is read.
+    static constexpr int kSlots = 3;
     static constexpr int kSlot = kTile * kRow + 4 * kTile + 16;
     static constexpr int kRing = kSlots * kSlot;  // of a warp
     static constexpr int kSmem = kAttendWarps * kRing;
-    // CTAs per SM, as many as registers and shared memory allow: a warp waits about four
-    // cycles from one instruction to the next
-    static constexpr int kCtas = kRow <= 64 ? 4 : HDT <= 128 ? 3 : 2;
+    // CTAs per SM such that about 68 KB are on their way: more queue up in the memory
+    // system, which then serves the SMs unevenly (two rows of 131072 and 64 ragged ones:
+    // 67 and 74 us with 2 CTAs of 128-byte rows, 72 and 75 with 3, 74 and 81 with a
+    // fourth slot too).
+    static constexpr int kCtas = kRow <= 64 ? 4 : 2;
 };
 
 struct AttendArgs {
@@ -438,8 +440,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
                     qv[s] = __ldg(reinterpret_cast<const float4*>(qh + d));
             }
         }
-        // Fill all slots but one.  While half q of the tiles' halves is read, the following
-        // kSlots - 1 are on their way.
+        // Fill two slots.  While half q of the tiles' halves is read, q + 1 and q + 2 are on
+        // their way.
         int64_t at1 = row_at(look, id0);
         uint32_t live1 = __ballot_sync(0xFFFFFFFFu, at1 >= 0), by1 = scale_by(look);
         auto next_tile = [&]() {  // at1, by1 and live1 to the tile after, whose page is in id1
@@ -450,10 +452,6 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
         };
         issue(ta + member < tb, at1, by1, live1, false, 0);
         issue(ta + member < tb, at1, by1, live1, true, 1);
-        if (S::kSlots == 4) {
-            next_tile();
-            issue(ta + member + TEAM < tb, at1, by1, live1, false, 2);
-        }
 
         const bool whole = ta == 0 && tb == (int)tiles;
         if (!whole && member == 0 && lane == 0) {
@@ -499,8 +497,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
         for (int t = ta + member; t < tb; t += TEAM) {
             cp_async_wait<S::kSlots - 2>();
             __syncwarp();  // the keys are here for every lane, and the slot before is read out
-            if (S::kSlots == 3) next_tile();
-            issue(t + TEAM < tb, at1, by1, live1, S::kSlots == 4, turn(S::kSlots - 1));
+            next_tile();
+            issue(t + TEAM < tb, at1, by1, live1, false, turn(2));
             const uint32_t st = ring_u + slot * S::kSlot;
             const uint8_t* tail = ring + slot * S::kSlot + TILE * ROW;  // scales, then the mask
             const uint32_t live = *reinterpret_cast<const uint32_t*>(tail + 4 * TILE);
@@ -569,8 +567,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
             slot = turn(1);
             cp_async_wait<S::kSlots - 2>();
             __syncwarp();  // the values are here, the keys are read out
-            if (S::kSlots == 4) next_tile();
-            issue(t + (S::kSlots - 2) * TEAM < tb, at1, by1, live1, S::kSlots == 3, turn(S::kSlots - 1));
+            issue(t + TEAM < tb, at1, by1, live1, true, turn(2));
             const uint32_t sv = ring_u + slot * S::kSlot;
             const float* vs = reinterpret_cast<const float*>(ring + slot * S::kSlot + TILE * ROW);
             const float v_lane = TYPE == QMM_KV_Q8 && lane < TILE ? fabsf(vs[lane]) : 0.0f;
