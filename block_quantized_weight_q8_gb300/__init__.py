@@ -357,9 +357,9 @@ def _device() -> int:
 
 
 def _refuse(name, t, dtype, shape, dev):
-    raise ValueError("%s: %s of shape %s on the current device (cuda:%d) with contiguous heads or values is needed, got %s "
-                     "of shape %s (strides %s) on %s" % (name, dtype, shape, dev, t.dtype, tuple(t.shape), t.stride(),
-                                                        t.device))
+    raise ValueError("%s: %s of shape %s on the current device (cuda:%d), contiguous or with contiguous heads, is needed, "
+                     "got %s of shape %s (strides %s) on %s" % (name, dtype, shape, dev, t.dtype, tuple(t.shape),
+                                                                t.stride(), t.device))
 
 
 def _heads(name, t, dev, T, H, hd):
@@ -425,8 +425,9 @@ class KvPages(ctypes.Structure):
 
 def qmm_rope_freqs(freqs, base=10000.0, scaling="plain", factor=1.0, orig_len=0.0, lo=0.0, hi=0.0, stream=None):
     """Fills the frequency table freqs (int64 CUDA tensor [n_rot / 2])."""
-    _call("qmm_rope_freqs", _plain("freqs", freqs, _device(), "int64", 1), 2 * freqs.shape[0], float(base), ROPE_SCALINGS[scaling], float(factor),
-          float(orig_len), float(lo), float(hi), stream_handle(stream))
+    at = _plain("freqs", freqs, _device(), "int64", 1)
+    _call("qmm_rope_freqs", at, 2 * freqs.shape[0], float(base), ROPE_SCALINGS[scaling], float(factor), float(orig_len),
+          float(lo), float(hi), stream_handle(stream))
 
 
 def qmm_rope(rope, x, y, pos, inverse=False, stream=None):
@@ -457,7 +458,8 @@ def qmm_kv_store(pages, k, v, pos, seq=None, rope=None, q=None, q_out=None, stre
         pq, ldq = _heads("q", q, dev, T, Hq, hd)
         po, ldo = _heads("q_out", q_out, dev, T, Hq, hd)
     _call("qmm_kv_store", pages.ref, pk, ldk, pv, ldv, _ints("pos", pos, dev, T), _ints("seq", seq, dev, T), T,
-          rope.ref if rope is not None else None, pq, ldq, po, ldo, Hq, _raw_stream(dev) if stream is None else stream_handle(stream))
+          rope.ref if rope is not None else None, pq, ldq, po, ldo, Hq,
+          _raw_stream(dev) if stream is None else stream_handle(stream))
 
 
 def qmm_kv_load(pages, pos, k_out=None, v_out=None, seq=None, stream=None):
@@ -481,11 +483,13 @@ def qmm_kv_attend(pages, q, lens, out, scratch, scratch_bytes, scale, lse=None, 
     po, ldo = _heads("out", out, dev, R, Hq, hd)
     pl = None
     if lse is not None:
-        if lse.dtype is not _torch.float32 or lse.get_device() != dev or lse.shape != (R, Hq) or not lse.is_contiguous():
+        if (lse.dtype is not _torch.float32 or lse.get_device() != dev or lse.shape != (R, Hq)
+                or not lse.is_contiguous()):
             _refuse("lse", lse, "float32", (R, Hq), dev)
         pl = lse.data_ptr()
-    _call("qmm_kv_attend", pages.ref, pq, ldq, _ints("lens", lens, dev, R), _ints("seq", seq, dev, R) if seq is not None
-          else None, po, ldo, pl, scratch if type(scratch) is int else scratch.data_ptr(), scratch_bytes, R, Hq, scale, window,
+    ps = scratch if type(scratch) is int else scratch.data_ptr()
+    _call("qmm_kv_attend", pages.ref, pq, ldq, _ints("lens", lens, dev, R), _ints("seq", seq, dev, R), po, ldo, pl, ps,
+          scratch_bytes, R, Hq, scale, window,
           _raw_stream(dev) if stream is None else stream_handle(stream))
 
 

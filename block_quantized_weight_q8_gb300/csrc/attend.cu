@@ -14,8 +14,8 @@
 //   f32     a query, and the weights times the value scales, are split into two
 //           f16 (hi + lo, 22 bits) and take two rows of the tile: rows 0-7 are
 //           the heads' hi, rows 8-15 their lo, and one thread holds both sums.
-//           Each is first brought near f16's upper end by a power of two (per head; per tile
-//           of positions), so that lo does not fall below f16's range
+//           Each is first brought near f16's upper end by a power of two (of a head's
+//           query; of the value scales so far), so that lo stays in f16's range
 //   layout  the order of the 16 values within a step is free as long as both
 //           operands share it, so a lane takes its operand straight from 16-byte
 //           loads of natural rows, and a tile's scores are in the registers where
@@ -56,7 +56,7 @@ constexpr int kJoinFew = 8;  // parts that one CTA joins for all heads
 constexpr int64_t kTeamUnits = 152;
 // what a unit costs a team besides its tiles, in tiles
 __host__ __device__ constexpr uint32_t unit_cost(int team) { return team == 1 ? 2 : 12; }
-constexpr float kSlack = 4.0f;     // what scores may be over the running reference, in powers of two
+constexpr float kSlack = 4.0f;  // what scores may be over the running reference, in powers of two
 
 template <int TYPE, int HDT>
 struct AttendShape {
@@ -196,17 +196,16 @@ __device__ __forceinline__ float exp2_approx(float x) {  // within 2 units in th
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ void mma_f16(float d[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 // the same from a zero sum
 __device__ __forceinline__ void mma_f16_first(float d[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
-}
-__device__ __forceinline__ void mma_f16(float d[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // (lo, hi) to two f16, the first in the low half
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
@@ -368,7 +367,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
         // of this piece are those below `span`.
         const int last_p = (tile0 + tb) * TILE < x.len ? (tile0 + tb) * TILE : x.len;
         const unsigned span = (unsigned)(last_p - x.first);
-        int look = lane < TILE ? (tile0 + ta + member) * TILE + lane - x.first : -(1 << 30);
+        int look = lane < TILE ? (tile0 + ta + member) * TILE + lane - x.first : -(1 << 30) - 4096;
         // the page there as the table has it; -1: no position
         auto page_at = [&](int at) -> int {
             return (unsigned)at < span ? __ldg(pages + ((at + x.first) >> c.page_shift)) : -1;
@@ -383,7 +382,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
         };
         // from there to its scale: as far behind the page's scales as the row behind the page
         auto scale_by = [&](int at) -> uint32_t {
-            return (uint32_t)(c.scales - (int64_t)((kvh << c.page_shift) + ((at + x.first) & mask_o)) * (c.row_bytes - 4));
+            const int64_t row = (kvh << c.page_shift) + ((at + x.first) & mask_o);
+            return (uint32_t)(c.scales - row * (c.row_bytes - 4));
         };
         // one half of a tile, its keys or its values, into a slot of the ring; at: this
         // lane's position's row, by: from there to its scale, live: the positions that have one
@@ -401,7 +401,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
 #pragma unroll
                         for (int i = 0; i < kN; i++) {
                             if (!QMM_IN_BOUNDS(g_attend_error, from + i * 512 + 15, c.num_pages * c.stride)) continue;
-                            cp_async16(dst + (values ? put_v(b * kN + i) : put_k(b * kN + i)), pool + from + i * 512, 16);
+                            const uint32_t to = dst + (values ? put_v(b * kN + i) : put_k(b * kN + i));
+                            cp_async16(to, pool + from + i * 512, 16);
                         }
                     }
                 } else {
@@ -636,7 +637,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
                             mma(4 * w + 2, codes_h2(ah, 0x4140u), codes_h2(bh, 0x4140u));
                             mma(4 * w + 3, codes_h2(ah, 0x4342u), codes_h2(bh, 0x4342u));
                         } else {
-                            mma(2 * w, __byte_perm(vw[0][w], vw[1][w], 0x5410u), __byte_perm(vw[2][w], vw[3][w], 0x5410u));
+                            mma(2 * w, __byte_perm(vw[0][w], vw[1][w], 0x5410u),
+                                __byte_perm(vw[2][w], vw[3][w], 0x5410u));
                             mma(2 * w + 1, __byte_perm(vw[0][w], vw[1][w], 0x7632u),
                                 __byte_perm(vw[2][w], vw[3][w], 0x7632u));
                         }
@@ -718,8 +720,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
             float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kAttendWarps; w++) {
-                const float4 z = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(smem) +
-                                                                  (w * kAttendHeads + h) * HDT + 4 * exchange_quad(h, q));
+                const float* xw = reinterpret_cast<float*>(smem) + (w * kAttendHeads + h) * HDT;
+                const float4 z = *reinterpret_cast<const float4*>(xw + 4 * exchange_quad(h, q));
                 const float f = part_f[w][h];
                 y.x = __fmaf_rn(z.x, f, y.x), y.y = __fmaf_rn(z.y, f, y.y);
                 y.z = __fmaf_rn(z.z, f, y.z), y.w = __fmaf_rn(z.w, f, y.w);
@@ -843,7 +845,8 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(KvPages c, At
                 }
                 const float by = all == 0.0f ? 0.0f : __fdiv_rn(1.0f, all);
                 if (there)
-                    *reinterpret_cast<float4*>(out + h * c.hd + d) = make_float4(y.x * by, y.y * by, y.z * by, y.w * by);
+                    *reinterpret_cast<float4*>(out + h * c.hd + d) =
+                        make_float4(y.x * by, y.y * by, y.z * by, y.w * by);
                 if (lse && d == 0) lse[h] = (top + log2f(all)) * 0.693147180559945309f;
             }
             __syncthreads();
@@ -886,7 +889,8 @@ qmm_status qmm_kv_attend(const qmm_kv_pages* cache, const float* q, int64_t ldq,
     // the list of tiles is counted in 32 bits
     const int64_t room = c.max_pages << c.page_shift, seen = window > 0 && window < room ? window + 16 : room;
     const int64_t blocks = (Hq / c.Hkv + kAttendHeads - 1) / kAttendHeads;
-    if (room > kMaxDim || R * c.Hkv * blocks > kMaxDim / (seen / 16 + 2 + unit_cost(kAttendWarps))) return QMM_E_SHAPE;
+    if (room > ((int64_t)1 << 30) || R * c.Hkv * blocks > kMaxDim / (seen / 16 + 2 + unit_cost(kAttendWarps)))
+        return QMM_E_SHAPE;
     if (!aligned16(q) || !aligned16(out) || !aligned4(lens) || !aligned4(seq) || !aligned4(lse) || !aligned16(scratch))
         return QMM_E_ALIGN;
     if (scratch_bytes < need) return QMM_E_SCRATCH;
@@ -916,8 +920,8 @@ qmm_status qmm_kv_attend(const qmm_kv_pages* cache, const float* q, int64_t ldq,
         });
         if (set != QMM_OK) return set;
         runs = S::kCtas * kAttendSms * (kAttendWarps / TEAM);
-        return launch_pdl(attend_kernel<TYPE, HDT, TEAM>, dim3((unsigned)(S::kCtas * kAttendSms)), kAttendThreads, S::kSmem,
-                          cs, c, a);
+        return launch_pdl(attend_kernel<TYPE, HDT, TEAM>, dim3((unsigned)(S::kCtas * kAttendSms)), kAttendThreads,
+                          S::kSmem, cs, c, a);
     };
     using std::integral_constant;
     auto by_team = [&](auto type, auto hdt) -> qmm_status {

@@ -120,80 +120,85 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas) rows_kernel(KvPages c, 
 
     const bool codes = TYPE == QMM_KV_Q8 && __any_sync(0xFFFFFFFFu, live && !query);  // the warp quantizes
     for (int b0 = 0, buf = 0; b0 < nt; b0 += block, buf ^= 1) {
-      if (b0 > 0) __syncthreads();  // the block before is done, and this one prepared
-      if (b0 + block < nt) prepare(b0 + block, buf ^ 1);
-      const int bn = nt - b0 < block ? nt - b0 : block;
-      for (int i0 = 0; i0 < bn; i0 += par) {  // the same count for every lane: the shuffles need whole warps
-        const int tb = i0 + tl, t = b0 + tb;  // of the block, of the CTA
-        if (t + par < nt) x += step * ld;
-        fetch(ahead);
-        const bool here = live && tb < bn;
-        Place p;
-        p.page = -1, p.o = 0;
-        if (TYPE != kNoPages) p = places[buf][here ? tb : 0];
-        if (here) row_turn8<PAIRS>(share, v, tables[buf] + tb * 4 * run + o, run);
-        if (query) {
-            if (here && p.o >= 0 && QMM_IN_BOUNDS(g_pages_error, (y - a.q_out) + hd - 1, a.T * a.ldqo))
-                row_store8<PAIRS>(share, a.n_rot, o, y, v);
-            y += step * a.ldqo;
-        }
-        if (TYPE != kNoPages) {
-            float amax = 0.0f;
-            if (codes) {
-#pragma unroll
-                for (int i = 0; i < 8; i++) amax = fmaxf(amax, fabsf(v[i]));
-                amax = here ? amax : 0.0f;
-                for (int m = 1 << lw >> 1; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, m));
+        if (b0 > 0) __syncthreads();  // the block before is done, and this one prepared
+        if (b0 + block < nt) prepare(b0 + block, buf ^ 1);
+        const int bn = nt - b0 < block ? nt - b0 : block;
+        for (int i0 = 0; i0 < bn; i0 += par) {  // the same count for every lane: the shuffles need whole warps
+            const int tb = i0 + tl, t = b0 + tb;  // of the block, of the CTA
+            if (t + par < nt) x += step * ld;
+            fetch(ahead);
+            const bool here = live && tb < bn;
+            Place p;
+            p.page = -1, p.o = 0;
+            if (TYPE != kNoPages) p = places[buf][here ? tb : 0];
+            if (here) row_turn8<PAIRS>(share, v, tables[buf] + tb * 4 * run + o, run);
+            if (query) {
+                if (here && p.o >= 0 && QMM_IN_BOUNDS(g_pages_error, (y - a.q_out) + hd - 1, a.T * a.ldqo))
+                    row_store8<PAIRS>(share, a.n_rot, o, y, v);
+                y += step * a.ldqo;
             }
-            if (here && !query && p.page >= 0) {
-                const int64_t at = p.page + (int64_t)p.o * c.row_bytes;
-                if (!QMM_IN_BOUNDS(g_pages_error, at + (int64_t)(h << c.page_shift) * c.row_bytes + c.row_bytes - 1,
-                                   c.num_pages * c.stride)) {
-                } else if (TYPE == QMM_KV_Q8) {
-                    // |x * (127 / amax)| does not round beyond 127: no saturation is needed
-                    const float inv = amax != 0.0f ? __fdiv_rn(127.0f, amax) : 0.0f;
-                    uint32_t b[8];
+            if (TYPE != kNoPages) {
+                float amax = 0.0f;
+                if (codes) {
 #pragma unroll
-                    for (int i = 0; i < 8; i++) b[i] = (uint32_t)__float2int_rn(__fmul_rn(v[i], inv));
-                    if (PAIRS == kPairsScattered) {
+                    for (int i = 0; i < 8; i++) amax = fmaxf(amax, fabsf(v[i]));
+                    amax = here ? amax : 0.0f;
+                    for (int m = 1 << lw >> 1; m > 0; m >>= 1)
+                        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, m));
+                }
+                if (here && !query && p.page >= 0) {
+                    const int64_t at = p.page + (int64_t)p.o * c.row_bytes;
+                    if (!QMM_IN_BOUNDS(g_pages_error, at + (int64_t)(h << c.page_shift) * c.row_bytes + c.row_bytes - 1,
+                                       c.num_pages * c.stride)) {
+                    } else if (TYPE == QMM_KV_Q8) {
+                        // |x * (127 / amax)| rounds beyond 127 only where the quotient is infinite
+                        const float inv = amax != 0.0f ? __fdiv_rn(127.0f, amax) : 0.0f;
+                        uint32_t b[8];
 #pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            const int2 e = scattered_at(a.n_rot, 4 * o + i);
-                            pool[at + e.x] = (uint8_t)b[i];
-                            pool[at + e.y] = (uint8_t)b[i + 4];
+                        for (int i = 0; i < 8; i++) b[i] = (uint32_t)__float2int_rn(__fmul_rn(v[i], inv));
+                        if (inv == INFINITY) {
+#pragma unroll
+                            for (int i = 0; i < 8; i++) b[i] = (uint32_t)clampi((int)b[i], -128, 127);
                         }
-                    } else {
-                        const uint32_t w0 = __byte_perm(__byte_perm(b[0], b[1], 0x0040u),
-                                                        __byte_perm(b[2], b[3], 0x0040u), 0x5410u);
-                        const uint32_t w1 = __byte_perm(__byte_perm(b[4], b[5], 0x0040u),
-                                                        __byte_perm(b[6], b[7], 0x0040u), 0x5410u);
-                        *reinterpret_cast<uint32_t*>(pool + at + share.first) = w0;
-                        *reinterpret_cast<uint32_t*>(pool + at + share.second) = w1;
-                    }
-                    if (o == 0) *reinterpret_cast<float*>(pool_scale + p.page + 4 * p.o) = __fdiv_rn(amax, 127.0f);
-                } else {
-                    __half* to = reinterpret_cast<__half*>(pool + at);
-                    if (PAIRS == kPairsScattered) {
+                        if (PAIRS == kPairsScattered) {
 #pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            const int2 e = scattered_at(a.n_rot, 4 * o + i);
-                            to[e.x] = __float2half_rn(v[i]);
-                            to[e.y] = __float2half_rn(v[i + 4]);
+                            for (int i = 0; i < 4; i++) {
+                                const int2 e = scattered_at(a.n_rot, 4 * o + i);
+                                pool[at + e.x] = (uint8_t)b[i];
+                                pool[at + e.y] = (uint8_t)b[i + 4];
+                            }
+                        } else {
+                            const uint32_t w0 = __byte_perm(__byte_perm(b[0], b[1], 0x0040u),
+                                                            __byte_perm(b[2], b[3], 0x0040u), 0x5410u);
+                            const uint32_t w1 = __byte_perm(__byte_perm(b[4], b[5], 0x0040u),
+                                                            __byte_perm(b[6], b[7], 0x0040u), 0x5410u);
+                            *reinterpret_cast<uint32_t*>(pool + at + share.first) = w0;
+                            *reinterpret_cast<uint32_t*>(pool + at + share.second) = w1;
                         }
+                        if (o == 0) *reinterpret_cast<float*>(pool_scale + p.page + 4 * p.o) = __fdiv_rn(amax, 127.0f);
                     } else {
-                        const uint32_t w0 = f2h_bits(v[0]) | f2h_bits(v[1]) << 16;
-                        const uint32_t w1 = f2h_bits(v[2]) | f2h_bits(v[3]) << 16;
-                        const uint32_t w2 = f2h_bits(v[4]) | f2h_bits(v[5]) << 16;
-                        const uint32_t w3 = f2h_bits(v[6]) | f2h_bits(v[7]) << 16;
-                        *reinterpret_cast<uint2*>(to + share.first) = make_uint2(w0, w1);
-                        *reinterpret_cast<uint2*>(to + share.second) = make_uint2(w2, w3);
+                        __half* to = reinterpret_cast<__half*>(pool + at);
+                        if (PAIRS == kPairsScattered) {
+#pragma unroll
+                            for (int i = 0; i < 4; i++) {
+                                const int2 e = scattered_at(a.n_rot, 4 * o + i);
+                                to[e.x] = __float2half_rn(v[i]);
+                                to[e.y] = __float2half_rn(v[i + 4]);
+                            }
+                        } else {
+                            const uint32_t w0 = f2h_bits(v[0]) | f2h_bits(v[1]) << 16;
+                            const uint32_t w1 = f2h_bits(v[2]) | f2h_bits(v[3]) << 16;
+                            const uint32_t w2 = f2h_bits(v[4]) | f2h_bits(v[5]) << 16;
+                            const uint32_t w3 = f2h_bits(v[6]) | f2h_bits(v[7]) << 16;
+                            *reinterpret_cast<uint2*>(to + share.first) = make_uint2(w0, w1);
+                            *reinterpret_cast<uint2*>(to + share.second) = make_uint2(w2, w3);
+                        }
                     }
                 }
             }
-        }
 #pragma unroll
-        for (int i = 0; i < 8; i++) v[i] = ahead[i];
-      }
+            for (int i = 0; i < 8; i++) v[i] = ahead[i];
+        }
     }
 }
 

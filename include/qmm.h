@@ -48,7 +48,8 @@
  *             dependents early (griddepcontrol.launch_dependents); ordinary
  *             kernels, and this library's weight and activation quantizers,
  *             never release early, so a multiply right after them sees all of
- *             W.
+ *             W.  The rotary and paged-cache kernels release early too, after
+ *             their own wait; none of them writes weights.
  *   Errors.   Every call returns a qmm_status.  Arguments are checked on the
  *             host before anything is launched; a failed check launches
  *             nothing.  A launch failure returns QMM_E_CUDA.  No call aborts,
@@ -543,6 +544,9 @@ QMM_API qmm_status qmm_kv_load(const qmm_kv_pages* cache, const int32_t* pos, co
  * (status as above).  Several rows may read one sequence (tokens of one step
  * checked at their own lengths).  Hq a multiple of Hkv, Hq / Hkv <= 64.
  * q is taken in f32 (split into two f16, 22 bits), sums and the softmax in f32.
+ * A table's room, max_pages * page_size, is 2^30 positions at most, and the tiles of
+ * 16 positions that R rows of that room (or of the window) could have, over all KV
+ * heads and eights of their query heads, are fewer than 2^31.
  * The launch does not depend on the lengths, so a captured call serves any; the
  * order of the sums depends on lens, window and the shapes alone.  scratch: at
  * least qmm_kv_attend_scratch_bytes(Hq, Hkv, hd) bytes, written before it is read;

@@ -125,6 +125,37 @@ def test_rows_are_those_of_kv_quantize():
             assert np.array_equal(pool[p, at: at + 4], rows[t, h, :4])
 
 
+def test_special_rows_are_those_of_kv_quantize():
+    """Rows of subnormal values (127 / amax overflows), infinities, NaN and ties: the same codes and scales."""
+    Hkv, hd, page, T = 2, 32, 16, 6
+    c = plain.Cache("q8", Hkv, hd, page, T, page, seed=1, fill=0)
+    pages, k, v, _ = on_gpu(c)
+    x = workloads.activations_f32(T * Hkv, hd, seed=19).reshape(T, Hkv, hd)
+    x[0] *= np.float32(1e-41)
+    x[1, 0, 3], x[1, 1, 5] = np.inf, -np.inf
+    x[2, 0, 4] = np.nan
+    x[3, 0], x[3, 1] = np.float32(3e38), 0.0
+    x[4, 0, 0], x[4, 0, 1], x[4, 0, 2], x[4, 0, 3:] = 127.0, 2.5, -3.5, 0.5
+    rows = torch.empty(T * Hkv * qmm.qmm_kv_row_bytes(hd), dtype=torch.uint8, device="cuda")
+    qmm.qmm_kv_quantize(dev(x), rows, T * Hkv, hd)
+    for layout in (None, "half", "interleaved"):  # at position 0 a rotation copies
+        pos = np.zeros(T, np.int32)
+        rope = qmm.RopeSpec(dev(plain.turns(plain.freqs(hd))), layout) if layout else None
+        qmm.qmm_kv_store(pages, dev(x), dev(x), dev(pos), rope=rope)
+        want = host(rows).reshape(T, Hkv, 4 + hd)
+        # an infinity or NaN, and what overflows, reaches its pair through the rotation's products: keys 1 .. 3 then
+        # hold other rows
+        for which, pool in (("k", host(k)), ("v", host(v))):
+            for t in range(T):
+                if layout and which == "k" and t in (1, 2, 3):
+                    continue
+                p, o = c.place(t, 0)
+                for h in range(Hkv):
+                    at, sc = (h * page + o) * hd, Hkv * page * hd + 4 * (h * page + o)
+                    assert np.array_equal(pool[p, at: at + hd], want[t, h, 4:]), (layout, which, t, h)
+                    assert np.array_equal(pool[p, sc: sc + 4], want[t, h, :4]), (layout, which, t, h)
+
+
 ATTEND = [  # type, Hq, Hkv, hd, page, lens, window
     ("q8", 1, 1, 16, 16, [1], 0), ("q8", 14, 2, 64, 16, [33], 0), ("q8", 32, 8, 128, 16, [1, 31, 32, 33, 0, -1, 129, 700], 0),
     ("q8", 8, 8, 128, 64, [257, 5], 0), ("q8", 3, 1, 48, 1, [40, 2, 300], 0), ("q8", 10, 5, 80, 8, [77, 513], 0),
