@@ -122,7 +122,7 @@ __device__ __forceinline__ uint32_t unit_weight(uint32_t tiles) {
     return tiles ? tiles + unit_cost(TEAM) : 0u;
 }
 
-// n / d for n < 2^31, d > 0, by the approximate reciprocal (relative error below 2^-21
+// n / d for 0 <= n < 2^31, d > 0, by the approximate reciprocal (relative error below 2^-21
 // with the conversions') and two corrections: the whole-number division takes twice as
 // long, and these stand one behind the other before the first byte is fetched.
 __device__ __forceinline__ uint32_t quick_div(uint32_t n, uint32_t d) {
@@ -739,118 +739,129 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
 // One CTA per run, for the unit that its team continued and the one that it began and
 // left unfinished (a.joins: row, unit, first run, number of runs).  Up to kJoinFew parts
 // are joined by the first run's CTA, a thread per four values; the values of a unit in
-// more parts are shared out among its runs' CTAs, 32 values at a time, sixteen threads
-// side by side over the parts.  Either way in an order that the number of parts fixes.
+// more parts are shared out among its runs' CTAs, 32 values at a time, with 4 threads
+// side by side over the parts and four such pieces in hand at once (16 and one, where
+// there is a single piece or more than kJoinMany parts).  The order of the sums depends
+// on the runs alone.
+constexpr int kJoinMany = 64;
+struct JoinUnit {
+    const float* parts;
+    int n, row, head0, heads;
+};
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(KvPages c, AttendArgs a) {
-    constexpr int kSide = kJoinThreads / 8;  // threads side by side over the parts
-    constexpr int kBatch = 4;                // parts that a thread fetches at once
-    __shared__ __align__(16) float4 sum[kSide][8];
-    __shared__ float fold_m[kSide], fold_l[kSide];
+    constexpr int kLanes = kJoinThreads / 8;  // threads that share four neighbouring values' column
+    constexpr int kBatch = 4;                 // parts that a thread fetches at once
+    static_assert(kLanes == 16, "side, below");
+    __shared__ __align__(16) float4 sum[kLanes][8];
+    __shared__ float fold_m[kLanes], fold_l[kLanes];
     pdl_wait();
     pdl_launch_dependents();
-    const int Hq = a.G * c.Hkv, size = kAttendHeads * (c.hd + 2);
+    const int Hq = a.G * c.Hkv, size = kAttendHeads * (c.hd + 2), per_head = (c.hd + 31) >> 5;
     const int4 jobs[2] = {a.joins[2 * blockIdx.x], a.joins[2 * blockIdx.x + 1]};
-    for (int side = 0; side < 2; side++) {
-        const int4 job = side ? jobs[1] : jobs[0];
-        const int n = job.w;
-        if (n == 0) continue;
-        const int kvh = job.y / a.blocks, hb = job.y - kvh * a.blocks, head0 = kvh * a.G + hb * kAttendHeads;
-        const int heads = a.G - hb * kAttendHeads < kAttendHeads ? a.G - hb * kAttendHeads : kAttendHeads;
-        const float* parts = a.parts + 2 * (int64_t)job.z * size;
-        // the unit begins in its first run, the others continue it
-        auto part = [&](int i) -> const float* { return parts + (2 * (int64_t)i + (i == 0 ? 1 : 0)) * size; };
-        float* out = a.out + job.x * a.ldo + (int64_t)head0 * c.hd;
-        float* lse = a.lse ? a.lse + (int64_t)job.x * Hq + head0 : nullptr;
-        if (n <= kJoinFew) {
-            if (side == 0) continue;  // the first run's
-            const int quads = c.hd >> 2;
-            for (int e = threadIdx.x; e < heads * quads; e += kJoinThreads) {
-                const int h = e / quads, d = 4 * (e - h * quads);
-                float4 z[kJoinFew];
-                float pm[kJoinFew], pl[kJoinFew], m = -INFINITY, l = 0.0f;
+    if (jobs[0].w == 0 && jobs[1].w == 0) return;
+    auto unit_of = [&](const int4& job) {
+        JoinUnit x;
+        const int kvh = a.blocks == 1 ? job.y : job.y / a.blocks, hb = job.y - kvh * a.blocks;
+        x.parts = a.parts + 2 * (int64_t)job.z * size;
+        x.n = job.w, x.row = job.x, x.head0 = kvh * a.G + hb * kAttendHeads;
+        x.heads = a.G - hb * kAttendHeads < kAttendHeads ? a.G - hb * kAttendHeads : kAttendHeads;
+        return x;
+    };
+    // the unit begins in its first run, the others continue it
+    auto part = [&](const JoinUnit& x, int i) -> const float* {
+        return x.parts + (2 * i + (i == 0 ? 1 : 0)) * (int64_t)size;
+    };
+    auto put = [&](const JoinUnit& x, int h, int d, float4 y, float m, float l) {
+        const float by = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+        float* out = a.out + x.row * a.ldo + (int64_t)(x.head0 + h) * c.hd + d;
+        *reinterpret_cast<float4*>(out) = make_float4(y.x * by, y.y * by, y.z * by, y.w * by);
+        if (a.lse && d == 0) a.lse[(int64_t)x.row * Hq + x.head0 + h] = (m + log2f(l)) * 0.693147180559945309f;
+    };
+    auto add = [](float4& y, float& l, const float4& z, float pl, float f) {
+        l = __fmaf_rn(pl, f, l);
+        y.x = __fmaf_rn(z.x, f, y.x), y.y = __fmaf_rn(z.y, f, y.y);
+        y.z = __fmaf_rn(z.z, f, y.z), y.w = __fmaf_rn(z.w, f, y.w);
+    };
+    if (jobs[1].w > 0 && jobs[1].w <= kJoinFew) {
+        const JoinUnit x = unit_of(jobs[1]);
+        const int quads = c.hd >> 2;
+        for (int e = threadIdx.x; e < x.heads * quads; e += kJoinThreads) {
+            const int h = e / quads, d = 4 * (e - h * quads);
+            float4 z[kJoinFew];
+            float pm[kJoinFew], pl[kJoinFew], m = -INFINITY, l = 0.0f;
 #pragma unroll
-                for (int i = 0; i < kJoinFew; i++) {
-                    const float* p = part(i < n ? i : 0);
-                    z[i] = *reinterpret_cast<const float4*>(p + h * c.hd + d);
-                    pm[i] = p[kAttendHeads * c.hd + h], pl[i] = p[kAttendHeads * c.hd + kAttendHeads + h];
-                }
-#pragma unroll
-                for (int i = 0; i < kJoinFew; i++)
-                    if (i < n) m = fmaxf(m, pm[i]);
-                const float ref = m == -INFINITY ? 0.0f : m;
-                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int i = 0; i < kJoinFew; i++)
-                    if (i < n) {
-                        const float f = exp2_approx(pm[i] - ref);
-                        l = __fmaf_rn(pl[i], f, l);
-                        y.x = __fmaf_rn(z[i].x, f, y.x), y.y = __fmaf_rn(z[i].y, f, y.y);
-                        y.z = __fmaf_rn(z[i].z, f, y.z), y.w = __fmaf_rn(z[i].w, f, y.w);
-                    }
-                const float by = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
-                *reinterpret_cast<float4*>(out + h * c.hd + d) = make_float4(y.x * by, y.y * by, y.z * by, y.w * by);
-                if (lse && d == 0) lse[h] = (m + log2f(l)) * 0.693147180559945309f;
+            for (int i = 0; i < kJoinFew; i++) {
+                const float* p = part(x, i < x.n ? i : 0);
+                z[i] = *reinterpret_cast<const float4*>(p + h * c.hd + d);
+                pm[i] = p[kAttendHeads * c.hd + h], pl[i] = p[kAttendHeads * (c.hd + 1) + h];
             }
-            continue;
-        }
-        // pieces of 32 values of a head (the last one of a head may be 16)
-        const int per_head = (c.hd + 31) >> 5, s = threadIdx.x >> 3, q = threadIdx.x & 7;
-        for (int e = blockIdx.x - job.z; e < heads * per_head; e += n) {
-            const int h = e / per_head, d = 32 * (e - h * per_head) + 4 * q;
-            const bool there = d < c.hd;
-            // each thread's parts about their own maximum, then the threads' about theirs
-            float m = -INFINITY, l = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kJoinFew; i++)
+                if (i < x.n) m = fmaxf(m, pm[i]);
+            const float ref = m == -INFINITY ? 0.0f : m;
             float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int i0 = s; i0 < n; i0 += kBatch * kSide) {
-                float4 z[kBatch];
-                float pm[kBatch], pl[kBatch], top = m;
 #pragma unroll
-                for (int k = 0; k < kBatch; k++) {
-                    const int i = i0 + k * kSide;
-                    const float* p = part(i < n ? i : s);
-                    z[k] = *reinterpret_cast<const float4*>(p + h * c.hd + (there ? d : 0));
-                    pm[k] = p[kAttendHeads * c.hd + h], pl[k] = p[kAttendHeads * c.hd + kAttendHeads + h];
-                }
-#pragma unroll
-                for (int k = 0; k < kBatch; k++)
-                    if (i0 + k * kSide < n) top = fmaxf(top, pm[k]);
-                const float ref = top == -INFINITY ? 0.0f : top, keep = exp2_approx(m - ref);
-                m = top;
-                l *= keep, y.x *= keep, y.y *= keep, y.z *= keep, y.w *= keep;
-#pragma unroll
-                for (int k = 0; k < kBatch; k++)
-                    if (i0 + k * kSide < n) {
-                        const float f = exp2_approx(pm[k] - ref);
-                        l = __fmaf_rn(pl[k], f, l);
-                        y.x = __fmaf_rn(z[k].x, f, y.x), y.y = __fmaf_rn(z[k].y, f, y.y);
-                        y.z = __fmaf_rn(z[k].z, f, y.z), y.w = __fmaf_rn(z[k].w, f, y.w);
-                    }
-            }
-            sum[s][q] = y;
-            if (q == 0) fold_m[s] = m, fold_l[s] = l;
-            __syncthreads();
-            if (s == 0) {
-                float top = -INFINITY, all = 0.0f;
-#pragma unroll
-                for (int k = 0; k < kSide; k++) top = fmaxf(top, fold_m[k]);
-                const float ref = top == -INFINITY ? 0.0f : top;
-                y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int k = 0; k < kSide; k++) {
-                    const float f = exp2_approx(fold_m[k] - ref);
-                    const float4 z = sum[k][q];
-                    all = __fmaf_rn(fold_l[k], f, all);
-                    y.x = __fmaf_rn(z.x, f, y.x), y.y = __fmaf_rn(z.y, f, y.y);
-                    y.z = __fmaf_rn(z.z, f, y.z), y.w = __fmaf_rn(z.w, f, y.w);
-                }
-                const float by = all == 0.0f ? 0.0f : __fdiv_rn(1.0f, all);
-                if (there)
-                    *reinterpret_cast<float4*>(out + h * c.hd + d) =
-                        make_float4(y.x * by, y.y * by, y.z * by, y.w * by);
-                if (lse && d == 0) lse[h] = (top + log2f(all)) * 0.693147180559945309f;
-            }
-            __syncthreads();
+            for (int i = 0; i < kJoinFew; i++)
+                if (i < x.n) add(y, l, z[i], pl[i], exp2_approx(pm[i] - ref));
+            put(x, h, d, y, m, l);
         }
+    }
+    // this CTA's pieces of both units
+    int pieces[2];
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+        const int4 job = jobs[k];
+        pieces[k] = 0;
+        if (job.w > kJoinFew) {
+            const int all = unit_of(job).heads * per_head, first = blockIdx.x - job.z;
+            pieces[k] = first < all ? (int)quick_div(all - first - 1, job.w) + 1 : 0;
+        }
+    }
+    const bool many = jobs[0].w > kJoinMany || jobs[1].w > kJoinMany || pieces[0] + pieces[1] == 1;
+    const int lg = many ? 4 : 2, side = 1 << lg, q = threadIdx.x & 7, at = threadIdx.x >> 3, s = at & (side - 1);
+    const int slots = kLanes >> lg;
+    for (int e0 = 0; e0 < pieces[0] + pieces[1]; e0 += slots) {
+        const int e = e0 + (at >> lg);
+        const bool there = e < pieces[0] + pieces[1];
+        const int4 job = e < pieces[0] ? jobs[0] : jobs[1];
+        const JoinUnit x = unit_of(job);
+        const int piece = there ? (int)blockIdx.x - job.z + (e < pieces[0] ? e : e - pieces[0]) * job.w : 0;
+        const int h = (int)quick_div(piece, per_head), d = 32 * (piece - h * per_head) + 4 * q;
+        // each thread's parts about their own maximum, then the threads' about theirs
+        float m = -INFINITY, l = 0.0f;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i0 = s; there && i0 < x.n; i0 += kBatch * side) {
+            float4 z[kBatch];
+            float pm[kBatch], pl[kBatch], top = m;
+#pragma unroll
+            for (int k = 0; k < kBatch; k++) {
+                const int i = i0 + k * side;
+                const float* p = part(x, i < x.n ? i : s);
+                z[k] = *reinterpret_cast<const float4*>(p + h * c.hd + (d < c.hd ? d : 0));
+                pm[k] = p[kAttendHeads * c.hd + h], pl[k] = p[kAttendHeads * (c.hd + 1) + h];
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; k++)
+                if (i0 + k * side < x.n) top = fmaxf(top, pm[k]);
+            const float ref = top == -INFINITY ? 0.0f : top, keep = exp2_approx(m - ref);
+            m = top;
+            l *= keep, y.x *= keep, y.y *= keep, y.z *= keep, y.w *= keep;
+#pragma unroll
+            for (int k = 0; k < kBatch; k++)
+                if (i0 + k * side < x.n) add(y, l, z[k], pl[k], exp2_approx(pm[k] - ref));
+        }
+        sum[at][q] = y;
+        if (q == 0) fold_m[at] = m, fold_l[at] = l;
+        __syncthreads();
+        if (s == 0 && there) {
+            float top = -INFINITY, all = 0.0f;
+            for (int k = at; k < at + side; k++) top = fmaxf(top, fold_m[k]);
+            const float ref = top == -INFINITY ? 0.0f : top;
+            y = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = at; k < at + side; k++) add(y, all, sum[k][q], fold_l[k], exp2_approx(fold_m[k] - ref));
+            if (d < c.hd) put(x, h, d, y, top, all);
+        }
+        __syncthreads();
     }
 }
 
