@@ -60,13 +60,14 @@ struct CtaTokens {
     }
 };
 
-// Grid (CTAs that share the tokens, groups of kRowThreads / width rows).  lw: log2 of the
-// lanes per row, hd / 8 rounded up to a power of two; par: tokens side by side (more
-// than one where a token has fewer rows than the CTA takes); block: tokens whose
-// places and tables are in shared memory, the next block's prepared ahead.
+// Grid (CTAs that share the tokens, parts of a token's rows).  width: lanes per row, hd / 8
+// (for 8-bit rows rounded up to a power of two: the largest value goes round by
+// shuffles); rows_per: rows of a CTA; par: tokens side by side (more than one where a
+// token has fewer rows than a CTA takes); block: tokens whose places and tables are in
+// shared memory, the next block's prepared ahead.
 template <int TYPE, int PAIRS>
-__global__ void __launch_bounds__(kRowThreads, kRowCtas) rows_kernel(KvPages c, RowArgs a, int hd, int lw, int par,
-                                                                     int block) {
+__global__ void __launch_bounds__(kRowThreads, kRowCtas) rows_kernel(KvPages c, RowArgs a, int hd, int width,
+                                                                     int rows_per, int par, int block) {
     __shared__ float4 tables[2][kRowTable];
     __shared__ Place places[2][TYPE == kNoPages ? 1 : kRowTokens];
     pdl_wait();
@@ -74,8 +75,8 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas) rows_kernel(KvPages c, 
     const CtaTokens own(a.T, par);
     const int nt = own.count;
     const int Hkv = TYPE == kNoPages ? 0 : c.Hkv, rows = 2 * Hkv + a.Hq;
-    const int group = threadIdx.x >> lw, o = threadIdx.x & ((1 << lw) - 1);
-    const int tl = par > 1 ? group / rows : 0, row = blockIdx.y * (kRowThreads >> lw) + group - tl * rows;
+    const int group = threadIdx.x / width, o = threadIdx.x - group * width;
+    const int tl = group / rows_per, row = blockIdx.y * rows_per + group - tl * rows_per;
     const bool live = tl < par && row < rows && 8 * o < hd;
     const bool query = row >= 2 * Hkv, value = !query && row >= Hkv;
     const int h = query ? row - 2 * Hkv : (value ? row - Hkv : row);
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas) rows_kernel(KvPages c, 
         const int n = nt - b0 < block ? nt - b0 : block;
         if (TYPE != kNoPages && (int)threadIdx.x < n)
             places[buf][threadIdx.x] = place_of(c, a.pos, a.seq, own.at(b0 + threadIdx.x));
-        for (int i = threadIdx.x; i < n * half; i += kRowThreads) {
+        for (int i = threadIdx.x; i < n * half; i += blockDim.x) {
             const int t = i / half;
             float4 e = turn_cos_sin((uint64_t)(int64_t)a.pos[own.at(b0 + t)] * a.freqs[i - t * half], a.mscale);
             if (a.inverse) e.z = -e.z, e.w = -e.w;
@@ -143,7 +144,7 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas) rows_kernel(KvPages c, 
 #pragma unroll
                     for (int i = 0; i < 8; i++) amax = fmaxf(amax, fabsf(v[i]));
                     amax = here ? amax : 0.0f;
-                    for (int m = 1 << lw >> 1; m > 0; m >>= 1)
+                    for (int m = width >> 1; m > 0; m >>= 1)
                         amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, m));
                 }
                 if (here && !query && p.page >= 0) {
@@ -209,17 +210,22 @@ static unsigned token_ctas(int64_t T, int64_t parts, int ctas, int par) {
 }
 
 qmm_status rows_launch(int type, const KvPages& c, const RowArgs& a, int hd, cudaStream_t stream) {
-    int lw = 1;
-    while (8 << lw < hd) lw++;
-    const int groups = kRowThreads >> lw, rows = (type == kNoPages ? 0 : 2 * c.Hkv) + a.Hq;
-    int par = rows < groups ? groups / rows : 1;
-    const int64_t parts = (rows + groups - 1) / groups;
+    int width = hd / 8;
+    if (type == QMM_KV_Q8)
+        for (width = 2; 8 * width < hd;) width *= 2;
+    const int groups = kRowThreads / width, rows = (type == kNoPages ? 0 : 2 * c.Hkv) + a.Hq;
     int block = kRowTokens;  // the tables and places in shared memory
     if (a.n_rot && block > kRowTable / (4 * turn_run(a.n_rot / 2))) block = kRowTable / (4 * turn_run(a.n_rot / 2));
+    const int parts = (rows + groups - 1) / groups, rows_per = (rows + parts - 1) / parts;
+    int par = parts > 1 ? 1 : groups / rows;
     if (par > block) par = block;
+    if (par > a.T) par = (int)a.T;
     block -= block % par;
-    const dim3 grid(token_ctas(a.T, parts, kRowCtas, par), (unsigned)parts);
-    auto go = [&](auto kern) { return launch_pdl(kern, grid, kRowThreads, 0, stream, c, a, hd, lw, par, block); };
+    const int threads = (par * rows_per * width + 31) / 32 * 32;
+    const dim3 grid(token_ctas(a.T, parts, kRowCtas * kRowThreads / threads, par), (unsigned)parts);
+    auto go = [&](auto kern) {
+        return launch_pdl(kern, grid, threads, 0, stream, c, a, hd, width, rows_per, par, block);
+    };
     auto by_pairs = [&](auto t) -> qmm_status {
         constexpr int TYPE = decltype(t)::value;
         switch (a.pairs) {
