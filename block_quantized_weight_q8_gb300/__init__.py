@@ -4,7 +4,9 @@ Argument marshalling only: every function here has the name of the C entry
 point it calls, converts tensors to device pointers and the current torch
 stream to a cudaStream_t, and raises QmmError on a non-OK status.  All
 arithmetic runs in the CUDA kernels of libqmm.so; there is no other path.
-Tensors may be torch CUDA tensors or raw integer device addresses.
+Tensors may be torch CUDA tensors or raw integer device addresses; the rotary
+and paged-cache calls take tensors only, read the sizes from them and raise
+ValueError for one of another type, shape, layout or device.
 """
 from __future__ import annotations
 
@@ -387,6 +389,12 @@ def _ints(name, t, dev, n):
     return t.data_ptr()
 
 
+def _ref(name, x, dev):
+    if x.device != dev:
+        raise ValueError("%s: on cuda:%d, the current device is cuda:%d" % (name, x.device, dev))
+    return x.ref
+
+
 class RopeSpec(ctypes.Structure):
     """qmm_rope_spec: a frequency table (int64 CUDA tensor [n_rot / 2], filled by qmm_rope_freqs), how values are
     paired ("half" or "interleaved") and the factor of the result.  Keeps the table alive."""
@@ -395,7 +403,7 @@ class RopeSpec(ctypes.Structure):
 
     def __init__(self, freqs, layout="half", mscale=1.0):
         super().__init__(_plain("freqs", freqs, _device(), "int64", 1), 2 * freqs.shape[0], ROPE_LAYOUTS[layout], mscale)
-        self.tensor, self.ref = freqs, ctypes.addressof(self)
+        self.tensor, self.ref, self.device = freqs, ctypes.addressof(self), freqs.get_device()
 
 
 class KvPages(ctypes.Structure):
@@ -420,7 +428,7 @@ class KvPages(ctypes.Structure):
         stride = k.stride(0) if k.shape[0] > 1 else -(-k.shape[1] // 16) * 16
         super().__init__(k.data_ptr(), v.data_ptr(), rows, k.shape[0], stride, table.shape[0],
                          table.shape[1], Hkv, hd, KV_TYPES[type], page_size)
-        self.tensors, self.ref = (k, v, table), ctypes.addressof(self)
+        self.tensors, self.ref, self.device = (k, v, table), ctypes.addressof(self), dev
 
 
 def qmm_rope_freqs(freqs, base=10000.0, scaling="plain", factor=1.0, orig_len=0.0, lo=0.0, hi=0.0, stream=None):
@@ -438,7 +446,7 @@ def qmm_rope(rope, x, y, pos, inverse=False, stream=None):
     T, H, hd = x.shape
     px, ldx = _heads("x", x, dev, T, H, hd)
     py, ldy = _heads("y", y, dev, T, H, hd)
-    _call("qmm_rope", rope.ref, px, ldx, py, ldy, _ints("pos", pos, dev, T), T, H, hd, 1 if inverse else 0,
+    _call("qmm_rope", _ref("rope", rope, dev), px, ldx, py, ldy, _ints("pos", pos, dev, T), T, H, hd, 1 if inverse else 0,
           _raw_stream(dev) if stream is None else stream_handle(stream))
 
 
@@ -454,11 +462,13 @@ def qmm_kv_store(pages, k, v, pos, seq=None, rope=None, q=None, q_out=None, stre
     pv, ldv = _heads("v", v, dev, T, Hkv, hd)
     pq = ldq = po = ldo = Hq = 0
     if q is not None:
+        if q_out is None or rope is None:
+            raise ValueError("queries need q_out and rope")
         Hq = q.shape[1]
         pq, ldq = _heads("q", q, dev, T, Hq, hd)
         po, ldo = _heads("q_out", q_out, dev, T, Hq, hd)
-    _call("qmm_kv_store", pages.ref, pk, ldk, pv, ldv, _ints("pos", pos, dev, T), _ints("seq", seq, dev, T), T,
-          rope.ref if rope is not None else None, pq, ldq, po, ldo, Hq,
+    _call("qmm_kv_store", _ref("pages", pages, dev), pk, ldk, pv, ldv, _ints("pos", pos, dev, T), _ints("seq", seq, dev, T), T,
+          _ref("rope", rope, dev) if rope is not None else None, pq, ldq, po, ldo, Hq,
           _raw_stream(dev) if stream is None else stream_handle(stream))
 
 
@@ -467,7 +477,7 @@ def qmm_kv_load(pages, pos, k_out=None, v_out=None, seq=None, stream=None):
     dev, T, Hkv, hd = _device(), pos.shape[0], pages.Hkv, pages.hd
     pk, ldk = _heads("k_out", k_out, dev, T, Hkv, hd) if k_out is not None else (None, 0)
     pv, ldv = _heads("v_out", v_out, dev, T, Hkv, hd) if v_out is not None else (None, 0)
-    _call("qmm_kv_load", pages.ref, _ints("pos", pos, dev, T), _ints("seq", seq, dev, T), T, pk, ldk, pv, ldv,
+    _call("qmm_kv_load", _ref("pages", pages, dev), _ints("pos", pos, dev, T), _ints("seq", seq, dev, T), T, pk, ldk, pv, ldv,
           _raw_stream(dev) if stream is None else stream_handle(stream))
 
 
@@ -487,9 +497,10 @@ def qmm_kv_attend(pages, q, lens, out, scratch, scratch_bytes, scale, lse=None, 
                 or not lse.is_contiguous()):
             _refuse("lse", lse, "float32", (R, Hq), dev)
         pl = lse.data_ptr()
-    ps = scratch if type(scratch) is int else scratch.data_ptr()
-    _call("qmm_kv_attend", pages.ref, pq, ldq, _ints("lens", lens, dev, R), _ints("seq", seq, dev, R), po, ldo, pl, ps,
-          scratch_bytes, R, Hq, scale, window,
+    if scratch.get_device() != dev or scratch.nbytes < scratch_bytes or not scratch.is_contiguous():
+        _refuse("scratch", scratch, "memory", "of %d bytes" % scratch_bytes, dev)
+    _call("qmm_kv_attend", _ref("pages", pages, dev), pq, ldq, _ints("lens", lens, dev, R), _ints("seq", seq, dev, R), po, ldo,
+          pl, scratch.data_ptr(), scratch_bytes, R, Hq, scale, window,
           _raw_stream(dev) if stream is None else stream_handle(stream))
 
 

@@ -15,7 +15,9 @@
 //           f16 (hi + lo, 22 bits) and take two rows of the tile: rows 0-7 are
 //           the heads' hi, rows 8-15 their lo, and one thread holds both sums.
 //           Each is first brought near f16's upper end by a power of two (of a head's
-//           query; of the value scales so far), so that lo stays in f16's range
+//           query; of the value scales so far), so that lo stays in f16's
+//           range; a weight below 2^-12 of the largest, with lo at f16's least step, is
+//           off by 2^-34 of the largest at most
 //   layout  the order of the 16 values within a step is free as long as both
 //           operands share it, so a lane takes its operand straight from 16-byte
 //           loads of natural rows, and a tile's scores are in the registers where

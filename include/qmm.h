@@ -475,7 +475,7 @@ QMM_API qmm_status qmm_rope_freqs(void* freqs, int64_t n_rot, double base, int s
  * H * hd (a part of a fused projection's row is x with its row's ldx).  y may be x
  * (then ldy = ldx); otherwise they do not overlap.  inverse != 0 turns by -t: with
  * the same m that is the transposed map, the gradient of the rotation.
- * hd: a multiple of 16 in 16..256; H <= 65536. */
+ * hd: a multiple of 16 in 16..256; T >= 1; H in 1..65536. */
 QMM_API qmm_status qmm_rope(const qmm_rope_spec* rope, const float* x, int64_t ldx, float* y, int64_t ldy,
                             const int32_t* pos, int64_t T, int64_t H, int64_t hd, int inverse, qmm_stream_t stream);
 
@@ -494,7 +494,8 @@ QMM_API qmm_status qmm_rope(const qmm_rope_spec* rope, const float* x, int64_t l
  *   a page  row (KV head h, position o) at byte (h * page_size + o) * row, row = hd
  *           (Q8) or 2 hd (F16); Q8 scales follow all codes: f32 (h, o) at
  *           Hkv * page_size * hd + 4 * (h * page_size + o)
- * hd: a multiple of 16 in 16..256; Hkv 1..1024; page_size a power of two up to 4096.
+ * hd: a multiple of 16 in 16..256; Hkv 1..1024; page_size a power of two up to 4096;
+ * at least one token or row a call.
  * The struct is read by the call; its device pointers stay valid until the stream
  * has passed it.  k, v 16-byte aligned, int32 arrays and lse 4-byte, every other
  * device pointer 16-byte.  Token and row strides (ld*) are in values, multiples of
@@ -543,7 +544,8 @@ QMM_API qmm_status qmm_kv_load(const qmm_kv_pages* cache, const int32_t* pos, co
  * row, which is left as it was; a length beyond max_pages * page_size is cut there
  * (status as above).  Several rows may read one sequence (tokens of one step
  * checked at their own lengths).  Hq a multiple of Hkv, Hq / Hkv <= 64.
- * q is taken in f32 (split into two f16, 22 bits), sums and the softmax in f32.
+ * q and the weights are split into two f16 (22 bits; a position whose weight is far
+ * below the largest counts to 2^-34 of the largest value), sums and the softmax in f32.
  * A table's room, max_pages * page_size, is 2^30 positions at most, and the tiles of
  * 16 positions that R rows of that room (or of the window) could have, over all KV
  * heads and eights of their query heads, are fewer than 2^31.

@@ -117,7 +117,15 @@ def attend(cache, q, lens, seqs, scale, window=0):
     summed by hd / 16 matrix steps that cut off (2^-23 of the largest partial sum each, at most A = scale sum |q k|),
     four f32 products and the softmax's argument (2^-24 of A each): d = A (2^-22 + (hd / 16) 2^-23 + 5 * 2^-24).  A
     weight is off by d and the exponential's 2^-22, twice (numerator and sum), by its split (2^-22) and by the sums: two
-    matrix steps per tile and one f32 FMA per tile of its warp, the four warps and the joined parts (2^-24 each)."""
+    matrix steps per tile and one f32 FMA per tile of its warp, the four warps and the joined parts (2^-24 each).
+
+    A split into two f16 is off by 2^-22 of the value only while its low half is normal; below, by half of f16's least
+    step, 2^-25.  Queries are split times 2^(14 - e), 2^e <= max |q|: 2^-39 max |q| a term, so d grows by scale 2^-39
+    max |q| sum |k|.  Weights w, relative to 2^m_run, are split as w d 2^(10 - e), 2^e at most the largest value scale d
+    (f16 rows: d = 1, e = 0): 2^-35 max(d) a position, times a code: 2^-35 max |v|.  m_run is less than 1 over the
+    warp's largest score, so that score's w is over 1/2 and what a join scales by is at most 2^(own maximum - the
+    row's): with the softmax's weights relative to the row's largest, 2^-34 max |v| a position, over their sum.
+    (Without it: one position takes the softmax and its code is 0, so the result is the others' far smaller weights.)"""
     R, Hq, hd = q.shape
     G = Hq // cache.Hkv
     out, bound = np.full((R, Hq, hd), np.nan), np.zeros((R, Hq, hd))
@@ -140,7 +148,9 @@ def attend(cache, q, lens, seqs, scale, window=0):
             out[r, h] = (w / total) @ v[:, h // G]
             lse[r, h] = t.max() + np.log(total)
             d = A * (2.0 ** -22 + hd / 16 * 2.0 ** -23 + 5 * 2.0 ** -24)
+            d += abs(scale) * 2.0 ** -39 * np.abs(q[r, h]).max() * np.abs(k[:, h // G]).sum(-1).max()
             steps = 2 * 2.0 ** -22 + ((n - first) / 16 + 8) * 2.0 ** -24
             bound[r, h] = (2 * (d + 2.0 ** -22) + 2.0 ** -22 + steps) * ((w / total) @ np.abs(v[:, h // G])) + 2.0 ** -120
+            bound[r, h] += 2.0 ** -34 * np.abs(v[:, h // G]).max() * (n - first) / total
             lbound[r, h] = d + 2.0 ** -22 + steps + 3 * 2.0 ** -24 * abs(lse[r, h])
     return out, lse, bound, lbound

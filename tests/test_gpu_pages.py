@@ -250,6 +250,97 @@ def test_extreme_values(typ):
     assert np.all(np.abs(host(lse) - wlse) <= lbound)
 
 
+@pytest.mark.parametrize("typ,Hq,Hkv,hd,window,R", [("q8", 16, 2, 64, 0, 5000), ("f16", 3, 3, 32, 19, 700), ("q8", 9, 1, 128, 7, 129)])
+def test_thousands_of_rows(typ, Hq, Hkv, hd, window, R):
+    """Rows of every length, empty and padding ones among them, with one set of queries: a result per sequence and length."""
+    rng = np.random.default_rng(R)
+    c = plain.Cache(typ, Hkv, hd, 8, 3, 44, seed=3)
+    for s in range(3):
+        c.fill(s, 44, rng)
+    lens, seq = rng.integers(-1, 45, size=R).astype(np.int32), rng.integers(0, 3, size=R).astype(np.int32)
+    lens[R // 2: R // 2 + R // 7] = 0  # long runs of rows without work
+    lens[-R // 9:] = -1
+    q = np.repeat(rng.standard_normal((1, Hq, hd)).astype(np.float32), 135, axis=0)
+    at, of = np.tile(np.arange(45), 3), np.repeat(np.arange(3), 45)
+    want, wlse, bound, lbound = plain.attend(c, q, at, of, 0.2, window)
+    scratch, n = scratch_for(Hq, c)
+    out, lse = torch.full((R, Hq, hd), 9.0, device="cuda"), torch.full((R, Hq), 9.0, device="cuda")
+    qs = dev(q[:1]).expand(R, Hq, hd).contiguous()
+    qmm.qmm_kv_attend(on_gpu(c)[0], qs, dev(lens), out, scratch, n, 0.2, lse=lse, seq=dev(seq), window=window)
+    got, glse = host(out), host(lse)
+    kept, some, which = lens >= 0, lens > 0, seq * 45 + lens
+    assert np.all(got[~kept] == 9.0) and np.all(glse[~kept] == 9.0)
+    assert np.all(np.abs(got[kept].astype(np.float64) - want[which[kept]]) <= bound[which[kept]])
+    assert np.all(np.abs(glse[some].astype(np.float64) - wlse[which[some]]) <= lbound[which[some]])
+    assert np.all(np.isneginf(glse[lens == 0]))
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 3.0])
+def test_scales(scale):
+    """No scale (the mean of the values), a negative one (the softmax prefers the smallest products), a large one."""
+    rng = np.random.default_rng(23)
+    c = plain.Cache("q8", 2, 64, 16, 2, 90, seed=5)
+    c.fill(0, 90, rng, loud=False)
+    c.fill(1, 33, rng, loud=False)
+    q = rng.standard_normal((2, 6, 64)).astype(np.float32)
+    want, wlse, bound, lbound = plain.attend(c, q, [90, 33], [0, 1], scale)
+    scratch, m = scratch_for(6, c)
+    out, lse = torch.empty(q.shape, device="cuda"), torch.empty(2, 6, device="cuda")
+    qmm.qmm_kv_attend(on_gpu(c)[0], dev(q), dev(np.array([90, 33], np.int32)), out, scratch, m, scale, lse=lse)
+    assert np.all(np.abs(host(out) - want) <= bound)
+    assert np.all(np.abs(host(lse) - wlse) <= lbound)
+
+
+def test_store_of_a_fused_projection_rotates_in_place():
+    """Queries, keys and values as columns of one row buffer, the queries rotated where they stand."""
+    rng = np.random.default_rng(24)
+    T, Hq, Hkv, hd = 21, 6, 2, 96
+    c = plain.Cache("q8", Hkv, hd, 16, 1, 64, seed=6, fill=0)
+    pages, k, v, _ = on_gpu(c)
+    buf = rng.standard_normal((T, Hq + 2 * Hkv, hd)).astype(np.float32)
+    t = dev(buf)
+    pos, seq = np.arange(5, 5 + T, dtype=np.int32), np.zeros(T, np.int32)
+    table = plain.turns(plain.freqs(64))
+    rope = qmm.RopeSpec(dev(table))
+    q = t[:, :Hq]
+    qmm.qmm_kv_store(pages, t[:, Hq: Hq + Hkv], t[:, Hq + Hkv:], dev(pos), seq=dev(seq), rope=rope, q=q, q_out=q)
+    kr = plain.rotate(buf[:, Hq: Hq + Hkv], pos, table)[0].astype(np.float32)
+    for i in range(T):
+        c.put(c.k, 0, pos[i], kr[i])
+        c.put(c.v, 0, pos[i], buf[i, Hq + Hkv:])
+    assert np.array_equal(host(k), c.k) and np.array_equal(host(v), c.v)
+    want = torch.empty(T, Hq, hd, device="cuda")
+    qmm.qmm_rope(rope, dev(buf[:, :Hq]), want, dev(pos))
+    got = host(t)
+    assert np.array_equal(got[:, :Hq].copy().view(np.int32), host(want).view(np.int32))
+    assert np.array_equal(got[:, Hq:], buf[:, Hq:])
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with its own scratch, over one cache: the results of the same calls one by one."""
+    rng = np.random.default_rng(25)
+    c = plain.Cache("q8", 2, 128, 16, 3, 600, seed=7)
+    for s, n in enumerate((600, 31, 290)):
+        c.fill(s, n, rng)
+    pages = on_gpu(c)[0]
+    lens = dev(np.array([600, 31, 290], np.int32))
+    qs = [dev(rng.standard_normal((3, 8, 128)).astype(np.float32)) for _ in range(2)]
+    want = [torch.empty(3, 8, 128, device="cuda") for _ in range(2)]
+    got = [[torch.empty(3, 8, 128, device="cuda") for _ in range(10)] for _ in range(2)]
+    scratch = [scratch_for(8, c) for _ in range(2)]
+    for q, w in zip(qs, want):
+        qmm.qmm_kv_attend(pages, q, lens, w, *scratch[0], 0.1)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for i in range(10):
+        for j, s in enumerate(streams):
+            qmm.qmm_kv_attend(pages, qs[j], lens, got[j][i], *scratch[j], 0.1, stream=s)
+    torch.cuda.synchronize()
+    for j in range(2):
+        for i in range(10):
+            assert torch.equal(got[j][i].view(torch.int32), want[j].view(torch.int32))
+
+
 def test_nan_query_stays_with_its_head():
     rng = np.random.default_rng(22)
     c = plain.Cache("q8", 1, 64, 16, 1, 50, seed=5)
@@ -455,5 +546,13 @@ def test_binding_refuses():
         qmm.qmm_kv_attend(pages, q, pos, x, s, n, 0.1)
     with pytest.raises(ValueError):
         qmm.qmm_kv_attend(pages, q, pos, q, s, n, 0.1, lse=torch.zeros(2, 3, device="cuda"))
+    with pytest.raises(ValueError):
+        qmm.qmm_kv_attend(pages, q, pos, torch.zeros_like(q), s[:-16], n, 0.1)
+    with pytest.raises(ValueError):
+        qmm.qmm_kv_store(pages, x, x, pos, q=q)
+    pages.device += 1
+    with pytest.raises(ValueError):
+        qmm.qmm_kv_attend(pages, q, pos, torch.zeros_like(q), s, n, 0.1)
+    pages.device -= 1
     with pytest.raises(qmm.QmmError):
         qmm.qmm_kv_attend(pages, q, pos, torch.zeros_like(q), s, n - 1, 0.1)
