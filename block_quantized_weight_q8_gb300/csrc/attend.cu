@@ -15,9 +15,11 @@
 //           f16 (hi + lo, 22 bits) and take two rows of the tile: rows 0-7 are
 //           the heads' hi, rows 8-15 their lo, and one thread holds both sums.
 //           Each is first brought near f16's upper end by a power of two (of a head's
-//           query; of the value scales so far), so that lo stays in f16's
-//           range; a weight below 2^-12 of the largest, with lo at f16's least step, is
-//           off by 2^-34 of the largest at most
+//           query; of the head's largest weight times scale in the tile), so that lo
+//           stays in f16's range; what is below 2^-12 of that largest, with lo at f16's
+//           least step, is off by 2^-39 of it at most.  The power is the tile's own: one
+//           kept from earlier tiles let a single large row without weight cost all later
+//           ones their low bits
 //   layout  the order of the 16 values within a step is free as long as both
 //           operands share it, so a lane takes its operand straight from 16-byte
 //           loads of natural rows, and a tile's scores are in the registers where
@@ -490,10 +492,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
         // Of head n: m_run, a whole number that no score so far is over by more than kSlack,
         // the sum of weights 2^(score - m_run) of this lane's positions, and the weighted
         // values.  The slack makes raising m_run rare; as it is whole, rescaling is exact.
-        // In the tensor cores weights up to 2^kSlack stand times 2^(10 - e_run), value scales
-        // are at most 2^(e_run + 1) = most: their product stays in f16.
-        float m_run = -INFINITY, l_run = 0.0f, up = 1024.0f, down = 1.0f / 1024.0f, most = INFINITY;
-        if (TYPE == QMM_KV_Q8) most = 0.0f;  // set by the first tile
+        float m_run = -INFINITY, l_run = 0.0f;
         float o[kSets][8][2];
 #pragma unroll
         for (int s = 0; s < kSets; s++)
@@ -578,8 +577,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
             issue(t + TEAM < tb, at1, by1, live1, true, turn(2));
             const uint32_t sv = ring_u + slot * S::kSlot;
             const float* vs = reinterpret_cast<const float*>(ring + slot * S::kSlot + TILE * ROW);
-            const float v_lane = TYPE == QMM_KV_Q8 && lane < TILE ? fabsf(vs[lane]) : 0.0f;
-            if (__any_sync(0xFFFFFFFFu, top > m_run + kSlack || v_lane > most)) {
+            if (__any_sync(0xFFFFFFFFu, top > m_run + kSlack)) {
                 const float m_new = top > m_run + kSlack ? ceilf(top) : m_run;
                 const float keep = exp2_approx(m_run - (m_new == -INFINITY ? 0.0f : m_new));
                 m_run = m_new;
@@ -588,24 +586,35 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
                 for (int s = 0; s < kSets; s++)
 #pragma unroll
                     for (int t2 = 0; t2 < 8; t2++) o[s][t2][0] *= keep, o[s][t2][1] *= keep;
-                const float v_max = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v_lane)));
-                if (TYPE == QMM_KV_Q8 && v_max > most) {
-                    const int e = exponent_of(v_max) - 127;
-                    up = pow2i(10 - e), down = pow2i(e - 10);
-                    most = e == 128 ? INFINITY : 2.0f * pow2i(e);
-                }
             }
             const float m_at = m_run == -INFINITY ? 0.0f : m_run;  // nothing seen yet: every weight is 0
-            uint32_t pf[TILE / 16][4];
+            float big = 0.0f;
 #pragma unroll
             for (int i = 0; i < kMine; i += 4) {
-                float4 v4 = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
-                if (TYPE == QMM_KV_Q8) v4 = *reinterpret_cast<const float4*>(vs + j * kMine + i);
                 const float w0 = exp2_approx(wt[i] - m_at), w1 = exp2_approx(wt[i + 1] - m_at);
                 const float w2 = exp2_approx(wt[i + 2] - m_at), w3 = exp2_approx(wt[i + 3] - m_at);
                 l_run += (w0 + w1) + (w2 + w3);
-                split_h2(w0 * (v4.x * up), w1 * (v4.y * up), &pf[i >> 2][0], &pf[i >> 2][1]);
-                split_h2(w2 * (v4.z * up), w3 * (v4.w * up), &pf[i >> 2][2], &pf[i >> 2][3]);
+                wt[i] = w0, wt[i + 1] = w1, wt[i + 2] = w2, wt[i + 3] = w3;
+                if (TYPE == QMM_KV_Q8) {
+                    const float4 v4 = *reinterpret_cast<const float4*>(vs + j * kMine + i);
+                    wt[i] *= v4.x, wt[i + 1] *= v4.y, wt[i + 2] *= v4.z, wt[i + 3] *= v4.w;
+                    big = fmaxf(big, fmaxf(fmaxf(fabsf(wt[i]), fabsf(wt[i + 1])), fmaxf(fabsf(wt[i + 2]), fabsf(wt[i + 3]))));
+                }
+            }
+            int e;  // the head's largest is below 2^(e + 1) (f16 rows: its weight, known from the score)
+            if (TYPE == QMM_KV_Q8) {
+                big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
+                big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
+                e = exponent_of(big) - 127;
+            } else {
+                e = max(__float2int_rd(top - m_at), kExpLow - 127);
+            }
+            const float up = pow2i(14 - e), down = pow2i(e - 14);
+            uint32_t pf[TILE / 16][4];
+#pragma unroll
+            for (int i = 0; i < kMine; i += 4) {
+                split_h2(wt[i] * up, wt[i + 1] * up, &pf[i >> 2][0], &pf[i >> 2][1]);
+                split_h2(wt[i + 2] * up, wt[i + 3] * up, &pf[i >> 2][2], &pf[i >> 2][3]);
             }
             // Values: column n of n-tile (set, t) is value 64 set + 8 n + t.  Fresh sums per
             // tile, added to the running ones by f32 FMAs: the tensor core's own additions cut
