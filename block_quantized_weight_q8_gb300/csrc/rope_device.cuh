@@ -28,8 +28,8 @@
 namespace qmm {
 
 constexpr int kTurnSteps = 256;
-struct TurnTable {
-    float v[kTurnSteps][4];  // cos hi, cos lo, sin hi, sin lo of k/256 turn
+struct alignas(16) TurnTable {  // an entry is read as one float4
+    float v[kTurnSteps][4];       // cos hi, cos lo, sin hi, sin lo of k/256 turn
 };
 constexpr double kPi = 3.14159265358979323846264338327950288;
 
