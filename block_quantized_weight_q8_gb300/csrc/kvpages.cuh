@@ -36,14 +36,6 @@ __device__ __forceinline__ int kv_page_of(const KvPages& c, int64_t seq, int64_t
     const int id = __ldg(c.table + seq * c.max_pages + pg);
     return (unsigned)id < (unsigned)c.num_pages ? id : -1;
 }
-// Byte offsets from the pool's start of row (page id, head h, position o) and of
-// its scale.
-__device__ __forceinline__ int64_t kv_row_at(const KvPages& c, int id, int h, int o) {
-    return id * c.stride + (int64_t)(((unsigned)h << c.page_shift) + o) * c.row_bytes;
-}
-__device__ __forceinline__ int64_t kv_scale_at(const KvPages& c, int id, int h, int o) {
-    return id * c.stride + c.scales + 4 * (int64_t)(((unsigned)h << c.page_shift) + o);
-}
 
 constexpr unsigned kErrPlace = 2u;  // a position without a page, a sequence outside the table
 
