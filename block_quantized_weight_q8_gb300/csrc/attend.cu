@@ -95,6 +95,7 @@ struct AttendArgs {
     int64_t R, ldq, ldo, window;
     int G, blocks;  // query heads per KV head, units per KV head
     uint32_t chunk, chunks;  // rows per chunk, at most kAttendThreads chunks
+    uint32_t runs;           // of the launch: two parts and two notes each in the workspace
     float scale;
 };
 
@@ -304,16 +305,18 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
     for (uint32_t i = blockIdx.x * kAttendWarps + warp; i < R; i += gridDim.x * kAttendWarps)
         if (row_of(i).len == 0) {
             for (int d = lane; d < Hq * (c.hd >> 2); d += 32)
-                reinterpret_cast<float4*>(a.out + i * a.ldo)[d] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (a.lse)
-                for (int h = lane; h < Hq; h += 32) a.lse[(int64_t)i * Hq + h] = -INFINITY;
+                if (QMM_IN_BOUNDS(g_attend_error, i * a.ldo + 4 * d + 3, a.R * a.ldo))
+                    reinterpret_cast<float4*>(a.out + i * a.ldo)[d] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int h = lane; a.lse && h < Hq; h += 32)
+                if (QMM_IN_BOUNDS(g_attend_error, (int64_t)i * Hq + h, a.R * Hq)) a.lse[(int64_t)i * Hq + h] = -INFINITY;
         }
 
     // The team's run, and the row r in which it begins.  joins: for the second kernel,
     // the unit that the run continues and the one that it leaves unfinished.
     const uint32_t run = TEAM == 1 ? blockIdx.x * kAttendWarps + warp : blockIdx.x;
     const int member = TEAM == 1 ? 0 : warp;
-    if (member == 0 && lane < 2) a.joins[2 * run + lane] = make_int4(0, 0, 0, 0);
+    if (member == 0 && lane < 2 && QMM_IN_BOUNDS(g_attend_error, 2 * run + lane, 2 * a.runs))
+        a.joins[2 * run + lane] = make_int4(0, 0, 0, 0);
     __syncwarp();
     if (total == 0) return;
     const Runs<TEAM> runs(total * units, gridDim.x * (kAttendWarps / TEAM));
@@ -379,7 +382,9 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
         int look = lane < TILE ? (tile0 + ta + member) * TILE + lane - x.first : -(1 << 30) - 4096;
         // the page there as the table has it; -1: no position
         auto page_at = [&](int at) -> int {
-            return (unsigned)at < span ? __ldg(pages + ((at + x.first) >> c.page_shift)) : -1;
+            if ((unsigned)at >= span) return -1;
+            const int pg = (at + x.first) >> c.page_shift;
+            return QMM_IN_BOUNDS(g_attend_error, x.seq * c.max_pages + pg, c.num_seqs * c.max_pages) ? __ldg(pages + pg) : -1;
         };
         // its row in the pools, from their start; -1: none
         const int64_t head_at = (int64_t)(kvh << c.page_shift) * c.row_bytes;
@@ -467,7 +472,8 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
         if (!whole && member == 0 && lane == 0) {
             const uint32_t g0 = row_start + u * weight + kCost;  // the unit's first tile
             const uint32_t c0 = ta == 0 ? run : runs.of(g0), c1 = tb == (int)tiles ? run : runs.of(g0 + tiles - 1);
-            a.joins[2 * run + (ta == 0 ? 1 : 0)] = make_int4((int)r, (int)u, (int)c0, (int)(c1 - c0 + 1));
+            const uint32_t to = 2 * run + (ta == 0 ? 1 : 0);
+            if (QMM_IN_BOUNDS(g_attend_error, to, 2 * a.runs)) a.joins[to] = make_int4((int)r, (int)u, (int)c0, (int)(c1 - c0 + 1));
         }
 
         uint32_t qf[kSteps][4];
@@ -672,19 +678,25 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
         cp_async_wait<0>();
         l_run += __shfl_xor_sync(0xFFFFFFFFu, l_run, 1);
         l_run += __shfl_xor_sync(0xFFFFFFFFu, l_run, 2);
-        float* part = a.parts + (2 * (int64_t)run + (ta == 0 ? 1 : 0)) * (kAttendHeads * (c.hd + 2));
+        const int64_t part_at = (2 * (int64_t)run + (ta == 0 ? 1 : 0)) * (kAttendHeads * (c.hd + 2));
+        [[maybe_unused]] const int64_t parts_end = 2 * (int64_t)a.runs * (kAttendHeads * (c.hd + 2));
+        float* part = a.parts + part_at;
         float* out = a.out + r * a.ldo + (int64_t)head0 * c.hd;
         auto put_ml = [&](int h, float m, float l) {
             if (!whole) {
+                if (!QMM_IN_BOUNDS(g_attend_error, part_at + kAttendHeads * (c.hd + 1) + h, parts_end)) return;
                 part[kAttendHeads * c.hd + h] = m, part[kAttendHeads * (c.hd + 1) + h] = l;
             } else if (a.lse && QMM_IN_BOUNDS(g_attend_error, r * Hq + head0 + h, a.R * Hq)) {
                 a.lse[(int64_t)r * Hq + head0 + h] = (m + log2f(l)) * 0.693147180559945309f;
             }
         };
         auto put = [&](int h, int d, float4 y) {
-            if (!whole) *reinterpret_cast<float4*>(part + h * c.hd + d) = y;
-            else if (QMM_IN_BOUNDS(g_attend_error, r * a.ldo + (int64_t)(head0 + h) * c.hd + d + 3, a.R * a.ldo))
+            if (!whole) {
+                if (QMM_IN_BOUNDS(g_attend_error, part_at + h * c.hd + d + 3, parts_end))
+                    *reinterpret_cast<float4*>(part + h * c.hd + d) = y;
+            } else if (QMM_IN_BOUNDS(g_attend_error, r * a.ldo + (int64_t)(head0 + h) * c.hd + d + 3, a.R * a.ldo)) {
                 *reinterpret_cast<float4*>(out + h * c.hd + d) = y;
+            }
         };
         if (TEAM == 1) {
             const float by = !whole ? 1.0f : (l_run == 0.0f ? 0.0f : __fdiv_rn(1.0f, l_run));
@@ -773,6 +785,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(KvPages c, At
     pdl_wait();
     pdl_launch_dependents();
     const int Hq = a.G * c.Hkv, size = kAttendHeads * (c.hd + 2), per_head = (c.hd + 31) >> 5;
+    if (!QMM_IN_BOUNDS(g_attend_error, blockIdx.x, a.runs)) return;
     const int4 jobs[2] = {a.joins[2 * blockIdx.x], a.joins[2 * blockIdx.x + 1]};
     if (jobs[0].w == 0 && jobs[1].w == 0) return;
     auto unit_of = [&](const int4& job) {
@@ -785,13 +798,16 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(KvPages c, At
     };
     // the unit begins in its first run, the others continue it
     auto part = [&](const JoinUnit& x, int i) -> const float* {
-        return x.parts + (2 * i + (i == 0 ? 1 : 0)) * (int64_t)size;
+        const float* p = x.parts + (2 * i + (i == 0 ? 1 : 0)) * (int64_t)size;
+        return QMM_IN_BOUNDS(g_attend_error, p - a.parts + size - 1, 2 * (int64_t)a.runs * size) ? p : a.parts;
     };
     auto put = [&](const JoinUnit& x, int h, int d, float4 y, float m, float l) {
         const float by = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
-        float* out = a.out + x.row * a.ldo + (int64_t)(x.head0 + h) * c.hd + d;
-        *reinterpret_cast<float4*>(out) = make_float4(y.x * by, y.y * by, y.z * by, y.w * by);
-        if (a.lse && d == 0) a.lse[(int64_t)x.row * Hq + x.head0 + h] = (m + log2f(l)) * 0.693147180559945309f;
+        const int64_t to = x.row * a.ldo + (int64_t)(x.head0 + h) * c.hd + d, lse_to = (int64_t)x.row * Hq + x.head0 + h;
+        if (QMM_IN_BOUNDS(g_attend_error, to + 3, a.R * a.ldo))
+            *reinterpret_cast<float4*>(a.out + to) = make_float4(y.x * by, y.y * by, y.z * by, y.w * by);
+        if (a.lse && d == 0 && QMM_IN_BOUNDS(g_attend_error, lse_to, a.R * Hq))
+            a.lse[lse_to] = (m + log2f(l)) * 0.693147180559945309f;
     };
     auto add = [](float4& y, float& l, const float4& z, float pl, float f) {
         l = __fmaf_rn(pl, f, l);
@@ -936,7 +952,6 @@ qmm_status qmm_kv_attend(const qmm_kv_pages* cache, const float* q, int64_t ldq,
     if (st != QMM_OK) return st;
     const cudaStream_t cs = (cudaStream_t)stream;
     const bool ctas = R * c.Hkv * blocks <= kTeamUnits;
-    int runs = 0;
     auto go = [&](auto type, auto hdt, auto team) -> qmm_status {
         constexpr int TYPE = decltype(type)::value, HDT = decltype(hdt)::value, TEAM = decltype(team)::value;
         using S = AttendShape<TYPE, HDT>;
@@ -946,7 +961,7 @@ qmm_status qmm_kv_attend(const qmm_kv_pages* cache, const float* q, int64_t ldq,
                                         S::kSmem) == cudaSuccess ? QMM_OK : QMM_E_CUDA;
         });
         if (set != QMM_OK) return set;
-        runs = S::kCtas * kAttendSms * (kAttendWarps / TEAM);
+        a.runs = S::kCtas * kAttendSms * (kAttendWarps / TEAM);
         return launch_pdl(attend_kernel<TYPE, HDT, TEAM>, dim3((unsigned)(S::kCtas * kAttendSms)), kAttendThreads,
                           S::kSmem, cs, c, a);
     };
@@ -962,7 +977,7 @@ qmm_status qmm_kv_attend(const qmm_kv_pages* cache, const float* q, int64_t ldq,
     st = cache->type == QMM_KV_Q8 ? by_width(integral_constant<int, QMM_KV_Q8>())
                                   : by_width(integral_constant<int, QMM_KV_F16>());
     if (st != QMM_OK) return st;
-    return launch_pdl(attend_join_kernel, dim3((unsigned)runs), kJoinThreads, 0, cs, c, a);
+    return launch_pdl(attend_join_kernel, dim3(a.runs), kJoinThreads, 0, cs, c, a);
 }
 
 }  // extern "C"

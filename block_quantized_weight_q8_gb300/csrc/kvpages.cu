@@ -181,7 +181,9 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas) rows_kernel(KvPages c, 
                             *reinterpret_cast<uint32_t*>(pool + at + share.first) = w0;
                             *reinterpret_cast<uint32_t*>(pool + at + share.second) = w1;
                         }
-                        if (o == 0) *reinterpret_cast<float*>(pool_scale + p.page + 4 * p.o) = __fdiv_rn(amax, 127.0f);
+                        if (o == 0 && QMM_IN_BOUNDS(g_pages_error, p.page + c.scales + 4 * ((int64_t)(h << c.page_shift) + p.o) + 3,
+                                                    c.num_pages * c.stride))
+                            *reinterpret_cast<float*>(pool_scale + p.page + 4 * p.o) = __fdiv_rn(amax, 127.0f);
                     } else {
                         __half* to = reinterpret_cast<__half*>(pool + at);
                         if (PAIRS == kPairsScattered) {
@@ -317,6 +319,8 @@ __global__ void __launch_bounds__(kLoadThreads, kLoadCtas)
                 if (!QMM_IN_BOUNDS(g_pages_error, at + (int64_t)head * c.row_bytes + kQuad * quad + kQuad - 1,
                                    c.num_pages * c.stride))
                     at = 0;
+                if (TYPE == QMM_KV_Q8 && !QMM_IN_BOUNDS(g_pages_error, sat + c.scales + 4 * (int64_t)head + 3, c.num_pages * c.stride))
+                    sat = 0;
                 if (TYPE == QMM_KV_Q8) {
                     w[u].x = ld_here(reinterpret_cast<const uint32_t*>(pool + at));
                     d[u] = __uint_as_float(ld_here(reinterpret_cast<const uint32_t*>(scales + sat)));
