@@ -961,9 +961,14 @@ qmm_status qmm_kv_attend(const qmm_kv_pages* cache, const float* q, int64_t ldq,
                                         S::kSmem) == cudaSuccess ? QMM_OK : QMM_E_CUDA;
         });
         if (set != QMM_OK) return set;
-        a.runs = S::kCtas * kAttendSms * (kAttendWarps / TEAM);
-        return launch_pdl(attend_kernel<TYPE, HDT, TEAM>, dim3((unsigned)(S::kCtas * kAttendSms)), kAttendThreads,
-                          S::kSmem, cs, c, a);
+        // no more CTAs than the runs of rows that fill the table's room (or the window): the list
+        // of any lengths is cut the same, and fewer are started
+        constexpr int kRuns = kAttendWarps / TEAM;  // of a CTA
+        const int64_t tiles = window > 0 && window < room ? (window - 1) / S::kTile + 2 : (room - 1) / S::kTile + 1;
+        const int64_t most = (R * c.Hkv * blocks * (tiles + unit_cost(TEAM)) / TEAM + kRuns - 1) / kRuns;
+        const unsigned grid = (unsigned)(most < S::kCtas * kAttendSms ? most : S::kCtas * kAttendSms);
+        a.runs = grid * kRuns;
+        return launch_pdl(attend_kernel<TYPE, HDT, TEAM>, dim3(grid), kAttendThreads, S::kSmem, cs, c, a);
     };
     using std::integral_constant;
     auto by_team = [&](auto type, auto hdt) -> qmm_status {
