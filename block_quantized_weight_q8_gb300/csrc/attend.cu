@@ -229,6 +229,12 @@ __device__ __forceinline__ void split_h2(float x, float y, uint32_t* hi, uint32_
     *hi = *reinterpret_cast<const uint32_t*>(&h);
     *lo = pack_h2(x - f.x, y - f.y);
 }
+// The sum of a hi and a lo row.  An infinity in an f16 row makes the lo row's sum a NaN (0
+// or the other sign times it), where the hi row's is the definition's.
+template <int TYPE>
+__device__ __forceinline__ float add_rows(float hi, float lo) {
+    return TYPE == QMM_KV_F16 && fabsf(hi) == INFINITY ? hi : hi + lo;
+}
 // biased bytes (code + 128) sel of w as two f16: 1024 + byte, less 1152
 __device__ __forceinline__ uint32_t codes_h2(uint32_t w, uint32_t sel) {
     const uint32_t b = __byte_perm(w, 0x64646464u, sel);
@@ -557,13 +563,13 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
             for (int i = 0; i < kMine; i += 4) {
                 const float* y0 = sc[i >> 1][0];
                 const float* y1 = sc[(i >> 1) + 1][0];
-                wt[i] = y0[0] + y0[2], wt[i + 1] = y0[1] + y0[3];
-                wt[i + 2] = y1[0] + y1[2], wt[i + 3] = y1[1] + y1[3];
+                wt[i] = add_rows<TYPE>(y0[0], y0[2]), wt[i + 1] = add_rows<TYPE>(y0[1], y0[3]);
+                wt[i + 2] = add_rows<TYPE>(y1[0], y1[2]), wt[i + 3] = add_rows<TYPE>(y1[1], y1[3]);
                 if (kChains == 2) {
                     const float* z0 = sc[i >> 1][kChains - 1];
                     const float* z1 = sc[(i >> 1) + 1][kChains - 1];
-                    wt[i] += z0[0] + z0[2], wt[i + 1] += z0[1] + z0[3];
-                    wt[i + 2] += z1[0] + z1[2], wt[i + 3] += z1[1] + z1[3];
+                    wt[i] += add_rows<TYPE>(z0[0], z0[2]), wt[i + 1] += add_rows<TYPE>(z0[1], z0[3]);
+                    wt[i + 2] += add_rows<TYPE>(z1[0], z1[2]), wt[i + 3] += add_rows<TYPE>(z1[1], z1[3]);
                 }
                 if (TYPE == QMM_KV_Q8) {
                     const float4 ks = *reinterpret_cast<const float4*>(tail + 4 * (j * kMine + i));
@@ -675,7 +681,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
                 for (int t2 = 0; t2 < 8; t2++)
 #pragma unroll
                     for (int i = 0; i < 2; i++)
-                        o[s][t2][i] = __fmaf_rn(acc[t2][i] + acc[t2][i + 2], down, o[s][t2][i]);
+                        o[s][t2][i] = __fmaf_rn(add_rows<TYPE>(acc[t2][i], acc[t2][i + 2]), down, o[s][t2][i]);
             }
             slot = turn(1);
         }
