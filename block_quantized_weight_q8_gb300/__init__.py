@@ -457,13 +457,18 @@ def qmm_kv_page_bytes(type, Hkv, page_size, hd):
 def qmm_kv_store(pages, k, v, pos, seq=None, rope=None, q=None, q_out=None, stream=None):
     """Stores keys k and values v ([T][Hkv][hd] f32) at positions pos of the sequences seq; with rope, keys are rotated
     first, and queries q ([T][Hq][hd]) into q_out."""
-    dev, T, Hkv, hd = _device(), k.shape[0], pages.Hkv, pages.hd
+    dev, Hkv, hd = _device(), pages.Hkv, pages.hd
+    if k.dim() != 3:
+        _refuse("k", k, "float32", ("T", Hkv, hd), dev)
+    T = k.shape[0]
     pk, ldk = _heads("k", k, dev, T, Hkv, hd)
     pv, ldv = _heads("v", v, dev, T, Hkv, hd)
     pq = ldq = po = ldo = Hq = 0
     if q is not None:
         if q_out is None or rope is None:
             raise ValueError("queries need q_out and rope")
+        if q.dim() != 3:
+            _refuse("q", q, "float32", (T, "Hq", hd), dev)
         Hq = q.shape[1]
         pq, ldq = _heads("q", q, dev, T, Hq, hd)
         po, ldo = _heads("q_out", q_out, dev, T, Hq, hd)
@@ -474,7 +479,10 @@ def qmm_kv_store(pages, k, v, pos, seq=None, rope=None, q=None, q_out=None, stre
 
 def qmm_kv_load(pages, pos, k_out=None, v_out=None, seq=None, stream=None):
     """The rows at positions pos of the sequences seq as f32 ([T][Hkv][hd]); either output may be None."""
-    dev, T, Hkv, hd = _device(), pos.shape[0], pages.Hkv, pages.hd
+    dev, Hkv, hd = _device(), pages.Hkv, pages.hd
+    if pos.dim() != 1:
+        _refuse("pos", pos, "int32", ("T",), dev)
+    T = pos.shape[0]
     pk, ldk = _heads("k_out", k_out, dev, T, Hkv, hd) if k_out is not None else (None, 0)
     pv, ldv = _heads("v_out", v_out, dev, T, Hkv, hd) if v_out is not None else (None, 0)
     _call("qmm_kv_load", _ref("pages", pages, dev), _ints("pos", pos, dev, T), _ints("seq", seq, dev, T), T, pk, ldk, pv, ldv,
@@ -488,7 +496,10 @@ def qmm_kv_attend_scratch_bytes(Hq, Hkv, hd):
 def qmm_kv_attend(pages, q, lens, out, scratch, scratch_bytes, scale, lse=None, seq=None, window=0, stream=None):
     """out[r] = the attention of query heads q[r] ([R][Hq][hd] f32) over the first lens[r] positions (the last window
     of them) of their sequences; lse ([R][Hq] f32) the log of the softmax's sum."""
-    dev, R, Hq, hd = _device(), q.shape[0], q.shape[1], pages.hd
+    dev, hd = _device(), pages.hd
+    if q.dim() != 3:
+        _refuse("q", q, "float32", ("R", "Hq", hd), dev)
+    R, Hq = q.shape[:2]
     pq, ldq = _heads("q", q, dev, R, Hq, hd)
     po, ldo = _heads("out", out, dev, R, Hq, hd)
     pl = None
