@@ -55,7 +55,6 @@ constexpr int kAttendWarps = 4;
 constexpr int kAttendThreads = 32 * kAttendWarps;
 constexpr int kAttendSms = 152;
 constexpr int kAttendHeads = 8;  // query heads per unit
-constexpr int kAttendMaxRuns = 4 * kAttendSms * kAttendWarps;
 constexpr int kJoinThreads = 128;
 constexpr int kJoinFew = 8;  // parts that one CTA joins for all heads
 // Up to so many units, a team is a CTA (the first tokens of one request: 5.7 us, a single
@@ -83,6 +82,15 @@ struct AttendShape {
     // fourth slot too).
     static constexpr int kCtas = kRow <= 64 ? 4 : 2;
 };
+
+// Runs at most, of single warps: what the workspace has room for.  Rows of more than 64
+// bytes, which 8-bit heads over 64 and all 16-bit ones have, get half as many.
+inline int64_t attend_max_runs(int64_t hd) {
+    static_assert(AttendShape<QMM_KV_Q8, 64>::kCtas == 4 && AttendShape<QMM_KV_F16, 64>::kCtas == 2 &&
+                  AttendShape<QMM_KV_Q8, 128>::kCtas == 2 && AttendShape<QMM_KV_F16, 128>::kCtas == 2 &&
+                  AttendShape<QMM_KV_Q8, 256>::kCtas == 2 && AttendShape<QMM_KV_F16, 256>::kCtas == 2, "CTAs per SM");
+    return (hd <= 64 ? 4 : 2) * kAttendSms * kAttendWarps;
+}
 
 struct AttendArgs {
     const float* q;
@@ -928,7 +936,7 @@ unsigned qmm_internal_attend_error(int clear) {
 
 size_t qmm_kv_attend_scratch_bytes(int64_t Hq, int64_t Hkv, int64_t hd) {
     if (!head_dim_ok(hd) || Hkv < 1 || Hkv > 1024 || Hq < 1 || Hq % Hkv || Hq / Hkv > 64) return 0;
-    return (size_t)kAttendMaxRuns * 2 * (kAttendHeads * (size_t)(hd + 2) * sizeof(float) + sizeof(int4));
+    return (size_t)attend_max_runs(hd) * 2 * (kAttendHeads * (size_t)(hd + 2) * sizeof(float) + sizeof(int4));
 }
 
 qmm_status qmm_kv_attend(const qmm_kv_pages* cache, const float* q, int64_t ldq, const int32_t* lens,
@@ -953,7 +961,7 @@ qmm_status qmm_kv_attend(const qmm_kv_pages* cache, const float* q, int64_t ldq,
     AttendArgs a;
     a.q = q, a.lens = lens, a.seq = seq, a.out = out, a.lse = lse;
     a.joins = (int4*)scratch;
-    a.parts = (float*)(a.joins + 2 * kAttendMaxRuns);
+    a.parts = (float*)(a.joins + 2 * attend_max_runs(c.hd));
     a.R = R, a.ldq = ldq, a.ldo = ldo, a.window = window;
     a.G = (int)(Hq / c.Hkv);
     a.blocks = (int)blocks;
