@@ -499,7 +499,7 @@ def qmm_kv_attend(pages, q, lens, out, scratch, scratch_bytes, scale, lse=None, 
     dev, hd = _device(), pages.hd
     if q.dim() != 3:
         _refuse("q", q, "float32", ("R", "Hq", hd), dev)
-    R, Hq = q.shape[:2]
+    R, Hq, _ = q.shape
     pq, ldq = _heads("q", q, dev, R, Hq, hd)
     po, ldo = _heads("out", out, dev, R, Hq, hd)
     pl = None
