@@ -789,10 +789,10 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<TYPE, HDT>::kCtas)
 // left unfinished (a.joins: row, unit, first run, number of runs).  Up to kJoinFew parts
 // are joined by the first run's CTA, a thread per four values; the values of a unit in
 // more parts are shared out among its runs' CTAs, 32 values at a time, with 4 threads
-// side by side over the parts and four such pieces in hand at once (16 and one, where
-// there is a single piece or more than kJoinMany parts).  The order of the sums depends
-// on the runs alone.
-constexpr int kJoinMany = 64;
+// side by side over the parts and four such pieces in hand at once (one at a time: 66.6 us
+// instead of 64 for the two long rows above, 71 instead of 70 for the ragged ones), or 16
+// threads where there is a single piece, as for a unit in more parts than it has pieces.
+// The order of the sums depends on the runs alone.
 struct JoinUnit {
     const float* parts;
     int n, row, head0, heads;
@@ -870,8 +870,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(KvPages c, At
             pieces[k] = first < all ? (int)quick_div(all - first - 1, job.w) + 1 : 0;
         }
     }
-    const bool many = jobs[0].w > kJoinMany || jobs[1].w > kJoinMany || pieces[0] + pieces[1] == 1;
-    const int lg = many ? 4 : 2, side = 1 << lg, q = threadIdx.x & 7, at = threadIdx.x >> 3, s = at & (side - 1);
+    const int lg = pieces[0] + pieces[1] == 1 ? 4 : 2, side = 1 << lg, q = threadIdx.x & 7, at = threadIdx.x >> 3, s = at & (side - 1);
     const int slots = kLanes >> lg;
     for (int e0 = 0; e0 < pieces[0] + pieces[1]; e0 += slots) {
         const int e = e0 + (at >> lg);
