@@ -42,7 +42,11 @@
 // Measured (32 query heads on 8 KV heads of 128, 8-bit): 64 rows of up to 8192
 // positions, 380 MB, 70 us = 5.4 TB/s; two rows of 131072 and 32768 (64 query heads),
 // 346 MB, 64 us, of which the same copies without any arithmetic take 54, the start
-// (lengths, pages, first copies, one after the other) 3.6 and the join 2 to 4.
+// (lengths, pages, first copies, one after the other) 3.6 and the join 2 to 4.  Nine to
+// 16 query heads per KV head are two units that copy and convert the same rows: 125 us
+// and 677 MB for the 64 rows with 128 query heads, 72 us and 380 MB with 64.  Rows that do
+// not fill 64, 128 or 256 values, and pages of fewer than 16 positions, take the slower
+// copies: 91 us for the 64 rows with heads of 80, 96 or 112, or with pages of 8.
 #include <type_traits>
 
 #include "kvpages.cuh"
@@ -57,10 +61,10 @@ constexpr int kAttendSms = 152;
 constexpr int kAttendHeads = 8;  // query heads per unit
 constexpr int kJoinThreads = 128;
 constexpr int kJoinFew = 8;  // parts that one CTA joins for all heads
-// Up to so many units, a team is a CTA (the first tokens of one request: 5.7 us, a single
-// warp per unit 7.2; a row of 4096 positions 8.7 and 9.7); with more, a warp (1000 rows
-// of 40 positions, 8 units each: 220 us by CTAs, 47 by warps; 64 ragged rows, 512 units:
-// 74 and 71).
+// Up to so many units, a team is a CTA (the first tokens of one request: 4.9 us, a single
+// warp per unit 6.3; a row of 4096 positions 8.7 and 9.6); with more, a warp (1000 rows
+// of 40 positions, 8 units each: 104 us by CTAs, 48 by warps; 64 ragged rows, 512 units:
+// 72 and 70).
 constexpr int64_t kTeamUnits = 152;
 // what a unit costs a team besides its tiles, in tiles
 __host__ __device__ constexpr uint32_t unit_cost(int team) { return team == 1 ? 2 : 12; }
@@ -76,10 +80,12 @@ struct AttendShape {
     static constexpr int kSlot = kTile * kRow + 4 * kTile + 16;
     static constexpr int kRing = kSlots * kSlot;  // of a warp
     static constexpr int kSmem = kAttendWarps * kRing;
-    // CTAs per SM such that about 68 KB are on their way: more queue up in the memory
-    // system, which then serves the SMs unevenly (two rows of 131072 and 64 ragged ones:
-    // 67 and 74 us with 2 CTAs of 128-byte rows, 72 and 75 with 3, 74 and 81 with a
-    // fourth slot too).
+    // CTAs per SM such that about 68 KB are on their way for rows of up to 256 bytes: more
+    // queue up in the memory system, which then serves the SMs unevenly (two rows of 131072
+    // and 64 ragged ones of 128-byte rows: 63.5 and 70.0 us; with a third CTA 75.7 and 82.1,
+    // with a fourth slot 63.7 and 71.3).  512-byte rows have 132 KB on their way, but with a
+    // single CTA four warps cannot keep up (a window of 1024: 52 us instead of 47; 60000
+    // positions 92 instead of 85).
     static constexpr int kCtas = kRow <= 64 ? 4 : 2;
 };
 

@@ -10,11 +10,13 @@
 //   kv_load   four values a thread, its column of each token in turn: 4 (8) bytes of
 //             codes in, 16 bytes out
 // The 8-bit rule is qmm_kv_quantize's, step by step.  The load is bound by memory: 32768
-// positions of 8 x 128 in 61 us, 5.5 TB/s.  So is a rotation alone (4096 x 32 x 128 in
-// 25.6 us, 5.2 TB/s; a bare product of the same size takes 21.4).  The store is bound by
-// issue, at 68% of the slots: of about 320 instructions for 8 values of a warp's lanes
+// positions of 8 x 128 in 61 us, 5.5 TB/s (16-bit rows 72 us, 5.6 TB/s).  So is a rotation
+// alone (4096 x 32 x 128 in 25.8 us, 5.2 TB/s; a bare product of the same size takes 21.4).
+// The store fills neither the issue slots (67%) nor the memory's rate (28%): a thread has
+// one token ahead in flight, and of about 320 instructions for 8 values of a warp's lanes
 // half are the rotation's pairs and a quarter the quantizing (8192 tokens of 8 + 8 rows
-// of 128 in 27 us; 19 without the rotation, 12.6 at the memory's rate).
+// of 128 in 27 us; 17 without the rotation, 12.6 at the memory's rate; 16-bit rows 22 and
+// 19.5, 15 at the memory's rate).
 #include <type_traits>
 
 #include "kvpages.cuh"

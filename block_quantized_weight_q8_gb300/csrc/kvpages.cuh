@@ -1,5 +1,5 @@
 // kvpages.cuh -- the paged key-value cache: its description as the kernels take
-// it, the host's checks of it, and the address of a position's row.
+// it, the host's checks of it, and the page of a position.
 //
 // A page holds page_size positions (a power of two) of every KV head.  Codes come
 // first, head by head: row (head h, position o) at (h * page_size + o) * row_bytes,

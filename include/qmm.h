@@ -539,8 +539,8 @@ QMM_API qmm_status qmm_kv_load(const qmm_kv_pages* cache, const int32_t* pos, co
 /* out[r][h] = sum_p w_p v_p, w = softmax over p of scale * (q[r][h] . k_p), p the
  * positions 0..lens[r] - 1 of row r's sequence (its last `window` of them where
  * window > 0), the KV head h / (Hq / Hkv); lse[r][h] (f32, may be NULL) the log of
- * the softmax's sum, natural, with its maximum.  q and out f32 [R][Hq][hd], lens
- * int32 [R], device.  lens[r] = 0 gives zeros and -inf; lens[r] < 0 is a padding
+ * the softmax's sum, natural, with its maximum.  q and out f32 [R][Hq][hd] (apart
+ * from each other in memory), lens int32 [R], device.  lens[r] = 0 gives zeros and -inf; lens[r] < 0 is a padding
  * row, which is left as it was; a length beyond max_pages * page_size is cut there
  * (status as above).  Several rows may read one sequence (tokens of one step
  * checked at their own lengths).  Hq a multiple of Hkv, Hq / Hkv <= 64.
