@@ -544,9 +544,9 @@ QMM_API qmm_status qmm_kv_load(const qmm_kv_pages* cache, const int32_t* pos, co
  * row, which is left as it was; a length beyond max_pages * page_size is cut there
  * (status as above).  Several rows may read one sequence (tokens of one step
  * checked at their own lengths).  Hq a multiple of Hkv, Hq / Hkv <= 64.
- * q and the weights (for Q8 times the value scales) are split into two f16 (22 bits; of
- * what is far below the largest among its 16 or 32 neighbouring positions, to 2^-39 of
- * that), sums and the softmax in f32.
+ * q and the weights (for Q8 times the value scales) are split into two f16: 22 bits, or
+ * 2^-39 of the largest among the 16 or 32 neighbouring positions where that is more.
+ * Sums and the softmax are f32.
  * A table's room, max_pages * page_size, is 2^30 positions at most, and the tiles of
  * 16 positions that R rows of that room (or of the window) could have, over all KV
  * heads and eights of their query heads, are fewer than 2^31.
