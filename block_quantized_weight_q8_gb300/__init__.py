@@ -4,8 +4,8 @@ Argument marshalling only: every function here has the name of the C entry
 point it calls, converts tensors to device pointers and the current torch
 stream to a cudaStream_t, and raises QmmError on a non-OK status.  All
 arithmetic runs in the CUDA kernels of libqmm.so; there is no other path.
-Tensors may be torch CUDA tensors or raw integer device addresses; the rotary
-and paged-cache calls take tensors only, read the sizes from them and raise
+Tensors may be torch CUDA tensors or raw integer device addresses; the rotary,
+paged-cache and mixture-of-experts calls take tensors only, read the sizes from them and raise
 ValueError for one of another type, shape, layout or device.
 """
 from __future__ import annotations
@@ -80,6 +80,11 @@ SIGNATURES = {
     "qmm_kv_load": ("pppipipiq", ctypes.c_int),
     "qmm_kv_attend_scratch_bytes": ("iii", ctypes.c_size_t),
     "qmm_kv_attend": ("ppipppippsiifiq", ctypes.c_int),
+    "qmm_add_rmsnorm_quantize": ("tppppfppiiq", ctypes.c_int),
+    "qmm_route": ("ppipppiiq", ctypes.c_int),
+    "qmm_experts_scratch_bytes": ("tiiiii", ctypes.c_size_t),
+    "qmm_experts_glu": ("ttppppppsiiiiiq", ctypes.c_int),
+    "qmm_experts_sum": ("tppppppps" + "iiiiiq", ctypes.c_int),
     "qmm_matmul_q4_K": ("pppiiiq", ctypes.c_int),
     "qmm_matmul_q6_K": ("pppiiiq", ctypes.c_int),
     "qmm_matmul_q5_K": ("pppiiiq", ctypes.c_int),
@@ -512,6 +517,102 @@ def qmm_kv_attend(pages, q, lens, out, scratch, scratch_bytes, scale, lse=None, 
         _refuse("scratch", scratch, "memory", "of %d bytes" % scratch_bytes, dev)
     _call("qmm_kv_attend", _ref("pages", pages, dev), pq, ldq, _ints("lens", lens, dev, R), _ints("seq", seq, dev, R), po, ldo,
           pl, scratch.data_ptr(), scratch_bytes, R, Hq, scale, window,
+          _raw_stream(dev) if stream is None else stream_handle(stream))
+
+
+# ---- mixture of experts
+ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
+GLU_KINDS = {"silu": 0, "gelu": 1}
+
+
+class RouteSpec(ctypes.Structure):
+    """qmm_route_spec: how tokens choose their experts."""
+    _fields_ = [("score", ctypes.c_int32), ("k", ctypes.c_int32), ("groups", ctypes.c_int32), ("groups_kept", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("renorm", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+def _whole(name, t, dev, dtype, shape):
+    """The address of a contiguous tensor of this type and shape (None for None)."""
+    if t is None:
+        return None
+    if t.dtype is not getattr(_torch, dtype) or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        _refuse(name, t, dtype, shape, dev)
+    return t.data_ptr()
+
+
+def _workspace(t, size, dev):
+    if t.get_device() != dev or t.nbytes < size or not t.is_contiguous():
+        _refuse("scratch", t, "memory", "of %d bytes" % size, dev)
+    return t.data_ptr()
+
+
+def qmm_add_rmsnorm_quantize(act, x, r, w, eps, xq=None, sum=None, h=None, stream=None):
+    """sum = x + r, h = its RMSNorm with the weight w, xq = h quantized to act ("q8_0" or "q8_K"); x and r f32 [M][K], xq
+    uint8 [M][qmm_row_bytes(act, K)]; sum (may be x or r) and one of h and xq may be None."""
+    dev = _device()
+    if x.dim() != 2:
+        _refuse("x", x, "float32", ("M", "K"), dev)
+    rows = M, K = x.shape
+    _call("qmm_add_rmsnorm_quantize", _type(act), _whole("x", x, dev, "float32", rows), _whole("r", r, dev, "float32", rows),
+          _whole("sum", sum, dev, "float32", rows), _whole("w", w, dev, "float32", (K,)), eps,
+          _whole("h", h, dev, "float32", rows), _whole("xq", xq, dev, "uint8", (M, qmm_row_bytes(act, K))), M, K,
+          _raw_stream(dev) if stream is None else stream_handle(stream))
+
+
+def qmm_route(logits, ids, weights, score="softmax", bias=None, groups=1, groups_kept=1, group_top=1, renorm=True, scale=1.0,
+              stream=None):
+    """ids and weights ([T][k], int32 and f32): the experts that each token's logits ([T][E] f32, rows any stride apart)
+    choose, and what they weigh (see include/qmm.h)."""
+    dev = _device()
+    if logits.dtype is not _torch.float32 or logits.get_device() != dev or logits.dim() != 2 or (
+            logits.stride(1) != 1 and logits.shape[1] > 1):
+        _refuse("logits", logits, "float32", ("T", "E"), dev)
+    T, E = logits.shape
+    if ids.dim() != 2:
+        _refuse("ids", ids, "int32", (T, "k"), dev)
+    k = ids.shape[1]
+    spec = RouteSpec(ROUTE_SCORES[score], k, groups, groups_kept, group_top, 1 if renorm else 0, scale)
+    _call("qmm_route", ctypes.addressof(spec), logits.data_ptr(), logits.stride(0) if T > 1 else E,
+          _whole("bias", bias, dev, "float32", (E,)), _whole("ids", ids, dev, "int32", (T, k)),
+          _whole("weights", weights, dev, "float32", (T, k)), T, E,
+          _raw_stream(dev) if stream is None else stream_handle(stream))
+
+
+def qmm_experts_scratch_bytes(wtype, T, k, E, N, K):
+    return int(load().qmm_experts_scratch_bytes(_type(wtype), int(T), int(k), int(E), int(N), int(K)))
+
+
+def qmm_experts_glu(wtype, Wg, Wu, xq, ids, h, scratch, scratch_bytes, gate="silu", stream=None):
+    """h[t][j] = gate(Wg[e] x_t) * (Wu[e] x_t), e = ids[t][j]: h f32 [T][k][N], Wg and Wu uint8 [E][N][row bytes], xq uint8
+    [T][qmm_row_bytes(qmm_act_type(wtype), K)], ids int32 [T][k] (negative: no expert, zeros)."""
+    dev, wt = _device(), _type(wtype)
+    if h.dim() != 3 or Wg.dim() != 3:
+        _refuse("h, Wg", h if h.dim() != 3 else Wg, "float32, uint8", "of 3 dimensions", dev)
+    T, k, N = h.shape
+    matrix = E, _, row = Wg.shape
+    size = qmm_block_bytes(wt)
+    if size == 0 or row == 0 or row % size:
+        raise ValueError("Wg: rows of %d bytes are no whole blocks of type %r" % (row, wtype))
+    K = row // size * qmm_block_values(wt)
+    _call("qmm_experts_glu", wt, GLU_KINDS[gate], _whole("Wg", Wg, dev, "uint8", (E, N, row)),
+          _whole("Wu", Wu, dev, "uint8", matrix), _whole("xq", xq, dev, "uint8", (T, qmm_row_bytes(qmm_act_type(wt), K))),
+          _whole("ids", ids, dev, "int32", (T, k)), _whole("h", h, dev, "float32", (T, k, N)),
+          _workspace(scratch, scratch_bytes, dev), scratch_bytes, T, k, E, N, K,
+          _raw_stream(dev) if stream is None else stream_handle(stream))
+
+
+def qmm_experts_sum(wtype, W, h, ids, weights, y, scratch, scratch_bytes, residual=None, stream=None):
+    """y[t] = residual[t] + sum_j weights[t][j] (W[ids[t][j]] q(h[t][j])): y f32 [T][N], W uint8 [E][N][row bytes], h f32
+    [T][k][K] (quantized on the way), ids int32 and weights f32 (or None: 1) [T][k]; residual f32 [T][N], may be y."""
+    dev, wt = _device(), _type(wtype)
+    if h.dim() != 3 or W.dim() != 3:
+        _refuse("h, W", h if h.dim() != 3 else W, "float32, uint8", "of 3 dimensions", dev)
+    T, k, K = h.shape
+    E, N = W.shape[:2]
+    _call("qmm_experts_sum", wt, _whole("W", W, dev, "uint8", (E, N, qmm_row_bytes(wt, K))),
+          _whole("h", h, dev, "float32", (T, k, K)), _whole("ids", ids, dev, "int32", (T, k)),
+          _whole("weights", weights, dev, "float32", (T, k)), _whole("residual", residual, dev, "float32", (T, N)),
+          _whole("y", y, dev, "float32", (T, N)), _workspace(scratch, scratch_bytes, dev), scratch_bytes, T, k, E, N, K,
           _raw_stream(dev) if stream is None else stream_handle(stream))
 
 

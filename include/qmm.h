@@ -560,6 +560,82 @@ QMM_API qmm_status qmm_kv_attend(const qmm_kv_pages* cache, const float* q, int6
                                  size_t scratch_bytes, int64_t R, int64_t Hq, float scale, int64_t window,
                                  qmm_stream_t stream);
 
+/* ---- mixture of experts ---------------------------------------------------- */
+/* Additions for layers whose feed-forward network is a choice of experts: the norm
+ * ahead of them, the choice, and the experts' products with a weight matrix that an
+ * index on the device names.  (qmm_linear_group multiplies by matrices that the host
+ * names.)  A layer's step, with device buffers:
+ *
+ *   qmm_add_rmsnorm_quantize(act, x, attn, x, w, eps, NULL, xq, T, K, stream);
+ *   qmm_matmul_q8_0(W_router, xq, logits, T, E, K, stream);     // or any other router
+ *   qmm_route(&spec, logits, E, bias, ids, weights, T, E, stream);
+ *   qmm_experts_glu(wt, QMM_GLU_SILU, Wg, Wu, xq, ids, h, scratch, bytes, T, k, E, F, K, stream);
+ *   qmm_experts_sum(wd, Wd, h, ids, weights, x, x, scratch, bytes, T, k, E, K, F, stream);
+ *
+ * qmm_add_rmsnorm_quantize: y = x + r, one f32 rounding; h_i = (y_i s) w_i, s =
+ * 1 / sqrt(ss / K + eps), ss = sum of y_i^2 summed to 2^-44 relative and rounded to
+ * f32 once, every other step an f32 operation rounded once; xq the rows of h as
+ * qmm_quantize_q8_0 / q8_K (act) gives them.  So sum, h and xq are those of a scalar
+ * implementation with an exact sum of squares (where y^2 neither overflows f32 nor
+ * falls below 2^-100).  x, r f32 [M][K]; w f32 [K]; sum f32 [M][K] receives y, NULL:
+ * not kept; it may be x or r; h f32 [M][K] or xq may be NULL, not both.  Apart from sum
+ * no output overlaps another argument.  K as for qmm_rmsnorm_quantize; every pointer
+ * 16-byte aligned. */
+QMM_API qmm_status qmm_add_rmsnorm_quantize(int act, const float* x, const float* r, float* sum, const float* w, float eps,
+                                            float* h, void* xq, int64_t M, int64_t K, qmm_stream_t stream);
+
+/* The experts of each token.  score_e = softmax(logits)_e or 1 / (1 + exp(-logit_e));
+ * key_e = score_e + bias_e.  Experts lie in `groups` equal runs; a group's worth is its
+ * largest key, or the sum of its two largest (group_top 1 or 2), and the groups_kept
+ * worthiest groups stay open.  ids[t][0..k-1] are the open experts of the k largest
+ * keys, largest first, weights[t][j] = scale * score (without the bias), divided by the
+ * chosen scores' sum where renorm != 0 (a sum of 0 leaves zeros).  Ties go to the lower
+ * index.  Choices are those of keys in binary64 (without a bias, and with group_top 1 or
+ * one group, of the logits themselves); weights are f32.
+ * An expert whose logit or key is -inf or NaN is closed to the token; a token with fewer
+ * than k open experts has ids -1 and weights 0 behind them.  +inf counts as the largest
+ * f32.  softmax runs over all experts that are not closed by their logit.
+ * logits f32 [T][E], ld values from one token to the next (at least E); bias f32 [E] or
+ * NULL; ids int32 [T][k], weights f32 [T][k], all device, 4-byte aligned.  E 1..1024, k
+ * 1..32 and at most groups_kept * E / groups, groups 1..64, dividing E; scale finite.
+ * The spec is read by the call. */
+typedef enum { QMM_ROUTE_SOFTMAX = 0, QMM_ROUTE_SIGMOID = 1 } qmm_route_score;
+typedef struct {
+    int32_t score;
+    int32_t k;
+    int32_t groups, groups_kept, group_top;
+    int32_t renorm;
+    float scale;
+} qmm_route_spec;
+QMM_API qmm_status qmm_route(const qmm_route_spec* spec, const float* logits, int64_t ld, const float* bias, int32_t* ids,
+                             float* weights, int64_t T, int64_t E, qmm_stream_t stream);
+
+/* The experts' products.  W, Wg, Wu: [E][N] rows of qmm_row_bytes(wtype, K) bytes (any
+ * weight type); ids int32 [T][k]: the experts of token t.  A negative id is a choice that
+ * is not there; an id of E or more is one too and makes qmm_device_status() return
+ * QMM_E_SHAPE.  One token may name an expert more than once.
+ *   glu  h[t][j][n] = act(Wg[e][n] . x_t) * (Wu[e][n] . x_t), e = ids[t][j]; xq [T] rows of
+ *        qmm_act_type(wtype); h f32 [T][k][N], zeros for a choice that is not there.  act:
+ *        silu, g / (1 + e^-g), or gelu, 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3)))
+ *   sum  y[t][n] = residual[t][n] + sum_j weights[t][j] (W[e][n] . q(h[t][j])), q the rule of
+ *        qmm_quantize_q8_0 / q8_K; h f32 [T][k][K] (without effect for a choice that is
+ *        not there); weights f32 [T][k], NULL: 1; residual f32 [T][N], NULL: 0, may be y
+ * Products agree with the block-wise definition (qmm_matvec) within 1e-5 of their row's
+ * L2 norm, and are the same on every run.  k 1..64, E 1..1024, T * k <= 2^24, E * N <=
+ * 2^31 - 1; N, K and the alignment (ids and weights: 4 bytes) as for qmm_matvec.
+ * scratch: at least qmm_experts_scratch_bytes(wtype, T, k, E, N, K) bytes (0: a bad
+ * argument), enough for either call of this shape, written before it is read; calls that
+ * may overlap on the GPU take one each.  The launches depend on the shapes alone, so a
+ * captured call serves any ids. */
+typedef enum { QMM_GLU_SILU = 0, QMM_GLU_GELU = 1 } qmm_glu_kind;
+QMM_API size_t qmm_experts_scratch_bytes(int wtype, int64_t T, int64_t k, int64_t E, int64_t N, int64_t K);
+QMM_API qmm_status qmm_experts_glu(int wtype, int kind, const void* Wg, const void* Wu, const void* xq, const int32_t* ids,
+                                   float* h, void* scratch, size_t scratch_bytes, int64_t T, int64_t k, int64_t E,
+                                   int64_t N, int64_t K, qmm_stream_t stream);
+QMM_API qmm_status qmm_experts_sum(int wtype, const void* W, const float* h, const int32_t* ids, const float* weights,
+                                   const float* residual, float* y, void* scratch, size_t scratch_bytes, int64_t T,
+                                   int64_t k, int64_t E, int64_t N, int64_t K, qmm_stream_t stream);
+
 /* ---- verification hooks (not on the hot path) --------------------------- */
 /* The exact int32 block sums the kernels fold, for bit-exact checking:
  * s[t][o][b] for every token t, row o and block b; Q4_0/Q8_0 give one int32 per
@@ -587,8 +663,8 @@ QMM_API qmm_status qmm_blocksums(int wtype, const void* W, const void* xq, int32
 QMM_API qmm_status qmm_test_wait_timeout(uint64_t limit_ns, qmm_stream_t stream);
 
 /* Reads (and with clear != 0 resets) the device error words that bounded waits
- * (QMM_E_TIMEOUT), qmm_get_rows (QMM_E_SHAPE for an id outside [0, N)), the paged
- * cache's calls (QMM_E_SHAPE for a position without a page) and, in a
+ * (QMM_E_TIMEOUT), qmm_get_rows (QMM_E_SHAPE for an id outside [0, N)), the experts'
+ * calls (QMM_E_SHAPE for an id of E or more), the paged cache's calls (QMM_E_SHAPE for a position without a page) and, in a
  * bounds-checked build, the kernels' index checks (QMM_E_BOUNDS) set; a timeout
  * is reported first, then a bounds record.  Synchronizes the device.  QMM_OK
  * when nothing was recorded. */
