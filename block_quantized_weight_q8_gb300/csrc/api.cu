@@ -198,6 +198,9 @@ unsigned qmm_internal_addnorm_error(int clear);
 unsigned qmm_internal_route_error(int clear);
 unsigned qmm_internal_expert_vec_error(int clear);
 unsigned qmm_internal_experts_error(int clear);
+unsigned qmm_internal_expert_mma_32_error(int clear);
+unsigned qmm_internal_expert_mma_five_error(int clear);
+unsigned qmm_internal_expert_mma_k_error(int clear);
 
 qmm_status qmm_linear_group(int wtype, int G, const void* const* W, const int64_t* N, const float* x, void* xq_scratch,
                             size_t scratch_bytes, float* const* y, int64_t M, int64_t K, qmm_stream_t stream) {
@@ -324,7 +327,9 @@ qmm_status qmm_device_status(int clear) {
                  qmm_internal_matmul_kq_error(clear) | qmm_internal_getrows_error(clear) |
                  qmm_internal_kv_error(clear) | qmm_internal_quantize_error(clear) | qmm_internal_pages_error(clear) |
                  qmm_internal_attend_error(clear) | qmm_internal_addnorm_error(clear) | qmm_internal_route_error(clear) |
-                 qmm_internal_expert_vec_error(clear) | qmm_internal_experts_error(clear);
+                 qmm_internal_expert_vec_error(clear) | qmm_internal_experts_error(clear) |
+                 qmm_internal_expert_mma_32_error(clear) | qmm_internal_expert_mma_five_error(clear) |
+                 qmm_internal_expert_mma_k_error(clear);
     {
         unsigned v = 0;
         if (cudaMemcpyFromSymbol(&v, g_test_error, sizeof(v)) != cudaSuccess) return QMM_E_CUDA;

@@ -1,0 +1,755 @@
+// experts_mma.cuh -- the experts' products for many rows, on the 5th-generation tensor cores.
+//
+//   P[s][n] = W[e_s][n] . x_s        for the rows s of a call, sorted by their expert e_s
+//
+// sm_103a's tensor cores take no integers, and a row has one scale for each 32 (or 256) values, so a fold of every
+// block's sum in registers would cost as much as the product.  Instead each weight becomes two f16, hi + lo (22 bits of
+// the value over a power of two that the row's 256 values share), and for activations with a scale per 32 values so does
+// each activation; the products hi hi + lo hi (+ hi lo) run on tcgen05.mma with f32 sums in tensor memory.  Activations
+// with one scale per 256 values stay whole numbers, exact in f16.  Sums leave the tensor core every 256 values, where
+// both powers of two (or the activation's scale) meet them in one fma: the sum's error stays that of 48 steps, whatever
+// the row's length, and the fold costs 1/8 of one per block.  The minimums of the formats that have them multiply the
+// activations' sums of 16 values: one further step of 16.
+//
+// A tile is 128 weight rows (gated: 64 rows of the gate's and of the up matrix, row by row, so that both sums of an
+// output lie in neighbouring lanes) by up to 128 rows of one expert; CTAs, one per SM, walk over the tiles.  Its warps:
+//   0-15   converters and epilogue: warp w has the 32 weight rows of lane quadrant w % 4 and of each chunk of 256 values
+//          the blocks 2 (w / 4) and 2 (w / 4) + 1, turned into f16 in its tensor-memory lanes; then, for the chunk before,
+//          the sums of 32 activation rows times its 32 weight rows, which it adds up in registers
+//   16-19  activation converters: 8-bit codes into the f16 operand in shared memory
+//   20     issues the MMAs
+//   21, 22 copy the weight rows' and the activation rows' bytes, a bulk copy for each row and chunk
+// Weights are read once per 128 rows of their expert; converting them, not the MMA, bounds tiles of few rows, and the
+// MMA's two or three terms those of many.
+#pragma once
+
+#include <cuda.h>
+
+#include "experts.h"
+#include "experts_mma.h"
+#include "tc_device.cuh"
+
+namespace qmm {
+
+static __device__ unsigned int g_expert_mma_error = 0;
+
+namespace em {
+
+constexpr int BM = 128;       // weight rows of a tile
+constexpr int CONV = 16, XW0 = CONV, XWARPS = 4, MMA_WARP = XW0 + XWARPS, WCOPY = MMA_WARP + 1, XCOPY = WCOPY + 1;
+constexpr int THREADS = (XCOPY + 1) * 32;
+constexpr int W_SLOTS = 8;    // weight operands in tensor memory: 16 columns hi, 16 lo
+constexpr int A_COL0 = 2 * kTileRows;  // after two accumulators
+constexpr int XOP = kTileRows * 64;    // bytes of one term of an activation operand: 32 values of 128 rows
+constexpr int XST = 2;        // stages of activation records
+constexpr int SX_RING = 8;    // chunks of activation scales
+static_assert(A_COL0 + W_SLOTS * 32 == 512, "tensor memory");
+
+template <int WT>
+struct Lay {
+    using F = Fmt<WT>;
+    static constexpr bool KQ = F::BV == 256;
+    static constexpr bool MIN = WT == QMM_Q4_1 || WT == QMM_Q5_1 || WT == QMM_Q4_K || WT == QMM_Q5_K || WT == QMM_Q2_K;
+    static constexpr int XTERMS = KQ ? 1 : 2;
+    static constexpr int X_SLOTS = KQ ? 8 : 4;
+    static constexpr int CHUNK = KQ ? F::BB : 8 * F::BB;  // bytes of a row's 256 values
+    // a copied row: the 16-byte superset at any offset that blocks can have, an odd number of 16-byte words
+    static constexpr int ALIGN = WT == QMM_Q4_K || WT == QMM_Q5_K ? 16 : WT == QMM_Q2_K || WT == QMM_Q4_1 ? 4 : WT == QMM_Q5_1 ? 8 : 2;
+    static constexpr int WORDS = (CHUNK + 16 - ALIGN + 15) / 16;
+    static constexpr int PITCH = 16 * (WORDS | 1);
+    static constexpr int XSTAGE = kTileRows * kRecord;
+    static constexpr int FIXED = XST * XSTAGE + X_SLOTS * XTERMS * XOP + SX_RING * kTileRows * 4 + 512;
+    static constexpr int FIT = (232448 - 128 - FIXED) / (BM * PITCH);
+    static constexpr int WST = FIT >= 4 ? 4 : 2;  // a power of two
+    static_assert(WST >= 2, "two stages of weight rows");
+    static constexpr int OFF_W = 0;
+    static constexpr int OFF_X = OFF_W + WST * BM * PITCH;
+    static constexpr int OFF_OP = OFF_X + XST * XSTAGE;
+    static constexpr int OFF_SX = OFF_OP + X_SLOTS * XTERMS * XOP;
+    static constexpr int OFF_BAR = OFF_SX + SX_RING * kTileRows * 4;
+    static constexpr int NBARS = 2 * WST + 2 * XST + W_SLOTS + X_SLOTS + W_SLOTS + 4;
+    static constexpr int OFF_TMEM = OFF_BAR + NBARS * 8;
+    static constexpr int SMEM = OFF_TMEM + 16;
+    static_assert(SMEM <= 232448 && OFF_OP % 128 == 0 && NBARS * 8 + 16 <= 512, "shared memory");
+};
+
+template <int WT>
+struct Bars {
+    using L = Lay<WT>;
+    uint32_t base;
+    __device__ uint32_t w_full(int s) const { return base + 8u * s; }                       // weight rows landed
+    __device__ uint32_t w_empty(int s) const { return base + 8u * (L::WST + s); }           // converted
+    __device__ uint32_t x_full(int s) const { return base + 8u * (2 * L::WST + s); }
+    __device__ uint32_t x_empty(int s) const { return base + 8u * (2 * L::WST + XST + s); }
+    __device__ uint32_t w_op(int i) const { return base + 8u * (2 * L::WST + 2 * XST + i); }  // operand written
+    __device__ uint32_t x_op(int i) const { return base + 8u * (2 * L::WST + 2 * XST + W_SLOTS + i); }
+    // the MMAs of item n are done: barrier n % 8
+    __device__ uint32_t done(int n) const { return base + 8u * (2 * L::WST + 2 * XST + W_SLOTS + L::X_SLOTS + (n & 7)); }
+    __device__ uint32_t acc_full(int i) const { return base + 8u * (2 * L::WST + 2 * XST + 2 * W_SLOTS + L::X_SLOTS + i); }
+    __device__ uint32_t acc_empty(int i) const { return base + 8u * (2 * L::WST + 2 * XST + 2 * W_SLOTS + L::X_SLOTS + 2 + i); }
+};
+
+__device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (mbar_wait_bounded(bar, parity, kWaitLimitNs)) return true;
+    atomicOr(&g_expert_mma_error, kErrTimeout);
+    *abort_flag = 1;
+    return false;
+}
+// the same for a whole warp, which stays together
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag));
+}
+
+__device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+__device__ __forceinline__ uint32_t h2_neg(uint32_t a) { return a ^ 0x80008000u; }
+__device__ __forceinline__ uint32_t h2_dup(uint32_t h) { return (h & 0xFFFFu) * 0x10001u; }
+// v as two f16, each in both halves of a word
+__device__ __forceinline__ void split2(float v, uint32_t* hi, uint32_t* lo) {
+    const uint32_t h = f2h_bits(v);
+    *hi = h2_dup(h);
+    *lo = h2_dup(f2h_bits(v - h2f(h)));
+}
+// The power of two that brings f16 magnitudes up to `bits` (sign cleared) below 2: its exponent field (at least the
+// smallest normal one, at most the largest), 2^(15 - e) as f32, and its inverse.
+__device__ __forceinline__ int exponent_of(uint32_t bits) {
+    const int e = (int)(bits >> 10);
+    return e < 1 ? 1 : e > 30 ? 30 : e;
+}
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+__device__ __forceinline__ uint32_t pow2_half(int e) {  // -24 <= e <= 15
+    return e >= -14 ? (uint32_t)(e + 15) << 10 : 1u << (e + 24);
+}
+
+// What a chunk's blocks share: the power of two, and (K-quants) the block's scales over it.
+struct WRow {
+    float scale;      // what the sums of the chunk are multiplied by
+    int e;            // exponent field
+};
+
+// The 32 codes of block kb of the chunk at byte `o` of the row, in K order, four to a word, and the f16 offset word.
+template <int WT>
+__device__ __forceinline__ uint32_t codes_of(const SmemBytes& w, uint32_t o, int kb, uint32_t (&c)[8]) {
+    if constexpr (WT == QMM_Q8_0) {
+        w.words<8>(o + 34 * kb + 2, c);
+#pragma unroll
+        for (int i = 0; i < 8; i++) c[i] ^= 0x80808080u;
+        return 0x64806480u;
+    } else if constexpr (WT == QMM_Q4_0 || WT == QMM_Q4_1 || WT == QMM_Q5_0 || WT == QMM_Q5_1) {
+        constexpr bool FIVE = WT == QMM_Q5_0 || WT == QMM_Q5_1;
+        const uint32_t b = o + Fmt<WT>::BB * kb;
+        uint32_t q[5];
+        uint32_t qh = 0;
+        if constexpr (WT == QMM_Q4_0) w.words<4>(b + 2, q);
+        if constexpr (WT == QMM_Q4_1) w.words_aligned<4>(b + 4, q);
+        if constexpr (WT == QMM_Q5_0) {
+            w.words<5>(b + 2, q);
+            qh = q[0], q[0] = q[1], q[1] = q[2], q[2] = q[3], q[3] = q[4];
+        }
+        if constexpr (WT == QMM_Q5_1) {
+            qh = w.w32(b + 4);
+            w.words_aligned<4>(b + 8, q);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            c[i] = q[i] & 0x0F0F0F0Fu;
+            c[4 + i] = (q[i] >> 4) & 0x0F0F0F0Fu;
+            if constexpr (FIVE) {
+                c[i] |= spread4(qh >> (4 * i)) << 4;
+                c[4 + i] |= spread4(qh >> (16 + 4 * i)) << 4;
+            }
+        }
+        return WT == QMM_Q4_0 ? 0x64086408u : WT == QMM_Q5_0 ? 0x64106410u : 0x64006400u;
+    } else if constexpr (WT == QMM_Q4_K || WT == QMM_Q5_K) {
+        const uint32_t b = o + (WT == QMM_Q4_K ? 16 : 48) + 32 * (kb >> 1);
+        const int sh = 4 * (kb & 1);
+        const uint4 q0 = *reinterpret_cast<const uint4*>(w.base + b), q1 = *reinterpret_cast<const uint4*>(w.base + b + 16);
+        const uint32_t q[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+#pragma unroll
+        for (int i = 0; i < 8; i++) c[i] = (q[i] >> sh) & 0x0F0F0F0Fu;
+        if constexpr (WT == QMM_Q5_K) {
+            const uint4 h0 = *reinterpret_cast<const uint4*>(w.base + o + 16), h1 = *reinterpret_cast<const uint4*>(w.base + o + 32);
+            const uint32_t h[8] = {h0.x, h0.y, h0.z, h0.w, h1.x, h1.y, h1.z, h1.w};
+#pragma unroll
+            for (int i = 0; i < 8; i++) c[i] |= ((h[i] >> kb) & 0x01010101u) << 4;
+        }
+        return 0x64006400u;
+    } else if constexpr (WT == QMM_Q2_K) {
+        uint32_t q[8];
+        w.words_aligned<8>(o + 16 + 32 * (kb >> 2), q);
+        const int sh = 2 * (kb & 3);
+#pragma unroll
+        for (int i = 0; i < 8; i++) c[i] = (q[i] >> sh) & 0x03030303u;
+        return 0x64006400u;
+    } else {  // Q6_K
+        const int half = kb >> 2, part = kb & 3;
+        uint32_t q[8], h[8];
+        w.words<8>(o + 64 * half + 32 * (part & 1), q);
+        w.words<8>(o + 128 + 32 * half, h);
+        const int sh = 4 * (part >> 1), hs = 2 * part;
+#pragma unroll
+        for (int i = 0; i < 8; i++) c[i] = ((q[i] >> sh) & 0x0F0F0F0Fu) | (((h[i] >> hs) & 0x03030303u) << 4);
+        return 0x64206420u;
+    }
+}
+
+// The power of two of a row's chunk.
+template <int WT>
+__device__ __forceinline__ WRow row_scale(const SmemBytes& w, uint32_t o, int blocks) {
+    uint32_t top = 0;
+    if constexpr (WT == QMM_Q4_K || WT == QMM_Q5_K) {
+        const uint32_t dd = w.w32(o);
+        top = max(dd & 0x7FFFu, (dd >> 16) & 0x7FFFu);
+    } else if constexpr (WT == QMM_Q2_K) {
+        const uint32_t dd = w.w32(o + 80);
+        top = max(dd & 0x7FFFu, (dd >> 16) & 0x7FFFu);
+    } else if constexpr (WT == QMM_Q6_K) {
+        top = w.u16(o + 208) & 0x7FFFu;
+    } else {
+#pragma unroll
+        for (int kb = 0; kb < 8; kb++) {
+            if (kb >= blocks) break;
+            const uint32_t b = o + Fmt<WT>::BB * kb;
+            if constexpr (Lay<WT>::MIN) {
+                const uint32_t dm = w.w32(b);
+                top = max(top, max(dm & 0x7FFFu, (dm >> 16) & 0x7FFFu));
+            } else {
+                top = max(top, w.u16(b) & 0x7FFFu);
+            }
+        }
+    }
+    const int e = exponent_of(top);
+    return {pow2(e - 15), e};
+}
+
+// Block kb of a row's chunk as hi and lo f16 words in K order.
+template <int WT>
+__device__ __forceinline__ void convert_block(const SmemBytes& w, uint32_t o, int kb, const WRow& row, uint32_t (&hi)[16],
+                                              uint32_t (&lo)[16]) {
+    uint32_t c[8];
+    const uint32_t magic = codes_of<WT>(w, o, kb, c);
+    // the scales of the block's two halves
+    uint32_t d0, d1, r0 = 0, r1 = 0;  // rounded, and (K-quants) the rest
+    if constexpr (Lay<WT>::KQ) {
+        float s0, s1;
+        if constexpr (WT == QMM_Q4_K || WT == QMM_Q5_K) {
+            // 6-bit scales: bytes 0-3 (and their two top bits for 4-7, whose low bits are in bytes 8-11)
+            const float d = h2f(w.u16(o)) * pow2(15 - row.e);
+            const uint32_t a = w.base[o + 4 + (kb & 3)];
+            const uint32_t sc = kb < 4 ? a & 63u : (w.base[o + 8 + kb] & 15u) | ((a >> 6) << 4);
+            s0 = s1 = d * (float)sc;
+        } else if constexpr (WT == QMM_Q2_K) {
+            const float d = h2f(w.u16(o + 80)) * pow2(15 - row.e);
+            const uint32_t sc = w.u16(o + 2 * kb);
+            s0 = d * (float)(sc & 15u), s1 = d * (float)((sc >> 8) & 15u);
+        } else {
+            const float d = h2f(w.u16(o + 208)) * pow2(15 - row.e);
+            const uint32_t sc = w.u16(o + 192 + 2 * kb);
+            s0 = d * (float)(int8_t)(sc & 0xFFu), s1 = d * (float)(int8_t)(sc >> 8);
+        }
+        split2(s0, &d0, &r0);
+        d1 = d0, r1 = r0;
+        if constexpr (WT == QMM_Q2_K || WT == QMM_Q6_K) split2(s1, &d1, &r1);
+    } else {
+        d0 = h2_mul(h2_dup(w.u16(o + Fmt<WT>::BB * kb)), h2_dup(pow2_half(15 - row.e)));
+        d1 = d0;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        const uint32_t d = i < 4 ? d0 : d1, r = i < 4 ? r0 : r1;
+        const uint32_t q0 = h2_sub(bytes_to_h2(c[i], 0x5140), magic), q1 = h2_sub(bytes_to_h2(c[i], 0x7362), magic);
+        hi[2 * i] = h2_mul(d, q0), hi[2 * i + 1] = h2_mul(d, q1);
+        lo[2 * i] = h2_fma(d, q0, h2_neg(hi[2 * i])), lo[2 * i + 1] = h2_fma(d, q1, h2_neg(hi[2 * i + 1]));
+        if constexpr (Lay<WT>::KQ) lo[2 * i] = h2_fma(r, q0, lo[2 * i]), lo[2 * i + 1] = h2_fma(r, q1, lo[2 * i + 1]);
+    }
+}
+
+// The chunk's minimums over 16 groups of 16 values: what an activation group's sum is multiplied by, as hi and lo (for
+// Q4_1 and Q5_1 the minimum is an f16 and lo is not used).
+template <int WT>
+__device__ __forceinline__ void convert_min(const SmemBytes& w, uint32_t o, int blocks, const WRow& row, uint32_t (&hi)[8],
+                                            uint32_t (&lo)[8]) {
+    if constexpr (WT == QMM_Q4_1 || WT == QMM_Q5_1) {
+        const uint32_t f = h2_dup(pow2_half(15 - row.e));
+#pragma unroll
+        for (int b = 0; b < 8; b++) {
+            hi[b] = b < blocks ? h2_mul(h2_dup(w.u16(o + Fmt<WT>::BB * b + 2)), f) : 0u;
+            lo[b] = 0u;
+        }
+    } else if constexpr (WT == QMM_Q4_K || WT == QMM_Q5_K) {
+        const float d = -(h2f(w.u16(o + 2)) * pow2(15 - row.e));
+        const uint32_t y = w.w32(o + 8), z = w.w32(o + 12);
+        const uint32_t m0 = y & 0x3F3F3F3Fu, m1 = ((z >> 4) & 0x0F0F0F0Fu) | ((y >> 2) & 0x30303030u);
+#pragma unroll
+        for (int b = 0; b < 8; b++) split2(d * (float)byte_of(b < 4 ? m0 : m1, b & 3), &hi[b], &lo[b]);
+    } else if constexpr (WT == QMM_Q2_K) {
+        const float d = -(h2f(w.u16(o + 82)) * pow2(15 - row.e));
+        uint32_t sc[4];
+        w.words_aligned<4>(o, sc);
+#pragma unroll
+        for (int b = 0; b < 8; b++) {
+            const uint32_t two = sc[b >> 1] >> (16 * (b & 1));
+            uint32_t h0, l0, h1, l1;
+            split2(d * (float)((two >> 4) & 15u), &h0, &l0);
+            split2(d * (float)((two >> 12) & 15u), &h1, &l1);
+            hi[b] = (h0 & 0xFFFFu) | (h1 << 16), lo[b] = (l0 & 0xFFFFu) | (l1 << 16);
+        }
+    }
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// 16 bytes of an activation operand: values 8 kq .. 8 kq + 7 of row r
+__device__ __forceinline__ void put_x(uint8_t* op, int r, int kq, const uint32_t* v) {
+    *reinterpret_cast<uint4*>(op + ((r >> 3) * 4 + kq) * 128 + (r & 7) * 16) = make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+template <int WT, bool GATED>
+__global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_constant__ ExpertMma a) {
+    using L = Lay<WT>;
+    pdl_launch_dependents();
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sbase = smem_u32(smem);
+    if (!QMM_IN_BOUNDS(g_expert_mma_error, L::SMEM - 1, dynamic_smem_bytes())) return;
+    const Bars<WT> bars{sbase + L::OFF_BAR};
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_TMEM);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_TMEM + 8);
+    float* const sx = reinterpret_cast<float*>(smem + L::OFF_SX);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < L::WST; i++) mbar_init(bars.w_full(i), 1), mbar_init(bars.w_empty(i), CONV);
+        for (int i = 0; i < XST; i++) mbar_init(bars.x_full(i), 1), mbar_init(bars.x_empty(i), XWARPS);
+        for (int i = 0; i < W_SLOTS; i++) mbar_init(bars.w_op(i), 4), mbar_init(bars.done(i), 1);
+        for (int i = 0; i < L::X_SLOTS; i++) mbar_init(bars.x_op(i), XWARPS);
+        for (int i = 0; i < 2; i++) mbar_init(bars.acc_full(i), 1), mbar_init(bars.acc_empty(i), CONV);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == MMA_WARP) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();  // the tiles and the activation records come from the kernel before
+
+    constexpr int NROWS = GATED ? BM / 2 : BM;  // output columns of a tile
+    const int N = a.N;
+    const int nt = (N + NROWS - 1) / NROWS;
+    const int nb = a.K / 32;
+    const int nchunks = (a.K + 255) / 256;
+    const int ntiles = *a.ntiles * nt;
+    const uint64_t rb = (uint64_t)(a.K / Fmt<WT>::BV) * Fmt<WT>::BB;
+    const uint64_t total = (uint64_t)a.E * (uint64_t)N * rb;
+    const uint64_t total_al = total & ~15ull;
+    auto blocks_of = [&](int c) { return L::KQ ? 8 : min(8, nb - 8 * c); };
+    // the weight row of tile row r (rows behind the last repeat it)
+    auto weight_row = [&](const ExpertTile& t, int n0, int r) {
+        const int n = min(n0 + (GATED ? r >> 1 : r), N - 1);
+        return (int64_t)t.expert * N + n;
+    };
+
+    if (warp == WCOPY) {
+        // ------------------------------------------------------------ the weight rows' bytes
+        uint32_t gc = 0;
+        bool ok = true;
+        for (int ti = blockIdx.x; ti < ntiles && ok; ti += gridDim.x) {
+            const ExpertTile t = a.tiles[ti / nt];
+            const int n0 = ti % nt * NROWS;
+            uint64_t row[4];
+            const uint8_t* base[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int r = 32 * i + lane;
+                row[i] = (uint64_t)weight_row(t, n0, r) * rb;
+                base[i] = GATED && (r & 1) ? a.W1 : a.W0;
+            }
+            for (int c = 0; c < nchunks; c++, gc++) {
+                const int s = (int)(gc % L::WST);
+                if (gc >= L::WST && !warp_wait(bars.w_empty(s), (uint32_t)(gc / L::WST - 1) & 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                const int blocks = blocks_of(c);
+                const uint32_t bytes = L::KQ ? L::CHUNK : blocks * Fmt<WT>::BB;
+                uint64_t a0[4];
+                uint32_t len[4], sum = 0;
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const uint64_t g0 = row[i] + (uint64_t)c * L::CHUNK;
+                    a0[i] = g0 & ~15ull;
+                    uint64_t a1 = (g0 + bytes + 15ull) & ~15ull;
+                    if (a1 > total_al) a1 = total_al;
+                    len[i] = a1 > a0[i] ? (uint32_t)(a1 - a0[i]) : 0u;
+                    if (!QMM_IN_BOUNDS(g_expert_mma_error, len[i], L::PITCH + 1)) len[i] = 0;
+                    sum += len[i];
+                }
+                sum = __reduce_add_sync(0xffffffffu, sum);
+                if (lane == 0) mbar_arrive_expect_tx(bars.w_full(s), sum);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    if (len[i])
+                        bulk_g2s_nohint(sbase + L::OFF_W + (uint32_t)((s * BM + 32 * i + lane) * L::PITCH), base[i] + a0[i], len[i],
+                                        bars.w_full(s));
+            }
+        }
+        // after a timeout: the copies in flight land before the CTA ends
+        if (!ok && lane == 0)
+            for (uint32_t g = gc > L::WST ? gc - L::WST : 0; g < gc; g++)
+                mbar_wait_bounded(bars.w_full((int)(g % L::WST)), (uint32_t)(g / L::WST) & 1u, kWaitLimitNs);
+    } else if (warp == XCOPY) {
+        // ------------------------------------------------------------ the activation rows' records
+        uint32_t gc = 0;
+        bool ok = true;
+        for (int ti = blockIdx.x; ti < ntiles && ok; ti += gridDim.x) {
+            const ExpertTile t = a.tiles[ti / nt];
+            const uint8_t* src[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int r = 32 * i + lane;
+                const int64_t slot = r < t.count ? a.order[t.first + r] : 0;
+                src[i] = a.records + (slot / a.per_row) * (int64_t)nchunks * kRecord;
+            }
+            for (int c = 0; c < nchunks; c++, gc++) {
+                const int s = (int)(gc % XST);
+                if (gc >= XST && !warp_wait(bars.x_empty(s), (uint32_t)(gc / XST - 1) & 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) mbar_arrive_expect_tx(bars.x_full(s), (uint32_t)(t.count * kRecord));
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    if (32 * i + lane < t.count)
+                        bulk_g2s_nohint(sbase + L::OFF_X + (uint32_t)(s * L::XSTAGE + (32 * i + lane) * kRecord),
+                                        src[i] + (int64_t)c * kRecord, kRecord, bars.x_full(s));
+            }
+        }
+        if (!ok && lane == 0)
+            for (uint32_t g = gc > XST ? gc - XST : 0; g < gc; g++)
+                mbar_wait_bounded(bars.x_full((int)(g % XST)), (uint32_t)(g / XST) & 1u, kWaitLimitNs);
+    } else if (warp == MMA_WARP) {
+        // ------------------------------------------------------------ the MMAs
+        if (lane == 0) {
+            uint32_t gc = 0;
+            int64_t n = 0;
+            bool ok = true;
+            for (int ti = blockIdx.x; ti < ntiles && ok; ti += gridDim.x) {
+                const int cols = (a.tiles[ti / nt].count + 15) & ~15;
+                const uint32_t idesc = instr_desc_f16(BM, cols);
+                for (int c = 0; c < nchunks && ok; c++, gc++) {
+                    const int blocks = blocks_of(c);
+                    const uint32_t d = tmem + (uint32_t)((gc & 1) * kTileRows);
+                    if (gc >= 2 && !wait_or_abort(bars.acc_empty((int)(gc & 1)), (uint32_t)(gc / 2 - 1) & 1u, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    uint32_t more = 0;
+                    for (int i = 0; i < blocks + (L::MIN ? 1 : 0); i++, n++) {
+                        const int ws = (int)(n % W_SLOTS), xs = (int)(n % L::X_SLOTS);
+                        if (!wait_or_abort(bars.w_op(ws), (uint32_t)(n / W_SLOTS) & 1u, abort_flag) ||
+                            !wait_or_abort(bars.x_op(xs), (uint32_t)(n / L::X_SLOTS) & 1u, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t ah = tmem + (uint32_t)(A_COL0 + ws * 32);
+                        const uint64_t xh = smem_desc(sbase + L::OFF_OP + (uint32_t)(xs * L::XTERMS * XOP), 128, 512);
+                        const uint64_t xl = xh + (XOP >> 4);
+                        if (L::MIN && i == blocks) {
+                            mma_f16_ts(d, ah, xh, idesc, more);
+                            if constexpr (L::KQ) mma_f16_ts(d, ah + 16, xh, idesc, 1);
+                            else mma_f16_ts(d, ah, xl, idesc, 1);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 2; k++) {
+                                mma_f16_ts(d, ah + 8 * k, xh + k * (256 >> 4), idesc, more);
+                                more = 1;
+                                mma_f16_ts(d, ah + 16 + 8 * k, xh + k * (256 >> 4), idesc, 1);
+                                if constexpr (!L::KQ) mma_f16_ts(d, ah + 8 * k, xl + k * (256 >> 4), idesc, 1);
+                            }
+                        }
+                        mma_commit(bars.done((int)n));
+                    }
+                    if (ok) mma_commit(bars.acc_full((int)(gc & 1)));
+                }
+            }
+            // the last commits land before the CTA ends
+            for (uint32_t i = n > 8 ? n - 8 : 0; i < n; i++)
+                mbar_wait_bounded(bars.done((int)i), (uint32_t)(i / 8) & 1u, kWaitLimitNs);
+        }
+    } else if (warp >= XW0) {
+        // ------------------------------------------------------------ activation operands
+        const int x = warp - XW0;
+        uint32_t gc = 0, n = 0;
+        bool ok = true;
+        for (int ti = blockIdx.x; ti < ntiles && ok; ti += gridDim.x) {
+            const int count = a.tiles[ti / nt].count;
+            const int ng = (count + 31) / 32;  // row groups: block i of group g belongs to warp (i ng + g) % 4
+            for (int c = 0; c < nchunks && ok; c++, gc++) {
+                const int s = (int)(gc % XST), blocks = blocks_of(c);
+                if (!warp_wait(bars.x_full(s), (uint32_t)(gc / XST) & 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                const uint8_t* stage = smem + L::OFF_X + s * L::XSTAGE;
+                if (x < ng) {
+                    const uint8_t* rec = stage + (32 * x + lane) * kRecord;
+                    float scale;
+                    if constexpr (L::KQ) {
+                        scale = *reinterpret_cast<const float*>(rec + 256);
+                    } else {
+                        const uint4 d = *reinterpret_cast<const uint4*>(rec + 256);
+                        const uint32_t m = __vmaxu2(__vmaxu2(d.x, d.y), __vmaxu2(d.z, d.w));
+                        scale = pow2(exponent_of(max(m & 0x7FFFu, (m >> 16) & 0x7FFFu)) - 15);
+                    }
+                    sx[(gc & (SX_RING - 1)) * kTileRows + 32 * x + lane] = scale;
+                }
+                for (int i = 0; i < blocks + (L::MIN ? 1 : 0); i++, n++) {
+                    const int xs = (int)(n % L::X_SLOTS);
+                    if (n >= L::X_SLOTS) {
+                        const uint32_t p = n - L::X_SLOTS;
+                        if (!warp_wait(bars.done((int)p), (uint32_t)(p / 8) & 1u, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                    }
+                    uint8_t* op = smem + L::OFF_OP + xs * L::XTERMS * XOP;
+                    for (int g = 0; g < ng; g++) {
+                        if (((i * ng + g) & 3) != x) continue;
+                        const int r = 32 * g + lane;
+                        const uint8_t* rec = stage + r * kRecord;
+                        uint32_t f = 0;  // the power of two that the row's scales are over
+                        if constexpr (!L::KQ) {
+                            const uint4 d = *reinterpret_cast<const uint4*>(rec + 256);
+                            const uint32_t m = __vmaxu2(__vmaxu2(d.x, d.y), __vmaxu2(d.z, d.w));
+                            f = h2_dup(pow2_half(15 - exponent_of(max(m & 0x7FFFu, (m >> 16) & 0x7FFFu))));
+                        }
+                        if (L::MIN && i == blocks) {
+                            const uint4 s0 = *reinterpret_cast<const uint4*>(rec + 272), s1 = *reinterpret_cast<const uint4*>(rec + 288);
+                            uint32_t v[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+                            if constexpr (!L::KQ) {
+                                uint32_t lo[8];
+#pragma unroll
+                                for (int b = 0; b < 8; b++) {  // block b's two sums times its scale
+                                    const uint32_t d = h2_mul(h2_dup(*reinterpret_cast<const unsigned short*>(rec + 256 + 2 * b)), f);
+                                    const uint32_t h = h2_mul(d, v[b]);
+                                    lo[b] = h2_fma(d, v[b], h2_neg(h));
+                                    v[b] = h;
+                                }
+                                put_x(op + XOP, r, 0, lo);
+                                put_x(op + XOP, r, 1, lo + 4);
+                            }
+                            put_x(op, r, 0, v);
+                            put_x(op, r, 1, v + 4);
+                            continue;
+                        }
+                        const uint4 c0 = *reinterpret_cast<const uint4*>(rec + 32 * i), c1 = *reinterpret_cast<const uint4*>(rec + 32 * i + 16);
+                        const uint32_t cw[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+                        uint32_t v[16];
+#pragma unroll
+                        for (int b = 0; b < 8; b++) {
+                            const uint32_t w = cw[b] ^ 0x80808080u;
+                            v[2 * b] = h2_sub(bytes_to_h2(w, 0x5140), 0x64806480u);
+                            v[2 * b + 1] = h2_sub(bytes_to_h2(w, 0x7362), 0x64806480u);
+                        }
+                        if constexpr (!L::KQ) {
+                            const uint32_t d = h2_mul(h2_dup(*reinterpret_cast<const unsigned short*>(rec + 256 + 2 * i)), f);
+                            uint32_t lo[16];
+#pragma unroll
+                            for (int b = 0; b < 16; b++) {
+                                const uint32_t h = h2_mul(d, v[b]);
+                                lo[b] = h2_fma(d, v[b], h2_neg(h));
+                                v[b] = h;
+                            }
+#pragma unroll
+                            for (int kq = 0; kq < 4; kq++) put_x(op + XOP, r, kq, lo + 4 * kq);
+                        }
+#pragma unroll
+                        for (int kq = 0; kq < 4; kq++) put_x(op, r, kq, v + 4 * kq);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bars.x_op(xs));
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bars.x_empty(s));
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ weight operands, sums
+        const int quad = warp & 3, grp = warp >> 2;
+        const int r = quad * 32 + lane;  // tile row
+        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+        float acc[32];
+        uint32_t gc = 0, n = 0;
+        float last_scale = 0.0f;  // of the chunk before
+        bool ok = true;
+        // adds the sums of chunk g (times its scales) to the registers
+        auto fold = [&](uint32_t g, int count, float scale) {
+            if (!warp_wait(bars.acc_full((int)(g & 1)), (uint32_t)(g / 2) & 1u, abort_flag)) return false;
+            tc_fence_after();
+            if (grp * 32 < count) {
+                const uint32_t cols = lanes + (uint32_t)((g & 1) * kTileRows + grp * 32);
+                const float4* s4 = reinterpret_cast<const float4*>(sx + (g & (SX_RING - 1)) * kTileRows + grp * 32);
+                uint32_t v[2][8];
+                tmem_ld8(cols, v[0]);
+                tmem_ld_wait_regs8(v[0]);
+#pragma unroll
+                for (int q = 0; q < 4; q++) {
+                    if (q < 3) tmem_ld8(cols + 8 * (q + 1), v[(q + 1) & 1]);
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        const float4 s = s4[2 * q + h];
+                        const uint32_t* u = v[q & 1] + 4 * h;
+                        float* o = acc + 8 * q + 4 * h;
+                        o[0] = fmaf(__uint_as_float(u[0]), scale * s.x, o[0]);
+                        o[1] = fmaf(__uint_as_float(u[1]), scale * s.y, o[1]);
+                        o[2] = fmaf(__uint_as_float(u[2]), scale * s.z, o[2]);
+                        o[3] = fmaf(__uint_as_float(u[3]), scale * s.w, o[3]);
+                    }
+                    if (q < 3) tmem_ld_wait_regs8(v[(q + 1) & 1]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars.acc_empty((int)(g & 1)));
+            return true;
+        };
+        // writes the finished sums of a tile
+        auto store = [&](const ExpertTile& t, int n0) {
+            if constexpr (GATED) {
+                const int col = n0 + quad * 16 + (lane >> 1);
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                    if (grp * 32 + j >= t.count) break;  // the whole warp
+                    // even lanes hold the gate's sum and take token j, odd ones the up sum and token j + 1
+                    const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? acc[j] : acc[j + 1], 1);
+                    const float g = lane & 1 ? other : acc[j], u = lane & 1 ? acc[j + 1] : other;
+                    const int tok = grp * 32 + j + (lane & 1);
+                    if (tok < t.count && col < N) {
+                        const int64_t o = (int64_t)a.order[t.first + tok] * N + col;
+                        if (QMM_IN_BOUNDS(g_expert_mma_error, o, a.out_values)) a.y[o] = gated(a.kind, g, u);
+                    }
+                }
+            } else {
+                const int col = n0 + r;
+#pragma unroll
+                for (int j = 0; j < 32; j++) {
+                    if (grp * 32 + j >= t.count) break;
+                    const int64_t o = (int64_t)a.order[t.first + grp * 32 + j] * N + col;
+                    if (col < N && QMM_IN_BOUNDS(g_expert_mma_error, o, a.out_values)) a.y[o] = acc[j];
+                }
+            }
+        };
+        for (int ti = blockIdx.x; ti < ntiles && ok; ti += gridDim.x) {
+            const ExpertTile t = a.tiles[ti / nt];
+            const int n0 = ti % nt * NROWS;
+            const uint64_t row = (uint64_t)weight_row(t, n0, r) * rb;
+#pragma unroll
+            for (int j = 0; j < 32; j++) acc[j] = 0.0f;
+            for (int c = 0; c < nchunks && ok; c++, gc++) {
+                const int s = (int)(gc % L::WST), blocks = blocks_of(c);
+                if (!warp_wait(bars.w_full(s), (uint32_t)(gc / L::WST) & 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t* const buf = smem + L::OFF_W + (s * BM + r) * L::PITCH;
+                const uint64_t g0 = row + (uint64_t)c * L::CHUNK;
+                const uint32_t o = (uint32_t)(g0 & 15ull);
+                if (total > total_al && g0 + (L::KQ ? L::CHUNK : blocks * Fmt<WT>::BB) == total) {
+                    // the last < 16 bytes of the weights: not reachable by a 16-byte bulk copy
+                    const uint8_t* W = GATED && (r & 1) ? a.W1 : a.W0;
+                    for (uint64_t i = total_al; i < total; i++)
+                        if (QMM_IN_BOUNDS(g_expert_mma_error, i - (g0 & ~15ull), L::PITCH)) buf[i - (g0 & ~15ull)] = W[i];
+                }
+                const SmemBytes w{buf};
+                const WRow ws = row_scale<WT>(w, o, blocks);
+                for (int i = 0; i < blocks + (L::MIN ? 1 : 0); i++) {
+                    if ((i < blocks ? i >> 1 : (int)(gc & 3)) != grp) continue;
+                    const uint32_t m = n + i;
+                    if (m >= W_SLOTS && !warp_wait(bars.done((int)m), (uint32_t)(m / 8 - 1) & 1u, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t slot = lanes + (uint32_t)(A_COL0 + (int)(m % W_SLOTS) * 32);
+                    tc_fence_after();
+                    if (i < blocks) {
+                        uint32_t hi[16], lo[16];
+                        convert_block<WT>(w, o, i, ws, hi, lo);
+                        tmem_st16(slot, hi);
+                        tmem_st16(slot + 16, lo);
+                    } else if constexpr (L::MIN) {
+                        uint32_t hi[8], lo[8];
+                        convert_min<WT>(w, o, blocks, ws, hi, lo);
+                        tmem_st8(slot, hi);
+                        if constexpr (L::KQ) tmem_st8(slot + 16, lo);
+                    }
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bars.w_op((int)(m % W_SLOTS)));
+                }
+                n += blocks + (L::MIN ? 1 : 0);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bars.w_empty(s));
+                if (ok && c > 0) ok = fold(gc - 1, t.count, last_scale);
+                last_scale = ws.scale;
+            }
+            if (ok) ok = fold(gc - 1, t.count, last_scale);
+            if (ok) store(t, n0);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == MMA_WARP) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    }
+}
+
+}  // namespace em
+
+template <int WT, bool GATED>
+static qmm_status expert_mma_launch(const ExpertMma& a, int64_t tiles_most, cudaStream_t stream) {
+    using L = em::Lay<WT>;
+    DeviceInfo dev;
+    qmm_status st = current_device(&dev);
+    if (st != QMM_OK) return st;
+    static PerDeviceOnce once;
+    st = once.run(dev.device, [] {
+        return cudaFuncSetAttribute(em::expert_mma_kernel<WT, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) ==
+                       cudaSuccess
+                   ? QMM_OK
+                   : QMM_E_CUDA;
+    });
+    if (st != QMM_OK) return st;
+    const int64_t most = tiles_most * ((a.N + (GATED ? 63 : 127)) / (GATED ? 64 : 128));
+    const int64_t grid = most < dev.sms ? most : dev.sms;
+    return launch_pdl(em::expert_mma_kernel<WT, GATED>, dim3((unsigned)grid), em::THREADS, L::SMEM, stream, a);
+}
+
+template <int WT>
+static qmm_status expert_mma_either(const ExpertMma& a, bool gate, int64_t tiles_most, cudaStream_t stream) {
+    return gate ? expert_mma_launch<WT, true>(a, tiles_most, stream) : expert_mma_launch<WT, false>(a, tiles_most, stream);
+}
+
+}  // namespace qmm
