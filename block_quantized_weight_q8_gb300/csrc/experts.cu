@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_cons
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         if (!QMM_IN_BOUNDS(g_experts_error, i, total)) continue;
         uint8_t* rec = a.records + i * kRecord;
-        *reinterpret_cast<uint2*>(rec + 8 * lane) = make_uint2(w0, w1);
+        *reinterpret_cast<uint2*>(rec + 8 * lane) = make_uint2(w0 ^ 0x80808080u, w1 ^ 0x80808080u);
         if (!(lane & 1)) st_u16(rec + 272 + lane, f2h_bits((float)sum));
         if (ACT == QMM_Q8_0 && !(lane & 3)) st_u16(rec + 256 + (lane >> 1), dbits);
         if (ACT == QMM_Q8_K && lane == 0) *reinterpret_cast<float*>(rec + 256) = d;

@@ -18,7 +18,8 @@
 //          the sums of 32 activation rows times its 32 weight rows, which it adds up in registers
 //   16-19  activation converters: 8-bit codes into the f16 operand in shared memory
 //   20     issues the MMAs
-//   21, 22 copy the weight rows' and the activation rows' bytes, a bulk copy for each row and chunk
+//   21-23  copy the weight rows' and the activation rows' bytes, 16 at a time (a bulk copy for each row and chunk left the
+//          copying warp with 84 cycles a row, 10,800 a chunk where the MMAs take 2,200)
 // Weights are read once per 128 rows of their expert; converting them, not the MMA, bounds tiles of few rows, and the
 // MMA's two or three terms those of many.
 #pragma once
@@ -36,8 +37,11 @@ static __device__ unsigned int g_expert_mma_error = 0;
 namespace em {
 
 constexpr int BM = 128;       // weight rows of a tile
-constexpr int CONV = 16, XW0 = CONV, XWARPS = 4, MMA_WARP = XW0 + XWARPS, WCOPY = MMA_WARP + 1, XCOPY = WCOPY + 1;
-constexpr int THREADS = (XCOPY + 1) * 32;
+constexpr int CONV = 16, XW0 = CONV, XWARPS = 4, MMA_WARP = XW0 + XWARPS, WCOPY = MMA_WARP + 1, XCOPY = WCOPY + 1, XCOPIES = 2;
+constexpr int THREADS = (XCOPY + XCOPIES) * 32;
+// Registers a thread: 768 threads start with 80; the converters, with their sums, go up to what the others give away.
+constexpr int REGS_CONV = 96, REGS_OTHER = 48;
+static_assert(THREADS == 768 && CONV * 32 * REGS_CONV + (THREADS - CONV * 32) * REGS_OTHER <= THREADS * 80, "registers");
 constexpr int W_SLOTS = 8;    // weight operands in tensor memory: 16 columns hi, 16 lo
 constexpr int A_COL0 = 2 * kTileRows;  // after two accumulators
 constexpr int XOP = kTileRows * 64;    // bytes of one term of an activation operand: 32 values of 128 rows
@@ -57,6 +61,8 @@ struct Lay {
     static constexpr int ALIGN = WT == QMM_Q4_K || WT == QMM_Q5_K ? 16 : WT == QMM_Q2_K || WT == QMM_Q4_1 ? 4 : WT == QMM_Q5_1 ? 8 : 2;
     static constexpr int WORDS = (CHUNK + 16 - ALIGN + 15) / 16;
     static constexpr int PITCH = 16 * (WORDS | 1);
+    // blocks of an accumulation: where activations have two terms, sums leave the tensor core twice as often
+    static constexpr int FOLD = KQ ? 8 : 4;
     static constexpr int XSTAGE = kTileRows * kRecord;
     static constexpr int FIXED = XST * XSTAGE + X_SLOTS * XTERMS * XOP + SX_RING * kTileRows * 4 + 512;
     static constexpr int FIT = (232448 - 128 - FIXED) / (BM * PITCH);
@@ -112,7 +118,20 @@ __device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
 }
-__device__ __forceinline__ uint32_t h2_neg(uint32_t a) { return a ^ 0x80008000u; }
+__device__ __forceinline__ uint32_t h2_neg(uint32_t a) {
+    uint32_t d;
+    asm("neg.f16x2 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+// 16 bytes (of which `bytes` are read, zeros behind them) into shared memory; the arrival is counted when this thread's
+// copies so far have landed.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ uint32_t h2_dup(uint32_t h) { return (h & 0xFFFFu) * 0x10001u; }
 // v as two f16, each in both halves of a word
 __device__ __forceinline__ void split2(float v, uint32_t* hi, uint32_t* lo) {
@@ -131,11 +150,19 @@ __device__ __forceinline__ uint32_t pow2_half(int e) {  // -24 <= e <= 15
     return e >= -14 ? (uint32_t)(e + 15) << 10 : 1u << (e + 24);
 }
 
-// What a chunk's blocks share: the power of two, and (K-quants) the block's scales over it.
+// What a chunk's blocks share: the power of two (its exponent field, and what the chunk's sums are multiplied by) and the
+// first 16 bytes of a Q4_K or Q5_K block.
 struct WRow {
-    float scale;      // what the sums of the chunk are multiplied by
-    int e;            // exponent field
+    float scale;
+    int e;
+    uint4 head;
 };
+// What is taken from the codes of formats with a minimum, so that neither the products nor the minimums' share are much
+// larger than their sum (the minimum gets it back times the scale).
+template <int WT>
+constexpr int center() {
+    return WT == QMM_Q4_1 || WT == QMM_Q4_K ? 8 : WT == QMM_Q5_1 || WT == QMM_Q5_K ? 16 : WT == QMM_Q2_K ? 2 : 0;
+}
 
 // The 32 codes of block kb of the chunk at byte `o` of the row, in K order, four to a word, and the f16 offset word.
 template <int WT>
@@ -169,7 +196,7 @@ __device__ __forceinline__ uint32_t codes_of(const SmemBytes& w, uint32_t o, int
                 c[4 + i] |= spread4(qh >> (16 + 4 * i)) << 4;
             }
         }
-        return WT == QMM_Q4_0 ? 0x64086408u : WT == QMM_Q5_0 ? 0x64106410u : 0x64006400u;
+        return WT == QMM_Q4_0 || WT == QMM_Q4_1 ? 0x64086408u : 0x64106410u;
     } else if constexpr (WT == QMM_Q4_K || WT == QMM_Q5_K) {
         const uint32_t b = o + (WT == QMM_Q4_K ? 16 : 48) + 32 * (kb >> 1);
         const int sh = 4 * (kb & 1);
@@ -183,14 +210,14 @@ __device__ __forceinline__ uint32_t codes_of(const SmemBytes& w, uint32_t o, int
 #pragma unroll
             for (int i = 0; i < 8; i++) c[i] |= ((h[i] >> kb) & 0x01010101u) << 4;
         }
-        return 0x64006400u;
+        return (uint32_t)(0x6400 + center<WT>()) * 0x10001u;
     } else if constexpr (WT == QMM_Q2_K) {
         uint32_t q[8];
         w.words_aligned<8>(o + 16 + 32 * (kb >> 2), q);
         const int sh = 2 * (kb & 3);
 #pragma unroll
         for (int i = 0; i < 8; i++) c[i] = (q[i] >> sh) & 0x03030303u;
-        return 0x64006400u;
+        return 0x64026402u;
     } else {  // Q6_K
         const int half = kb >> 2, part = kb & 3;
         uint32_t q[8], h[8];
@@ -207,8 +234,10 @@ __device__ __forceinline__ uint32_t codes_of(const SmemBytes& w, uint32_t o, int
 template <int WT>
 __device__ __forceinline__ WRow row_scale(const SmemBytes& w, uint32_t o, int blocks) {
     uint32_t top = 0;
+    uint4 head = make_uint4(0u, 0u, 0u, 0u);
     if constexpr (WT == QMM_Q4_K || WT == QMM_Q5_K) {
-        const uint32_t dd = w.w32(o);
+        head = *reinterpret_cast<const uint4*>(w.base + o);
+        const uint32_t dd = head.x;
         top = max(dd & 0x7FFFu, (dd >> 16) & 0x7FFFu);
     } else if constexpr (WT == QMM_Q2_K) {
         const uint32_t dd = w.w32(o + 80);
@@ -229,7 +258,14 @@ __device__ __forceinline__ WRow row_scale(const SmemBytes& w, uint32_t o, int bl
         }
     }
     const int e = exponent_of(top);
-    return {pow2(e - 15), e};
+    return {pow2(e - 15), e, head};
+}
+
+// 6-bit field b (0-7) of a Q4_K header: low six bits of byte b of `first` for b < 4; else four low bits of byte b - 4 of
+// `second` under the two top bits of that byte of `top`.
+__device__ __forceinline__ uint32_t six_bits(int b, uint32_t first, uint32_t second, uint32_t top) {
+    const int sh = 8 * (b & 3);
+    return b < 4 ? (first >> sh) & 63u : ((second >> sh) & 15u) | (((top >> sh) >> 6) & 3u) << 4;
 }
 
 // Block kb of a row's chunk as hi and lo f16 words in K order.
@@ -243,10 +279,8 @@ __device__ __forceinline__ void convert_block(const SmemBytes& w, uint32_t o, in
     if constexpr (Lay<WT>::KQ) {
         float s0, s1;
         if constexpr (WT == QMM_Q4_K || WT == QMM_Q5_K) {
-            // 6-bit scales: bytes 0-3 (and their two top bits for 4-7, whose low bits are in bytes 8-11)
-            const float d = h2f(w.u16(o)) * pow2(15 - row.e);
-            const uint32_t a = w.base[o + 4 + (kb & 3)];
-            const uint32_t sc = kb < 4 ? a & 63u : (w.base[o + 8 + kb] & 15u) | ((a >> 6) << 4);
+            const float d = h2f(row.head.x) * pow2(15 - row.e);
+            const uint32_t sc = six_bits(kb, row.head.y, row.head.w, row.head.y);
             s0 = s1 = d * (float)sc;
         } else if constexpr (WT == QMM_Q2_K) {
             const float d = h2f(w.u16(o + 80)) * pow2(15 - row.e);
@@ -274,34 +308,38 @@ __device__ __forceinline__ void convert_block(const SmemBytes& w, uint32_t o, in
     }
 }
 
-// The chunk's minimums over 16 groups of 16 values: what an activation group's sum is multiplied by, as hi and lo (for
-// Q4_1 and Q5_1 the minimum is an f16 and lo is not used).
+// The chunk's minimums over 16 groups of 16 values (with what the codes gave away), as hi and lo: what an activation
+// group's sum is multiplied by.
 template <int WT>
 __device__ __forceinline__ void convert_min(const SmemBytes& w, uint32_t o, int blocks, const WRow& row, uint32_t (&hi)[8],
                                             uint32_t (&lo)[8]) {
+    const float f = pow2(15 - row.e);
+    constexpr float C = (float)center<WT>();
     if constexpr (WT == QMM_Q4_1 || WT == QMM_Q5_1) {
-        const uint32_t f = h2_dup(pow2_half(15 - row.e));
 #pragma unroll
         for (int b = 0; b < 8; b++) {
-            hi[b] = b < blocks ? h2_mul(h2_dup(w.u16(o + Fmt<WT>::BB * b + 2)), f) : 0u;
-            lo[b] = 0u;
+            const uint32_t dm = b < blocks ? w.w32(o + Fmt<WT>::BB * b) : 0u;
+            split2(fmaf(C, h2f(dm), h2f(dm >> 16)) * f, &hi[b], &lo[b]);
         }
     } else if constexpr (WT == QMM_Q4_K || WT == QMM_Q5_K) {
-        const float d = -(h2f(w.u16(o + 2)) * pow2(15 - row.e));
-        const uint32_t y = w.w32(o + 8), z = w.w32(o + 12);
-        const uint32_t m0 = y & 0x3F3F3F3Fu, m1 = ((z >> 4) & 0x0F0F0F0Fu) | ((y >> 2) & 0x30303030u);
+        const float d = C * (h2f(row.head.x) * f), dm = h2f(row.head.x >> 16) * f;
 #pragma unroll
-        for (int b = 0; b < 8; b++) split2(d * (float)byte_of(b < 4 ? m0 : m1, b & 3), &hi[b], &lo[b]);
+        for (int b = 0; b < 8; b++) {
+            const float sc = (float)six_bits(b, row.head.y, row.head.w, row.head.y);
+            const float mn = (float)six_bits(b, row.head.z, row.head.w >> 4, row.head.z);
+            split2(fmaf(d, sc, -(dm * mn)), &hi[b], &lo[b]);
+        }
     } else if constexpr (WT == QMM_Q2_K) {
-        const float d = -(h2f(w.u16(o + 82)) * pow2(15 - row.e));
+        const uint32_t dd = w.w32(o + 80);
+        const float d = C * (h2f(dd) * f), dm = h2f(dd >> 16) * f;
         uint32_t sc[4];
         w.words_aligned<4>(o, sc);
 #pragma unroll
         for (int b = 0; b < 8; b++) {
             const uint32_t two = sc[b >> 1] >> (16 * (b & 1));
             uint32_t h0, l0, h1, l1;
-            split2(d * (float)((two >> 4) & 15u), &h0, &l0);
-            split2(d * (float)((two >> 12) & 15u), &h1, &l1);
+            split2(fmaf(d, (float)(two & 15u), -(dm * (float)((two >> 4) & 15u))), &h0, &l0);
+            split2(fmaf(d, (float)((two >> 8) & 15u), -(dm * (float)((two >> 12) & 15u))), &h1, &l1);
             hi[b] = (h0 & 0xFFFFu) | (h1 << 16), lo[b] = (l0 & 0xFFFFu) | (l1 << 16);
         }
     }
@@ -331,8 +369,8 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
     float* const sx = reinterpret_cast<float*>(smem + L::OFF_SX);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < L::WST; i++) mbar_init(bars.w_full(i), 1), mbar_init(bars.w_empty(i), CONV);
-        for (int i = 0; i < XST; i++) mbar_init(bars.x_full(i), 1), mbar_init(bars.x_empty(i), XWARPS);
+        for (int i = 0; i < L::WST; i++) mbar_init(bars.w_full(i), 32), mbar_init(bars.w_empty(i), CONV);
+        for (int i = 0; i < XST; i++) mbar_init(bars.x_full(i), XCOPIES * 32), mbar_init(bars.x_empty(i), XWARPS);
         for (int i = 0; i < W_SLOTS; i++) mbar_init(bars.w_op(i), 4), mbar_init(bars.done(i), 1);
         for (int i = 0; i < L::X_SLOTS; i++) mbar_init(bars.x_op(i), XWARPS);
         for (int i = 0; i < 2; i++) mbar_init(bars.acc_full(i), 1), mbar_init(bars.acc_empty(i), CONV);
@@ -358,7 +396,6 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
     const int ntiles = *a.ntiles * nt;
     const uint64_t rb = (uint64_t)(a.K / Fmt<WT>::BV) * Fmt<WT>::BB;
     const uint64_t total = (uint64_t)a.E * (uint64_t)N * rb;
-    const uint64_t total_al = total & ~15ull;
     auto blocks_of = [&](int c) { return L::KQ ? 8 : min(8, nb - 8 * c); };
     // the weight row of tile row r (rows behind the last repeat it)
     auto weight_row = [&](const ExpertTile& t, int n0, int r) {
@@ -366,250 +403,33 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
         return (int64_t)t.expert * N + n;
     };
 
-    if (warp == WCOPY) {
-        // ------------------------------------------------------------ the weight rows' bytes
-        uint32_t gc = 0;
-        bool ok = true;
-        for (int ti = blockIdx.x; ti < ntiles && ok; ti += gridDim.x) {
-            const ExpertTile t = a.tiles[ti / nt];
-            const int n0 = ti % nt * NROWS;
-            uint64_t row[4];
-            const uint8_t* base[4];
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int r = 32 * i + lane;
-                row[i] = (uint64_t)weight_row(t, n0, r) * rb;
-                base[i] = GATED && (r & 1) ? a.W1 : a.W0;
-            }
-            for (int c = 0; c < nchunks; c++, gc++) {
-                const int s = (int)(gc % L::WST);
-                if (gc >= L::WST && !warp_wait(bars.w_empty(s), (uint32_t)(gc / L::WST - 1) & 1u, abort_flag)) {
-                    ok = false;
-                    break;
-                }
-                const int blocks = blocks_of(c);
-                const uint32_t bytes = L::KQ ? L::CHUNK : blocks * Fmt<WT>::BB;
-                uint64_t a0[4];
-                uint32_t len[4], sum = 0;
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const uint64_t g0 = row[i] + (uint64_t)c * L::CHUNK;
-                    a0[i] = g0 & ~15ull;
-                    uint64_t a1 = (g0 + bytes + 15ull) & ~15ull;
-                    if (a1 > total_al) a1 = total_al;
-                    len[i] = a1 > a0[i] ? (uint32_t)(a1 - a0[i]) : 0u;
-                    if (!QMM_IN_BOUNDS(g_expert_mma_error, len[i], L::PITCH + 1)) len[i] = 0;
-                    sum += len[i];
-                }
-                sum = __reduce_add_sync(0xffffffffu, sum);
-                if (lane == 0) mbar_arrive_expect_tx(bars.w_full(s), sum);
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 4; i++)
-                    if (len[i])
-                        bulk_g2s_nohint(sbase + L::OFF_W + (uint32_t)((s * BM + 32 * i + lane) * L::PITCH), base[i] + a0[i], len[i],
-                                        bars.w_full(s));
-            }
-        }
-        // after a timeout: the copies in flight land before the CTA ends
-        if (!ok && lane == 0)
-            for (uint32_t g = gc > L::WST ? gc - L::WST : 0; g < gc; g++)
-                mbar_wait_bounded(bars.w_full((int)(g % L::WST)), (uint32_t)(g / L::WST) & 1u, kWaitLimitNs);
-    } else if (warp == XCOPY) {
-        // ------------------------------------------------------------ the activation rows' records
-        uint32_t gc = 0;
-        bool ok = true;
-        for (int ti = blockIdx.x; ti < ntiles && ok; ti += gridDim.x) {
-            const ExpertTile t = a.tiles[ti / nt];
-            const uint8_t* src[4];
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int r = 32 * i + lane;
-                const int64_t slot = r < t.count ? a.order[t.first + r] : 0;
-                src[i] = a.records + (slot / a.per_row) * (int64_t)nchunks * kRecord;
-            }
-            for (int c = 0; c < nchunks; c++, gc++) {
-                const int s = (int)(gc % XST);
-                if (gc >= XST && !warp_wait(bars.x_empty(s), (uint32_t)(gc / XST - 1) & 1u, abort_flag)) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) mbar_arrive_expect_tx(bars.x_full(s), (uint32_t)(t.count * kRecord));
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 4; i++)
-                    if (32 * i + lane < t.count)
-                        bulk_g2s_nohint(sbase + L::OFF_X + (uint32_t)(s * L::XSTAGE + (32 * i + lane) * kRecord),
-                                        src[i] + (int64_t)c * kRecord, kRecord, bars.x_full(s));
-            }
-        }
-        if (!ok && lane == 0)
-            for (uint32_t g = gc > XST ? gc - XST : 0; g < gc; g++)
-                mbar_wait_bounded(bars.x_full((int)(g % XST)), (uint32_t)(g / XST) & 1u, kWaitLimitNs);
-    } else if (warp == MMA_WARP) {
-        // ------------------------------------------------------------ the MMAs
-        if (lane == 0) {
-            uint32_t gc = 0;
-            int64_t n = 0;
-            bool ok = true;
-            for (int ti = blockIdx.x; ti < ntiles && ok; ti += gridDim.x) {
-                const int cols = (a.tiles[ti / nt].count + 15) & ~15;
-                const uint32_t idesc = instr_desc_f16(BM, cols);
-                for (int c = 0; c < nchunks && ok; c++, gc++) {
-                    const int blocks = blocks_of(c);
-                    const uint32_t d = tmem + (uint32_t)((gc & 1) * kTileRows);
-                    if (gc >= 2 && !wait_or_abort(bars.acc_empty((int)(gc & 1)), (uint32_t)(gc / 2 - 1) & 1u, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    uint32_t more = 0;
-                    for (int i = 0; i < blocks + (L::MIN ? 1 : 0); i++, n++) {
-                        const int ws = (int)(n % W_SLOTS), xs = (int)(n % L::X_SLOTS);
-                        if (!wait_or_abort(bars.w_op(ws), (uint32_t)(n / W_SLOTS) & 1u, abort_flag) ||
-                            !wait_or_abort(bars.x_op(xs), (uint32_t)(n / L::X_SLOTS) & 1u, abort_flag)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint32_t ah = tmem + (uint32_t)(A_COL0 + ws * 32);
-                        const uint64_t xh = smem_desc(sbase + L::OFF_OP + (uint32_t)(xs * L::XTERMS * XOP), 128, 512);
-                        const uint64_t xl = xh + (XOP >> 4);
-                        if (L::MIN && i == blocks) {
-                            mma_f16_ts(d, ah, xh, idesc, more);
-                            if constexpr (L::KQ) mma_f16_ts(d, ah + 16, xh, idesc, 1);
-                            else mma_f16_ts(d, ah, xl, idesc, 1);
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 2; k++) {
-                                mma_f16_ts(d, ah + 8 * k, xh + k * (256 >> 4), idesc, more);
-                                more = 1;
-                                mma_f16_ts(d, ah + 16 + 8 * k, xh + k * (256 >> 4), idesc, 1);
-                                if constexpr (!L::KQ) mma_f16_ts(d, ah + 8 * k, xl + k * (256 >> 4), idesc, 1);
-                            }
-                        }
-                        mma_commit(bars.done((int)n));
-                    }
-                    if (ok) mma_commit(bars.acc_full((int)(gc & 1)));
-                }
-            }
-            // the last commits land before the CTA ends
-            for (uint32_t i = n > 8 ? n - 8 : 0; i < n; i++)
-                mbar_wait_bounded(bars.done((int)i), (uint32_t)(i / 8) & 1u, kWaitLimitNs);
-        }
-    } else if (warp >= XW0) {
-        // ------------------------------------------------------------ activation operands
-        const int x = warp - XW0;
-        uint32_t gc = 0, n = 0;
-        bool ok = true;
-        for (int ti = blockIdx.x; ti < ntiles && ok; ti += gridDim.x) {
-            const int count = a.tiles[ti / nt].count;
-            const int ng = (count + 31) / 32;  // row groups: block i of group g belongs to warp (i ng + g) % 4
-            for (int c = 0; c < nchunks && ok; c++, gc++) {
-                const int s = (int)(gc % XST), blocks = blocks_of(c);
-                if (!warp_wait(bars.x_full(s), (uint32_t)(gc / XST) & 1u, abort_flag)) {
-                    ok = false;
-                    break;
-                }
-                const uint8_t* stage = smem + L::OFF_X + s * L::XSTAGE;
-                if (x < ng) {
-                    const uint8_t* rec = stage + (32 * x + lane) * kRecord;
-                    float scale;
-                    if constexpr (L::KQ) {
-                        scale = *reinterpret_cast<const float*>(rec + 256);
-                    } else {
-                        const uint4 d = *reinterpret_cast<const uint4*>(rec + 256);
-                        const uint32_t m = __vmaxu2(__vmaxu2(d.x, d.y), __vmaxu2(d.z, d.w));
-                        scale = pow2(exponent_of(max(m & 0x7FFFu, (m >> 16) & 0x7FFFu)) - 15);
-                    }
-                    sx[(gc & (SX_RING - 1)) * kTileRows + 32 * x + lane] = scale;
-                }
-                for (int i = 0; i < blocks + (L::MIN ? 1 : 0); i++, n++) {
-                    const int xs = (int)(n % L::X_SLOTS);
-                    if (n >= L::X_SLOTS) {
-                        const uint32_t p = n - L::X_SLOTS;
-                        if (!warp_wait(bars.done((int)p), (uint32_t)(p / 8) & 1u, abort_flag)) {
-                            ok = false;
-                            break;
-                        }
-                    }
-                    uint8_t* op = smem + L::OFF_OP + xs * L::XTERMS * XOP;
-                    for (int g = 0; g < ng; g++) {
-                        if (((i * ng + g) & 3) != x) continue;
-                        const int r = 32 * g + lane;
-                        const uint8_t* rec = stage + r * kRecord;
-                        uint32_t f = 0;  // the power of two that the row's scales are over
-                        if constexpr (!L::KQ) {
-                            const uint4 d = *reinterpret_cast<const uint4*>(rec + 256);
-                            const uint32_t m = __vmaxu2(__vmaxu2(d.x, d.y), __vmaxu2(d.z, d.w));
-                            f = h2_dup(pow2_half(15 - exponent_of(max(m & 0x7FFFu, (m >> 16) & 0x7FFFu))));
-                        }
-                        if (L::MIN && i == blocks) {
-                            const uint4 s0 = *reinterpret_cast<const uint4*>(rec + 272), s1 = *reinterpret_cast<const uint4*>(rec + 288);
-                            uint32_t v[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-                            if constexpr (!L::KQ) {
-                                uint32_t lo[8];
-#pragma unroll
-                                for (int b = 0; b < 8; b++) {  // block b's two sums times its scale
-                                    const uint32_t d = h2_mul(h2_dup(*reinterpret_cast<const unsigned short*>(rec + 256 + 2 * b)), f);
-                                    const uint32_t h = h2_mul(d, v[b]);
-                                    lo[b] = h2_fma(d, v[b], h2_neg(h));
-                                    v[b] = h;
-                                }
-                                put_x(op + XOP, r, 0, lo);
-                                put_x(op + XOP, r, 1, lo + 4);
-                            }
-                            put_x(op, r, 0, v);
-                            put_x(op, r, 1, v + 4);
-                            continue;
-                        }
-                        const uint4 c0 = *reinterpret_cast<const uint4*>(rec + 32 * i), c1 = *reinterpret_cast<const uint4*>(rec + 32 * i + 16);
-                        const uint32_t cw[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-                        uint32_t v[16];
-#pragma unroll
-                        for (int b = 0; b < 8; b++) {
-                            const uint32_t w = cw[b] ^ 0x80808080u;
-                            v[2 * b] = h2_sub(bytes_to_h2(w, 0x5140), 0x64806480u);
-                            v[2 * b + 1] = h2_sub(bytes_to_h2(w, 0x7362), 0x64806480u);
-                        }
-                        if constexpr (!L::KQ) {
-                            const uint32_t d = h2_mul(h2_dup(*reinterpret_cast<const unsigned short*>(rec + 256 + 2 * i)), f);
-                            uint32_t lo[16];
-#pragma unroll
-                            for (int b = 0; b < 16; b++) {
-                                const uint32_t h = h2_mul(d, v[b]);
-                                lo[b] = h2_fma(d, v[b], h2_neg(h));
-                                v[b] = h;
-                            }
-#pragma unroll
-                            for (int kq = 0; kq < 4; kq++) put_x(op + XOP, r, kq, lo + 4 * kq);
-                        }
-#pragma unroll
-                        for (int kq = 0; kq < 4; kq++) put_x(op, r, kq, v + 4 * kq);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bars.x_op(xs));
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bars.x_empty(s));
-            }
-        }
-    } else {
+    if (warp < CONV) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_CONV));
         // ------------------------------------------------------------ weight operands, sums
         const int quad = warp & 3, grp = warp >> 2;
         const int r = quad * 32 + lane;  // tile row
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
         float acc[32];
-        uint32_t gc = 0, n = 0;
-        float last_scale = 0.0f;  // of the chunk before
+#pragma unroll
+        for (int j = 0; j < 32; j++) acc[j] = 0.0f;
+        uint32_t gc = 0, n = 0, folded = 0;  // chunks, items, accumulations
         bool ok = true;
-        // adds the sums of chunk g (times its scales) to the registers
-        auto fold = [&](uint32_t g, int count, float scale) {
-            if (!warp_wait(bars.acc_full((int)(g & 1)), (uint32_t)(g / 2) & 1u, abort_flag)) return false;
+        // The chunk before: its sums are added while the MMAs of the next run, also across tiles.
+        bool pending = false, pending_last = false;
+        float pending_scale = 0.0f;
+        int pending_halves = 0, pending_n0 = 0;
+        ExpertTile pending_tile = {};
+        // adds the next accumulation of the pending chunk, times its scales, to the registers
+        auto fold = [&] {
+            const uint32_t buf = folded & 1;
+            if (!warp_wait(bars.acc_full((int)buf), (folded / 2) & 1u, abort_flag)) return false;
+            folded++;
             tc_fence_after();
-            if (grp * 32 < count) {
-                const uint32_t cols = lanes + (uint32_t)((g & 1) * kTileRows + grp * 32);
-                const float4* s4 = reinterpret_cast<const float4*>(sx + (g & (SX_RING - 1)) * kTileRows + grp * 32);
+            if (grp * 32 < pending_tile.count) {
+                const uint32_t cols = lanes + buf * kTileRows + (uint32_t)(grp * 32);
+                const uint4* s4 = reinterpret_cast<const uint4*>(sx + ((gc - 1) & (SX_RING - 1)) * kTileRows + grp * 32);
+                const uint32_t sb = __float_as_uint(pending_scale);
+                const uint64_t s2 = f2_pack(sb, sb);
                 uint32_t v[2][8];
                 tmem_ld8(cols, v[0]);
                 tmem_ld_wait_regs8(v[0]);
@@ -618,24 +438,27 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
                     if (q < 3) tmem_ld8(cols + 8 * (q + 1), v[(q + 1) & 1]);
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
-                        const float4 s = s4[2 * q + h];
+                        const uint4 s = s4[2 * q + h];
+                        const uint64_t p0 = f2_mul(s2, f2_pack(s.x, s.y)), p1 = f2_mul(s2, f2_pack(s.z, s.w));
                         const uint32_t* u = v[q & 1] + 4 * h;
                         float* o = acc + 8 * q + 4 * h;
-                        o[0] = fmaf(__uint_as_float(u[0]), scale * s.x, o[0]);
-                        o[1] = fmaf(__uint_as_float(u[1]), scale * s.y, o[1]);
-                        o[2] = fmaf(__uint_as_float(u[2]), scale * s.z, o[2]);
-                        o[3] = fmaf(__uint_as_float(u[3]), scale * s.w, o[3]);
+                        o[0] = fmaf(__uint_as_float(u[0]), __uint_as_float((uint32_t)p0), o[0]);
+                        o[1] = fmaf(__uint_as_float(u[1]), __uint_as_float((uint32_t)(p0 >> 32)), o[1]);
+                        o[2] = fmaf(__uint_as_float(u[2]), __uint_as_float((uint32_t)p1), o[2]);
+                        o[3] = fmaf(__uint_as_float(u[3]), __uint_as_float((uint32_t)(p1 >> 32)), o[3]);
                     }
                     if (q < 3) tmem_ld_wait_regs8(v[(q + 1) & 1]);
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bars.acc_empty((int)(g & 1)));
+            if (lane == 0) mbar_arrive(bars.acc_empty((int)buf));
             return true;
         };
         // writes the finished sums of a tile
-        auto store = [&](const ExpertTile& t, int n0) {
+        auto finish = [&] {
+            const ExpertTile& t = pending_tile;
+            const int n0 = pending_n0;
             if constexpr (GATED) {
                 const int col = n0 + quad * 16 + (lane >> 1);
 #pragma unroll
@@ -659,63 +482,275 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
                     if (col < N && QMM_IN_BOUNDS(g_expert_mma_error, o, a.out_values)) a.y[o] = acc[j];
                 }
             }
+#pragma unroll
+            for (int j = 0; j < 32; j++) acc[j] = 0.0f;
+        };
+        // the operand of item n + i of the chunk, once its slot's last MMAs are done
+        auto put = [&](const SmemBytes& w, uint32_t o, int blocks, const WRow& row, int i) {
+            const uint32_t m = n + i;
+            if (m >= W_SLOTS && !warp_wait(bars.done((int)m), (m / 8 - 1) & 1u, abort_flag)) return false;
+            const uint32_t slot = lanes + (uint32_t)A_COL0 + m % W_SLOTS * 32;
+            tc_fence_after();
+            if (!L::MIN || i < blocks) {
+                uint32_t hi[16], lo[16];
+                convert_block<WT>(w, o, i, row, hi, lo);
+                tmem_st16(slot, hi);
+                tmem_st16(slot + 16, lo);
+            } else if constexpr (L::MIN) {
+                uint32_t hi[8], lo[8];
+                convert_min<WT>(w, o, blocks, row, hi, lo);
+                tmem_st8(slot, hi);
+                tmem_st8(slot + 16, lo);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars.w_op((int)(m % W_SLOTS)));
+            return true;
         };
         for (int ti = blockIdx.x; ti < ntiles && ok; ti += gridDim.x) {
             const ExpertTile t = a.tiles[ti / nt];
             const int n0 = ti % nt * NROWS;
             const uint64_t row = (uint64_t)weight_row(t, n0, r) * rb;
-#pragma unroll
-            for (int j = 0; j < 32; j++) acc[j] = 0.0f;
-            for (int c = 0; c < nchunks && ok; c++, gc++) {
-                const int s = (int)(gc % L::WST), blocks = blocks_of(c);
-                if (!warp_wait(bars.w_full(s), (uint32_t)(gc / L::WST) & 1u, abort_flag)) {
-                    ok = false;
-                    break;
-                }
-                uint8_t* const buf = smem + L::OFF_W + (s * BM + r) * L::PITCH;
-                const uint64_t g0 = row + (uint64_t)c * L::CHUNK;
-                const uint32_t o = (uint32_t)(g0 & 15ull);
-                if (total > total_al && g0 + (L::KQ ? L::CHUNK : blocks * Fmt<WT>::BB) == total) {
-                    // the last < 16 bytes of the weights: not reachable by a 16-byte bulk copy
-                    const uint8_t* W = GATED && (r & 1) ? a.W1 : a.W0;
-                    for (uint64_t i = total_al; i < total; i++)
-                        if (QMM_IN_BOUNDS(g_expert_mma_error, i - (g0 & ~15ull), L::PITCH)) buf[i - (g0 & ~15ull)] = W[i];
-                }
-                const SmemBytes w{buf};
+            for (int c = 0; c < nchunks; c++, gc++) {
+                const uint32_t s = gc % L::WST;
+                const int blocks = blocks_of(c);
+                // the first half of the chunk before, for which the MMAs of this one wait
+                if (pending && pending_halves == 2 && !(ok = fold())) break;
+                if (!(ok = warp_wait(bars.w_full(s), (gc / L::WST) & 1u, abort_flag))) break;
+                const SmemBytes w{smem + L::OFF_W + (s * BM + r) * L::PITCH};
+                const uint32_t o = (uint32_t)(row + (uint64_t)c * L::CHUNK) & 15u;
                 const WRow ws = row_scale<WT>(w, o, blocks);
-                for (int i = 0; i < blocks + (L::MIN ? 1 : 0); i++) {
-                    if ((i < blocks ? i >> 1 : (int)(gc & 3)) != grp) continue;
-                    const uint32_t m = n + i;
-                    if (m >= W_SLOTS && !warp_wait(bars.done((int)m), (uint32_t)(m / 8 - 1) & 1u, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t slot = lanes + (uint32_t)(A_COL0 + (int)(m % W_SLOTS) * 32);
-                    tc_fence_after();
-                    if (i < blocks) {
-                        uint32_t hi[16], lo[16];
-                        convert_block<WT>(w, o, i, ws, hi, lo);
-                        tmem_st16(slot, hi);
-                        tmem_st16(slot + 16, lo);
-                    } else if constexpr (L::MIN) {
-                        uint32_t hi[8], lo[8];
-                        convert_min<WT>(w, o, blocks, ws, hi, lo);
-                        tmem_st8(slot, hi);
-                        if constexpr (L::KQ) tmem_st8(slot + 16, lo);
-                    }
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bars.w_op((int)(m % W_SLOTS)));
-                }
+                for (int i = 2 * grp; i < 2 * grp + 2 && ok; i++)
+                    if (L::KQ || i < blocks) ok = put(w, o, blocks, ws, i);
+                if (L::MIN && ok && (int)(gc & 3) == grp) ok = put(w, o, blocks, ws, blocks);
+                if (!ok) break;
                 n += blocks + (L::MIN ? 1 : 0);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bars.w_empty(s));
-                if (ok && c > 0) ok = fold(gc - 1, t.count, last_scale);
-                last_scale = ws.scale;
+                if (pending) {
+                    if (!(ok = fold())) break;
+                    if (pending_last) finish();
+                }
+                pending = true, pending_last = c + 1 == nchunks, pending_scale = ws.scale;
+                pending_halves = blocks > L::FOLD ? 2 : 1, pending_tile = t, pending_n0 = n0;
             }
-            if (ok) ok = fold(gc - 1, t.count, last_scale);
-            if (ok) store(t, n0);
+        }
+        if (ok && pending && (pending_halves == 1 || fold()) && fold()) finish();
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
+        if (warp == WCOPY) {
+            // ------------------------------------------------------------ the weight rows' bytes
+            // Piece i of a chunk: 16 bytes, word i % WORDS of the aligned superset of tile row i / WORDS.  Bytes behind the
+            // last weight are not read.
+            uint32_t gc = 0;
+            bool ok = true;
+            for (int ti = blockIdx.x; ti < ntiles && ok; ti += gridDim.x) {
+                const int expert = a.tiles[ti / nt].expert, n0 = ti % nt * NROWS;
+                const uint64_t first = ((uint64_t)expert * N + n0) * rb;  // of the tile's rows
+                const uint32_t last = (uint32_t)(N - 1 - n0);
+                for (int c = 0; c < nchunks; c++, gc++) {
+                    const uint32_t s = gc % L::WST;
+                    if (gc >= L::WST && !warp_wait(bars.w_empty(s), (gc / L::WST - 1) & 1u, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bytes = L::KQ ? L::CHUNK : blocks_of(c) * Fmt<WT>::BB;
+                    const uint64_t at = first + (uint64_t)c * L::CHUNK;
+                    const uint32_t dst = sbase + L::OFF_W + s * (BM * L::PITCH);
+#pragma unroll 4
+                    for (int i = lane; i < BM * L::WORDS; i += 32) {
+                        const uint32_t r = (uint32_t)i / L::WORDS, p = (uint32_t)i % L::WORDS;
+                        const uint64_t g0 = at + (uint64_t)min(GATED ? r >> 1 : r, last) * rb;
+                        const uint64_t src = (g0 & ~15ull) + 16 * p;
+                        if (src >= g0 + bytes || !QMM_IN_BOUNDS(g_expert_mma_error, src, total)) continue;
+                        const uint64_t left = total - src;
+                        copy16(dst + r * L::PITCH + 16 * p, (GATED && (r & 1) ? a.W1 : a.W0) + src, left < 16 ? (uint32_t)left : 16u);
+                    }
+                    copies_arrive(bars.w_full(s));
+                }
+            }
+            copies_wait();
+        } else if (warp >= XCOPY) {
+            // ------------------------------------------------------------ the activation rows' records
+            // Warp j has the tile's rows j, j + 2, ...; lanes keep where two of them lie each.
+            const int me = warp - XCOPY;
+            uint32_t gc = 0;
+            bool ok = true;
+            for (int ti = blockIdx.x; ti < ntiles && ok; ti += gridDim.x) {
+                const ExpertTile t = a.tiles[ti / nt];
+                const int mine = (t.count - me + XCOPIES - 1) / XCOPIES;
+                uint32_t from[2];
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    const int r = XCOPIES * (lane + 32 * i) + me;
+                    from[i] = r < t.count ? (uint32_t)(a.order[t.first + r] / a.per_row) * (uint32_t)nchunks : 0u;
+                }
+                for (int c = 0; c < nchunks; c++, gc++) {
+                    const uint32_t s = gc % XST;
+                    if (gc >= XST && !warp_wait(bars.x_empty(s), (gc / XST - 1) & 1u, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t dst = sbase + L::OFF_X + s * L::XSTAGE;
+                    const int pieces = mine * (kRecord / 16);
+#pragma unroll 2
+                    for (int i0 = 0; i0 < pieces; i0 += 32) {  // the whole warp
+                        const uint32_t i = (uint32_t)(i0 + lane), q = i / (kRecord / 16), p = i % (kRecord / 16);
+                        const uint32_t f0 = __shfl_sync(0xffffffffu, from[0], q & 31), f1 = __shfl_sync(0xffffffffu, from[1], q & 31);
+                        if ((int)i < pieces)
+                            copy16(dst + (XCOPIES * q + me) * kRecord + 16 * p,
+                                   a.records + ((uint64_t)(q < 32 ? f0 : f1) + c) * kRecord + 16 * p, 16u);
+                    }
+                    copies_arrive(bars.x_full(s));
+                }
+            }
+            copies_wait();
+        } else if (warp == MMA_WARP) {
+            // ------------------------------------------------------------ the MMAs
+            if (lane == 0) {
+                uint32_t acc = 0, n = 0;  // accumulations, items
+                bool ok = true;
+                for (int ti = blockIdx.x; ti < ntiles && ok; ti += gridDim.x) {
+                    const int cols = (a.tiles[ti / nt].count + 15) & ~15;
+                    const uint32_t idesc = instr_desc_f16(BM, cols);
+                    for (int c = 0; c < nchunks && ok; c++) {
+                        const int blocks = blocks_of(c), items = blocks + (L::MIN ? 1 : 0);
+                        uint32_t d = 0, more = 0;
+                        for (int i = 0; i < items; i++, n++) {
+                            if (i % L::FOLD == 0 && i < blocks) {  // another accumulation
+                                d = tmem + (acc & 1) * kTileRows;
+                                more = 0;
+                                if (acc >= 2 && !wait_or_abort(bars.acc_empty((int)(acc & 1)), (acc / 2 - 1) & 1u, abort_flag)) {
+                                    ok = false;
+                                    break;
+                                }
+                            }
+                            const int ws = (int)(n % W_SLOTS), xs = (int)(n % L::X_SLOTS);
+                            if (!wait_or_abort(bars.w_op(ws), (n / W_SLOTS) & 1u, abort_flag) ||
+                                !wait_or_abort(bars.x_op(xs), (n / L::X_SLOTS) & 1u, abort_flag)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            const uint32_t ah = tmem + (uint32_t)(A_COL0 + ws * 32);
+                            const uint64_t xh = smem_desc(sbase + L::OFF_OP + (uint32_t)(xs * L::XTERMS * XOP), 128, 512);
+                            const uint64_t xl = xh + (XOP >> 4);
+#pragma unroll
+                            for (int k = 0; k < 2; k++) {
+                                if (k == 1 && L::MIN && i == blocks) break;  // the minimums: 16 groups
+                                mma_f16_ts(d, ah + 16 + 8 * k, xh + k * (256 >> 4), idesc, more);
+                                more = 1;
+                                if constexpr (!L::KQ) mma_f16_ts(d, ah + 8 * k, xl + k * (256 >> 4), idesc, 1);
+                                mma_f16_ts(d, ah + 8 * k, xh + k * (256 >> 4), idesc, 1);
+                            }
+                            mma_commit(bars.done((int)n));
+                            if (i + 1 == items || ((i + 1) % L::FOLD == 0 && i + 1 < blocks)) mma_commit(bars.acc_full((int)(acc++ & 1)));
+                        }
+                    }
+                }
+                // the last commits land before the CTA ends
+                for (uint32_t i = n > 8 ? n - 8 : 0; i < n; i++)
+                    mbar_wait_bounded(bars.done((int)i), (uint32_t)(i / 8) & 1u, kWaitLimitNs);
+            }
+        } else if (warp >= XW0) {
+            // ------------------------------------------------------------ activation operands
+            const int x = warp - XW0;
+            uint32_t gc = 0, n = 0;
+            bool ok = true;
+            for (int ti = blockIdx.x; ti < ntiles && ok; ti += gridDim.x) {
+                const int count = a.tiles[ti / nt].count;
+                const int ng = (count + 31) / 32;  // row groups: block i of group g belongs to warp (i ng + g) % 4
+                for (int c = 0; c < nchunks && ok; c++, gc++) {
+                    const int s = (int)(gc % XST), blocks = blocks_of(c);
+                    if (!warp_wait(bars.x_full(s), (uint32_t)(gc / XST) & 1u, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint8_t* stage = smem + L::OFF_X + s * L::XSTAGE;
+                    if (x < ng) {
+                        const uint8_t* rec = stage + (32 * x + lane) * kRecord;
+                        float scale;
+                        if constexpr (L::KQ) {
+                            scale = *reinterpret_cast<const float*>(rec + 256);
+                        } else {
+                            const uint4 d = *reinterpret_cast<const uint4*>(rec + 256);
+                            const uint32_t m = __vmaxu2(__vmaxu2(d.x, d.y), __vmaxu2(d.z, d.w));
+                            scale = pow2(exponent_of(max(m & 0x7FFFu, (m >> 16) & 0x7FFFu)) - 15);
+                        }
+                        sx[(gc & (SX_RING - 1)) * kTileRows + 32 * x + lane] = scale;
+                    }
+                    for (int i = 0; i < blocks + (L::MIN ? 1 : 0); i++, n++) {
+                        const int xs = (int)(n % L::X_SLOTS);
+                        if (n >= L::X_SLOTS) {
+                            const uint32_t p = n - L::X_SLOTS;
+                            if (!warp_wait(bars.done((int)p), (uint32_t)(p / 8) & 1u, abort_flag)) {
+                                ok = false;
+                                break;
+                            }
+                        }
+                        uint8_t* op = smem + L::OFF_OP + xs * L::XTERMS * XOP;
+                        for (int g = 0; g < ng; g++) {
+                            if (((i * ng + g) & 3) != x) continue;
+                            const int r = 32 * g + lane;
+                            const uint8_t* rec = stage + r * kRecord;
+                            uint32_t f = 0;  // the power of two that the row's scales are over
+                            if constexpr (!L::KQ) {
+                                const uint4 d = *reinterpret_cast<const uint4*>(rec + 256);
+                                const uint32_t m = __vmaxu2(__vmaxu2(d.x, d.y), __vmaxu2(d.z, d.w));
+                                f = h2_dup(pow2_half(15 - exponent_of(max(m & 0x7FFFu, (m >> 16) & 0x7FFFu))));
+                            }
+                            if (L::MIN && i == blocks) {
+                                const uint4 s0 = *reinterpret_cast<const uint4*>(rec + 272), s1 = *reinterpret_cast<const uint4*>(rec + 288);
+                                uint32_t v[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+                                if constexpr (!L::KQ) {
+                                    uint32_t lo[8];
+#pragma unroll
+                                    for (int b = 0; b < 8; b++) {  // block b's two sums times its scale
+                                        const uint32_t d = h2_mul(h2_dup(*reinterpret_cast<const unsigned short*>(rec + 256 + 2 * b)), f);
+                                        const uint32_t h = h2_mul(d, v[b]);
+                                        lo[b] = h2_fma(d, v[b], h2_neg(h));
+                                        v[b] = h;
+                                    }
+                                    put_x(op + XOP, r, 0, lo);
+                                    put_x(op + XOP, r, 1, lo + 4);
+                                }
+                                put_x(op, r, 0, v);
+                                put_x(op, r, 1, v + 4);
+                                continue;
+                            }
+                            const uint4 c0 = *reinterpret_cast<const uint4*>(rec + 32 * i), c1 = *reinterpret_cast<const uint4*>(rec + 32 * i + 16);
+                            const uint32_t cw[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+                            uint32_t v[16];
+#pragma unroll
+                            for (int b = 0; b < 8; b++) {
+                                const uint32_t w = cw[b];
+                                v[2 * b] = h2_sub(bytes_to_h2(w, 0x5140), 0x64806480u);
+                                v[2 * b + 1] = h2_sub(bytes_to_h2(w, 0x7362), 0x64806480u);
+                            }
+                            if constexpr (!L::KQ) {
+                                const uint32_t d = h2_mul(h2_dup(*reinterpret_cast<const unsigned short*>(rec + 256 + 2 * i)), f);
+                                uint32_t lo[16];
+#pragma unroll
+                                for (int b = 0; b < 16; b++) {
+                                    const uint32_t h = h2_mul(d, v[b]);
+                                    lo[b] = h2_fma(d, v[b], h2_neg(h));
+                                    v[b] = h;
+                                }
+#pragma unroll
+                                for (int kq = 0; kq < 4; kq++) put_x(op + XOP, r, kq, lo + 4 * kq);
+                            }
+#pragma unroll
+                            for (int kq = 0; kq < 4; kq++) put_x(op, r, kq, v + 4 * kq);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bars.x_op(xs));
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bars.x_empty(s));
+                }
+            }
         }
     }
     tc_fence_before();
@@ -736,10 +771,13 @@ static qmm_status expert_mma_launch(const ExpertMma& a, int64_t tiles_most, cuda
     if (st != QMM_OK) return st;
     static PerDeviceOnce once;
     st = once.run(dev.device, [] {
-        return cudaFuncSetAttribute(em::expert_mma_kernel<WT, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) ==
-                       cudaSuccess
-                   ? QMM_OK
-                   : QMM_E_CUDA;
+        auto* f = em::expert_mma_kernel<WT, GATED>;
+        // the converters' registers come out of what the launch has
+        cudaFuncAttributes at;
+        if (cudaFuncGetAttributes(&at, f) != cudaSuccess) return QMM_E_CUDA;
+        if (at.numRegs * em::THREADS < em::CONV * 32 * em::REGS_CONV + (em::THREADS - em::CONV * 32) * em::REGS_OTHER)
+            return QMM_E_CUDA;
+        return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) == cudaSuccess ? QMM_OK : QMM_E_CUDA;
     });
     if (st != QMM_OK) return st;
     const int64_t most = tiles_most * ((a.N + (GATED ? 63 : 127)) / (GATED ? 64 : 128));

@@ -9,7 +9,7 @@
 namespace qmm {
 
 constexpr int kTileRows = 128;  // activation rows of a tile
-// 256 values of an activation row: 256 codes; 8 f16 scales (Q8_0) or one f32 (Q8_K) at 256; the codes' sums over groups of
+// 256 values of an activation row: 256 codes (plus 128); 8 f16 scales (Q8_0) or one f32 (Q8_K) at 256; the codes' sums over groups of
 // 16 as f16 (whole numbers up to 2048, exact) at 272.  19 16-byte words: neighbouring rows' words fall in other banks.
 constexpr int kRecord = 304;
 
