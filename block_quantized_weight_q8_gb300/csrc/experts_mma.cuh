@@ -12,14 +12,15 @@
 // activations' sums of 16 values: one further step of 16.
 //
 // A tile is 128 weight rows (gated: 64 rows of the gate's and of the up matrix, row by row, so that both sums of an
-// output lie in neighbouring lanes) by up to 128 rows of one expert; CTAs, one per SM, walk over the tiles.  Its warps:
+// output lie in neighbouring lanes) by up to 128 rows of one expert; CTAs, one per SM, walk over the tiles, and a tile's
+// last sums are added while the next one's operands are made.  The warps hand each other pairs of blocks (64 values):
 //   0-15   converters and epilogue: warp w has the 32 weight rows of lane quadrant w % 4 and of each chunk of 256 values
-//          the blocks 2 (w / 4) and 2 (w / 4) + 1, turned into f16 in its tensor-memory lanes; then, for the chunk before,
-//          the sums of 32 activation rows times its 32 weight rows, which it adds up in registers
-//   16-19  activation converters: 8-bit codes into the f16 operand in shared memory
-//   20     issues the MMAs
-//   21-23  copy the weight rows' and the activation rows' bytes, 16 at a time (a bulk copy for each row and chunk left the
-//          copying warp with 84 cycles a row, 10,800 a chunk where the MMAs take 2,200)
+//          pair w / 4, turned into f16 in its tensor-memory lanes; then, for the chunk before, the sums of 32 activation
+//          rows times its 32 weight rows, which it adds up in registers
+//   16-23  activation converters: 8-bit codes into the f16 operand in shared memory
+//   24     issues the MMAs
+//   25-27  copy the weight rows' and the activation rows' bytes, 16 at a time (a bulk copy for each row and chunk left
+//          the copying warp with 84 cycles a row)
 // Weights are read once per 128 rows of their expert; converting them, not the MMA, bounds tiles of few rows, and the
 // MMA's two or three terms those of many.
 #pragma once
@@ -37,17 +38,25 @@ static __device__ unsigned int g_expert_mma_error = 0;
 namespace em {
 
 constexpr int BM = 128;       // weight rows of a tile
-constexpr int CONV = 16, XW0 = CONV, XWARPS = 4, MMA_WARP = XW0 + XWARPS, WCOPY = MMA_WARP + 1, XCOPY = WCOPY + 1, XCOPIES = 2;
+constexpr int CONV = 16, XW0 = CONV, XWARPS = 8, MMA_WARP = XW0 + XWARPS, WCOPY = MMA_WARP + 1, XCOPY = WCOPY + 1, XCOPIES = 2;
 constexpr int THREADS = (XCOPY + XCOPIES) * 32;
-// Registers a thread: 768 threads start with 80; the converters, with their sums, go up to what the others give away.
-constexpr int REGS_CONV = 96, REGS_OTHER = 48;
-static_assert(THREADS == 768 && CONV * 32 * REGS_CONV + (THREADS - CONV * 32) * REGS_OTHER <= THREADS * 80, "registers");
-constexpr int W_SLOTS = 8;    // weight operands in tensor memory: 16 columns hi, 16 lo
+// Registers a thread: 896 threads start with 72; the converters, with their sums, go up to what the others give away.
+constexpr int REGS_CONV = 96, REGS_OTHER = 40;
+static_assert(THREADS == 896 && CONV * 32 * REGS_CONV + (THREADS - CONV * 32) * REGS_OTHER <= THREADS * 72, "registers");
+// Weight operands in tensor memory, one for a pair of blocks (a chunk's minimums take one too): each block's 16 columns of
+// hi and 16 of lo
+constexpr int SLOTS = 4, SLOT_COLS = 64;
+// "The MMAs of item n are done" is told on barrier n % 16.  A warp waits only for the items whose slots it takes over and
+// may skip others, so that a barrier of few phases could show it the parity of the phase before the one it means (seen
+// with 4: a slot taken over early, its barrier arrived at once too often).  A weight converter has added up all of the
+// chunk before last, an activation converter cannot be two chunks ahead of the other seven; either way what it waits for
+// is less than two chunks, 10 items, behind the last that is surely done.
+constexpr int DONE = 16;
 constexpr int A_COL0 = 2 * kTileRows;  // after two accumulators
-constexpr int XOP = kTileRows * 64;    // bytes of one term of an activation operand: 32 values of 128 rows
+constexpr int XOP = kTileRows * 64;    // bytes of one term of a block's activation operand: 32 values of 128 rows
 constexpr int XST = 2;        // stages of activation records
 constexpr int SX_RING = 8;    // chunks of activation scales
-static_assert(A_COL0 + W_SLOTS * 32 == 512, "tensor memory");
+static_assert(A_COL0 + SLOTS * SLOT_COLS == 512, "tensor memory");
 
 template <int WT>
 struct Lay {
@@ -55,25 +64,26 @@ struct Lay {
     static constexpr bool KQ = F::BV == 256;
     static constexpr bool MIN = WT == QMM_Q4_1 || WT == QMM_Q5_1 || WT == QMM_Q4_K || WT == QMM_Q5_K || WT == QMM_Q2_K;
     static constexpr int XTERMS = KQ ? 1 : 2;
-    static constexpr int X_SLOTS = KQ ? 8 : 4;
+    static constexpr int X_SLOTS = KQ ? 4 : 2;
+    static constexpr int XSLOT = 2 * XTERMS * XOP;  // a pair: block by block, hi then lo
     static constexpr int CHUNK = KQ ? F::BB : 8 * F::BB;  // bytes of a row's 256 values
     // a copied row: the 16-byte superset at any offset that blocks can have, an odd number of 16-byte words
     static constexpr int ALIGN = WT == QMM_Q4_K || WT == QMM_Q5_K ? 16 : WT == QMM_Q2_K || WT == QMM_Q4_1 ? 4 : WT == QMM_Q5_1 ? 8 : 2;
     static constexpr int WORDS = (CHUNK + 16 - ALIGN + 15) / 16;
     static constexpr int PITCH = 16 * (WORDS | 1);
-    // blocks of an accumulation: where activations have two terms, sums leave the tensor core twice as often
-    static constexpr int FOLD = KQ ? 8 : 4;
+    // pairs of an accumulation: where activations have two terms, sums leave the tensor core twice as often
+    static constexpr int FOLD = KQ ? 4 : 2;
     static constexpr int XSTAGE = kTileRows * kRecord;
-    static constexpr int FIXED = XST * XSTAGE + X_SLOTS * XTERMS * XOP + SX_RING * kTileRows * 4 + 512;
+    static constexpr int FIXED = XST * XSTAGE + X_SLOTS * XSLOT + SX_RING * kTileRows * 4 + 512;
     static constexpr int FIT = (232448 - 128 - FIXED) / (BM * PITCH);
     static constexpr int WST = FIT >= 4 ? 4 : 2;  // a power of two
     static_assert(WST >= 2, "two stages of weight rows");
     static constexpr int OFF_W = 0;
     static constexpr int OFF_X = OFF_W + WST * BM * PITCH;
     static constexpr int OFF_OP = OFF_X + XST * XSTAGE;
-    static constexpr int OFF_SX = OFF_OP + X_SLOTS * XTERMS * XOP;
+    static constexpr int OFF_SX = OFF_OP + X_SLOTS * XSLOT;
     static constexpr int OFF_BAR = OFF_SX + SX_RING * kTileRows * 4;
-    static constexpr int NBARS = 2 * WST + 2 * XST + W_SLOTS + X_SLOTS + W_SLOTS + 4;
+    static constexpr int NBARS = 2 * WST + 2 * XST + SLOTS + DONE + 4;
     static constexpr int OFF_TMEM = OFF_BAR + NBARS * 8;
     static constexpr int SMEM = OFF_TMEM + 16;
     static_assert(SMEM <= 232448 && OFF_OP % 128 == 0 && NBARS * 8 + 16 <= 512, "shared memory");
@@ -87,12 +97,10 @@ struct Bars {
     __device__ uint32_t w_empty(int s) const { return base + 8u * (L::WST + s); }           // converted
     __device__ uint32_t x_full(int s) const { return base + 8u * (2 * L::WST + s); }
     __device__ uint32_t x_empty(int s) const { return base + 8u * (2 * L::WST + XST + s); }
-    __device__ uint32_t w_op(int i) const { return base + 8u * (2 * L::WST + 2 * XST + i); }  // operand written
-    __device__ uint32_t x_op(int i) const { return base + 8u * (2 * L::WST + 2 * XST + W_SLOTS + i); }
-    // the MMAs of item n are done: barrier n % 8
-    __device__ uint32_t done(int n) const { return base + 8u * (2 * L::WST + 2 * XST + W_SLOTS + L::X_SLOTS + (n & 7)); }
-    __device__ uint32_t acc_full(int i) const { return base + 8u * (2 * L::WST + 2 * XST + 2 * W_SLOTS + L::X_SLOTS + i); }
-    __device__ uint32_t acc_empty(int i) const { return base + 8u * (2 * L::WST + 2 * XST + 2 * W_SLOTS + L::X_SLOTS + 2 + i); }
+    __device__ uint32_t op(int i) const { return base + 8u * (2 * L::WST + 2 * XST + i); }  // item n % 4: operands written
+    __device__ uint32_t done(uint32_t n) const { return base + 8u * (2 * L::WST + 2 * XST + SLOTS + n % DONE); }
+    __device__ uint32_t acc_full(int i) const { return base + 8u * (2 * L::WST + 2 * XST + SLOTS + DONE + i); }
+    __device__ uint32_t acc_empty(int i) const { return base + 8u * (2 * L::WST + 2 * XST + SLOTS + DONE + 2 + i); }
 };
 
 __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
@@ -351,6 +359,21 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
                  : "memory");
 }
 
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+// the f16 products of d and v, and what their rounding left
+__device__ __forceinline__ uint32_t times_scale(uint32_t v, uint32_t d, uint32_t* lo) {
+    const uint32_t h = h2_mul(d, v);
+    *lo = h2_fma(d, v, h2_neg(h));
+    return h;
+}
+
 // 16 bytes of an activation operand: values 8 kq .. 8 kq + 7 of row r
 __device__ __forceinline__ void put_x(uint8_t* op, int r, int kq, const uint32_t* v) {
     *reinterpret_cast<uint4*>(op + ((r >> 3) * 4 + kq) * 128 + (r & 7) * 16) = make_uint4(v[0], v[1], v[2], v[3]);
@@ -371,8 +394,9 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
     if (threadIdx.x == 0) {
         for (int i = 0; i < L::WST; i++) mbar_init(bars.w_full(i), 32), mbar_init(bars.w_empty(i), CONV);
         for (int i = 0; i < XST; i++) mbar_init(bars.x_full(i), XCOPIES * 32), mbar_init(bars.x_empty(i), XWARPS);
-        for (int i = 0; i < W_SLOTS; i++) mbar_init(bars.w_op(i), 4), mbar_init(bars.done(i), 1);
-        for (int i = 0; i < L::X_SLOTS; i++) mbar_init(bars.x_op(i), XWARPS);
+        // an operand: its four warps of weights, and four shares of activations
+        for (int i = 0; i < SLOTS; i++) mbar_init(bars.op(i), 8);
+        for (int i = 0; i < DONE; i++) mbar_init(bars.done(i), 1);
         for (int i = 0; i < 2; i++) mbar_init(bars.acc_full(i), 1), mbar_init(bars.acc_empty(i), CONV);
         *abort_flag = 0;
         fence_mbar_init();
@@ -485,47 +509,53 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
 #pragma unroll
             for (int j = 0; j < 32; j++) acc[j] = 0.0f;
         };
-        // the operand of item n + i of the chunk, once its slot's last MMAs are done
-        auto put = [&](const SmemBytes& w, uint32_t o, int blocks, const WRow& row, int i) {
-            const uint32_t m = n + i;
-            if (m >= W_SLOTS && !warp_wait(bars.done((int)m), (m / 8 - 1) & 1u, abort_flag)) return false;
-            const uint32_t slot = lanes + (uint32_t)A_COL0 + m % W_SLOTS * 32;
-            tc_fence_after();
-            if (!L::MIN || i < blocks) {
-                uint32_t hi[16], lo[16];
-                convert_block<WT>(w, o, i, row, hi, lo);
-                tmem_st16(slot, hi);
-                tmem_st16(slot + 16, lo);
-            } else if constexpr (L::MIN) {
-                uint32_t hi[8], lo[8];
-                convert_min<WT>(w, o, blocks, row, hi, lo);
-                tmem_st8(slot, hi);
-                tmem_st8(slot + 16, lo);
-            }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bars.w_op((int)(m % W_SLOTS)));
-            return true;
-        };
         for (int ti = blockIdx.x; ti < ntiles && ok; ti += gridDim.x) {
             const ExpertTile t = a.tiles[ti / nt];
             const int n0 = ti % nt * NROWS;
             const uint64_t row = (uint64_t)weight_row(t, n0, r) * rb;
             for (int c = 0; c < nchunks; c++, gc++) {
                 const uint32_t s = gc % L::WST;
-                const int blocks = blocks_of(c);
+                const int blocks = blocks_of(c), pairs = (blocks + 1) / 2;
                 // the first half of the chunk before, for which the MMAs of this one wait
                 if (pending && pending_halves == 2 && !(ok = fold())) break;
                 if (!(ok = warp_wait(bars.w_full(s), (gc / L::WST) & 1u, abort_flag))) break;
                 const SmemBytes w{smem + L::OFF_W + (s * BM + r) * L::PITCH};
                 const uint32_t o = (uint32_t)(row + (uint64_t)c * L::CHUNK) & 15u;
                 const WRow ws = row_scale<WT>(w, o, blocks);
-                for (int i = 2 * grp; i < 2 * grp + 2 && ok; i++)
-                    if (L::KQ || i < blocks) ok = put(w, o, blocks, ws, i);
-                if (L::MIN && ok && (int)(gc & 3) == grp) ok = put(w, o, blocks, ws, blocks);
-                if (!ok) break;
-                n += blocks + (L::MIN ? 1 : 0);
+                // this warp's operands, each once its slot's last MMAs are done
+                if (L::KQ || grp < pairs) {
+                    const uint32_t m = n + grp, slot = lanes + (uint32_t)A_COL0 + m % SLOTS * SLOT_COLS;
+                    if (m >= SLOTS && !(ok = warp_wait(bars.done(m - SLOTS), ((m - SLOTS) / DONE) & 1u, abort_flag))) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        if (!L::KQ && 2 * grp + h >= blocks) break;
+                        uint32_t hi[16], lo[16];
+                        convert_block<WT>(w, o, 2 * grp + h, ws, hi, lo);
+                        tmem_st16(slot + 32 * h, hi);
+                        tmem_st16(slot + 32 * h + 16, lo);
+                    }
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bars.op(m % SLOTS));
+                }
+                if constexpr (L::MIN) {
+                    if ((int)(gc & 3) == grp) {
+                        const uint32_t m = n + pairs, slot = lanes + (uint32_t)A_COL0 + m % SLOTS * SLOT_COLS;
+                        if (m >= SLOTS && !(ok = warp_wait(bars.done(m - SLOTS), ((m - SLOTS) / DONE) & 1u, abort_flag))) break;
+                        tc_fence_after();
+                        uint32_t hi[8], lo[8];
+                        convert_min<WT>(w, o, blocks, ws, hi, lo);
+                        tmem_st8(slot, hi);
+                        tmem_st8(slot + 16, lo);
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bars.op(m % SLOTS));
+                    }
+                }
+                n += pairs + (L::MIN ? 1 : 0);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bars.w_empty(s));
                 if (pending) {
@@ -533,22 +563,26 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
                     if (pending_last) finish();
                 }
                 pending = true, pending_last = c + 1 == nchunks, pending_scale = ws.scale;
-                pending_halves = blocks > L::FOLD ? 2 : 1, pending_tile = t, pending_n0 = n0;
+                pending_halves = pairs > L::FOLD ? 2 : 1, pending_tile = t, pending_n0 = n0;
             }
         }
         if (ok && pending && (pending_halves == 1 || fold()) && fold()) finish();
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
         if (warp == WCOPY) {
-            // ------------------------------------------------------------ the weight rows' bytes
-            // Piece i of a chunk: 16 bytes, word i % WORDS of the aligned superset of tile row i / WORDS.  Bytes behind the
-            // last weight are not read.
+            // -------------------------------------------------------- the weight rows' bytes
+            // Lanes 0-15 and 16-31 have a row each (gated: of the gate's and of the up matrix), a lane the 16-byte words
+            // lane % 16 (and, behind the 16th, + 16) of the row's aligned superset.  Rows behind the last are left out:
+            // what is converted in their place goes nowhere.  Bytes behind the last weight are not read.
+            const int half = lane >> 4, p = lane & 15;
+            const uint8_t* const W = GATED && half ? a.W1 : a.W0;
+            constexpr int ROWS = GATED ? 1 : 2;  // of a matrix and step
             uint32_t gc = 0;
             bool ok = true;
             for (int ti = blockIdx.x; ti < ntiles && ok; ti += gridDim.x) {
                 const int expert = a.tiles[ti / nt].expert, n0 = ti % nt * NROWS;
-                const uint64_t first = ((uint64_t)expert * N + n0) * rb;  // of the tile's rows
-                const uint32_t last = (uint32_t)(N - 1 - n0);
+                const int mine = (min(NROWS, N - n0) - (GATED ? 0 : half) + ROWS - 1) / ROWS;  // rows of this lane
+                const uint64_t first = ((uint64_t)expert * N + n0 + (GATED ? 0 : half)) * rb;
                 for (int c = 0; c < nchunks; c++, gc++) {
                     const uint32_t s = gc % L::WST;
                     if (gc >= L::WST && !warp_wait(bars.w_empty(s), (gc / L::WST - 1) & 1u, abort_flag)) {
@@ -556,24 +590,25 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
                         break;
                     }
                     const uint32_t bytes = L::KQ ? L::CHUNK : blocks_of(c) * Fmt<WT>::BB;
-                    const uint64_t at = first + (uint64_t)c * L::CHUNK;
-                    const uint32_t dst = sbase + L::OFF_W + s * (BM * L::PITCH);
-#pragma unroll 4
-                    for (int i = lane; i < BM * L::WORDS; i += 32) {
-                        const uint32_t r = (uint32_t)i / L::WORDS, p = (uint32_t)i % L::WORDS;
-                        const uint64_t g0 = at + (uint64_t)min(GATED ? r >> 1 : r, last) * rb;
+                    uint64_t g0 = first + (uint64_t)c * L::CHUNK;
+                    uint32_t dst = sbase + L::OFF_W + (s * BM + half) * L::PITCH + 16 * p;
+#pragma unroll 8
+                    for (int i = 0; i < BM / 2; i++) {
                         const uint64_t src = (g0 & ~15ull) + 16 * p;
-                        if (src >= g0 + bytes || !QMM_IN_BOUNDS(g_expert_mma_error, src, total)) continue;
-                        const uint64_t left = total - src;
-                        copy16(dst + r * L::PITCH + 16 * p, (GATED && (r & 1) ? a.W1 : a.W0) + src, left < 16 ? (uint32_t)left : 16u);
+                        if (i < mine && src < g0 + bytes && QMM_IN_BOUNDS(g_expert_mma_error, src, total))
+                            copy16(dst, W + src, (uint32_t)min((uint64_t)16, total - src));
+                        if (L::WORDS > 16 && i < mine && src + 256 < g0 + bytes && QMM_IN_BOUNDS(g_expert_mma_error, src + 256, total))
+                            copy16(dst + 256, W + src + 256, (uint32_t)min((uint64_t)16, total - src - 256));
+                        g0 += (uint64_t)ROWS * rb;
+                        dst += 2 * L::PITCH;
                     }
                     copies_arrive(bars.w_full(s));
                 }
             }
             copies_wait();
         } else if (warp >= XCOPY) {
-            // ------------------------------------------------------------ the activation rows' records
-            // Warp j has the tile's rows j, j + 2, ...; lanes keep where two of them lie each.
+            // -------------------------------------------------------- the activation rows' records
+            // Warp j has the tile's rows j, j + 2, ..., one in a step; lanes keep where two of them lie each.
             const int me = warp - XCOPY;
             uint32_t gc = 0;
             bool ok = true;
@@ -592,161 +627,152 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
                         ok = false;
                         break;
                     }
-                    const uint32_t dst = sbase + L::OFF_X + s * L::XSTAGE;
-                    const int pieces = mine * (kRecord / 16);
-#pragma unroll 2
-                    for (int i0 = 0; i0 < pieces; i0 += 32) {  // the whole warp
-                        const uint32_t i = (uint32_t)(i0 + lane), q = i / (kRecord / 16), p = i % (kRecord / 16);
-                        const uint32_t f0 = __shfl_sync(0xffffffffu, from[0], q & 31), f1 = __shfl_sync(0xffffffffu, from[1], q & 31);
-                        if ((int)i < pieces)
-                            copy16(dst + (XCOPIES * q + me) * kRecord + 16 * p,
-                                   a.records + ((uint64_t)(q < 32 ? f0 : f1) + c) * kRecord + 16 * p, 16u);
-                    }
+                    const uint8_t* const src = a.records + (uint64_t)c * kRecord + 16 * lane;
+                    const uint32_t dst = sbase + L::OFF_X + s * L::XSTAGE + me * kRecord + 16 * lane;
+#pragma unroll 1
+                    for (int h = 0; h < 2; h++)
+#pragma unroll 8
+                        for (int q = 0; q < 32; q++) {
+                            const uint32_t f = __shfl_sync(0xffffffffu, h ? from[1] : from[0], q);
+                            if (32 * h + q < mine && lane < kRecord / 16)
+                                copy16(dst + XCOPIES * (32 * h + q) * kRecord, src + (uint64_t)f * kRecord, 16u);
+                            if (32 * h + q >= mine) break;
+                        }
                     copies_arrive(bars.x_full(s));
                 }
             }
             copies_wait();
         } else if (warp == MMA_WARP) {
-            // ------------------------------------------------------------ the MMAs
-            if (lane == 0) {
-                uint32_t acc = 0, n = 0;  // accumulations, items
-                bool ok = true;
-                for (int ti = blockIdx.x; ti < ntiles && ok; ti += gridDim.x) {
-                    const int cols = (a.tiles[ti / nt].count + 15) & ~15;
-                    const uint32_t idesc = instr_desc_f16(BM, cols);
-                    for (int c = 0; c < nchunks && ok; c++) {
-                        const int blocks = blocks_of(c), items = blocks + (L::MIN ? 1 : 0);
-                        uint32_t d = 0, more = 0;
-                        for (int i = 0; i < items; i++, n++) {
-                            if (i % L::FOLD == 0 && i < blocks) {  // another accumulation
-                                d = tmem + (acc & 1) * kTileRows;
-                                more = 0;
-                                if (acc >= 2 && !wait_or_abort(bars.acc_empty((int)(acc & 1)), (acc / 2 - 1) & 1u, abort_flag)) {
-                                    ok = false;
-                                    break;
-                                }
-                            }
-                            const int ws = (int)(n % W_SLOTS), xs = (int)(n % L::X_SLOTS);
-                            if (!wait_or_abort(bars.w_op(ws), (n / W_SLOTS) & 1u, abort_flag) ||
-                                !wait_or_abort(bars.x_op(xs), (n / L::X_SLOTS) & 1u, abort_flag)) {
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
-                            const uint32_t ah = tmem + (uint32_t)(A_COL0 + ws * 32);
-                            const uint64_t xh = smem_desc(sbase + L::OFF_OP + (uint32_t)(xs * L::XTERMS * XOP), 128, 512);
-                            const uint64_t xl = xh + (XOP >> 4);
-#pragma unroll
-                            for (int k = 0; k < 2; k++) {
-                                if (k == 1 && L::MIN && i == blocks) break;  // the minimums: 16 groups
-                                mma_f16_ts(d, ah + 16 + 8 * k, xh + k * (256 >> 4), idesc, more);
-                                more = 1;
-                                if constexpr (!L::KQ) mma_f16_ts(d, ah + 8 * k, xl + k * (256 >> 4), idesc, 1);
-                                mma_f16_ts(d, ah + 8 * k, xh + k * (256 >> 4), idesc, 1);
-                            }
-                            mma_commit(bars.done((int)n));
-                            if (i + 1 == items || ((i + 1) % L::FOLD == 0 && i + 1 < blocks)) mma_commit(bars.acc_full((int)(acc++ & 1)));
+            // -------------------------------------------------------- the MMAs
+            // The whole warp walks, so that addresses and descriptors stay in uniform registers; one lane issues.
+            const bool leader = elect_one();
+            uint32_t acc = 0, n = 0;  // accumulations, items
+            bool ok = true;
+            for (int ti = blockIdx.x; ti < ntiles && ok; ti += gridDim.x) {
+                const int cols = (a.tiles[ti / nt].count + 15) & ~15;
+                const uint32_t idesc = instr_desc_f16(BM, cols);
+                for (int c = 0; c < nchunks && ok; c++) {
+                    const int blocks = blocks_of(c), pairs = (blocks + 1) / 2, items = pairs + (L::MIN ? 1 : 0);
+                    uint32_t d = 0, more = 0;
+                    for (int i = 0; i < items; i++, n++) {
+                        if (i % L::FOLD == 0 && i < pairs) {  // another accumulation
+                            d = tmem + (acc & 1) * kTileRows;
+                            more = 0;
+                            if (acc >= 2 && !(ok = warp_wait(bars.acc_empty(acc & 1), (acc / 2 - 1) & 1u, abort_flag))) break;
                         }
+                        if (!(ok = warp_wait(bars.op(n % SLOTS), (n / SLOTS) & 1u, abort_flag))) break;
+                        tc_fence_after();
+                        const uint32_t ah = tmem + (uint32_t)A_COL0 + n % SLOTS * SLOT_COLS;
+                        const uint64_t x0 = smem_desc(sbase + L::OFF_OP + n % L::X_SLOTS * L::XSLOT, 128, 512);
+                        const int steps = L::MIN && i == pairs ? 1 : min(4, 2 * (blocks - 2 * i));  // of 16 values
+                        const bool ends = i + 1 == items || ((i + 1) % L::FOLD == 0 && i + 1 < pairs);
+                        if (leader) {
+#pragma unroll
+                            for (int k = 0; k < 4; k++) {
+                                if (k >= steps) break;
+                                const uint32_t al = ah + 32 * (k >> 1) + 8 * (k & 1);
+                                const uint64_t xh = x0 + (k >> 1) * (L::XTERMS * XOP >> 4) + (k & 1) * (256 >> 4);
+                                mma_f16_ts(d, al + 16, xh, idesc, more);
+                                more = 1;
+                                if constexpr (!L::KQ) mma_f16_ts(d, al, xh + (XOP >> 4), idesc, 1);
+                                mma_f16_ts(d, al, xh, idesc, 1);
+                            }
+                            mma_commit(bars.done(n));
+                            if (ends) mma_commit(bars.acc_full(acc & 1));
+                        }
+                        more = 1;
+                        if (ends) acc++;
+                        __syncwarp();
                     }
                 }
-                // the last commits land before the CTA ends
-                for (uint32_t i = n > 8 ? n - 8 : 0; i < n; i++)
-                    mbar_wait_bounded(bars.done((int)i), (uint32_t)(i / 8) & 1u, kWaitLimitNs);
             }
-        } else if (warp >= XW0) {
-            // ------------------------------------------------------------ activation operands
+            // the last commits land before the CTA ends
+            for (uint32_t i = n > SLOTS ? n - SLOTS : 0; i < n; i++)
+                mbar_wait_bounded(bars.done(i), (i / DONE) & 1u, kWaitLimitNs);
+        } else {
+            // -------------------------------------------------------- activation operands
+            // Item i of row group g (32 rows) is share i * groups + g, of warp share % 8; a slot's arrivals count four
+            // in all, whatever the number of groups.
             const int x = warp - XW0;
             uint32_t gc = 0, n = 0;
             bool ok = true;
             for (int ti = blockIdx.x; ti < ntiles && ok; ti += gridDim.x) {
                 const int count = a.tiles[ti / nt].count;
-                const int ng = (count + 31) / 32;  // row groups: block i of group g belongs to warp (i ng + g) % 4
+                const int ng = (count + 31) / 32;
                 for (int c = 0; c < nchunks && ok; c++, gc++) {
-                    const int s = (int)(gc % XST), blocks = blocks_of(c);
-                    if (!warp_wait(bars.x_full(s), (uint32_t)(gc / XST) & 1u, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint8_t* stage = smem + L::OFF_X + s * L::XSTAGE;
-                    if (x < ng) {
-                        const uint8_t* rec = stage + (32 * x + lane) * kRecord;
+                    const uint32_t s = gc % XST;
+                    const int blocks = blocks_of(c), pairs = (blocks + 1) / 2, items = pairs + (L::MIN ? 1 : 0);
+                    if (!(ok = warp_wait(bars.x_full(s), (gc / XST) & 1u, abort_flag))) break;
+                    for (int share = x; share < items * ng; share += XWARPS) {
+                        const int i = share / ng, g = share - i * ng, r = 32 * g + lane;
+                        const uint32_t m = n + i;
+                        const uint8_t* rec = smem + L::OFF_X + s * L::XSTAGE + r * kRecord;
+                        uint32_t f = 0;  // the power of two that the row's scales are over
                         float scale;
                         if constexpr (L::KQ) {
                             scale = *reinterpret_cast<const float*>(rec + 256);
                         } else {
                             const uint4 d = *reinterpret_cast<const uint4*>(rec + 256);
-                            const uint32_t m = __vmaxu2(__vmaxu2(d.x, d.y), __vmaxu2(d.z, d.w));
-                            scale = pow2(exponent_of(max(m & 0x7FFFu, (m >> 16) & 0x7FFFu)) - 15);
+                            const uint32_t t = __vmaxu2(__vmaxu2(d.x, d.y), __vmaxu2(d.z, d.w));
+                            const int e = exponent_of(max(t & 0x7FFFu, (t >> 16) & 0x7FFFu));
+                            f = h2_dup(pow2_half(15 - e));
+                            scale = pow2(e - 15);
                         }
-                        sx[(gc & (SX_RING - 1)) * kTileRows + 32 * x + lane] = scale;
-                    }
-                    for (int i = 0; i < blocks + (L::MIN ? 1 : 0); i++, n++) {
-                        const int xs = (int)(n % L::X_SLOTS);
-                        if (n >= L::X_SLOTS) {
-                            const uint32_t p = n - L::X_SLOTS;
-                            if (!warp_wait(bars.done((int)p), (uint32_t)(p / 8) & 1u, abort_flag)) {
-                                ok = false;
-                                break;
-                            }
+                        if (i == 0) sx[(gc & (SX_RING - 1)) * kTileRows + r] = scale;
+                        if (m >= L::X_SLOTS) {
+                            const uint32_t q = m - L::X_SLOTS;
+                            if (!(ok = warp_wait(bars.done(q), (q / DONE) & 1u, abort_flag))) break;
                         }
-                        uint8_t* op = smem + L::OFF_OP + xs * L::XTERMS * XOP;
-                        for (int g = 0; g < ng; g++) {
-                            if (((i * ng + g) & 3) != x) continue;
-                            const int r = 32 * g + lane;
-                            const uint8_t* rec = stage + r * kRecord;
-                            uint32_t f = 0;  // the power of two that the row's scales are over
-                            if constexpr (!L::KQ) {
-                                const uint4 d = *reinterpret_cast<const uint4*>(rec + 256);
-                                const uint32_t m = __vmaxu2(__vmaxu2(d.x, d.y), __vmaxu2(d.z, d.w));
-                                f = h2_dup(pow2_half(15 - exponent_of(max(m & 0x7FFFu, (m >> 16) & 0x7FFFu))));
-                            }
-                            if (L::MIN && i == blocks) {
-                                const uint4 s0 = *reinterpret_cast<const uint4*>(rec + 272), s1 = *reinterpret_cast<const uint4*>(rec + 288);
-                                uint32_t v[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+                        uint8_t* op = smem + L::OFF_OP + m % L::X_SLOTS * L::XSLOT;
+                        if (L::MIN && i == pairs) {
+#pragma unroll
+                            for (int kq = 0; kq < 2; kq++) {
+                                const uint4 u = *reinterpret_cast<const uint4*>(rec + 272 + 16 * kq);
+                                uint32_t v[4] = {u.x, u.y, u.z, u.w};
                                 if constexpr (!L::KQ) {
-                                    uint32_t lo[8];
+                                    uint32_t lo[4];
 #pragma unroll
-                                    for (int b = 0; b < 8; b++) {  // block b's two sums times its scale
-                                        const uint32_t d = h2_mul(h2_dup(*reinterpret_cast<const unsigned short*>(rec + 256 + 2 * b)), f);
-                                        const uint32_t h = h2_mul(d, v[b]);
-                                        lo[b] = h2_fma(d, v[b], h2_neg(h));
-                                        v[b] = h;
+                                    for (int b = 0; b < 4; b++)  // block b's two sums times its scale
+                                        v[b] = times_scale(v[b], h2_mul(h2_dup(*reinterpret_cast<const unsigned short*>(rec + 256 + 8 * kq + 2 * b)), f), &lo[b]);
+                                    put_x(op + XOP, r, kq, lo);
+                                }
+                                put_x(op, r, kq, v);
+                            }
+                        } else {
+#pragma unroll
+                            for (int h = 0; h < 2; h++) {
+                                const int kb = 2 * i + h;
+                                if (!L::KQ && kb >= blocks) break;
+                                uint32_t d = 0;
+                                if constexpr (!L::KQ) d = h2_mul(h2_dup(*reinterpret_cast<const unsigned short*>(rec + 256 + 2 * kb)), f);
+                                uint8_t* const oh = op + h * L::XTERMS * XOP;
+#pragma unroll
+                                for (int half = 0; half < 2; half++) {
+                                    const uint4 u = *reinterpret_cast<const uint4*>(rec + 32 * kb + 16 * half);
+                                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                                    uint32_t v[8];
+#pragma unroll
+                                    for (int b = 0; b < 4; b++) {
+                                        v[2 * b] = h2_sub(bytes_to_h2(w[b], 0x5140), 0x64806480u);
+                                        v[2 * b + 1] = h2_sub(bytes_to_h2(w[b], 0x7362), 0x64806480u);
                                     }
-                                    put_x(op + XOP, r, 0, lo);
-                                    put_x(op + XOP, r, 1, lo + 4);
+                                    if constexpr (!L::KQ) {
+                                        uint32_t lo[8];
+#pragma unroll
+                                        for (int b = 0; b < 8; b++) v[b] = times_scale(v[b], d, &lo[b]);
+                                        put_x(oh + XOP, r, 2 * half, lo);
+                                        put_x(oh + XOP, r, 2 * half + 1, lo + 4);
+                                    }
+                                    put_x(oh, r, 2 * half, v);
+                                    put_x(oh, r, 2 * half + 1, v + 4);
                                 }
-                                put_x(op, r, 0, v);
-                                put_x(op, r, 1, v + 4);
-                                continue;
                             }
-                            const uint4 c0 = *reinterpret_cast<const uint4*>(rec + 32 * i), c1 = *reinterpret_cast<const uint4*>(rec + 32 * i + 16);
-                            const uint32_t cw[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-                            uint32_t v[16];
-#pragma unroll
-                            for (int b = 0; b < 8; b++) {
-                                const uint32_t w = cw[b];
-                                v[2 * b] = h2_sub(bytes_to_h2(w, 0x5140), 0x64806480u);
-                                v[2 * b + 1] = h2_sub(bytes_to_h2(w, 0x7362), 0x64806480u);
-                            }
-                            if constexpr (!L::KQ) {
-                                const uint32_t d = h2_mul(h2_dup(*reinterpret_cast<const unsigned short*>(rec + 256 + 2 * i)), f);
-                                uint32_t lo[16];
-#pragma unroll
-                                for (int b = 0; b < 16; b++) {
-                                    const uint32_t h = h2_mul(d, v[b]);
-                                    lo[b] = h2_fma(d, v[b], h2_neg(h));
-                                    v[b] = h;
-                                }
-#pragma unroll
-                                for (int kq = 0; kq < 4; kq++) put_x(op + XOP, r, kq, lo + 4 * kq);
-                            }
-#pragma unroll
-                            for (int kq = 0; kq < 4; kq++) put_x(op, r, kq, v + 4 * kq);
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(bars.x_op(xs));
+                        if (lane == 0) mbar_arrive_n(bars.op(m % SLOTS), g + 1 == ng ? 5 - ng : 1);
                     }
+                    n += items;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bars.x_empty(s));
                 }
