@@ -571,36 +571,58 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
         if (warp == WCOPY) {
             // -------------------------------------------------------- the weight rows' bytes
-            // Lanes 0-15 and 16-31 have a row each (gated: of the gate's and of the up matrix), a lane the 16-byte words
-            // lane % 16 (and, behind the 16th, + 16) of the row's aligned superset.  Rows behind the last are left out:
-            // what is converted in their place goes nowhere.  Bytes behind the last weight are not read.
+            // Lanes 0-15 and 16-31 have a row each (gated: of the gate's and of the up matrix), a lane the 16-byte word
+            // lane % 16 of the row's aligned superset, four instructions a step: the words of all 128 rows are copied,
+            // also behind a row's end or the expert's last row, where the next ones' bytes lie.  Only tiles near the last
+            // row of all leave out what is not there.
             const int half = lane >> 4, p = lane & 15;
             const uint8_t* const W = GATED && half ? a.W1 : a.W0;
-            constexpr int ROWS = GATED ? 1 : 2;  // of a matrix and step
+            const uint32_t step = (uint32_t)rb * (GATED ? 1 : 2);
             uint32_t gc = 0;
             bool ok = true;
             for (int ti = blockIdx.x; ti < ntiles && ok; ti += gridDim.x) {
                 const int expert = a.tiles[ti / nt].expert, n0 = ti % nt * NROWS;
-                const int mine = (min(NROWS, N - n0) - (GATED ? 0 : half) + ROWS - 1) / ROWS;  // rows of this lane
-                const uint64_t first = ((uint64_t)expert * N + n0 + (GATED ? 0 : half)) * rb;
+                const uint64_t first = ((uint64_t)expert * N + n0) * rb;  // of the tile's rows
                 for (int c = 0; c < nchunks; c++, gc++) {
                     const uint32_t s = gc % L::WST;
                     if (gc >= L::WST && !warp_wait(bars.w_empty(s), (gc / L::WST - 1) & 1u, abort_flag)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t bytes = L::KQ ? L::CHUNK : blocks_of(c) * Fmt<WT>::BB;
-                    uint64_t g0 = first + (uint64_t)c * L::CHUNK;
-                    uint32_t dst = sbase + L::OFF_W + (s * BM + half) * L::PITCH + 16 * p;
-#pragma unroll 8
-                    for (int i = 0; i < BM / 2; i++) {
-                        const uint64_t src = (g0 & ~15ull) + 16 * p;
-                        if (i < mine && src < g0 + bytes && QMM_IN_BOUNDS(g_expert_mma_error, src, total))
-                            copy16(dst, W + src, (uint32_t)min((uint64_t)16, total - src));
-                        if (L::WORDS > 16 && i < mine && src + 256 < g0 + bytes && QMM_IN_BOUNDS(g_expert_mma_error, src + 256, total))
-                            copy16(dst + 256, W + src + 256, (uint32_t)min((uint64_t)16, total - src - 256));
-                        g0 += (uint64_t)ROWS * rb;
-                        dst += 2 * L::PITCH;
+                    const uint64_t at = first + (uint64_t)c * L::CHUNK;
+                    const uint32_t stage = sbase + L::OFF_W + s * (BM * L::PITCH);
+                    if (at + (uint64_t)(NROWS - 1) * rb + 16 * L::WORDS <= total) {
+                        const uint64_t from = at & ~15ull;
+                        const uint8_t* const src = W + from + 16 * p;
+                        uint32_t off = (uint32_t)(at - from) + (GATED ? 0u : half * (uint32_t)rb);
+                        const uint32_t dst = stage + half * L::PITCH + 16 * p;
+                        if (p < L::WORDS)
+#pragma unroll 16
+                            for (int i = 0; i < BM / 2; i++) {
+                                copy16(dst + i * (2 * L::PITCH), src + (off & ~15u), 16u);
+                                off += step;
+                            }
+                        if constexpr (L::WORDS > 16) {  // the words behind the 16th: lanes 2 i and 2 i + 1 have row i's
+                            static_assert(L::WORDS == 18, "two words are left");
+                            const int q = lane >> 1;
+                            const uint8_t* const src2 = (GATED && (q & 1) ? a.W1 : a.W0) + from + 256 + 16 * (lane & 1);
+                            uint32_t off2 = (uint32_t)(at - from) + (uint32_t)(GATED ? q >> 1 : q) * (uint32_t)rb;
+                            const uint32_t dst2 = stage + q * L::PITCH + 256 + 16 * (lane & 1);
+#pragma unroll
+                            for (int i = 0; i < BM / 16; i++) {
+                                copy16(dst2 + i * (16 * L::PITCH), src2 + (off2 & ~15u), 16u);
+                                off2 += 8 * step;
+                            }
+                        }
+                    } else {
+                        const uint32_t bytes = L::KQ ? L::CHUNK : blocks_of(c) * Fmt<WT>::BB;
+                        for (int i = lane; i < BM * L::WORDS; i += 32) {
+                            const int r = i / L::WORDS, w = i - r * L::WORDS, n = GATED ? r >> 1 : r;
+                            const uint64_t g0 = at + (uint64_t)n * rb, from = (g0 & ~15ull) + 16 * w;
+                            if (n0 + n < N && from < g0 + bytes && QMM_IN_BOUNDS(g_expert_mma_error, from, total))
+                                copy16(stage + r * L::PITCH + 16 * w, (GATED && (r & 1) ? a.W1 : a.W0) + from,
+                                       (uint32_t)min((uint64_t)16, total - from));
+                        }
                     }
                     copies_arrive(bars.w_full(s));
                 }
@@ -629,15 +651,16 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
                     }
                     const uint8_t* const src = a.records + (uint64_t)c * kRecord + 16 * lane;
                     const uint32_t dst = sbase + L::OFF_X + s * L::XSTAGE + me * kRecord + 16 * lane;
-#pragma unroll 1
+#pragma unroll
                     for (int h = 0; h < 2; h++)
-#pragma unroll 8
-                        for (int q = 0; q < 32; q++) {
-                            const uint32_t f = __shfl_sync(0xffffffffu, h ? from[1] : from[0], q);
-                            if (32 * h + q < mine && lane < kRecord / 16)
-                                copy16(dst + XCOPIES * (32 * h + q) * kRecord, src + (uint64_t)f * kRecord, 16u);
-                            if (32 * h + q >= mine) break;
-                        }
+#pragma unroll 1
+                        for (int q = 0; q < 32 && 32 * h + q < mine; q += 8)
+#pragma unroll
+                            for (int k = 0; k < 8; k++) {  // behind the tile's last row: another copy of the first record
+                                const uint32_t f = __shfl_sync(0xffffffffu, from[h], q + k);
+                                if (lane < kRecord / 16)
+                                    copy16(dst + (32 * h + q + k) * (XCOPIES * kRecord), src + (uint64_t)f * kRecord, 16u);
+                            }
                     copies_arrive(bars.x_full(s));
                 }
             }
