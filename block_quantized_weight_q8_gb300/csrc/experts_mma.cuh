@@ -17,10 +17,11 @@
 //   0-15   converters and epilogue: warp w has the 32 weight rows of lane quadrant w % 4 and of each chunk of 256 values
 //          pair w / 4, turned into f16 in its tensor-memory lanes; then, for the chunk before, the sums of 32 activation
 //          rows times its 32 weight rows, which it adds up in registers
-//   16-23  activation converters: 8-bit codes into the f16 operand in shared memory
+//   16-23  copy the activation rows' records and turn their 8-bit codes into the f16 operand in shared memory
 //   24     issues the MMAs
-//   25-27  copy the weight rows' and the activation rows' bytes, 16 at a time (a bulk copy for each row and chunk left
-//          the copying warp with 84 cycles a row)
+//   25-27  copy the weight rows' bytes
+// Copies are cp.async of 16 bytes a lane: a bulk copy for each row and chunk left the copying warp with 84 cycles a row,
+// and one warp's cp.async come 65 cycles apart, so that several warps share them.
 // Weights are read once per 128 rows of their expert; converting them, not the MMA, bounds tiles of few rows, and the
 // MMA's two or three terms those of many.
 #pragma once
@@ -38,8 +39,8 @@ static __device__ unsigned int g_expert_mma_error = 0;
 namespace em {
 
 constexpr int BM = 128;       // weight rows of a tile
-constexpr int CONV = 16, XW0 = CONV, XWARPS = 8, MMA_WARP = XW0 + XWARPS, WCOPY = MMA_WARP + 1, XCOPY = WCOPY + 1, XCOPIES = 2;
-constexpr int THREADS = (XCOPY + XCOPIES) * 32;
+constexpr int CONV = 16, XW0 = CONV, XWARPS = 8, MMA_WARP = XW0 + XWARPS, WCOPY = MMA_WARP + 1, WCOPIES = 3;
+constexpr int THREADS = (WCOPY + WCOPIES) * 32;
 // Registers a thread: 896 threads start with 72; the converters, with their sums, go up to what the others give away.
 constexpr int REGS_CONV = 96, REGS_OTHER = 40;
 static_assert(THREADS == 896 && CONV * 32 * REGS_CONV + (THREADS - CONV * 32) * REGS_OTHER <= THREADS * 72, "registers");
@@ -392,8 +393,8 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
     float* const sx = reinterpret_cast<float*>(smem + L::OFF_SX);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < L::WST; i++) mbar_init(bars.w_full(i), 32), mbar_init(bars.w_empty(i), CONV);
-        for (int i = 0; i < XST; i++) mbar_init(bars.x_full(i), XCOPIES * 32), mbar_init(bars.x_empty(i), XWARPS);
+        for (int i = 0; i < L::WST; i++) mbar_init(bars.w_full(i), WCOPIES * 32), mbar_init(bars.w_empty(i), CONV);
+        for (int i = 0; i < XST; i++) mbar_init(bars.x_full(i), XWARPS * 32), mbar_init(bars.x_empty(i), XWARPS);
         // an operand: its four warps of weights, and four shares of activations
         for (int i = 0; i < SLOTS; i++) mbar_init(bars.op(i), 8);
         for (int i = 0; i < DONE; i++) mbar_init(bars.done(i), 1);
@@ -569,15 +570,15 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
         if (ok && pending && (pending_halves == 1 || fold()) && fold()) finish();
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
-        if (warp == WCOPY) {
+        if (warp >= WCOPY) {
             // -------------------------------------------------------- the weight rows' bytes
             // Lanes 0-15 and 16-31 have a row each (gated: of the gate's and of the up matrix), a lane the 16-byte word
             // lane % 16 of the row's aligned superset, four instructions a step: the words of all 128 rows are copied,
             // also behind a row's end or the expert's last row, where the next ones' bytes lie.  Only tiles near the last
             // row of all leave out what is not there.
-            const int half = lane >> 4, p = lane & 15;
+            const int half = lane >> 4, p = lane & 15, me = warp - WCOPY;
             const uint8_t* const W = GATED && half ? a.W1 : a.W0;
-            const uint32_t step = (uint32_t)rb * (GATED ? 1 : 2);
+            const uint32_t step = (uint32_t)rb * (GATED ? 1 : 2);  // warp j takes steps j, j + 3, ...
             uint32_t gc = 0;
             bool ok = true;
             for (int ti = blockIdx.x; ti < ntiles && ok; ti += gridDim.x) {
@@ -594,13 +595,14 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
                     if (at + (uint64_t)(NROWS - 1) * rb + 16 * L::WORDS <= total) {
                         const uint64_t from = at & ~15ull;
                         const uint8_t* const src = W + from + 16 * p;
-                        uint32_t off = (uint32_t)(at - from) + (GATED ? 0u : half * (uint32_t)rb);
-                        const uint32_t dst = stage + half * L::PITCH + 16 * p;
+                        uint32_t off = (uint32_t)(at - from) + (GATED ? 0u : half * (uint32_t)rb) + me * step;
+                        const uint32_t dst = stage + (2 * me + half) * L::PITCH + 16 * p;
                         if (p < L::WORDS)
-#pragma unroll 16
-                            for (int i = 0; i < BM / 2; i++) {
-                                copy16(dst + i * (2 * L::PITCH), src + (off & ~15u), 16u);
-                                off += step;
+#pragma unroll 11
+                            for (int i = 0; i < (BM / 2 + WCOPIES - 1) / WCOPIES; i++) {
+                                if (WCOPIES * i + me < BM / 2)
+                                    copy16(dst + i * (2 * WCOPIES * L::PITCH), src + (off & ~15u), 16u);
+                                off += WCOPIES * step;
                             }
                         if constexpr (L::WORDS > 16) {  // the words behind the 16th: lanes 2 i and 2 i + 1 have row i's
                             static_assert(L::WORDS == 18, "two words are left");
@@ -610,13 +612,13 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
                             const uint32_t dst2 = stage + q * L::PITCH + 256 + 16 * (lane & 1);
 #pragma unroll
                             for (int i = 0; i < BM / 16; i++) {
-                                copy16(dst2 + i * (16 * L::PITCH), src2 + (off2 & ~15u), 16u);
+                                if (i % WCOPIES == me) copy16(dst2 + i * (16 * L::PITCH), src2 + (off2 & ~15u), 16u);
                                 off2 += 8 * step;
                             }
                         }
                     } else {
                         const uint32_t bytes = L::KQ ? L::CHUNK : blocks_of(c) * Fmt<WT>::BB;
-                        for (int i = lane; i < BM * L::WORDS; i += 32) {
+                        for (int i = 32 * me + lane; i < BM * L::WORDS; i += 32 * WCOPIES) {
                             const int r = i / L::WORDS, w = i - r * L::WORDS, n = GATED ? r >> 1 : r;
                             const uint64_t g0 = at + (uint64_t)n * rb, from = (g0 & ~15ull) + 16 * w;
                             if (n0 + n < N && from < g0 + bytes && QMM_IN_BOUNDS(g_expert_mma_error, from, total))
@@ -625,43 +627,6 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
                         }
                     }
                     copies_arrive(bars.w_full(s));
-                }
-            }
-            copies_wait();
-        } else if (warp >= XCOPY) {
-            // -------------------------------------------------------- the activation rows' records
-            // Warp j has the tile's rows j, j + 2, ..., one in a step; lanes keep where two of them lie each.
-            const int me = warp - XCOPY;
-            uint32_t gc = 0;
-            bool ok = true;
-            for (int ti = blockIdx.x; ti < ntiles && ok; ti += gridDim.x) {
-                const ExpertTile t = a.tiles[ti / nt];
-                const int mine = (t.count - me + XCOPIES - 1) / XCOPIES;
-                uint32_t from[2];
-#pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    const int r = XCOPIES * (lane + 32 * i) + me;
-                    from[i] = r < t.count ? (uint32_t)(a.order[t.first + r] / a.per_row) * (uint32_t)nchunks : 0u;
-                }
-                for (int c = 0; c < nchunks; c++, gc++) {
-                    const uint32_t s = gc % XST;
-                    if (gc >= XST && !warp_wait(bars.x_empty(s), (gc / XST - 1) & 1u, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint8_t* const src = a.records + (uint64_t)c * kRecord + 16 * lane;
-                    const uint32_t dst = sbase + L::OFF_X + s * L::XSTAGE + me * kRecord + 16 * lane;
-#pragma unroll
-                    for (int h = 0; h < 2; h++)
-#pragma unroll 1
-                        for (int q = 0; q < 32 && 32 * h + q < mine; q += 8)
-#pragma unroll
-                            for (int k = 0; k < 8; k++) {  // behind the tile's last row: another copy of the first record
-                                const uint32_t f = __shfl_sync(0xffffffffu, from[h], q + k);
-                                if (lane < kRecord / 16)
-                                    copy16(dst + (32 * h + q + k) * (XCOPIES * kRecord), src + (uint64_t)f * kRecord, 16u);
-                            }
-                    copies_arrive(bars.x_full(s));
                 }
             }
             copies_wait();
@@ -719,13 +684,45 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
             const int x = warp - XW0;
             uint32_t gc = 0, n = 0;
             bool ok = true;
+            // The copies run a chunk ahead of the conversion: warp x has the tile's rows x, x + 8, ..., one in a step;
+            // lane l keeps where the l-th of them lies.
+            int copy_ti = blockIdx.x, copy_c = 0;
+            uint32_t copied = 0, from = 0;
+            int copy_rows = 0;
+            auto copy_next = [&] {
+                if (copy_ti >= ntiles) return true;
+                if (copy_c == 0) {
+                    const ExpertTile t = a.tiles[copy_ti / nt];
+                    const int r = XWARPS * lane + x;  // behind the last row: another copy of the first record
+                    from = r < t.count ? (uint32_t)(a.order[t.first + r] / a.per_row) * (uint32_t)nchunks : 0u;
+                    copy_rows = (t.count - x + XWARPS - 1) / XWARPS;
+                }
+                const uint32_t s = copied % XST;
+                if (copied >= XST && !warp_wait(bars.x_empty(s), (copied / XST - 1) & 1u, abort_flag)) return false;
+                const uint8_t* const src = a.records + (uint64_t)copy_c * kRecord + 16 * lane;
+                const uint32_t dst = sbase + L::OFF_X + s * L::XSTAGE + x * kRecord + 16 * lane;
+#pragma unroll
+                for (int q = 0; q < kTileRows / XWARPS; q += 4)
+                    if (q < copy_rows)
+#pragma unroll
+                        for (int k = 0; k < 4; k++) {
+                            const uint32_t f = __shfl_sync(0xffffffffu, from, q + k);
+                            if (lane < kRecord / 16)
+                                copy16(dst + (q + k) * (XWARPS * kRecord), src + (uint64_t)f * kRecord, 16u);
+                        }
+                copies_arrive(bars.x_full(s));
+                copied++;
+                if (++copy_c == nchunks) copy_c = 0, copy_ti += gridDim.x;
+                return true;
+            };
+            ok = copy_next();
             for (int ti = blockIdx.x; ti < ntiles && ok; ti += gridDim.x) {
                 const int count = a.tiles[ti / nt].count;
                 const int ng = (count + 31) / 32;
                 for (int c = 0; c < nchunks && ok; c++, gc++) {
                     const uint32_t s = gc % XST;
                     const int blocks = blocks_of(c), pairs = (blocks + 1) / 2, items = pairs + (L::MIN ? 1 : 0);
-                    if (!(ok = warp_wait(bars.x_full(s), (gc / XST) & 1u, abort_flag))) break;
+                    if (!(ok = copy_next()) || !(ok = warp_wait(bars.x_full(s), (gc / XST) & 1u, abort_flag))) break;
                     for (int share = x; share < items * ng; share += XWARPS) {
                         const int i = share / ng, g = share - i * ng, r = 32 * g + lane;
                         const uint32_t m = n + i;
@@ -800,6 +797,7 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
                     if (lane == 0) mbar_arrive(bars.x_empty(s));
                 }
             }
+            copies_wait();
         }
     }
     tc_fence_before();
