@@ -1,6 +1,7 @@
 // experts.cu -- the entry points of the experts' products: checks, workspaces and the choice of the path.
 #include "experts.h"
 #include "experts_mma.h"
+#include "tc_device.cuh"
 
 namespace qmm {
 
@@ -15,29 +16,27 @@ static qmm_status check_experts(int wt, const ExpertShape& s) {
     return QMM_OK;
 }
 
-// The workspace of the tensor-core path: the plan (rows sorted by expert, tiles), the activation records, and one f32 row
+// The workspace of the tensor-core path: the plan (rows sorted by expert, tiles), the activation operands, and one f32 row
 // of products for each choice, which the other path may use too.
 struct Scratch {
-    size_t order, tiles, records, products, bytes;
+    size_t order, tiles, operand, products, bytes;
     int64_t tiles_most;
 };
-static Scratch scratch_of(const ExpertShape& s) {
+static Scratch scratch_of(int wt, const ExpertShape& s) {
     const int64_t S = s.T * s.k;
     Scratch l;
     l.tiles_most = S / kTileRows + (S < s.E ? S : s.E);
     auto up = [](size_t v) { return (v + 127) / 128 * 128; };
     l.order = 128;  // the number of tiles lies at 0
     l.tiles = l.order + up((size_t)S * 4);
-    l.records = l.tiles + up((size_t)l.tiles_most * sizeof(ExpertTile));
-    l.products = l.records + up((size_t)S * (size_t)((s.K + 255) / 256) * kRecord);
+    l.operand = l.tiles + up((size_t)l.tiles_most * sizeof(ExpertTile));
+    // each expert's rows are made a multiple of 16
+    const size_t rows = (size_t)(S + 15 * (S < s.E ? S : s.E)), chunks = (size_t)((s.K + 255) / 256);
+    l.products = l.operand + up(rows * chunks * (size_t)operand_bytes(act_type_of(wt)));
     l.bytes = l.products + (size_t)S * (size_t)s.N * 4;
     return l;
 }
 
-// Block 0 sorts the choices by their expert and cuts each expert's into tiles; the others write the activation records
-// (from 8-bit rows, or quantizing f32 rows) and, for gated products, the zero rows of choices that are not there.
-// Counting and placing use shared-memory counters, one addition for a warp's choices of one expert; the order within an
-// expert varies from run to run, and no result depends on it (a row's sums do not meet another row's).
 struct Prepare {
     const int32_t* ids;
     const uint8_t* xq;  // [T] rows, or
@@ -46,17 +45,25 @@ struct Prepare {
     int32_t* ntiles;
     int32_t* order;
     ExpertTile* tiles;
-    uint8_t* records;
+    uint8_t* operand;
     int S, k, E, N, K;
 };
-constexpr int kPrepThreads = 512;
+__device__ __forceinline__ __half2 half2_of(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
+__device__ __forceinline__ uint32_t bits_of(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+constexpr int kPlanThreads = 1024, kOperandThreads = 256;
 
-__device__ void plan_tiles(const Prepare& a, int* count, int* start) {
+// Sorts the choices by their expert and cuts each expert's into tiles.  Counting and placing use shared-memory counters,
+// one addition for a warp's choices of one expert; the order within an expert varies from run to run, and no result
+// depends on it (a row's sums do not meet another row's).  One CTA: bound by its passes over the ids, 2 x S / 1024 steps.
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ Prepare a) {
+    __shared__ int count[kMaxExperts], start[kMaxExperts];
+    pdl_launch_dependents();
+    pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31;
-    for (int e = tid; e < a.E; e += kPrepThreads) count[e] = 0;
+    for (int e = tid; e < a.E; e += kPlanThreads) count[e] = 0;
     __syncthreads();
     const int Sr = (a.S + 31) & ~31;  // whole warps
-    for (int i = tid; i < Sr; i += kPrepThreads) {
+    for (int i = tid; i < Sr; i += kPlanThreads) {
         const int e = i < a.S ? a.ids[i] : -1;
         if (e >= a.E) atomicOr(&g_experts_error, kErrIndex);
         const bool real = e >= 0 && e < a.E;
@@ -64,25 +71,27 @@ __device__ void plan_tiles(const Prepare& a, int* count, int* start) {
         if (real && lane == __ffs(same) - 1) atomicAdd(&count[e], __popc(same));
     }
     __syncthreads();
-    if (tid < 32) {  // exclusive sums of the counts and of the experts' tiles
-        int rows = 0, tiles = 0;
+    if (tid < 32) {  // exclusive sums of the counts, of the operands' rows and of the experts' tiles
+        int rows = 0, padded = 0, tiles = 0;
         for (int e0 = 0; e0 < a.E; e0 += 32) {
-            const int e = e0 + lane, c = e < a.E ? count[e] : 0, t = (c + kTileRows - 1) / kTileRows;
-            int cs = c, ts = t;
+            const int e = e0 + lane, c = e < a.E ? count[e] : 0, p = (c + 15) & ~15, t = (c + kTileRows - 1) / kTileRows;
+            int cs = c, ps = p, ts = t;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
-                const int co = __shfl_up_sync(0xffffffffu, cs, off), to = __shfl_up_sync(0xffffffffu, ts, off);
-                if (lane >= off) cs += co, ts += to;
+                const int co = __shfl_up_sync(0xffffffffu, cs, off), po = __shfl_up_sync(0xffffffffu, ps, off),
+                          to = __shfl_up_sync(0xffffffffu, ts, off);
+                if (lane >= off) cs += co, ps += po, ts += to;
             }
             if (e < a.E) start[e] = rows + cs - c;
             for (int j = 0, at = tiles + ts - t; j < t; j++)
-                a.tiles[at + j] = {e, rows + cs - c + j * kTileRows, min(c - j * kTileRows, kTileRows), 0};
-            rows += __shfl_sync(0xffffffffu, cs, 31), tiles += __shfl_sync(0xffffffffu, ts, 31);
+                a.tiles[at + j] = {e, rows + cs - c + j * kTileRows, min(c - j * kTileRows, kTileRows), padded + ps - p + j * kTileRows};
+            rows += __shfl_sync(0xffffffffu, cs, 31), padded += __shfl_sync(0xffffffffu, ps, 31);
+            tiles += __shfl_sync(0xffffffffu, ts, 31);
         }
         if (lane == 0) *a.ntiles = tiles;
     }
     __syncthreads();
-    for (int i = tid; i < Sr; i += kPrepThreads) {
+    for (int i = tid; i < Sr; i += kPlanThreads) {
         const int e = i < a.S ? a.ids[i] : -1;
         const bool real = e >= 0 && e < a.E;
         const unsigned same = __match_any_sync(0xffffffffu, real ? e : -1);
@@ -94,63 +103,126 @@ __device__ void plan_tiles(const Prepare& a, int* count, int* start) {
     }
 }
 
+// The tiles' activation operands, from 8-bit rows or from f32 rows (quantized by the activations' rule on the way), and,
+// for gated products, the zero rows of choices that are not there.  A warp makes a chunk of 8 rows at a time, lane 4 r + q
+// the values 8 q .. 8 q + 7 of each block of row r: its 16-byte stores lie side by side.  Bound by what it writes, 2 (Q8_K)
+// or 4 bytes a value.
 template <int ACT, bool FROM_F32>
-__global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_constant__ Prepare a) {
-    __shared__ int count[kMaxExperts], start[kMaxExperts];
+__global__ void __launch_bounds__(kOperandThreads) operand_kernel(const __grid_constant__ Prepare a) {
+    constexpr int TERMS = operand_terms(ACT);
     pdl_launch_dependents();
     pdl_wait();
-    if (blockIdx.x == 0) {
-        plan_tiles(a, count, start);
-        return;
-    }
-    const int lane = threadIdx.x & 31;
-    const int64_t warp = ((int64_t)(blockIdx.x - 1) * kPrepThreads + threadIdx.x) >> 5;
-    const int64_t warps = (int64_t)(gridDim.x - 1) * (kPrepThreads / 32);
+    const int lane = threadIdx.x & 31, row = lane >> 2, kq = lane & 3;
+    const int warp = (blockIdx.x * kOperandThreads + threadIdx.x) >> 5, warps = gridDim.x * (kOperandThreads / 32);
     const int nchunks = (a.K + 255) / 256;
-    const int64_t total = (int64_t)(FROM_F32 ? a.S : a.S / a.k) * nchunks;
-    for (int64_t i = warp; i < total; i += warps) {
-        const int64_t row = i / nchunks;
-        const int c = (int)(i - row * nchunks);
-        if (FROM_F32) {
-            const int e = a.ids[row];
-            if (e < 0 || e >= a.E) continue;  // the row has no effect
-        }
-        // lane l: values 8l .. 8l + 7 of the chunk
-        const bool in = 256 * c + 8 * lane < a.K;
-        uint32_t w0 = 0, w1 = 0, dbits = 0;
-        float d = 0.0f;
+    const int64_t total = (int64_t)*a.ntiles * (kTileRows / 8) * nchunks;
+    for (int64_t item = warp; item < total; item += warps) {
+        const int tile = (int)(item / (kTileRows / 8 * nchunks)), rest = (int)(item - (int64_t)tile * (kTileRows / 8 * nchunks));
+        const int g = rest / nchunks, c = rest - g * nchunks;
+        const ExpertTile t = a.tiles[tile];
+        const int rows = (t.count + 15) & ~15;
+        if (8 * g >= rows) continue;
+        const bool real = 8 * g + row < t.count;
+        const int64_t slot = real ? a.order[t.first + 8 * g + row] : 0;
+        const int blocks = min(8, a.K / 32 - 8 * c);
+        uint2 w[8];         // this lane's codes
+        uint32_t dbits[8];  // Q8_0: the blocks' scales
+        float d = 0.0f;     // Q8_K: the chunk's
         if constexpr (FROM_F32) {
-            const float4* x4 = reinterpret_cast<const float4*>(a.x + row * a.K) + 64 * c + 2 * lane;
+            const float4* x4 = reinterpret_cast<const float4*>(a.x + slot * a.K) + 64 * c + 2 * kq;
             const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-            float4 v[2] = {in ? x4[0] : zero, in ? x4[1] : zero};
+            float4 v[8][2];
+#pragma unroll
+            for (int b = 0; b < 8; b++)
+#pragma unroll
+                for (int i = 0; i < 2; i++) v[b][i] = real && b < blocks ? x4[8 * b + i] : zero;
             if constexpr (ACT == QMM_Q8_0) {
-                uint32_t w[8];
-                quant_q8_0_block_lanes<4>(v, lane & 3, &dbits, w);
-                // the first lane of four has all words; each lane keeps its own two
-                w0 = w[0], w1 = w[1];
+#pragma unroll
+                for (int b = 0; b < 8; b++) {
+                    uint32_t u[8];
+                    quant_q8_0_block_lanes<4>(v[b], kq, &dbits[b], u);
+                    w[b] = make_uint2(u[0], u[1]);  // every lane's own two words
+                }
             } else {
-                uint32_t pair;
-                quant_q8_K_core(v[0], v[1], &d, &w0, &w1, &pair);
+                float amax = 0.0f;
+#pragma unroll
+                for (int b = 0; b < 8; b++)
+#pragma unroll
+                    for (int i = 0; i < 2; i++)
+                        amax = fmaxf(amax, fmaxf(fmaxf(fabsf(v[b][i].x), fabsf(v[b][i].y)), fmaxf(fabsf(v[b][i].z), fabsf(v[b][i].w))));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                d = __fdiv_rn(amax, 127.0f);
+                const float id = amax != 0.0f ? __fdiv_rn(127.0f, amax) : 0.0f;
+                auto code = [&](float f) { return (uint32_t)clampi(__float2int_rn(__fmul_rn(f, id)), -128, 127) & 0xFFu; };
+                auto word = [&](float4 f) { return code(f.x) | code(f.y) << 8 | code(f.z) << 16 | code(f.w) << 24; };
+#pragma unroll
+                for (int b = 0; b < 8; b++) w[b] = make_uint2(word(v[b][0]), word(v[b][1]));
             }
         } else if constexpr (ACT == QMM_Q8_0) {
-            if (in) {
-                const unsigned short* p =
-                    reinterpret_cast<const unsigned short*>(a.xq + (row * (a.K / 32) + 8 * c + (lane >> 2)) * Q8_0_BB);
-                const unsigned short* q = p + 1 + 4 * (lane & 3);
-                dbits = p[0], w0 = q[0] | (uint32_t)q[1] << 16, w1 = q[2] | (uint32_t)q[3] << 16;
+#pragma unroll
+            for (int b = 0; b < 8; b++) {
+                w[b] = make_uint2(0u, 0u), dbits[b] = 0;
+                if (real && b < blocks) {
+                    const unsigned short* p =
+                        reinterpret_cast<const unsigned short*>(a.xq + (slot / a.k * (a.K / 32) + 8 * c + b) * Q8_0_BB);
+                    const unsigned short* q = p + 1 + 4 * kq;
+                    dbits[b] = p[0];
+                    w[b] = make_uint2(q[0] | (uint32_t)q[1] << 16, q[2] | (uint32_t)q[3] << 16);
+                }
             }
         } else {
-            const uint32_t* p = reinterpret_cast<const uint32_t*>(a.xq + (row * nchunks + c) * Q8_K_BB);
-            d = __uint_as_float(p[0]), w0 = p[1 + 2 * lane], w1 = p[2 + 2 * lane];
+            const uint32_t* p = reinterpret_cast<const uint32_t*>(a.xq + (slot / a.k * nchunks + c) * Q8_K_BB);
+            if (real) d = __uint_as_float(p[0]);
+#pragma unroll
+            for (int b = 0; b < 8; b++) w[b] = real ? make_uint2(p[1 + 8 * b + 2 * kq], p[2 + 8 * b + 2 * kq]) : make_uint2(0u, 0u);
         }
-        int sum = dp4a(w0, 0x01010101u, dp4a(w1, 0x01010101u, 0));
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        if (!QMM_IN_BOUNDS(g_experts_error, i, total)) continue;
-        uint8_t* rec = a.records + i * kRecord;
-        *reinterpret_cast<uint2*>(rec + 8 * lane) = make_uint2(w0 ^ 0x80808080u, w1 ^ 0x80808080u);
-        if (!(lane & 1)) st_u16(rec + 272 + lane, f2h_bits((float)sum));
-        if (ACT == QMM_Q8_0 && !(lane & 3)) st_u16(rec + 256 + (lane >> 1), dbits);
-        if (ACT == QMM_Q8_K && lane == 0) *reinterpret_cast<float*>(rec + 256) = d;
+        uint32_t f = 0;  // Q8_0: the power of two that brings the largest scale below 2
+        float scale = d;
+        if constexpr (ACT == QMM_Q8_0) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int b = 0; b < 8; b++) top = max(top, dbits[b] & 0x7FFFu);
+            const int e = min(max((int)(top >> 10), 1), 30);
+            f = (uint32_t)__half_as_ushort(__float2half_rn(__int_as_float((15 - e + 127) << 23)));
+            scale = __int_as_float((e - 15 + 127) << 23);
+        }
+        if (!QMM_IN_BOUNDS(g_experts_error, (int64_t)t.at + 8 * g + row, (int64_t)a.S + 15 * min(a.S, a.E))) continue;
+        uint8_t* const base = a.operand + ((int64_t)t.at * nchunks + (int64_t)c * rows) * operand_bytes(ACT);
+        uint8_t* const at = base + g * 512 + kq * 128 + row * 16;
+        uint32_t sums[8], lows[8];  // groups 2 b and 2 b + 1
+#pragma unroll
+        for (int b = 0; b < 8; b++) {
+            int s = dp4a(w[b].x, 0x01010101u, dp4a(w[b].y, 0x01010101u, 0));
+            s += __shfl_xor_sync(0xffffffffu, s, 1);
+            const int other = __shfl_xor_sync(0xffffffffu, s, 2);
+            sums[b] = f2h_bits((float)(kq < 2 ? s : other)) | f2h_bits((float)(kq < 2 ? other : s)) << 16;
+            const uint32_t x = w[b].x ^ 0x80808080u, y = w[b].y ^ 0x80808080u;
+            uint4 v = make_uint4(h2_sub(bytes_to_h2(x, 0x5140), 0x64806480u), h2_sub(bytes_to_h2(x, 0x7362), 0x64806480u),
+                                 h2_sub(bytes_to_h2(y, 0x5140), 0x64806480u), h2_sub(bytes_to_h2(y, 0x7362), 0x64806480u));
+            if constexpr (ACT == QMM_Q8_0) {
+                const __half2 dh = __hmul2(half2_of(dbits[b] * 0x10001u), half2_of(f * 0x10001u));
+                auto two = [&](uint32_t& u, uint32_t& l) {
+                    const __half2 h = __hmul2(dh, half2_of(u));
+                    l = bits_of(__hfma2(dh, half2_of(u), __hneg2(h)));
+                    u = bits_of(h);
+                };
+                uint4 l;
+                two(v.x, l.x), two(v.y, l.y), two(v.z, l.z), two(v.w, l.w);
+                two(sums[b], lows[b]);
+                if (b < blocks) *reinterpret_cast<uint4*>(at + (2 * b + 1) * 64 * rows) = l;
+            }
+            if (b < blocks) *reinterpret_cast<uint4*>(at + b * TERMS * 64 * rows) = v;
+        }
+        // the sums: lanes 0, 1 of a row write hi, 2, 3 (two terms) lo
+        uint8_t* const under = base + 8 * TERMS * 64 * rows;
+        if (kq < 2 * TERMS) {
+            const uint32_t* from = kq < 2 ? sums : lows;
+            const bool second = kq & 1;
+            *reinterpret_cast<uint4*>(under + (kq >> 1) * 32 * rows + g * 256 + (kq & 1) * 128 + row * 16) =
+                make_uint4(second ? from[4] : from[0], second ? from[5] : from[1], second ? from[6] : from[2], second ? from[7] : from[3]);
+        }
+        if (kq == 0) *reinterpret_cast<float*>(under + TERMS * 32 * rows + (8 * g + row) * 4) = scale;
     }
     if (a.h != nullptr)
         for (int64_t s = warp; s < a.S; s += warps) {
@@ -160,18 +232,19 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const __grid_cons
         }
 }
 
-static qmm_status prepare(int act, const Prepare& a, cudaStream_t stream) {
+static qmm_status prepare(int act, const Prepare& a, int64_t tiles_most, cudaStream_t stream) {
     DeviceInfo dev;
-    const qmm_status st = current_device(&dev);
+    qmm_status st = current_device(&dev);
+    if (st == QMM_OK) st = launch_pdl(plan_kernel, dim3(1), kPlanThreads, 0, stream, a);
     if (st != QMM_OK) return st;
-    const int64_t items = (int64_t)(a.x ? a.S : a.S / a.k) * ((a.K + 255) / 256) + (a.h ? a.S / 8 : 0);
-    const int64_t want = (items + kPrepThreads / 32 - 1) / (kPrepThreads / 32), most = (int64_t)dev.sms * 4 - 1;
-    const dim3 grid((unsigned)(1 + (want < most ? want : most)));
+    const int64_t items = tiles_most * (kTileRows / 8) * ((a.K + 255) / 256);
+    const int64_t want = (items + kOperandThreads / 32 - 1) / (kOperandThreads / 32), most = (int64_t)dev.sms * 4;
+    const dim3 grid((unsigned)(want < most ? want : most));
     if (act == QMM_Q8_0)
-        return a.x ? launch_pdl(prepare_kernel<QMM_Q8_0, true>, grid, kPrepThreads, 0, stream, a)
-                   : launch_pdl(prepare_kernel<QMM_Q8_0, false>, grid, kPrepThreads, 0, stream, a);
-    return a.x ? launch_pdl(prepare_kernel<QMM_Q8_K, true>, grid, kPrepThreads, 0, stream, a)
-               : launch_pdl(prepare_kernel<QMM_Q8_K, false>, grid, kPrepThreads, 0, stream, a);
+        return a.x ? launch_pdl(operand_kernel<QMM_Q8_0, true>, grid, kOperandThreads, 0, stream, a)
+                   : launch_pdl(operand_kernel<QMM_Q8_0, false>, grid, kOperandThreads, 0, stream, a);
+    return a.x ? launch_pdl(operand_kernel<QMM_Q8_K, true>, grid, kOperandThreads, 0, stream, a)
+               : launch_pdl(operand_kernel<QMM_Q8_K, false>, grid, kOperandThreads, 0, stream, a);
 }
 
 static qmm_status expert_mma(int wt, const ExpertMma& a, bool gate, int64_t tiles_most, cudaStream_t stream) {
@@ -183,25 +256,25 @@ static qmm_status expert_mma(int wt, const ExpertMma& a, bool gate, int64_t tile
 // Both steps on the tensor-core path: h (gated) or the choices' products.
 static qmm_status on_tensor_cores(int wt, int kind, const ExpertShape& s, const void* W0, const void* W1, const void* xq,
                                   const float* x, const int32_t* ids, float* out, uint8_t* scratch, cudaStream_t stream) {
-    const Scratch l = scratch_of(s);
+    const Scratch l = scratch_of(wt, s);
     const bool gate = W1 != nullptr;
     Prepare p = {};
     p.ids = ids, p.xq = (const uint8_t*)xq, p.x = x, p.h = gate ? out : nullptr;
     p.ntiles = reinterpret_cast<int32_t*>(scratch), p.order = reinterpret_cast<int32_t*>(scratch + l.order);
-    p.tiles = reinterpret_cast<ExpertTile*>(scratch + l.tiles), p.records = scratch + l.records;
+    p.tiles = reinterpret_cast<ExpertTile*>(scratch + l.tiles), p.operand = scratch + l.operand;
     p.S = (int)(s.T * s.k), p.k = (int)s.k, p.E = (int)s.E, p.N = (int)s.N, p.K = (int)s.K;
-    const qmm_status st = prepare(act_type_of(wt), p, stream);
+    const qmm_status st = prepare(act_type_of(wt), p, l.tiles_most, stream);
     if (st != QMM_OK) return st;
     ExpertMma a = {};
-    a.W0 = (const uint8_t*)W0, a.W1 = (const uint8_t*)W1, a.records = p.records, a.order = p.order, a.tiles = p.tiles;
-    a.ntiles = p.ntiles, a.y = out, a.out_values = s.T * s.k * s.N, a.per_row = x ? 1 : (int)s.k;
+    a.W0 = (const uint8_t*)W0, a.W1 = (const uint8_t*)W1, a.operand = p.operand, a.order = p.order, a.tiles = p.tiles;
+    a.ntiles = p.ntiles, a.y = out, a.out_values = s.T * s.k * s.N;
     a.E = (int)s.E, a.N = (int)s.N, a.K = (int)s.K, a.kind = kind;
     return expert_mma(wt, a, gate, l.tiles_most, stream);
 }
 
 // Which calls take the tensor cores.
-static bool many_rows(const ExpertShape& s) {
-    return s.T * s.k >= 32 && scratch_of(s).tiles_most * ((s.N + 63) / 64) <= kMaxDim;
+static bool many_rows(int wt, const ExpertShape& s) {
+    return s.T * s.k >= 32 && scratch_of(wt, s).tiles_most * ((s.N + 63) / 64) <= kMaxDim;
 }
 
 // y[t][n] = residual[t][n] + sum_j weights[t][j] p[t][j][n] over the choices that are there, in their order.  Bound by
@@ -243,7 +316,7 @@ extern "C" {
 
 size_t qmm_experts_scratch_bytes(int wtype, int64_t T, int64_t k, int64_t E, int64_t N, int64_t K) {
     const ExpertShape s{T, k, E, N, K};
-    return check_experts(wtype, s) == QMM_OK ? scratch_of(s).bytes : 0;
+    return check_experts(wtype, s) == QMM_OK ? scratch_of(wtype, s).bytes : 0;
 }
 
 qmm_status qmm_experts_glu(int wtype, int kind, const void* Wg, const void* Wu, const void* xq, const int32_t* ids, float* h,
@@ -256,8 +329,8 @@ qmm_status qmm_experts_glu(int wtype, int kind, const void* Wg, const void* Wu, 
     if (kind != QMM_GLU_SILU && kind != QMM_GLU_GELU) return QMM_E_TYPE;
     if (!aligned16(Wg) || !aligned16(Wu) || !aligned16(xq) || !aligned4(ids) || !aligned16(h) || !aligned16(scratch))
         return QMM_E_ALIGN;
-    if (scratch_bytes < scratch_of(s).bytes) return QMM_E_SCRATCH;
-    if (many_rows(s))
+    if (scratch_bytes < scratch_of(wtype, s).bytes) return QMM_E_SCRATCH;
+    if (many_rows(wtype, s))
         return on_tensor_cores(wtype, kind, s, Wg, Wu, xq, nullptr, ids, h, (uint8_t*)scratch, (cudaStream_t)stream);
     return expert_vec_glu(wtype, kind, s, Wg, Wu, xq, ids, h, (cudaStream_t)stream);
 }
@@ -272,10 +345,10 @@ qmm_status qmm_experts_sum(int wtype, const void* W, const float* h, const int32
     if (!aligned16(W) || !aligned16(h) || !aligned4(ids) || !aligned4(weights) || !aligned16(residual) || !aligned16(y) ||
         !aligned16(scratch))
         return QMM_E_ALIGN;
-    if (scratch_bytes < scratch_of(s).bytes) return QMM_E_SCRATCH;
+    if (scratch_bytes < scratch_of(wtype, s).bytes) return QMM_E_SCRATCH;
     cudaStream_t cs = (cudaStream_t)stream;
-    float* p = reinterpret_cast<float*>((uint8_t*)scratch + scratch_of(s).products);
-    if (many_rows(s)) {
+    float* p = reinterpret_cast<float*>((uint8_t*)scratch + scratch_of(wtype, s).products);
+    if (many_rows(wtype, s)) {
         const qmm_status all = on_tensor_cores(wtype, 0, s, W, nullptr, nullptr, h, ids, p, (uint8_t*)scratch, cs);
         return all != QMM_OK ? all : combine(s, p, ids, weights, residual, y, cs);
     }

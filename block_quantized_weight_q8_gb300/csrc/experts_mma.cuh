@@ -2,14 +2,18 @@
 //
 //   P[s][n] = W[e_s][n] . x_s        for the rows s of a call, sorted by their expert e_s
 //
-// sm_103a's tensor cores take no integers, and a row has one scale for each 32 (or 256) values, so a fold of every
-// block's sum in registers would cost as much as the product.  Instead each weight becomes two f16, hi + lo (22 bits of
-// the value over a power of two that the row's 256 values share), and for activations with a scale per 32 values so does
-// each activation; the products hi hi + lo hi (+ hi lo) run on tcgen05.mma with f32 sums in tensor memory.  Activations
-// with one scale per 256 values stay whole numbers, exact in f16.  Sums leave the tensor core every 256 values, where
-// both powers of two (or the activation's scale) meet them in one fma: the sum's error stays that of 48 steps, whatever
-// the row's length, and the fold costs 1/8 of one per block.  The minimums of the formats that have them multiply the
-// activations' sums of 16 values: one further step of 16.
+// sm_103a's tensor cores take no integers, and 32-value blocks have a scale each, so that a fold of every block's sum in
+// registers would cost as much as the product.  Both operands are f16 instead, exact or in two terms, and f32 sums leave
+// tensor memory every 256 values (128 where both operands have two terms): there one fma a sum multiplies what the row's
+// 256 weights share by what the row's 256 activations share.
+//   Q4_K, Q5_K, Q2_K   scale times code, a whole number up to 1953 (exact), over the block's d; the minimums over d, in
+//                      two terms, times the activations' sums of 16 values (one more step of 16)
+//   Q6_K               scale times code, a whole number up to 4096, in two exact terms
+//   32-value blocks    the value over a power of two that the row's 256 share, in two terms, hi + lo (22 bits); the codes
+//                      of Q4_1 and Q5_1 are centered and the minimums multiply the sums, as above
+//   activations        Q8_K: the codes (exact); Q8_0: the values over a shared power of two, in two terms
+// Products of two-term operands leave out lo lo.  Sums of steps are truncated to f32 by the tensor core; with at most 48
+// steps to a sum the errors measured are 0.1 to 1e-6 of the result.
 //
 // A tile is 128 weight rows (gated: 64 rows of the gate's and of the up matrix, row by row, so that both sums of an
 // output lie in neighbouring lanes) by up to 128 rows of one expert; CTAs, one per SM, walk over the tiles, and a tile's
@@ -17,13 +21,13 @@
 //   0-15   converters and epilogue: warp w has the 32 weight rows of lane quadrant w % 4 and of each chunk of 256 values
 //          pair w / 4, turned into f16 in its tensor-memory lanes; then, for the chunk before, the sums of 32 activation
 //          rows times its 32 weight rows, which it adds up in registers
-//   16-23  copy the activation rows' records and turn their 8-bit codes into the f16 operand in shared memory
-//   24     issues the MMAs
-//   25-27  copy the weight rows' bytes
-// Copies are cp.async of 16 bytes a lane: a bulk copy for each row and chunk left the copying warp with 84 cycles a row,
-// and one warp's cp.async come 65 cycles apart, so that several warps share them.
-// Weights are read once per 128 rows of their expert; converting them, not the MMA, bounds tiles of few rows, and the
-// MMA's two or three terms those of many.
+//   16     issues the MMAs
+//   17     copies the activation operands, which come ready made, sorted and laid out in tiles: a bulk copy a pair (made
+//          here from 8-bit rows by eight warps they took as many instructions as the weights)
+//   18-23  copy the weight rows' bytes, 16 to a lane (a bulk copy a row left the copying warp with 84 cycles each, one
+//          warp's cp.async come 65 cycles apart)
+// Weights are read once per 128 rows of their expert.  What bounds a tile is the converters' instructions, whatever the
+// number of its rows, until at about 128 rows the MMAs take as long.
 #pragma once
 
 #include <cuda.h>
@@ -39,33 +43,30 @@ static __device__ unsigned int g_expert_mma_error = 0;
 namespace em {
 
 constexpr int BM = 128;       // weight rows of a tile
-constexpr int CONV = 16, XW0 = CONV, XWARPS = 8, MMA_WARP = XW0 + XWARPS, WCOPY = MMA_WARP + 1, WCOPIES = 3;
+constexpr int CONV = 16, MMA_WARP = CONV, XCOPY = MMA_WARP + 1, WCOPY = XCOPY + 1, WCOPIES = 6;
 constexpr int THREADS = (WCOPY + WCOPIES) * 32;
-// Registers a thread: 896 threads start with 72; the converters, with their sums, go up to what the others give away.
-constexpr int REGS_CONV = 96, REGS_OTHER = 40;
-static_assert(THREADS == 896 && CONV * 32 * REGS_CONV + (THREADS - CONV * 32) * REGS_OTHER <= THREADS * 72, "registers");
-// Weight operands in tensor memory, one for a pair of blocks (a chunk's minimums take one too): each block's 16 columns of
-// hi and 16 of lo
-constexpr int SLOTS = 4, SLOT_COLS = 64;
-// "The MMAs of item n are done" is told on barrier n % 16.  A warp waits only for the items whose slots it takes over and
-// may skip others, so that a barrier of few phases could show it the parity of the phase before the one it means (seen
-// with 4: a slot taken over early, its barrier arrived at once too often).  A weight converter has added up all of the
-// chunk before last, an activation converter cannot be two chunks ahead of the other seven; either way what it waits for
-// is less than two chunks, 10 items, behind the last that is surely done.
+// Registers a thread: 768 threads start with 80; the converters, with their sums, go up to what the others give away.
+constexpr int REGS_CONV = 96, REGS_OTHER = 48;
+static_assert(THREADS == 768 && CONV * 32 * REGS_CONV + (THREADS - CONV * 32) * REGS_OTHER <= THREADS * 80, "registers");
+// "The MMAs of item n are done" is told on barrier n % 16 (an item is a pair, or a chunk's minimums).  A converter waits
+// only for the items whose slots it takes over and skips the others, so that a barrier of few phases could show it the
+// parity of the phase before the one it means (seen with 4: a slot taken over early, its barrier arrived at too often).
+// It has added up all of the chunk before last, so what it waits for is less than two chunks, 10 items, behind the last
+// that is surely done.
 constexpr int DONE = 16;
 constexpr int A_COL0 = 2 * kTileRows;  // after two accumulators
 constexpr int XOP = kTileRows * 64;    // bytes of one term of a block's activation operand: 32 values of 128 rows
-constexpr int XST = 2;        // stages of activation records
 constexpr int SX_RING = 8;    // chunks of activation scales
-static_assert(A_COL0 + SLOTS * SLOT_COLS == 512, "tensor memory");
 
 template <int WT>
 struct Lay {
     using F = Fmt<WT>;
     static constexpr bool KQ = F::BV == 256;
     static constexpr bool MIN = WT == QMM_Q4_1 || WT == QMM_Q5_1 || WT == QMM_Q4_K || WT == QMM_Q5_K || WT == QMM_Q2_K;
-    static constexpr int XTERMS = KQ ? 1 : 2;
-    static constexpr int X_SLOTS = KQ ? 4 : 2;
+    static constexpr int WTERMS = KQ && WT != QMM_Q6_K ? 1 : 2, XTERMS = operand_terms(F::ACT);
+    // weight operands in tensor memory, one for a pair of blocks: each block's 16 columns of hi and 16 of lo
+    static constexpr int BLOCK_COLS = 16 * WTERMS, SLOT_COLS = 2 * BLOCK_COLS, SLOTS = 256 / SLOT_COLS;
+    static constexpr int X_SLOTS = KQ ? 8 : 4;
     static constexpr int XSLOT = 2 * XTERMS * XOP;  // a pair: block by block, hi then lo
     static constexpr int CHUNK = KQ ? F::BB : 8 * F::BB;  // bytes of a row's 256 values
     // a copied row: the 16-byte superset at any offset that blocks can have, an odd number of 16-byte words
@@ -74,17 +75,15 @@ struct Lay {
     static constexpr int PITCH = 16 * (WORDS | 1);
     // pairs of an accumulation: where activations have two terms, sums leave the tensor core twice as often
     static constexpr int FOLD = KQ ? 4 : 2;
-    static constexpr int XSTAGE = kTileRows * kRecord;
-    static constexpr int FIXED = XST * XSTAGE + X_SLOTS * XSLOT + SX_RING * kTileRows * 4 + 512;
+    static constexpr int FIXED = X_SLOTS * XSLOT + SX_RING * kTileRows * 4 + 512;
     static constexpr int FIT = (232448 - 128 - FIXED) / (BM * PITCH);
     static constexpr int WST = FIT >= 4 ? 4 : 2;  // a power of two
-    static_assert(WST >= 2, "two stages of weight rows");
+    static_assert(FIT >= 2, "two stages of weight rows");
     static constexpr int OFF_W = 0;
-    static constexpr int OFF_X = OFF_W + WST * BM * PITCH;
-    static constexpr int OFF_OP = OFF_X + XST * XSTAGE;
+    static constexpr int OFF_OP = OFF_W + WST * BM * PITCH;
     static constexpr int OFF_SX = OFF_OP + X_SLOTS * XSLOT;
     static constexpr int OFF_BAR = OFF_SX + SX_RING * kTileRows * 4;
-    static constexpr int NBARS = 2 * WST + 2 * XST + SLOTS + DONE + 4;
+    static constexpr int NBARS = 2 * WST + X_SLOTS + SX_RING + SLOTS + DONE + 4;
     static constexpr int OFF_TMEM = OFF_BAR + NBARS * 8;
     static constexpr int SMEM = OFF_TMEM + 16;
     static_assert(SMEM <= 232448 && OFF_OP % 128 == 0 && NBARS * 8 + 16 <= 512, "shared memory");
@@ -96,12 +95,13 @@ struct Bars {
     uint32_t base;
     __device__ uint32_t w_full(int s) const { return base + 8u * s; }                       // weight rows landed
     __device__ uint32_t w_empty(int s) const { return base + 8u * (L::WST + s); }           // converted
-    __device__ uint32_t x_full(int s) const { return base + 8u * (2 * L::WST + s); }
-    __device__ uint32_t x_empty(int s) const { return base + 8u * (2 * L::WST + XST + s); }
-    __device__ uint32_t op(int i) const { return base + 8u * (2 * L::WST + 2 * XST + i); }  // item n % 4: operands written
-    __device__ uint32_t done(uint32_t n) const { return base + 8u * (2 * L::WST + 2 * XST + SLOTS + n % DONE); }
-    __device__ uint32_t acc_full(int i) const { return base + 8u * (2 * L::WST + 2 * XST + SLOTS + DONE + i); }
-    __device__ uint32_t acc_empty(int i) const { return base + 8u * (2 * L::WST + 2 * XST + SLOTS + DONE + 2 + i); }
+    __device__ uint32_t x_full(int i) const { return base + 8u * (2 * L::WST + i); }  // item n % X_SLOTS: activations landed
+    __device__ uint32_t sx_full(int i) const { return base + 8u * (2 * L::WST + L::X_SLOTS + i); }  // a chunk's scales landed
+    __device__ uint32_t w_op(int i) const { return base + 8u * (OPS + i); }  // item n % SLOTS: weights written
+    __device__ uint32_t done(uint32_t n) const { return base + 8u * (OPS + L::SLOTS + n % DONE); }  // its MMAs are done
+    __device__ uint32_t acc_full(int i) const { return base + 8u * (OPS + L::SLOTS + DONE + i); }
+    __device__ uint32_t acc_empty(int i) const { return base + 8u * (OPS + L::SLOTS + DONE + 2 + i); }
+    static constexpr int OPS = 2 * L::WST + L::X_SLOTS + SX_RING;
 };
 
 __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
@@ -159,18 +159,20 @@ __device__ __forceinline__ uint32_t pow2_half(int e) {  // -24 <= e <= 15
     return e >= -14 ? (uint32_t)(e + 15) << 10 : 1u << (e + 24);
 }
 
-// What a chunk's blocks share: the power of two (its exponent field, and what the chunk's sums are multiplied by) and the
-// first 16 bytes of a Q4_K or Q5_K block.
+// What the blocks of a row's chunk share: what their sums are multiplied by; the exponent field of the power of two
+// (32-value blocks), or what the scales and minimums are multiplied by over it (K-quants); the first 16 bytes of a Q4_K or
+// Q5_K block.
 struct WRow {
     float scale;
     int e;
+    float value, min;
     uint4 head;
 };
-// What is taken from the codes of formats with a minimum, so that neither the products nor the minimums' share are much
-// larger than their sum (the minimum gets it back times the scale).
+// What is taken from the codes of Q4_1 and Q5_1, so that neither the products nor the minimums' share are much larger than
+// their sum (the minimum gets it back times the scale).
 template <int WT>
 constexpr int center() {
-    return WT == QMM_Q4_1 || WT == QMM_Q4_K ? 8 : WT == QMM_Q5_1 || WT == QMM_Q5_K ? 16 : WT == QMM_Q2_K ? 2 : 0;
+    return WT == QMM_Q4_1 ? 8 : WT == QMM_Q5_1 ? 16 : 0;
 }
 
 // The 32 codes of block kb of the chunk at byte `o` of the row, in K order, four to a word, and the f16 offset word.
@@ -219,14 +221,14 @@ __device__ __forceinline__ uint32_t codes_of(const SmemBytes& w, uint32_t o, int
 #pragma unroll
             for (int i = 0; i < 8; i++) c[i] |= ((h[i] >> kb) & 0x01010101u) << 4;
         }
-        return (uint32_t)(0x6400 + center<WT>()) * 0x10001u;
+        return 0x64006400u;
     } else if constexpr (WT == QMM_Q2_K) {
         uint32_t q[8];
         w.words_aligned<8>(o + 16 + 32 * (kb >> 2), q);
         const int sh = 2 * (kb & 3);
 #pragma unroll
         for (int i = 0; i < 8; i++) c[i] = (q[i] >> sh) & 0x03030303u;
-        return 0x64026402u;
+        return 0x64006400u;
     } else {  // Q6_K
         const int half = kb >> 2, part = kb & 3;
         uint32_t q[8], h[8];
@@ -239,21 +241,30 @@ __device__ __forceinline__ uint32_t codes_of(const SmemBytes& w, uint32_t o, int
     }
 }
 
-// The power of two of a row's chunk.
+// A K-quant block's sums are over its d, unless its minimums' scale is over 1000 times that (no weights have that): then
+// over a 1000th of the latter, so that minimums up to 63 times it stay f16.  The scales' rounding to f16 is then 2^-11 of
+// what is less than 2^-5 of the values.
+__device__ __forceinline__ WRow shared_scale(float d, float m) {
+    const bool usual = fabsf(m) <= 1000.0f * fabsf(d);
+    const float D = usual ? d : m * 1e-3f;
+    const float inv = D != 0.0f ? __fdiv_rn(1.0f, D) : 0.0f;
+    return {D, 0, usual ? 1.0f : d * inv, -(m * inv), make_uint4(0u, 0u, 0u, 0u)};
+}
+
 template <int WT>
 __device__ __forceinline__ WRow row_scale(const SmemBytes& w, uint32_t o, int blocks) {
-    uint32_t top = 0;
-    uint4 head = make_uint4(0u, 0u, 0u, 0u);
     if constexpr (WT == QMM_Q4_K || WT == QMM_Q5_K) {
-        head = *reinterpret_cast<const uint4*>(w.base + o);
-        const uint32_t dd = head.x;
-        top = max(dd & 0x7FFFu, (dd >> 16) & 0x7FFFu);
+        const uint4 head = *reinterpret_cast<const uint4*>(w.base + o);
+        WRow r = shared_scale(h2f(head.x), h2f(head.x >> 16));
+        r.head = head;
+        return r;
     } else if constexpr (WT == QMM_Q2_K) {
         const uint32_t dd = w.w32(o + 80);
-        top = max(dd & 0x7FFFu, (dd >> 16) & 0x7FFFu);
+        return shared_scale(h2f(dd), h2f(dd >> 16));
     } else if constexpr (WT == QMM_Q6_K) {
-        top = w.u16(o + 208) & 0x7FFFu;
+        return {h2f(w.u16(o + 208)), 0, 1.0f, 0.0f, make_uint4(0u, 0u, 0u, 0u)};
     } else {
+        uint32_t top = 0;
 #pragma unroll
         for (int kb = 0; kb < 8; kb++) {
             if (kb >= blocks) break;
@@ -265,9 +276,9 @@ __device__ __forceinline__ WRow row_scale(const SmemBytes& w, uint32_t o, int bl
                 top = max(top, w.u16(b) & 0x7FFFu);
             }
         }
+        const int e = exponent_of(top);
+        return {pow2(e - 15), e, 0.0f, 0.0f, make_uint4(0u, 0u, 0u, 0u)};
     }
-    const int e = exponent_of(top);
-    return {pow2(e - 15), e, head};
 }
 
 // 6-bit field b (0-7) of a Q4_K header: low six bits of byte b of `first` for b < 4; else four low bits of byte b - 4 of
@@ -277,78 +288,69 @@ __device__ __forceinline__ uint32_t six_bits(int b, uint32_t first, uint32_t sec
     return b < 4 ? (first >> sh) & 63u : ((second >> sh) & 15u) | (((top >> sh) >> 6) & 3u) << 4;
 }
 
-// Block kb of a row's chunk as hi and lo f16 words in K order.
+// Block kb of a row's chunk as f16 words in K order: hi and (two terms) lo.
 template <int WT>
 __device__ __forceinline__ void convert_block(const SmemBytes& w, uint32_t o, int kb, const WRow& row, uint32_t (&hi)[16],
                                               uint32_t (&lo)[16]) {
     uint32_t c[8];
     const uint32_t magic = codes_of<WT>(w, o, kb, c);
     // the scales of the block's two halves
-    uint32_t d0, d1, r0 = 0, r1 = 0;  // rounded, and (K-quants) the rest
-    if constexpr (Lay<WT>::KQ) {
-        float s0, s1;
-        if constexpr (WT == QMM_Q4_K || WT == QMM_Q5_K) {
-            const float d = h2f(row.head.x) * pow2(15 - row.e);
-            const uint32_t sc = six_bits(kb, row.head.y, row.head.w, row.head.y);
-            s0 = s1 = d * (float)sc;
-        } else if constexpr (WT == QMM_Q2_K) {
-            const float d = h2f(w.u16(o + 80)) * pow2(15 - row.e);
-            const uint32_t sc = w.u16(o + 2 * kb);
-            s0 = d * (float)(sc & 15u), s1 = d * (float)((sc >> 8) & 15u);
-        } else {
-            const float d = h2f(w.u16(o + 208)) * pow2(15 - row.e);
-            const uint32_t sc = w.u16(o + 192 + 2 * kb);
-            s0 = d * (float)(int8_t)(sc & 0xFFu), s1 = d * (float)(int8_t)(sc >> 8);
-        }
-        split2(s0, &d0, &r0);
-        d1 = d0, r1 = r0;
-        if constexpr (WT == QMM_Q2_K || WT == QMM_Q6_K) split2(s1, &d1, &r1);
+    uint32_t d0, d1;
+    if constexpr (WT == QMM_Q4_K || WT == QMM_Q5_K) {
+        d0 = d1 = h2_dup(f2h_bits(row.value * (float)six_bits(kb, row.head.y, row.head.w, row.head.y)));
+    } else if constexpr (WT == QMM_Q2_K) {
+        const uint32_t sc = w.u16(o + 2 * kb);
+        d0 = h2_dup(f2h_bits(row.value * (float)(sc & 15u))), d1 = h2_dup(f2h_bits(row.value * (float)((sc >> 8) & 15u)));
+    } else if constexpr (WT == QMM_Q6_K) {
+        const uint32_t sc = w.u16(o + 192 + 2 * kb);
+        d0 = h2_dup(f2h_bits((float)(int8_t)(sc & 0xFFu))), d1 = h2_dup(f2h_bits((float)(int8_t)(sc >> 8)));
     } else {
-        d0 = h2_mul(h2_dup(w.u16(o + Fmt<WT>::BB * kb)), h2_dup(pow2_half(15 - row.e)));
-        d1 = d0;
+        d0 = d1 = h2_mul(h2_dup(w.u16(o + Fmt<WT>::BB * kb)), h2_dup(pow2_half(15 - row.e)));
     }
+    if constexpr (Lay<WT>::WTERMS == 1) {
+        // scale (1024 + code) - 1024 scale: every part is an f16 and so is the result
+        const uint32_t c0 = h2_mul(d0, 0xE400E400u), c1 = h2_mul(d1, 0xE400E400u);
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const uint32_t d = i < 4 ? d0 : d1, r = i < 4 ? r0 : r1;
-        const uint32_t q0 = h2_sub(bytes_to_h2(c[i], 0x5140), magic), q1 = h2_sub(bytes_to_h2(c[i], 0x7362), magic);
-        hi[2 * i] = h2_mul(d, q0), hi[2 * i + 1] = h2_mul(d, q1);
-        lo[2 * i] = h2_fma(d, q0, h2_neg(hi[2 * i])), lo[2 * i + 1] = h2_fma(d, q1, h2_neg(hi[2 * i + 1]));
-        if constexpr (Lay<WT>::KQ) lo[2 * i] = h2_fma(r, q0, lo[2 * i]), lo[2 * i + 1] = h2_fma(r, q1, lo[2 * i + 1]);
+        for (int i = 0; i < 8; i++) {
+            hi[2 * i] = h2_fma(i < 4 ? d0 : d1, bytes_to_h2(c[i], 0x5140), i < 4 ? c0 : c1);
+            hi[2 * i + 1] = h2_fma(i < 4 ? d0 : d1, bytes_to_h2(c[i], 0x7362), i < 4 ? c0 : c1);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const uint32_t d = i < 4 ? d0 : d1;
+            const uint32_t q0 = h2_sub(bytes_to_h2(c[i], 0x5140), magic), q1 = h2_sub(bytes_to_h2(c[i], 0x7362), magic);
+            hi[2 * i] = h2_mul(d, q0), hi[2 * i + 1] = h2_mul(d, q1);
+            lo[2 * i] = h2_fma(d, q0, h2_neg(hi[2 * i])), lo[2 * i + 1] = h2_fma(d, q1, h2_neg(hi[2 * i + 1]));
+        }
     }
 }
 
-// The chunk's minimums over 16 groups of 16 values (with what the codes gave away), as hi and lo: what an activation
-// group's sum is multiplied by.
+// The chunk's minimums over 16 groups of 16 values (Q4_1, Q5_1: with what the codes gave away), as hi and lo: what an
+// activation group's sum is multiplied by.
 template <int WT>
 __device__ __forceinline__ void convert_min(const SmemBytes& w, uint32_t o, int blocks, const WRow& row, uint32_t (&hi)[8],
                                             uint32_t (&lo)[8]) {
-    const float f = pow2(15 - row.e);
-    constexpr float C = (float)center<WT>();
     if constexpr (WT == QMM_Q4_1 || WT == QMM_Q5_1) {
+        const float f = pow2(15 - row.e);
 #pragma unroll
         for (int b = 0; b < 8; b++) {
             const uint32_t dm = b < blocks ? w.w32(o + Fmt<WT>::BB * b) : 0u;
-            split2(fmaf(C, h2f(dm), h2f(dm >> 16)) * f, &hi[b], &lo[b]);
+            split2(fmaf((float)center<WT>(), h2f(dm), h2f(dm >> 16)) * f, &hi[b], &lo[b]);
         }
     } else if constexpr (WT == QMM_Q4_K || WT == QMM_Q5_K) {
-        const float d = C * (h2f(row.head.x) * f), dm = h2f(row.head.x >> 16) * f;
 #pragma unroll
-        for (int b = 0; b < 8; b++) {
-            const float sc = (float)six_bits(b, row.head.y, row.head.w, row.head.y);
-            const float mn = (float)six_bits(b, row.head.z, row.head.w >> 4, row.head.z);
-            split2(fmaf(d, sc, -(dm * mn)), &hi[b], &lo[b]);
-        }
+        for (int b = 0; b < 8; b++)
+            split2(row.min * (float)six_bits(b, row.head.z, row.head.w >> 4, row.head.z), &hi[b], &lo[b]);
     } else if constexpr (WT == QMM_Q2_K) {
-        const uint32_t dd = w.w32(o + 80);
-        const float d = C * (h2f(dd) * f), dm = h2f(dd >> 16) * f;
         uint32_t sc[4];
         w.words_aligned<4>(o, sc);
 #pragma unroll
         for (int b = 0; b < 8; b++) {
             const uint32_t two = sc[b >> 1] >> (16 * (b & 1));
             uint32_t h0, l0, h1, l1;
-            split2(fmaf(d, (float)(two & 15u), -(dm * (float)((two >> 4) & 15u))), &h0, &l0);
-            split2(fmaf(d, (float)((two >> 8) & 15u), -(dm * (float)((two >> 12) & 15u))), &h1, &l1);
+            split2(row.min * (float)((two >> 4) & 15u), &h0, &l0);
+            split2(row.min * (float)((two >> 12) & 15u), &h1, &l1);
             hi[b] = (h0 & 0xFFFFu) | (h1 << 16), lo[b] = (l0 & 0xFFFFu) | (l1 << 16);
         }
     }
@@ -360,26 +362,11 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
                  : "memory");
 }
 
-__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
     return p != 0;
 }
-// the f16 products of d and v, and what their rounding left
-__device__ __forceinline__ uint32_t times_scale(uint32_t v, uint32_t d, uint32_t* lo) {
-    const uint32_t h = h2_mul(d, v);
-    *lo = h2_fma(d, v, h2_neg(h));
-    return h;
-}
-
-// 16 bytes of an activation operand: values 8 kq .. 8 kq + 7 of row r
-__device__ __forceinline__ void put_x(uint8_t* op, int r, int kq, const uint32_t* v) {
-    *reinterpret_cast<uint4*>(op + ((r >> 3) * 4 + kq) * 128 + (r & 7) * 16) = make_uint4(v[0], v[1], v[2], v[3]);
-}
-
 template <int WT, bool GATED>
 __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_constant__ ExpertMma a) {
     using L = Lay<WT>;
@@ -394,9 +381,9 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < L::WST; i++) mbar_init(bars.w_full(i), WCOPIES * 32), mbar_init(bars.w_empty(i), CONV);
-        for (int i = 0; i < XST; i++) mbar_init(bars.x_full(i), XWARPS * 32), mbar_init(bars.x_empty(i), XWARPS);
-        // an operand: its four warps of weights, and four shares of activations
-        for (int i = 0; i < SLOTS; i++) mbar_init(bars.op(i), 8);
+        for (int i = 0; i < L::X_SLOTS; i++) mbar_init(bars.x_full(i), 1);
+        for (int i = 0; i < SX_RING; i++) mbar_init(bars.sx_full(i), 1);
+        for (int i = 0; i < L::SLOTS; i++) mbar_init(bars.w_op(i), 4);
         for (int i = 0; i < DONE; i++) mbar_init(bars.done(i), 1);
         for (int i = 0; i < 2; i++) mbar_init(bars.acc_full(i), 1), mbar_init(bars.acc_empty(i), CONV);
         *abort_flag = 0;
@@ -446,13 +433,14 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
         ExpertTile pending_tile = {};
         // adds the next accumulation of the pending chunk, times its scales, to the registers
         auto fold = [&] {
-            const uint32_t buf = folded & 1;
+            const uint32_t buf = folded & 1, of = gc - 1;
             if (!warp_wait(bars.acc_full((int)buf), (folded / 2) & 1u, abort_flag)) return false;
+            if (!warp_wait(bars.sx_full((int)(of % SX_RING)), (of / SX_RING) & 1u, abort_flag)) return false;
             folded++;
             tc_fence_after();
             if (grp * 32 < pending_tile.count) {
                 const uint32_t cols = lanes + buf * kTileRows + (uint32_t)(grp * 32);
-                const uint4* s4 = reinterpret_cast<const uint4*>(sx + ((gc - 1) & (SX_RING - 1)) * kTileRows + grp * 32);
+                const uint4* s4 = reinterpret_cast<const uint4*>(sx + of % SX_RING * kTileRows + grp * 32);
                 const uint32_t sb = __float_as_uint(pending_scale);
                 const uint64_t s2 = f2_pack(sb, sb);
                 uint32_t v[2][8];
@@ -525,35 +513,35 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
                 const WRow ws = row_scale<WT>(w, o, blocks);
                 // this warp's operands, each once its slot's last MMAs are done
                 if (L::KQ || grp < pairs) {
-                    const uint32_t m = n + grp, slot = lanes + (uint32_t)A_COL0 + m % SLOTS * SLOT_COLS;
-                    if (m >= SLOTS && !(ok = warp_wait(bars.done(m - SLOTS), ((m - SLOTS) / DONE) & 1u, abort_flag))) break;
+                    const uint32_t m = n + grp, slot = lanes + (uint32_t)A_COL0 + m % L::SLOTS * L::SLOT_COLS;
+                    if (m >= L::SLOTS && !(ok = warp_wait(bars.done(m - L::SLOTS), ((m - L::SLOTS) / DONE) & 1u, abort_flag))) break;
                     tc_fence_after();
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
                         if (!L::KQ && 2 * grp + h >= blocks) break;
                         uint32_t hi[16], lo[16];
                         convert_block<WT>(w, o, 2 * grp + h, ws, hi, lo);
-                        tmem_st16(slot + 32 * h, hi);
-                        tmem_st16(slot + 32 * h + 16, lo);
+                        tmem_st16(slot + L::BLOCK_COLS * h, hi);
+                        if constexpr (L::WTERMS == 2) tmem_st16(slot + L::BLOCK_COLS * h + 16, lo);
                     }
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bars.op(m % SLOTS));
+                    if (lane == 0) mbar_arrive(bars.w_op(m % L::SLOTS));
                 }
                 if constexpr (L::MIN) {
                     if ((int)(gc & 3) == grp) {
-                        const uint32_t m = n + pairs, slot = lanes + (uint32_t)A_COL0 + m % SLOTS * SLOT_COLS;
-                        if (m >= SLOTS && !(ok = warp_wait(bars.done(m - SLOTS), ((m - SLOTS) / DONE) & 1u, abort_flag))) break;
+                        const uint32_t m = n + pairs, slot = lanes + (uint32_t)A_COL0 + m % L::SLOTS * L::SLOT_COLS;
+                        if (m >= L::SLOTS && !(ok = warp_wait(bars.done(m - L::SLOTS), ((m - L::SLOTS) / DONE) & 1u, abort_flag))) break;
                         tc_fence_after();
                         uint32_t hi[8], lo[8];
                         convert_min<WT>(w, o, blocks, ws, hi, lo);
                         tmem_st8(slot, hi);
-                        tmem_st8(slot + 16, lo);
+                        tmem_st8(slot + 8, lo);
                         tmem_st_wait();
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(bars.op(m % SLOTS));
+                        if (lane == 0) mbar_arrive(bars.w_op(m % L::SLOTS));
                     }
                 }
                 n += pairs + (L::MIN ? 1 : 0);
@@ -648,22 +636,36 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
                             more = 0;
                             if (acc >= 2 && !(ok = warp_wait(bars.acc_empty(acc & 1), (acc / 2 - 1) & 1u, abort_flag))) break;
                         }
-                        if (!(ok = warp_wait(bars.op(n % SLOTS), (n / SLOTS) & 1u, abort_flag))) break;
+                        if (!(ok = warp_wait(bars.x_full(n % L::X_SLOTS), (n / L::X_SLOTS) & 1u, abort_flag)) ||
+                            !(ok = warp_wait(bars.w_op(n % L::SLOTS), (n / L::SLOTS) & 1u, abort_flag)))
+                            break;
                         tc_fence_after();
-                        const uint32_t ah = tmem + (uint32_t)A_COL0 + n % SLOTS * SLOT_COLS;
-                        const uint64_t x0 = smem_desc(sbase + L::OFF_OP + n % L::X_SLOTS * L::XSLOT, 128, 512);
-                        const int steps = L::MIN && i == pairs ? 1 : min(4, 2 * (blocks - 2 * i));  // of 16 values
+                        const uint32_t ah = tmem + (uint32_t)A_COL0 + n % L::SLOTS * L::SLOT_COLS;
+                        const uint32_t op = sbase + L::OFF_OP + n % L::X_SLOTS * L::XSLOT;
                         const bool ends = i + 1 == items || ((i + 1) % L::FOLD == 0 && i + 1 < pairs);
                         if (leader) {
+                            if (L::MIN && i == pairs) {  // hi and lo of the minimums, their sums' rows 32 bytes apart
+                                const uint64_t xh = smem_desc(op, 128, 256);
+                                mma_f16_ts(d, ah + 8, xh, idesc, more);
+                                if constexpr (L::XTERMS == 2) mma_f16_ts(d, ah, smem_desc(op + cols * 32, 128, 256), idesc, 1);
+                                mma_f16_ts(d, ah, xh, idesc, 1);
+                            } else {
+                                const int steps = min(4, 2 * (blocks - 2 * i));  // of 16 values
+                                const uint64_t x0 = smem_desc(op, 128, 512);
+                                const uint64_t term = (uint64_t)(cols * 64 >> 4);
 #pragma unroll
-                            for (int k = 0; k < 4; k++) {
-                                if (k >= steps) break;
-                                const uint32_t al = ah + 32 * (k >> 1) + 8 * (k & 1);
-                                const uint64_t xh = x0 + (k >> 1) * (L::XTERMS * XOP >> 4) + (k & 1) * (256 >> 4);
-                                mma_f16_ts(d, al + 16, xh, idesc, more);
-                                more = 1;
-                                if constexpr (!L::KQ) mma_f16_ts(d, al, xh + (XOP >> 4), idesc, 1);
-                                mma_f16_ts(d, al, xh, idesc, 1);
+                                for (int k = 0; k < 4; k++) {
+                                    if (k >= steps) break;
+                                    const uint32_t al = ah + L::BLOCK_COLS * (k >> 1) + 8 * (k & 1);
+                                    const uint64_t xh = x0 + (k >> 1) * (L::XTERMS * term) + (k & 1) * (256 >> 4);
+                                    if constexpr (L::WTERMS == 2) {
+                                        mma_f16_ts(d, al + 16, xh, idesc, more);
+                                        more = 1;
+                                    }
+                                    if constexpr (L::XTERMS == 2) mma_f16_ts(d, al, xh + term, idesc, 1);
+                                    mma_f16_ts(d, al, xh, idesc, more);
+                                    more = 1;
+                                }
                             }
                             mma_commit(bars.done(n));
                             if (ends) mma_commit(bars.acc_full(acc & 1));
@@ -675,129 +677,42 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
                 }
             }
             // the last commits land before the CTA ends
-            for (uint32_t i = n > SLOTS ? n - SLOTS : 0; i < n; i++)
+            for (uint32_t i = n > L::SLOTS ? n - L::SLOTS : 0; i < n; i++)
                 mbar_wait_bounded(bars.done(i), (i / DONE) & 1u, kWaitLimitNs);
-        } else {
-            // -------------------------------------------------------- activation operands
-            // Item i of row group g (32 rows) is share i * groups + g, of warp share % 8; a slot's arrivals count four
-            // in all, whatever the number of groups.
-            const int x = warp - XW0;
+        } else if (elect_one()) {
+            // -------------------------------------------------------- the activation operands' copies
             uint32_t gc = 0, n = 0;
             bool ok = true;
-            // The copies run a chunk ahead of the conversion: warp x has the tile's rows x, x + 8, ..., one in a step;
-            // lane l keeps where the l-th of them lies.
-            int copy_ti = blockIdx.x, copy_c = 0;
-            uint32_t copied = 0, from = 0;
-            int copy_rows = 0;
-            auto copy_next = [&] {
-                if (copy_ti >= ntiles) return true;
-                if (copy_c == 0) {
-                    const ExpertTile t = a.tiles[copy_ti / nt];
-                    const int r = XWARPS * lane + x;  // behind the last row: another copy of the first record
-                    from = r < t.count ? (uint32_t)(a.order[t.first + r] / a.per_row) * (uint32_t)nchunks : 0u;
-                    copy_rows = (t.count - x + XWARPS - 1) / XWARPS;
-                }
-                const uint32_t s = copied % XST;
-                if (copied >= XST && !warp_wait(bars.x_empty(s), (copied / XST - 1) & 1u, abort_flag)) return false;
-                const uint8_t* const src = a.records + (uint64_t)copy_c * kRecord + 16 * lane;
-                const uint32_t dst = sbase + L::OFF_X + s * L::XSTAGE + x * kRecord + 16 * lane;
-#pragma unroll
-                for (int q = 0; q < kTileRows / XWARPS; q += 4)
-                    if (q < copy_rows)
-#pragma unroll
-                        for (int k = 0; k < 4; k++) {
-                            const uint32_t f = __shfl_sync(0xffffffffu, from, q + k);
-                            if (lane < kRecord / 16)
-                                copy16(dst + (q + k) * (XWARPS * kRecord), src + (uint64_t)f * kRecord, 16u);
-                        }
-                copies_arrive(bars.x_full(s));
-                copied++;
-                if (++copy_c == nchunks) copy_c = 0, copy_ti += gridDim.x;
-                return true;
-            };
-            ok = copy_next();
             for (int ti = blockIdx.x; ti < ntiles && ok; ti += gridDim.x) {
-                const int count = a.tiles[ti / nt].count;
-                const int ng = (count + 31) / 32;
-                for (int c = 0; c < nchunks && ok; c++, gc++) {
-                    const uint32_t s = gc % XST;
+                const ExpertTile t = a.tiles[ti / nt];
+                const uint32_t rows = (uint32_t)(t.count + 15) & ~15u;
+                constexpr uint32_t ROW = operand_bytes(Fmt<WT>::ACT);  // of a row's chunk
+                const uint8_t* src = a.operand + (uint64_t)t.at * (uint64_t)nchunks * ROW;
+                for (int c = 0; c < nchunks && ok; c++, gc++, src += rows * ROW) {
                     const int blocks = blocks_of(c), pairs = (blocks + 1) / 2, items = pairs + (L::MIN ? 1 : 0);
-                    if (!(ok = copy_next()) || !(ok = warp_wait(bars.x_full(s), (gc / XST) & 1u, abort_flag))) break;
-                    for (int share = x; share < items * ng; share += XWARPS) {
-                        const int i = share / ng, g = share - i * ng, r = 32 * g + lane;
-                        const uint32_t m = n + i;
-                        const uint8_t* rec = smem + L::OFF_X + s * L::XSTAGE + r * kRecord;
-                        uint32_t f = 0;  // the power of two that the row's scales are over
-                        float scale;
-                        if constexpr (L::KQ) {
-                            scale = *reinterpret_cast<const float*>(rec + 256);
-                        } else {
-                            const uint4 d = *reinterpret_cast<const uint4*>(rec + 256);
-                            const uint32_t t = __vmaxu2(__vmaxu2(d.x, d.y), __vmaxu2(d.z, d.w));
-                            const int e = exponent_of(max(t & 0x7FFFu, (t >> 16) & 0x7FFFu));
-                            f = h2_dup(pow2_half(15 - e));
-                            scale = pow2(e - 15);
+                    const uint8_t* const sums = src + 8 * L::XTERMS * 64 * rows;
+                    for (int i = 0; i < items; i++, n++) {
+                        if (n >= L::X_SLOTS && !(ok = wait_or_abort(bars.done(n - L::X_SLOTS), ((n - L::X_SLOTS) / DONE) & 1u, abort_flag)))
+                            break;
+                        if (i == 0) {
+                            mbar_arrive_expect_tx(bars.sx_full((int)(gc % SX_RING)), rows * 4);
+                            bulk_g2s_nohint(sbase + L::OFF_SX + gc % SX_RING * (kTileRows * 4), sums + L::XTERMS * 32 * rows, rows * 4,
+                                            bars.sx_full((int)(gc % SX_RING)));
                         }
-                        if (i == 0) sx[(gc & (SX_RING - 1)) * kTileRows + r] = scale;
-                        if (m >= L::X_SLOTS) {
-                            const uint32_t q = m - L::X_SLOTS;
-                            if (!(ok = warp_wait(bars.done(q), (q / DONE) & 1u, abort_flag))) break;
-                        }
-                        uint8_t* op = smem + L::OFF_OP + m % L::X_SLOTS * L::XSLOT;
-                        if (L::MIN && i == pairs) {
-#pragma unroll
-                            for (int kq = 0; kq < 2; kq++) {
-                                const uint4 u = *reinterpret_cast<const uint4*>(rec + 272 + 16 * kq);
-                                uint32_t v[4] = {u.x, u.y, u.z, u.w};
-                                if constexpr (!L::KQ) {
-                                    uint32_t lo[4];
-#pragma unroll
-                                    for (int b = 0; b < 4; b++)  // block b's two sums times its scale
-                                        v[b] = times_scale(v[b], h2_mul(h2_dup(*reinterpret_cast<const unsigned short*>(rec + 256 + 8 * kq + 2 * b)), f), &lo[b]);
-                                    put_x(op + XOP, r, kq, lo);
-                                }
-                                put_x(op, r, kq, v);
-                            }
-                        } else {
-#pragma unroll
-                            for (int h = 0; h < 2; h++) {
-                                const int kb = 2 * i + h;
-                                if (!L::KQ && kb >= blocks) break;
-                                uint32_t d = 0;
-                                if constexpr (!L::KQ) d = h2_mul(h2_dup(*reinterpret_cast<const unsigned short*>(rec + 256 + 2 * kb)), f);
-                                uint8_t* const oh = op + h * L::XTERMS * XOP;
-#pragma unroll
-                                for (int half = 0; half < 2; half++) {
-                                    const uint4 u = *reinterpret_cast<const uint4*>(rec + 32 * kb + 16 * half);
-                                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-                                    uint32_t v[8];
-#pragma unroll
-                                    for (int b = 0; b < 4; b++) {
-                                        v[2 * b] = h2_sub(bytes_to_h2(w[b], 0x5140), 0x64806480u);
-                                        v[2 * b + 1] = h2_sub(bytes_to_h2(w[b], 0x7362), 0x64806480u);
-                                    }
-                                    if constexpr (!L::KQ) {
-                                        uint32_t lo[8];
-#pragma unroll
-                                        for (int b = 0; b < 8; b++) v[b] = times_scale(v[b], d, &lo[b]);
-                                        put_x(oh + XOP, r, 2 * half, lo);
-                                        put_x(oh + XOP, r, 2 * half + 1, lo + 4);
-                                    }
-                                    put_x(oh, r, 2 * half, v);
-                                    put_x(oh, r, 2 * half + 1, v + 4);
-                                }
-                            }
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_n(bars.op(m % SLOTS), g + 1 == ng ? 5 - ng : 1);
+                        const bool mins = L::MIN && i == pairs;
+                        const uint32_t bytes = L::XTERMS * rows * (mins ? 32u : 64u * min(2, blocks - 2 * i));
+                        mbar_arrive_expect_tx(bars.x_full((int)(n % L::X_SLOTS)), bytes);
+                        bulk_g2s_nohint(sbase + L::OFF_OP + n % L::X_SLOTS * L::XSLOT, mins ? sums : src + 2 * i * L::XTERMS * 64 * rows,
+                                        bytes, bars.x_full((int)(n % L::X_SLOTS)));
                     }
-                    n += items;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bars.x_empty(s));
                 }
             }
-            copies_wait();
+            if (!ok) {  // after a timeout: the copies in flight land before the CTA ends
+                for (uint32_t i = n > L::X_SLOTS ? n - L::X_SLOTS : 0; i < n; i++)
+                    mbar_wait_bounded(bars.x_full((int)(i % L::X_SLOTS)), (i / L::X_SLOTS) & 1u, kWaitLimitNs);
+                for (uint32_t i = gc > 2 ? gc - 2 : 0; i < gc; i++)
+                    mbar_wait_bounded(bars.sx_full((int)(i % SX_RING)), (i / SX_RING) & 1u, kWaitLimitNs);
+            }
         }
     }
     tc_fence_before();

@@ -9,24 +9,29 @@
 namespace qmm {
 
 constexpr int kTileRows = 128;  // activation rows of a tile
-// 256 values of an activation row: 256 codes (plus 128); 8 f16 scales (Q8_0) or one f32 (Q8_K) at 256; the codes' sums over groups of
-// 16 as f16 (whole numbers up to 2048, exact) at 272.  19 16-byte words: neighbouring rows' words fall in other banks.
-constexpr int kRecord = 304;
+
+// The activation operand of a tile, its rows made a multiple of 16 (zeros behind the last), chunk of 256 values by chunk:
+//   for each of 8 blocks of 32 values, each term: rows / 8 groups of 8 rows, each 4 core matrices (8 values) of 8 rows
+//   the sums of 16 values, each term: rows / 8 groups of 2 core matrices
+//   the f32 scale of each row's chunk
+// Q8_0 rows have two terms, Q8_K rows one.
+constexpr int operand_terms(int act) { return act == QMM_Q8_0 ? 2 : 1; }
+constexpr int operand_bytes(int act) { return operand_terms(act) * (512 + 32) + 4; }  // of a row's chunk
 
 struct ExpertTile {
-    int32_t expert, first, count, unused;  // rows order[first .. first + count) of one expert
+    int32_t expert, first, count;  // rows order[first .. first + count) of one expert
+    int32_t at;                    // where its operand begins, in rows
 };
 
 struct ExpertMma {
     const uint8_t* W0;      // [E][N] rows: the product's, or the gate's
     const uint8_t* W1;      // gated: the up matrix's
-    const uint8_t* records; // [rows][ceil(K / 256)] records
+    const uint8_t* operand;
     const int32_t* order;   // the rows (choices) of the tiles
     const ExpertTile* tiles;
     const int32_t* ntiles;
     float* y;               // [choices][N]
     int64_t out_values;
-    int per_row;            // choices that share an activation row
     int E, N, K, kind;
 };
 
