@@ -17,13 +17,14 @@
 //
 // A tile is 128 weight rows (gated: 64 rows of the gate's and of the up matrix, row by row, so that both sums of an
 // output lie in neighbouring lanes) by up to 128 rows of one expert; CTAs, one per SM, walk over the tiles, and a tile's
-// last sums are added while the next one's operands are made.  The warps hand each other pairs of blocks (64 values):
-//   0-15   converters and epilogue: warp w has the 32 weight rows of lane quadrant w % 4 and of each chunk of 256 values
+// last sums are added while the next one's operands are made.  The warps hand each other items, a chunk of 256 values or,
+// where weights have two terms, half of one (a handover of 64 values left the issuing warp with 200 cycles an MMA of 64):
+//   0-15   converters and epilogue: warp w has the 32 weight rows of lane quadrant w % 4 and of each chunk the blocks of
 //          pair w / 4, turned into f16 in its tensor-memory lanes; then, for the chunk before, the sums of 32 activation
 //          rows times its 32 weight rows, which it adds up in registers
 //   16     issues the MMAs
-//   17     copies the activation operands, which come ready made, sorted and laid out in tiles: a bulk copy a pair (made
-//          here from 8-bit rows by eight warps they took as many instructions as the weights)
+//   17     copies the activation operands, which come ready made, sorted and laid out in tiles: a bulk copy an item
+//          (made here from 8-bit rows by eight warps they took as many instructions as the weights)
 //   18-23  copy the weight rows' bytes, 16 to a lane (a bulk copy a row left the copying warp with 84 cycles each, one
 //          warp's cp.async come 65 cycles apart)
 // Weights are read once per 128 rows of their expert.  What bounds a tile is the converters' instructions, whatever the
@@ -48,12 +49,6 @@ constexpr int THREADS = (WCOPY + WCOPIES) * 32;
 // Registers a thread: 768 threads start with 80; the converters, with their sums, go up to what the others give away.
 constexpr int REGS_CONV = 96, REGS_OTHER = 48;
 static_assert(THREADS == 768 && CONV * 32 * REGS_CONV + (THREADS - CONV * 32) * REGS_OTHER <= THREADS * 80, "registers");
-// "The MMAs of item n are done" is told on barrier n % 16 (an item is a pair, or a chunk's minimums).  A converter waits
-// only for the items whose slots it takes over and skips the others, so that a barrier of few phases could show it the
-// parity of the phase before the one it means (seen with 4: a slot taken over early, its barrier arrived at too often).
-// It has added up all of the chunk before last, so what it waits for is less than two chunks, 10 items, behind the last
-// that is surely done.
-constexpr int DONE = 16;
 constexpr int A_COL0 = 2 * kTileRows;  // after two accumulators
 constexpr int XOP = kTileRows * 64;    // bytes of one term of a block's activation operand: 32 values of 128 rows
 constexpr int SX_RING = 8;    // chunks of activation scales
@@ -64,26 +59,29 @@ struct Lay {
     static constexpr bool KQ = F::BV == 256;
     static constexpr bool MIN = WT == QMM_Q4_1 || WT == QMM_Q5_1 || WT == QMM_Q4_K || WT == QMM_Q5_K || WT == QMM_Q2_K;
     static constexpr int WTERMS = KQ && WT != QMM_Q6_K ? 1 : 2, XTERMS = operand_terms(F::ACT);
-    // weight operands in tensor memory, one for a pair of blocks: each block's 16 columns of hi and 16 of lo
-    static constexpr int BLOCK_COLS = 16 * WTERMS, SLOT_COLS = 2 * BLOCK_COLS, SLOTS = 256 / SLOT_COLS;
-    static constexpr int X_SLOTS = KQ ? 8 : 4;
-    static constexpr int XSLOT = 2 * XTERMS * XOP;  // a pair: block by block, hi then lo
+    // Items of a chunk, and the blocks of one.  A weight operand has 128 columns of tensor memory, each block 16 of hi and
+    // (two terms) 16 of lo; there are two.
+    static constexpr int ITEMS = WTERMS, BLOCKS = 8 / ITEMS, BLOCK_COLS = 16 * WTERMS;
+    // activation operands: block by block, hi then lo; behind them the sums
+    static constexpr int X_SLOTS = WT == QMM_Q6_K ? 4 : 2;
+    static constexpr int XSUMS = BLOCKS * XTERMS * XOP, XSLOT = XSUMS + (MIN ? XTERMS * XOP / 2 : 0);
+    // the minimums' operand, in shared memory: hi, lo; there are two
+    static constexpr int AMIN = MIN ? 2 * BM * 32 : 0;
     static constexpr int CHUNK = KQ ? F::BB : 8 * F::BB;  // bytes of a row's 256 values
     // a copied row: the 16-byte superset at any offset that blocks can have, an odd number of 16-byte words
     static constexpr int ALIGN = WT == QMM_Q4_K || WT == QMM_Q5_K ? 16 : WT == QMM_Q2_K || WT == QMM_Q4_1 ? 4 : WT == QMM_Q5_1 ? 8 : 2;
     static constexpr int WORDS = (CHUNK + 16 - ALIGN + 15) / 16;
     static constexpr int PITCH = 16 * (WORDS | 1);
-    // pairs of an accumulation: where activations have two terms, sums leave the tensor core twice as often
-    static constexpr int FOLD = KQ ? 4 : 2;
-    static constexpr int FIXED = X_SLOTS * XSLOT + SX_RING * kTileRows * 4 + 512;
+    static constexpr int FIXED = X_SLOTS * XSLOT + 2 * AMIN + SX_RING * kTileRows * 4 + 512;
     static constexpr int FIT = (232448 - 128 - FIXED) / (BM * PITCH);
-    static constexpr int WST = FIT >= 4 ? 4 : 2;  // a power of two
+    static constexpr int WST = FIT >= 4 ? 4 : FIT;
     static_assert(FIT >= 2, "two stages of weight rows");
     static constexpr int OFF_W = 0;
     static constexpr int OFF_OP = OFF_W + WST * BM * PITCH;
-    static constexpr int OFF_SX = OFF_OP + X_SLOTS * XSLOT;
+    static constexpr int OFF_AMIN = OFF_OP + X_SLOTS * XSLOT;
+    static constexpr int OFF_SX = OFF_AMIN + 2 * AMIN;
     static constexpr int OFF_BAR = OFF_SX + SX_RING * kTileRows * 4;
-    static constexpr int NBARS = 2 * WST + X_SLOTS + SX_RING + SLOTS + DONE + 4;
+    static constexpr int NBARS = 2 * WST + 2 * X_SLOTS + SX_RING + 2 + 4;
     static constexpr int OFF_TMEM = OFF_BAR + NBARS * 8;
     static constexpr int SMEM = OFF_TMEM + 16;
     static_assert(SMEM <= 232448 && OFF_OP % 128 == 0 && NBARS * 8 + 16 <= 512, "shared memory");
@@ -95,12 +93,14 @@ struct Bars {
     uint32_t base;
     __device__ uint32_t w_full(int s) const { return base + 8u * s; }                       // weight rows landed
     __device__ uint32_t w_empty(int s) const { return base + 8u * (L::WST + s); }           // converted
-    __device__ uint32_t x_full(int i) const { return base + 8u * (2 * L::WST + i); }  // item n % X_SLOTS: activations landed
+    __device__ uint32_t x_full(uint32_t m) const { return base + 8u * (2 * L::WST + m % L::X_SLOTS); }  // item m: activations
     __device__ uint32_t sx_full(int i) const { return base + 8u * (2 * L::WST + L::X_SLOTS + i); }  // a chunk's scales landed
-    __device__ uint32_t w_op(int i) const { return base + 8u * (OPS + i); }  // item n % SLOTS: weights written
-    __device__ uint32_t done(uint32_t n) const { return base + 8u * (OPS + L::SLOTS + n % DONE); }  // its MMAs are done
-    __device__ uint32_t acc_full(int i) const { return base + 8u * (OPS + L::SLOTS + DONE + i); }
-    __device__ uint32_t acc_empty(int i) const { return base + 8u * (OPS + L::SLOTS + DONE + 2 + i); }
+    __device__ uint32_t w_op(uint32_t m) const { return base + 8u * (OPS + m % 2); }  // item m: weights written
+    // Item m's MMAs are done.  Whoever waits for it has waited for the item before on this barrier: an activation slot's
+    // copies are of every item, and a weight converter's items are every (second) one.
+    __device__ uint32_t done(uint32_t m) const { return base + 8u * (OPS + 2 + m % L::X_SLOTS); }
+    __device__ uint32_t acc_full(int i) const { return base + 8u * (OPS + 2 + L::X_SLOTS + i); }
+    __device__ uint32_t acc_empty(int i) const { return base + 8u * (OPS + 2 + L::X_SLOTS + 2 + i); }
     static constexpr int OPS = 2 * L::WST + L::X_SLOTS + SX_RING;
 };
 
@@ -356,12 +356,15 @@ __device__ __forceinline__ void convert_min(const SmemBytes& w, uint32_t o, int 
     }
 }
 
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
-                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
+// The MMA with A in tensor memory and B in shared memory, K-major core matrices 128 bytes apart along K and `sbo` along N:
+// `x` is B's address over 16.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t x, uint32_t sbo, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 b;\n mov.b64 b, {%2, %3};\n setp.ne.u32 p, %5, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(x | 128u >> 4 << 16), "r"(sbo >> 4 | 1u << 14), "r"(idesc), "r"(add ? 1u : 0u)
+        : "memory");
 }
-
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
@@ -381,10 +384,9 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < L::WST; i++) mbar_init(bars.w_full(i), WCOPIES * 32), mbar_init(bars.w_empty(i), CONV);
-        for (int i = 0; i < L::X_SLOTS; i++) mbar_init(bars.x_full(i), 1);
+        for (int i = 0; i < L::X_SLOTS; i++) mbar_init(bars.x_full(i), 1), mbar_init(bars.done(i), 1);
         for (int i = 0; i < SX_RING; i++) mbar_init(bars.sx_full(i), 1);
-        for (int i = 0; i < L::SLOTS; i++) mbar_init(bars.w_op(i), 4);
-        for (int i = 0; i < DONE; i++) mbar_init(bars.done(i), 1);
+        for (int i = 0; i < 2; i++) mbar_init(bars.w_op(i), CONV / L::ITEMS);
         for (int i = 0; i < 2; i++) mbar_init(bars.acc_full(i), 1), mbar_init(bars.acc_empty(i), CONV);
         *abort_flag = 0;
         fence_mbar_init();
@@ -424,7 +426,7 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
         float acc[32];
 #pragma unroll
         for (int j = 0; j < 32; j++) acc[j] = 0.0f;
-        uint32_t gc = 0, n = 0, folded = 0;  // chunks, items, accumulations
+        uint32_t gc = 0, folded = 0;  // chunks, accumulations
         bool ok = true;
         // The chunk before: its sums are added while the MMAs of the next run, also across tiles.
         bool pending = false, pending_last = false;
@@ -504,55 +506,49 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
             const uint64_t row = (uint64_t)weight_row(t, n0, r) * rb;
             for (int c = 0; c < nchunks; c++, gc++) {
                 const uint32_t s = gc % L::WST;
-                const int blocks = blocks_of(c), pairs = (blocks + 1) / 2;
+                const int blocks = blocks_of(c);
                 // the first half of the chunk before, for which the MMAs of this one wait
                 if (pending && pending_halves == 2 && !(ok = fold())) break;
                 if (!(ok = warp_wait(bars.w_full(s), (gc / L::WST) & 1u, abort_flag))) break;
                 const SmemBytes w{smem + L::OFF_W + (s * BM + r) * L::PITCH};
                 const uint32_t o = (uint32_t)(row + (uint64_t)c * L::CHUNK) & 15u;
                 const WRow ws = row_scale<WT>(w, o, blocks);
-                // this warp's operands, each once its slot's last MMAs are done
-                if (L::KQ || grp < pairs) {
-                    const uint32_t m = n + grp, slot = lanes + (uint32_t)A_COL0 + m % L::SLOTS * L::SLOT_COLS;
-                    if (m >= L::SLOTS && !(ok = warp_wait(bars.done(m - L::SLOTS), ((m - L::SLOTS) / DONE) & 1u, abort_flag))) break;
-                    tc_fence_after();
+                // this warp's blocks of its item, once the MMAs of the one before in its place are done
+                const uint32_t m = L::ITEMS * gc + (L::ITEMS == 2 ? grp >> 1 : 0);
+                if (m >= 2 && !(ok = warp_wait(bars.done(m - 2), ((m - 2) / L::X_SLOTS) & 1u, abort_flag))) break;
+                tc_fence_after();
+                const uint32_t slot = lanes + (uint32_t)A_COL0 + (m & 1) * 128 + (2 * grp % L::BLOCKS) * L::BLOCK_COLS;
 #pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        if (!L::KQ && 2 * grp + h >= blocks) break;
-                        uint32_t hi[16], lo[16];
-                        convert_block<WT>(w, o, 2 * grp + h, ws, hi, lo);
-                        tmem_st16(slot + L::BLOCK_COLS * h, hi);
-                        if constexpr (L::WTERMS == 2) tmem_st16(slot + L::BLOCK_COLS * h + 16, lo);
-                    }
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bars.w_op(m % L::SLOTS));
+                for (int h = 0; h < 2; h++) {
+                    if (!L::KQ && 2 * grp + h >= blocks) break;
+                    uint32_t hi[16], lo[16];
+                    convert_block<WT>(w, o, 2 * grp + h, ws, hi, lo);
+                    tmem_st16(slot + L::BLOCK_COLS * h, hi);
+                    if constexpr (L::WTERMS == 2) tmem_st16(slot + L::BLOCK_COLS * h + 16, lo);
                 }
                 if constexpr (L::MIN) {
-                    if ((int)(gc & 3) == grp) {
-                        const uint32_t m = n + pairs, slot = lanes + (uint32_t)A_COL0 + m % L::SLOTS * L::SLOT_COLS;
-                        if (m >= L::SLOTS && !(ok = warp_wait(bars.done(m - L::SLOTS), ((m - L::SLOTS) / DONE) & 1u, abort_flag))) break;
-                        tc_fence_after();
+                    // the minimums go with the chunk's last item, by one of its groups in turn
+                    if (grp == (L::ITEMS == 1 ? (int)(gc & 3) : 2 * (blocks > 4) + (int)(gc & 1))) {
                         uint32_t hi[8], lo[8];
                         convert_min<WT>(w, o, blocks, ws, hi, lo);
-                        tmem_st8(slot, hi);
-                        tmem_st8(slot + 8, lo);
-                        tmem_st_wait();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bars.w_op(m % L::SLOTS));
+                        uint8_t* const at = smem + L::OFF_AMIN + (gc & 1) * L::AMIN + (r >> 3) * 256 + (r & 7) * 16;
+                        *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4*>(at + 128) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+                        *reinterpret_cast<uint4*>(at + BM * 32) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        *reinterpret_cast<uint4*>(at + BM * 32 + 128) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+                        fence_proxy_async_smem();
                     }
                 }
-                n += pairs + (L::MIN ? 1 : 0);
+                tmem_st_wait();
+                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bars.w_empty(s));
+                if (lane == 0) mbar_arrive(bars.w_op(m)), mbar_arrive(bars.w_empty(s));
                 if (pending) {
                     if (!(ok = fold())) break;
                     if (pending_last) finish();
                 }
                 pending = true, pending_last = c + 1 == nchunks, pending_scale = ws.scale;
-                pending_halves = pairs > L::FOLD ? 2 : 1, pending_tile = t, pending_n0 = n0;
+                pending_halves = !L::KQ && blocks > 4 ? 2 : 1, pending_tile = t, pending_n0 = n0;
             }
         }
         if (ok && pending && (pending_halves == 1 || fold()) && fold()) finish();
@@ -622,66 +618,66 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
             // -------------------------------------------------------- the MMAs
             // The whole warp walks, so that addresses and descriptors stay in uniform registers; one lane issues.
             const bool leader = elect_one();
-            uint32_t acc = 0, n = 0;  // accumulations, items
+            uint32_t acc = 0, m = 0, c0 = 0;  // accumulations, items, chunks of the tiles before
             bool ok = true;
             for (int ti = blockIdx.x; ti < ntiles && ok; ti += gridDim.x) {
-                const int cols = (a.tiles[ti / nt].count + 15) & ~15;
-                const uint32_t idesc = instr_desc_f16(BM, cols);
+                const uint32_t rows = (uint32_t)(a.tiles[ti / nt].count + 15) & ~15u;
+                const uint32_t idesc = instr_desc_f16(BM, (int)rows);
+                const uint32_t term = rows * 64 >> 4;  // of a block's activations, in descriptor units
                 for (int c = 0; c < nchunks && ok; c++) {
-                    const int blocks = blocks_of(c), pairs = (blocks + 1) / 2, items = pairs + (L::MIN ? 1 : 0);
-                    uint32_t d = 0, more = 0;
-                    for (int i = 0; i < items; i++, n++) {
-                        if (i % L::FOLD == 0 && i < pairs) {  // another accumulation
-                            d = tmem + (acc & 1) * kTileRows;
-                            more = 0;
-                            if (acc >= 2 && !(ok = warp_wait(bars.acc_empty(acc & 1), (acc / 2 - 1) & 1u, abort_flag))) break;
-                        }
-                        if (!(ok = warp_wait(bars.x_full(n % L::X_SLOTS), (n / L::X_SLOTS) & 1u, abort_flag)) ||
-                            !(ok = warp_wait(bars.w_op(n % L::SLOTS), (n / L::SLOTS) & 1u, abort_flag)))
+                    const int blocks = blocks_of(c);
+#pragma unroll
+                    for (int h = 0; h < L::ITEMS; h++, m++) {
+                        const int mine = min(blocks - h * L::BLOCKS, L::BLOCKS);  // a last chunk's second item may be empty
+                        const bool last = L::ITEMS == 1 || (blocks > 4) == h;     // of the chunk's
+                        const uint32_t d = tmem + (acc & 1) * kTileRows;
+                        if ((!L::KQ || h == 0) && mine > 0 && acc >= 2 &&
+                            !(ok = warp_wait(bars.acc_empty(acc & 1), (acc / 2 - 1) & 1u, abort_flag)))
+                            break;
+                        if (!(ok = warp_wait(bars.x_full(m), (m / L::X_SLOTS) & 1u, abort_flag)) ||
+                            !(ok = warp_wait(bars.w_op(m), (m / 2) & 1u, abort_flag)))
                             break;
                         tc_fence_after();
-                        const uint32_t ah = tmem + (uint32_t)A_COL0 + n % L::SLOTS * L::SLOT_COLS;
-                        const uint32_t op = sbase + L::OFF_OP + n % L::X_SLOTS * L::XSLOT;
-                        const bool ends = i + 1 == items || ((i + 1) % L::FOLD == 0 && i + 1 < pairs);
+                        const uint32_t ah = tmem + (uint32_t)A_COL0 + (m & 1) * 128;
+                        const uint32_t op = sbase + L::OFF_OP + m % L::X_SLOTS * L::XSLOT;
                         if (leader) {
-                            if (L::MIN && i == pairs) {  // hi and lo of the minimums, their sums' rows 32 bytes apart
-                                const uint64_t xh = smem_desc(op, 128, 256);
-                                mma_f16_ts(d, ah + 8, xh, idesc, more);
-                                if constexpr (L::XTERMS == 2) mma_f16_ts(d, ah, smem_desc(op + cols * 32, 128, 256), idesc, 1);
-                                mma_f16_ts(d, ah, xh, idesc, 1);
-                            } else {
-                                const int steps = min(4, 2 * (blocks - 2 * i));  // of 16 values
-                                const uint64_t x0 = smem_desc(op, 128, 512);
-                                const uint64_t term = (uint64_t)(cols * 64 >> 4);
+                            uint32_t x = op >> 4;
 #pragma unroll
-                                for (int k = 0; k < 4; k++) {
-                                    if (k >= steps) break;
-                                    const uint32_t al = ah + L::BLOCK_COLS * (k >> 1) + 8 * (k & 1);
-                                    const uint64_t xh = x0 + (k >> 1) * (L::XTERMS * term) + (k & 1) * (256 >> 4);
-                                    if constexpr (L::WTERMS == 2) {
-                                        mma_f16_ts(d, al + 16, xh, idesc, more);
-                                        more = 1;
-                                    }
-                                    if constexpr (L::XTERMS == 2) mma_f16_ts(d, al, xh + term, idesc, 1);
-                                    mma_f16_ts(d, al, xh, idesc, more);
-                                    more = 1;
+                            for (int b = 0; b < L::BLOCKS; b++) {
+                                if (!L::KQ && b >= mine) break;
+#pragma unroll
+                                for (int k = 0; k < 2; k++) {
+                                    const uint32_t al = ah + L::BLOCK_COLS * b + 8 * k, xh = x + 16 * k;
+                                    // the accumulation's first MMA starts its sums
+                                    const bool first = b == 0 && k == 0 && (!L::KQ || h == 0);
+                                    if constexpr (L::WTERMS == 2) mma_ts(d, al + 16, xh, 512, idesc, !first);
+                                    if constexpr (L::XTERMS == 2) mma_ts(d, al, xh + term, 512, idesc, true);
+                                    mma_ts(d, al, xh, 512, idesc, L::WTERMS == 2 || !first);
                                 }
+                                x += L::XTERMS * term;
                             }
-                            mma_commit(bars.done(n));
-                            if (ends) mma_commit(bars.acc_full(acc & 1));
+                            if (L::MIN && last) {  // hi and lo of the minimums, 16 sums a row
+                                const uint64_t al = smem_desc(sbase + L::OFF_AMIN + ((c0 + c) & 1) * L::AMIN, 128, 256);
+                                const uint64_t xh = smem_desc(op + L::XSUMS, 128, 256);
+                                mma_f16(d, al + (BM * 32 >> 4), xh, idesc, 1);
+                                if constexpr (L::XTERMS == 2) mma_f16(d, al, xh + (rows * 32 >> 4), idesc, 1);
+                                mma_f16(d, al, xh, idesc, 1);
+                            }
+                            mma_commit(bars.done(m));
+                            if (L::KQ ? last : mine > 0) mma_commit(bars.acc_full(acc & 1));
                         }
-                        more = 1;
-                        if (ends) acc++;
+                        if (L::KQ ? last : mine > 0) acc++;
                         __syncwarp();
                     }
                 }
+                c0 += nchunks;
             }
             // the last commits land before the CTA ends
-            for (uint32_t i = n > L::SLOTS ? n - L::SLOTS : 0; i < n; i++)
-                mbar_wait_bounded(bars.done(i), (i / DONE) & 1u, kWaitLimitNs);
+            for (uint32_t i = m > L::X_SLOTS ? m - L::X_SLOTS : 0; i < m; i++)
+                mbar_wait_bounded(bars.done(i), (i / L::X_SLOTS) & 1u, kWaitLimitNs);
         } else if (elect_one()) {
             // -------------------------------------------------------- the activation operands' copies
-            uint32_t gc = 0, n = 0;
+            uint32_t gc = 0, m = 0;
             bool ok = true;
             for (int ti = blockIdx.x; ti < ntiles && ok; ti += gridDim.x) {
                 const ExpertTile t = a.tiles[ti / nt];
@@ -689,27 +685,27 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
                 constexpr uint32_t ROW = operand_bytes(Fmt<WT>::ACT);  // of a row's chunk
                 const uint8_t* src = a.operand + (uint64_t)t.at * (uint64_t)nchunks * ROW;
                 for (int c = 0; c < nchunks && ok; c++, gc++, src += rows * ROW) {
-                    const int blocks = blocks_of(c), pairs = (blocks + 1) / 2, items = pairs + (L::MIN ? 1 : 0);
+                    const int blocks = blocks_of(c);
                     const uint8_t* const sums = src + 8 * L::XTERMS * 64 * rows;
-                    for (int i = 0; i < items; i++, n++) {
-                        if (n >= L::X_SLOTS && !(ok = wait_or_abort(bars.done(n - L::X_SLOTS), ((n - L::X_SLOTS) / DONE) & 1u, abort_flag)))
-                            break;
-                        if (i == 0) {
-                            mbar_arrive_expect_tx(bars.sx_full((int)(gc % SX_RING)), rows * 4);
-                            bulk_g2s_nohint(sbase + L::OFF_SX + gc % SX_RING * (kTileRows * 4), sums + L::XTERMS * 32 * rows, rows * 4,
-                                            bars.sx_full((int)(gc % SX_RING)));
+                    for (int h = 0; h < L::ITEMS; h++, m++) {
+                        if (m >= L::X_SLOTS && !(ok = wait_or_abort(bars.done(m), (m / L::X_SLOTS - 1) & 1u, abort_flag))) break;
+                        if (h == 0) {
+                            const uint32_t bar = bars.sx_full((int)(gc % SX_RING));
+                            mbar_arrive_expect_tx(bar, rows * 4);
+                            bulk_g2s_nohint(sbase + L::OFF_SX + gc % SX_RING * (kTileRows * 4), sums + L::XTERMS * 32 * rows, rows * 4, bar);
                         }
-                        const bool mins = L::MIN && i == pairs;
-                        const uint32_t bytes = L::XTERMS * rows * (mins ? 32u : 64u * min(2, blocks - 2 * i));
-                        mbar_arrive_expect_tx(bars.x_full((int)(n % L::X_SLOTS)), bytes);
-                        bulk_g2s_nohint(sbase + L::OFF_OP + n % L::X_SLOTS * L::XSLOT, mins ? sums : src + 2 * i * L::XTERMS * 64 * rows,
-                                        bytes, bars.x_full((int)(n % L::X_SLOTS)));
+                        const uint32_t dst = sbase + L::OFF_OP + m % L::X_SLOTS * L::XSLOT;
+                        const uint32_t bytes = L::XTERMS * 64 * rows * (uint32_t)max(0, min(blocks - h * L::BLOCKS, L::BLOCKS));
+                        const uint32_t sbytes = L::MIN && (L::ITEMS == 1 || (blocks > 4) == h) ? L::XTERMS * 32 * rows : 0u;
+                        mbar_arrive_expect_tx(bars.x_full(m), bytes + sbytes);
+                        if (bytes) bulk_g2s_nohint(dst, src + h * L::BLOCKS * L::XTERMS * 64 * rows, bytes, bars.x_full(m));
+                        if (sbytes) bulk_g2s_nohint(dst + L::XSUMS, sums, sbytes, bars.x_full(m));
                     }
                 }
             }
             if (!ok) {  // after a timeout: the copies in flight land before the CTA ends
-                for (uint32_t i = n > L::X_SLOTS ? n - L::X_SLOTS : 0; i < n; i++)
-                    mbar_wait_bounded(bars.x_full((int)(i % L::X_SLOTS)), (i / L::X_SLOTS) & 1u, kWaitLimitNs);
+                for (uint32_t i = m > L::X_SLOTS ? m - L::X_SLOTS : 0; i < m; i++)
+                    mbar_wait_bounded(bars.x_full(i), (i / L::X_SLOTS) & 1u, kWaitLimitNs);
                 for (uint32_t i = gc > 2 ? gc - 2 : 0; i < gc; i++)
                     mbar_wait_bounded(bars.sx_full((int)(i % SX_RING)), (i / SX_RING) & 1u, kWaitLimitNs);
             }
