@@ -67,12 +67,16 @@ struct Lay {
     static constexpr int XSUMS = BLOCKS * XTERMS * XOP, XSLOT = XSUMS + (MIN ? XTERMS * XOP / 2 : 0);
     // the minimums' operand, in shared memory: hi, lo; there are two
     static constexpr int AMIN = MIN ? 2 * BM * 32 : 0;
+    // 32-value blocks without minimums: the halves of a chunk are accumulated, and have their powers of two, each for itself;
+    // four chunks' powers lie in shared memory
+    static constexpr bool HALVES = !KQ && !MIN;
+    static constexpr int SW = HALVES ? 4 * 2 * BM * 4 : 0;
     static constexpr int CHUNK = KQ ? F::BB : 8 * F::BB;  // bytes of a row's 256 values
     // a copied row: the 16-byte superset at any offset that blocks can have, an odd number of 16-byte words
     static constexpr int ALIGN = WT == QMM_Q4_K || WT == QMM_Q5_K ? 16 : WT == QMM_Q2_K || WT == QMM_Q4_1 ? 4 : WT == QMM_Q5_1 ? 8 : 2;
     static constexpr int WORDS = (CHUNK + 16 - ALIGN + 15) / 16;
     static constexpr int PITCH = 16 * (WORDS | 1);
-    static constexpr int FIXED = X_SLOTS * XSLOT + 2 * AMIN + SX_RING * kTileRows * 4 + 512;
+    static constexpr int FIXED = X_SLOTS * XSLOT + 2 * AMIN + SX_RING * kTileRows * 4 + SW + 512;
     static constexpr int FIT = (232448 - 128 - FIXED) / (BM * PITCH);
     static constexpr int WST = FIT >= 4 ? 4 : FIT;
     static_assert(FIT >= 2, "two stages of weight rows");
@@ -80,7 +84,8 @@ struct Lay {
     static constexpr int OFF_OP = OFF_W + WST * BM * PITCH;
     static constexpr int OFF_AMIN = OFF_OP + X_SLOTS * XSLOT;
     static constexpr int OFF_SX = OFF_AMIN + 2 * AMIN;
-    static constexpr int OFF_BAR = OFF_SX + SX_RING * kTileRows * 4;
+    static constexpr int OFF_SW = OFF_SX + SX_RING * kTileRows * 4;
+    static constexpr int OFF_BAR = OFF_SW + SW;
     static constexpr int NBARS = 2 * WST + 2 * X_SLOTS + SX_RING + 2 + 4;
     static constexpr int OFF_TMEM = OFF_BAR + NBARS * 8;
     static constexpr int SMEM = OFF_TMEM + 16;
@@ -175,7 +180,8 @@ constexpr int center() {
     return WT == QMM_Q4_1 ? 8 : WT == QMM_Q5_1 ? 16 : 0;
 }
 
-// The 32 codes of block kb of the chunk at byte `o` of the row, in K order, four to a word, and the f16 offset word.
+// The 32 codes of block kb of the chunk at byte `o` of the row, in K order, four to a word (Q4_K: 16 times those of odd
+// blocks), and the f16 offset word.
 template <int WT>
 __device__ __forceinline__ uint32_t codes_of(const SmemBytes& w, uint32_t o, int kb, uint32_t (&c)[8]) {
     if constexpr (WT == QMM_Q8_0) {
@@ -210,11 +216,10 @@ __device__ __forceinline__ uint32_t codes_of(const SmemBytes& w, uint32_t o, int
         return WT == QMM_Q4_0 || WT == QMM_Q4_1 ? 0x64086408u : 0x64106410u;
     } else if constexpr (WT == QMM_Q4_K || WT == QMM_Q5_K) {
         const uint32_t b = o + (WT == QMM_Q4_K ? 16 : 48) + 32 * (kb >> 1);
-        const int sh = 4 * (kb & 1);
         const uint4 q0 = *reinterpret_cast<const uint4*>(w.base + b), q1 = *reinterpret_cast<const uint4*>(w.base + b + 16);
         const uint32_t q[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
 #pragma unroll
-        for (int i = 0; i < 8; i++) c[i] = (q[i] >> sh) & 0x0F0F0F0Fu;
+        for (int i = 0; i < 8; i++) c[i] = WT == QMM_Q4_K ? q[i] & (kb & 1 ? 0xF0F0F0F0u : 0x0F0F0F0Fu) : (q[i] >> (4 * (kb & 1))) & 0x0F0F0F0Fu;
         if constexpr (WT == QMM_Q5_K) {
             const uint4 h0 = *reinterpret_cast<const uint4*>(w.base + o + 16), h1 = *reinterpret_cast<const uint4*>(w.base + o + 32);
             const uint32_t h[8] = {h0.x, h0.y, h0.z, h0.w, h1.x, h1.y, h1.z, h1.w};
@@ -247,12 +252,12 @@ __device__ __forceinline__ uint32_t codes_of(const SmemBytes& w, uint32_t o, int
 __device__ __forceinline__ WRow shared_scale(float d, float m) {
     const bool usual = fabsf(m) <= 1000.0f * fabsf(d);
     const float D = usual ? d : m * 1e-3f;
-    const float inv = D != 0.0f ? __fdiv_rn(1.0f, D) : 0.0f;
+    const float inv = D != 0.0f ? __fdividef(1.0f, D) : 0.0f;  // 2 units of 2^-23, of what is 2^-22 in two terms
     return {D, 0, usual ? 1.0f : d * inv, -(m * inv), make_uint4(0u, 0u, 0u, 0u)};
 }
 
 template <int WT>
-__device__ __forceinline__ WRow row_scale(const SmemBytes& w, uint32_t o, int blocks) {
+__device__ __forceinline__ WRow row_scale(const SmemBytes& w, uint32_t o, int half, int blocks) {
     if constexpr (WT == QMM_Q4_K || WT == QMM_Q5_K) {
         const uint4 head = *reinterpret_cast<const uint4*>(w.base + o);
         WRow r = shared_scale(h2f(head.x), h2f(head.x >> 16));
@@ -266,7 +271,8 @@ __device__ __forceinline__ WRow row_scale(const SmemBytes& w, uint32_t o, int bl
     } else {
         uint32_t top = 0;
 #pragma unroll
-        for (int kb = 0; kb < 8; kb++) {
+        for (int i = 0; i < (Lay<WT>::HALVES ? 4 : 8); i++) {
+            const int kb = (Lay<WT>::HALVES ? 4 * half : 0) + i;
             if (kb >= blocks) break;
             const uint32_t b = o + Fmt<WT>::BB * kb;
             if constexpr (Lay<WT>::MIN) {
@@ -297,7 +303,8 @@ __device__ __forceinline__ void convert_block(const SmemBytes& w, uint32_t o, in
     // the scales of the block's two halves
     uint32_t d0, d1;
     if constexpr (WT == QMM_Q4_K || WT == QMM_Q5_K) {
-        d0 = d1 = h2_dup(f2h_bits(row.value * (float)six_bits(kb, row.head.y, row.head.w, row.head.y)));
+        const float over = WT == QMM_Q4_K && (kb & 1) ? 0.0625f : 1.0f;
+        d0 = d1 = h2_dup(f2h_bits(row.value * over * (float)six_bits(kb, row.head.y, row.head.w, row.head.y)));
     } else if constexpr (WT == QMM_Q2_K) {
         const uint32_t sc = w.u16(o + 2 * kb);
         d0 = h2_dup(f2h_bits(row.value * (float)(sc & 15u))), d1 = h2_dup(f2h_bits(row.value * (float)((sc >> 8) & 15u)));
@@ -381,6 +388,7 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_TMEM);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_TMEM + 8);
     float* const sx = reinterpret_cast<float*>(smem + L::OFF_SX);
+    float* const sw = reinterpret_cast<float*>(smem + L::OFF_SW);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < L::WST; i++) mbar_init(bars.w_full(i), WCOPIES * 32), mbar_init(bars.w_empty(i), CONV);
@@ -431,19 +439,18 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
         // The chunk before: its sums are added while the MMAs of the next run, also across tiles.
         bool pending = false, pending_last = false;
         float pending_scale = 0.0f;
-        int pending_halves = 0, pending_n0 = 0;
-        ExpertTile pending_tile = {};
+        int pending_halves = 0, pending_n0 = 0, pending_count = 0, pending_slot = 0;  // lane j: the choice of row 32 grp + j
         // adds the next accumulation of the pending chunk, times its scales, to the registers
-        auto fold = [&] {
+        auto fold = [&](int half) {
             const uint32_t buf = folded & 1, of = gc - 1;
             if (!warp_wait(bars.acc_full((int)buf), (folded / 2) & 1u, abort_flag)) return false;
             if (!warp_wait(bars.sx_full((int)(of % SX_RING)), (of / SX_RING) & 1u, abort_flag)) return false;
             folded++;
             tc_fence_after();
-            if (grp * 32 < pending_tile.count) {
+            if (grp * 32 < pending_count) {
                 const uint32_t cols = lanes + buf * kTileRows + (uint32_t)(grp * 32);
                 const uint4* s4 = reinterpret_cast<const uint4*>(sx + of % SX_RING * kTileRows + grp * 32);
-                const uint32_t sb = __float_as_uint(pending_scale);
+                const uint32_t sb = __float_as_uint(L::HALVES ? sw[((of & 3) * 2 + half) * BM + r] : pending_scale);
                 const uint64_t s2 = f2_pack(sb, sb);
                 uint32_t v[2][8];
                 tmem_ld8(cols, v[0]);
@@ -472,19 +479,17 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
         };
         // writes the finished sums of a tile
         auto finish = [&] {
-            const ExpertTile& t = pending_tile;
             const int n0 = pending_n0;
             if constexpr (GATED) {
                 const int col = n0 + quad * 16 + (lane >> 1);
 #pragma unroll
                 for (int j = 0; j < 32; j += 2) {
-                    if (grp * 32 + j >= t.count) break;  // the whole warp
+                    if (grp * 32 + j >= pending_count) break;  // the whole warp
                     // even lanes hold the gate's sum and take token j, odd ones the up sum and token j + 1
                     const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? acc[j] : acc[j + 1], 1);
                     const float g = lane & 1 ? other : acc[j], u = lane & 1 ? acc[j + 1] : other;
-                    const int tok = grp * 32 + j + (lane & 1);
-                    if (tok < t.count && col < N) {
-                        const int64_t o = (int64_t)a.order[t.first + tok] * N + col;
+                    const int64_t o = (int64_t)__shfl_sync(0xffffffffu, pending_slot, j + (lane & 1)) * N + col;
+                    if (grp * 32 + j + (lane & 1) < pending_count && col < N) {
                         if (QMM_IN_BOUNDS(g_expert_mma_error, o, a.out_values)) a.y[o] = gated(a.kind, g, u);
                     }
                 }
@@ -492,27 +497,31 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
                 const int col = n0 + r;
 #pragma unroll
                 for (int j = 0; j < 32; j++) {
-                    if (grp * 32 + j >= t.count) break;
-                    const int64_t o = (int64_t)a.order[t.first + grp * 32 + j] * N + col;
+                    if (grp * 32 + j >= pending_count) break;
+                    const int64_t o = (int64_t)__shfl_sync(0xffffffffu, pending_slot, j) * N + col;
                     if (col < N && QMM_IN_BOUNDS(g_expert_mma_error, o, a.out_values)) a.y[o] = acc[j];
                 }
             }
 #pragma unroll
             for (int j = 0; j < 32; j++) acc[j] = 0.0f;
         };
+        ExpertTile next = blockIdx.x < ntiles ? a.tiles[blockIdx.x / nt] : ExpertTile{};
         for (int ti = blockIdx.x; ti < ntiles && ok; ti += gridDim.x) {
-            const ExpertTile t = a.tiles[ti / nt];
+            const ExpertTile t = next;
+            if (ti + (int)gridDim.x < ntiles) next = a.tiles[(ti + gridDim.x) / nt];
             const int n0 = ti % nt * NROWS;
-            const uint64_t row = (uint64_t)weight_row(t, n0, r) * rb;
+            const uint32_t row = (uint32_t)((uint64_t)weight_row(t, n0, r) * rb);  // modulo 2^32: its low bits are used
+            const int slot_of = grp * 32 + lane < t.count ? a.order[t.first + grp * 32 + lane] : 0;
             for (int c = 0; c < nchunks; c++, gc++) {
                 const uint32_t s = gc % L::WST;
                 const int blocks = blocks_of(c);
                 // the first half of the chunk before, for which the MMAs of this one wait
-                if (pending && pending_halves == 2 && !(ok = fold())) break;
+                if (pending && pending_halves == 2 && !(ok = fold(0))) break;
                 if (!(ok = warp_wait(bars.w_full(s), (gc / L::WST) & 1u, abort_flag))) break;
                 const SmemBytes w{smem + L::OFF_W + (s * BM + r) * L::PITCH};
-                const uint32_t o = (uint32_t)(row + (uint64_t)c * L::CHUNK) & 15u;
-                const WRow ws = row_scale<WT>(w, o, blocks);
+                const uint32_t o = (row + (uint32_t)(c * L::CHUNK)) & 15u;
+                const WRow ws = row_scale<WT>(w, o, grp >> 1, blocks);
+                if (L::HALVES && !(grp & 1)) sw[((gc & 3) * 2 + (grp >> 1)) * BM + r] = ws.scale;
                 // this warp's blocks of its item, once the MMAs of the one before in its place are done
                 const uint32_t m = L::ITEMS * gc + (L::ITEMS == 2 ? grp >> 1 : 0);
                 if (m >= 2 && !(ok = warp_wait(bars.done(m - 2), ((m - 2) / L::X_SLOTS) & 1u, abort_flag))) break;
@@ -544,14 +553,14 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bars.w_op(m)), mbar_arrive(bars.w_empty(s));
                 if (pending) {
-                    if (!(ok = fold())) break;
+                    if (!(ok = fold(pending_halves - 1))) break;
                     if (pending_last) finish();
                 }
                 pending = true, pending_last = c + 1 == nchunks, pending_scale = ws.scale;
-                pending_halves = !L::KQ && blocks > 4 ? 2 : 1, pending_tile = t, pending_n0 = n0;
+                pending_halves = !L::KQ && blocks > 4 ? 2 : 1, pending_count = t.count, pending_n0 = n0, pending_slot = slot_of;
             }
         }
-        if (ok && pending && (pending_halves == 1 || fold()) && fold()) finish();
+        if (ok && pending && (pending_halves == 1 || fold(0)) && fold(pending_halves - 1)) finish();
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
         if (warp >= WCOPY) {
