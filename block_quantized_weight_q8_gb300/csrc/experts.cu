@@ -53,8 +53,23 @@ __device__ __forceinline__ uint32_t bits_of(__half2 h) { return *reinterpret_cas
 constexpr int kPlanThreads = 1024, kOperandThreads = 256;
 
 // Sorts the choices by their expert and cuts each expert's into tiles.  Counting and placing use shared-memory counters,
-// one addition for a warp's choices of one expert; the order within an expert varies from run to run, and no result
-// depends on it (a row's sums do not meet another row's).  One CTA: bound by its passes over the ids, 2 x S / 1024 steps.
+// where there are few experts one addition for a warp's choices of one; the order within an expert varies from run to run,
+// and no result depends on it (a row's sums do not meet another row's).  One CTA; its loads are issued eight at a time
+// (one by one, each waiting for the counter of the one before, 16384 choices took 34 us).
+constexpr int kFewExperts = 3;
+__device__ __forceinline__ int next_place(int* counter, int e, int lane, int E) {
+    if (E > kFewExperts) return e >= 0 ? atomicAdd(&counter[e], 1) : 0;
+    int at = 0;
+    for (int i = 0; i < E; i++) {
+        const unsigned same = __ballot_sync(0xffffffffu, e == i);
+        int base = 0;
+        if (lane == 0 && same) base = atomicAdd(&counter[i], __popc(same));
+        base = __shfl_sync(0xffffffffu, base, 0);
+        if (e == i) at = base + __popc(same & ((1u << lane) - 1));
+    }
+    return at;
+}
+
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ Prepare a) {
     __shared__ int count[kMaxExperts], start[kMaxExperts];
     pdl_launch_dependents();
@@ -62,13 +77,23 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     const int tid = threadIdx.x, lane = tid & 31;
     for (int e = tid; e < a.E; e += kPlanThreads) count[e] = 0;
     __syncthreads();
-    const int Sr = (a.S + 31) & ~31;  // whole warps
-    for (int i = tid; i < Sr; i += kPlanThreads) {
-        const int e = i < a.S ? a.ids[i] : -1;
-        if (e >= a.E) atomicOr(&g_experts_error, kErrIndex);
-        const bool real = e >= 0 && e < a.E;
-        const unsigned same = __match_any_sync(0xffffffffu, real ? e : -1);
-        if (real && lane == __ffs(same) - 1) atomicAdd(&count[e], __popc(same));
+    constexpr int U = 8;
+    auto read = [&](int i0, int (&e)[U]) {  // the choices i0 + tid, + 1024, ...; -1: none
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int64_t i = (int64_t)i0 + u * kPlanThreads + tid;
+            e[u] = i < a.S ? a.ids[i] : -1;
+        }
+    };
+    for (int64_t i0 = 0; i0 < a.S; i0 += U * kPlanThreads) {
+        int e[U];
+        read((int)i0, e);
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            if (i0 + u * kPlanThreads >= a.S) break;
+            if (e[u] >= a.E) atomicOr(&g_experts_error, kErrIndex);
+            next_place(count, e[u] < a.E ? e[u] : -1, lane, a.E);
+        }
     }
     __syncthreads();
     if (tid < 32) {  // exclusive sums of the counts, of the operands' rows and of the experts' tiles
@@ -91,15 +116,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         if (lane == 0) *a.ntiles = tiles;
     }
     __syncthreads();
-    for (int i = tid; i < Sr; i += kPlanThreads) {
-        const int e = i < a.S ? a.ids[i] : -1;
-        const bool real = e >= 0 && e < a.E;
-        const unsigned same = __match_any_sync(0xffffffffu, real ? e : -1);
-        const int first = __ffs(same) - 1;
-        int at = 0;
-        if (real && lane == first) at = atomicAdd(&start[e], __popc(same));
-        at = __shfl_sync(0xffffffffu, at, first) + __popc(same & ((1u << lane) - 1));
-        if (real && QMM_IN_BOUNDS(g_experts_error, at, a.S)) a.order[at] = i;
+    for (int64_t i0 = 0; i0 < a.S; i0 += U * kPlanThreads) {
+        int e[U];
+        read((int)i0, e);
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            if (i0 + u * kPlanThreads >= a.S) break;
+            const int mine = e[u] < a.E ? e[u] : -1, at = next_place(start, mine, lane, a.E);
+            if (mine >= 0 && QMM_IN_BOUNDS(g_experts_error, at, a.S)) a.order[at] = (int)i0 + u * kPlanThreads + tid;
+        }
     }
 }
 
@@ -278,23 +303,45 @@ static bool many_rows(int wt, const ExpertShape& s) {
 }
 
 // y[t][n] = residual[t][n] + sum_j weights[t][j] p[t][j][n] over the choices that are there, in their order.  Bound by
-// memory: 4 (k + 2) bytes a value.
+// memory: 4 (k + 2) bytes a value.  V values a thread: 4 where N is a multiple of it.
+template <int V>
 __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ p, const int32_t* __restrict__ ids,
                                                       const float* __restrict__ weights, const float* residual, float* y,
                                                       int T, int k, int E, int N) {
     pdl_launch_dependents();
     pdl_wait();
-    const int64_t total = (int64_t)T * N, step = (int64_t)gridDim.x * blockDim.x;
+    const int64_t total = (int64_t)T * (N / V), step = (int64_t)gridDim.x * blockDim.x;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += step) {
-        const int64_t t = i / N;
-        const int n = (int)(i - t * N);
-        float v = 0.0f;
-        for (int j = 0; j < k; j++) {
-            const int64_t c = t * k + j;
-            const int e = ids[c];
-            if (e >= 0 && e < E) v = fmaf(weights ? weights[c] : 1.0f, p[c * N + n], v);
+        const int64_t t = i / (N / V), at = i * V;
+        const int n = (int)(at - t * N);
+        float v[V] = {};
+        for (int j0 = 0; j0 < k; j0 += 4) {
+            float u[4][V], w[4];
+#pragma unroll
+            for (int j = 0; j < 4; j++) {  // four choices' loads at a time
+                const int64_t c = t * k + j0 + j;
+                const int e = j0 + j < k ? ids[c] : -1;
+                const bool real = e >= 0 && e < E;
+                w[j] = !real ? 0.0f : weights ? weights[c] : 1.0f;
+                if constexpr (V == 4) {
+                    const float4 q = real ? *reinterpret_cast<const float4*>(p + c * N + n) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    u[j][0] = q.x, u[j][1] = q.y, u[j][2] = q.z, u[j][3] = q.w;
+                } else {
+                    u[j][0] = real ? p[c * N + n] : 0.0f;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+#pragma unroll
+                for (int q = 0; q < V; q++) v[q] = fmaf(w[j], u[j][q], v[q]);
         }
-        if (QMM_IN_BOUNDS(g_experts_error, i, total)) y[i] = residual ? residual[i] + v : v;
+        if (!QMM_IN_BOUNDS(g_experts_error, i, total)) continue;
+        if constexpr (V == 4) {
+            float4 r = residual ? *reinterpret_cast<const float4*>(residual + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+            *reinterpret_cast<float4*>(y + at) = make_float4(r.x + v[0], r.y + v[1], r.z + v[2], r.w + v[3]);
+        } else {
+            y[at] = residual ? residual[at] + v[0] : v[0];
+        }
     }
 }
 
@@ -303,9 +350,9 @@ static qmm_status combine(const ExpertShape& s, const float* p, const int32_t* i
     DeviceInfo dev;
     const qmm_status st = current_device(&dev);
     if (st != QMM_OK) return st;
-    const int64_t want = (s.T * s.N + 255) / 256, most = (int64_t)dev.sms * 8;
-    return launch_pdl(combine_kernel, dim3((unsigned)(want < most ? want : most)), 256, 0, stream, p, ids, weights, residual, y,
-                      (int)s.T, (int)s.k, (int)s.E, (int)s.N);
+    const int64_t each = s.N % 4 ? 1 : 4, want = (s.T * s.N / each + 255) / 256, most = (int64_t)dev.sms * 8;
+    return launch_pdl(s.N % 4 ? combine_kernel<1> : combine_kernel<4>, dim3((unsigned)(want < most ? want : most)), 256, 0, stream,
+                      p, ids, weights, residual, y, (int)s.T, (int)s.k, (int)s.E, (int)s.N);
 }
 
 }  // namespace qmm

@@ -5,15 +5,17 @@
 //   ids = the k open experts with the largest keys, largest first, ties to the lower index
 //   weights_j = scale * score_j, over the chosen scores' sum where they are renormalised
 //
-// An expert whose logit (or key) is -inf or NaN is closed to the token.  One warp per token, expert e in lane e % 32: the
-// logits are read once, side by side.  Each choice is a maximum over the lane's keys, one over the warp (whole-number
-// keys in the floats' order) and one of the index, so a token costs a few hundred instructions; a batch is bound by the
-// launch, then by those.
+// An expert whose logit (or key) is -inf or NaN is closed to the token.  One warp per token: each group has L lanes (a
+// power of two, 32 where there is one group), lane l of it the group's experts l, l + L, ...; so all groups' worth comes of
+// one look at a lane's keys and log2 L exchanges.  A choice is a maximum over the lane's keys, one over the warp
+// (whole-number keys in the floats' order) and one of the index.  Bound by these instructions, about a thousand a token
+// (with expert e in lane e % 32 and the groups one after another they were four thousand: 43 us for 8192 tokens of 256
+// experts in 8 groups).
 //
 // The choice is that of binary64.  Without a bias the scores' order is the logits' and keys are the logits themselves
 // (but where groups count by two keys).  Otherwise keys carry rounding errors, bounded below; where two keys that decide
-// anything lie closer than both their errors, the warp computes the token's keys again in binary64 and chooses from those
-// (a few tokens in ten thousand).
+// anything lie closer than both their errors (a few tokens in ten thousand), the warp orders the candidates by their keys
+// in binary64, or, where the groups are in doubt, chooses again from all of the token's.
 #include <float.h>
 
 #include "experts.h"
@@ -28,7 +30,7 @@ struct Route {
     int32_t* ids;
     float* weights;
     int64_t ld;
-    int T, E, k, groups, each, kept, top;
+    int T, E, k, groups, each, kept, top, lanes;
     int sigmoid, renorm;
     float scale;
 };
@@ -55,137 +57,221 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t v) {
     return (uint64_t)hi << 32 | lo;
 }
 
-// The largest key of the warp (0: none) and its expert, the lowest of equals.
+// Lane and register of the experts.
+struct Place {
+    int L, per_group;  // lanes of a group; experts of a group
+    int base, lane_of;  // this lane's group's first expert (-1: none), its lane in the group
+    int second;         // more than 32 groups: registers from here on are those of the group 32 further on
+    __device__ __forceinline__ int expert(int j) const {
+        const int i = second && j >= second ? 32 * per_group + j - second : lane_of + L * j;
+        return base + i;
+    }
+    __device__ __forceinline__ bool there(int j, int E) const {
+        if (base < 0) return false;
+        if (second) return j < 2 * second && expert(j) < E;
+        return lane_of + L * j < per_group;
+    }
+};
+__device__ __forceinline__ Place place_of(const Route& a, int lane) {
+    if (a.groups > 32) return {1, a.each, lane * a.each, 0, a.each};
+    const int g = lane / a.lanes;
+    return {a.lanes, a.each, g < a.groups ? g * a.each : -1, lane - g * a.lanes, 0};
+}
+
+// Loops over a lane's keys are unrolled but for binary64 ones, which few warps of a launch run if any.
 template <int PER, class Key>
-__device__ __forceinline__ Key best_of(const Key (&key)[PER], int lane, int* expert) {
+constexpr int unrolled() {
+    return sizeof(Key) == 8 ? 1 : PER;
+}
+
+// The largest key of the warp (0: none) and its expert, the lowest of equals; the key is cleared.
+template <int PER, class Key>
+__device__ __forceinline__ Key take_best(Key (&key)[PER], const Place& at, int* expert) {
+    constexpr int U = unrolled<PER, Key>();
     Key b = 0;
-    int i = 0;
-#pragma unroll
-    for (int j = 0; j < PER; j++)
-        if (key[j] > b) b = key[j], i = j;
+#pragma unroll U
+    for (int j = 0; j < PER; j++) b = max(b, key[j]);
     const Key m = warp_max(b);
-    *expert = (int)__reduce_min_sync(0xffffffffu, b == m && m != 0 ? (uint32_t)(lane + 32 * i) : 0xFFFFFFFFu);
+    uint32_t e = 0xFFFFFFFFu;
+    int i = 0;
+    if (b == m && m != 0) {  // the lanes that have it
+#pragma unroll U
+        for (int j = PER - 1; j >= 0; j--)
+            if (key[j] == m) i = j;
+        e = (uint32_t)at.expert(i);
+    }
+    const uint32_t win = __reduce_min_sync(0xffffffffu, e);
+    *expert = (int)win;
+    if (e == win && m != 0) {
+#pragma unroll U
+        for (int j = 0; j < PER; j++)
+            if (j == i) key[j] = 0;
+    }
     return m;
 }
 
-// Chooses from the keys; returns false where two deciding keys lie nearer than near + rel (|a| + |b|) (near < 0: never).
-// Lane j has the j-th expert in *chosen (-1: none).
+// Chooses from the keys.  Two that lie nearer than near + rel (|a| + |b|) are not told apart (near < 0: all are).  Lane j has
+// the expert of the j-th largest key in *chosen (-1: none); the result is how many lanes have one: at most k where the
+// choice is sure; with *doubt more, up to where a key is surely smaller; 0 and *doubt where the groups are not sure, or
+// more than 32 keys.
 template <int PER, class Key, class Value>
-__device__ __forceinline__ bool choose(const Route& a, Key (&key)[PER], int lane, Value near, Value rel, int* chosen) {
-    bool clear = true;
+__device__ __forceinline__ int choose(const Route& a, const Place& at, Key (&key)[PER], int lane, Value near, Value rel, int* chosen, bool* doubt) {
+    constexpr int U = unrolled<PER, Key>();
+    *doubt = false;
     if (a.groups > 1) {
-        // the groups' worth, group g in lane g % 32 of register g / 32
-        Key worth[2] = {0, 0};
-        Value size[2] = {0, 0};  // the magnitudes that went into it: what its error goes by
-        for (int g = 0; g < a.groups; g++) {
-            const int e0 = g * a.each, e1 = e0 + a.each;
-            Key b = 0, second = 0;
-            int at = 0;
+        // the two largest keys of this lane's group (or of each of its two groups), then of the group's lanes
+        Key worth[2];
+        Value size[2];  // the magnitudes that went into the worth: what its error goes by
 #pragma unroll
+        for (int h = 0; h < 2; h++) {
+            Key b = 0, s = 0;
+#pragma unroll U
             for (int j = 0; j < PER; j++) {
-                const int e = lane + 32 * j;
-                if (e >= e0 && e < e1 && key[j] > b) second = b, b = key[j], at = e;
-                else if (e >= e0 && e < e1 && key[j] > second) second = key[j];
+                if (at.second && (j >= at.second) != (h == 1)) continue;
+                const Key v = key[j];
+                s = max(s, min(b, v));
+                b = max(b, v);
             }
-            const Key m = warp_max(b);
-            Key w = m;
-            Value sz = m != 0 ? fabs(unordered(m)) : (Value)0;
-            if (a.top == 2 && m != 0) {
-                const int win = (int)__reduce_min_sync(0xffffffffu, b == m ? (uint32_t)at : 0xFFFFFFFFu);
-                const Key m2 = warp_max(b == m && at == win ? second : b);
-                Value v = unordered(m);
-                if (m2 != 0) v += unordered(m2), sz += fabs(unordered(m2));
-                w = ordered(v);
+            for (int off = 1; off < at.L; off <<= 1) {
+                const Key ob = __shfl_xor_sync(0xffffffffu, b, off), os = __shfl_xor_sync(0xffffffffu, s, off);
+                s = max(min(b, ob), max(s, os));
+                b = max(b, ob);
             }
-            if ((g & 31) == lane) {
-                if (g < 32) worth[0] = w, size[0] = sz;
-                else worth[1] = w, size[1] = sz;
+            worth[h] = b, size[h] = b != 0 ? fabs(unordered(b)) : (Value)0;
+            if (a.top == 2 && b != 0 && s != 0) {
+                worth[h] = ordered(unordered(b) + unordered(s));
+                size[h] += fabs(unordered(s));
             }
+            if (h == 1 && !at.second) worth[h] = 0;
         }
+        if (at.lane_of != 0 || at.base < 0) worth[0] = 0;  // one lane speaks for its group
+        const int g = at.base < 0 ? 64 : at.base / at.per_group;
         uint64_t open = 0;
         Value last = 0, last_size = 0;
         for (int i = 0; i < a.kept + 1; i++) {
-            int g;
-            const Key m = best_of(worth, lane, &g);
+            const Key m = warp_max(max(worth[0], worth[1]));
             if (m == 0) break;
-            const Value v = unordered(m), sz = __shfl_sync(0xffffffffu, g < 32 ? size[0] : size[1], g & 31);
+            const uint32_t mine = worth[0] == m ? (uint32_t)g : worth[1] == m ? (uint32_t)g + 32 : 0xFFFFFFFFu;
+            const uint32_t win = __reduce_min_sync(0xffffffffu, mine);
+            const Value v = unordered(m);
+            const int from = a.groups > 32 ? win & 31 : win * at.L;
+            const Value sz = __shfl_sync(0xffffffffu, win < 32 || a.groups <= 32 ? size[0] : size[1], from);
             // the first that stays closed against the last that is open
-            if (i == a.kept && near >= 0 && !(last - v > 2 * (near + rel * (last_size + sz)))) clear = false;
+            if (i == a.kept && near >= 0 && !(last - v > 2 * near + rel * (last_size + sz))) {
+                *doubt = true;
+                return 0;
+            }
             last = v, last_size = sz;
-            if (i < a.kept) open |= 1ull << g;
-            if ((g & 31) == lane) {
-                if (g < 32) worth[0] = 0;
+            if (i < a.kept) open |= 1ull << win;
+            if (mine == win) {
+                if (win == (uint32_t)g) worth[0] = 0;
                 else worth[1] = 0;
             }
         }
-#pragma unroll
+        const bool open0 = g < 64 && (open >> g) & 1, open1 = g < 32 && (open >> (g + 32)) & 1;
+#pragma unroll U
         for (int j = 0; j < PER; j++)
-            if (!((open >> min((lane + 32 * j) / a.each, 63)) & 1)) key[j] = 0;
+            if (!(at.second && j >= at.second ? open1 : open0)) key[j] = 0;
     }
-    int mine = -1;
+    int mine = -1, count = 0;
     Value last = 0;
-    for (int i = 0; i < a.k + 1; i++) {
-        if (i == a.k && near < 0) break;
+    for (int i = 0; i <= 32; i++) {
+        if (i >= a.k && near < 0) break;
         int e;
-        const Key m = best_of(key, lane, &e);
+        const Key m = take_best(key, at, &e);
         if (m == 0) break;
+        const Value v = unordered(m);
         if (near >= 0 && i > 0) {
-            const Value v = unordered(m);
-            if (!(last - v > near + rel * (fabs(last) + fabs(v)))) clear = false;
+            const bool apart = last - v > near + rel * (fabs(last) + fabs(v));
+            if (i >= a.k && apart) break;
+            if (!apart) *doubt = true;
+            if (i == 32) return 0;
         }
-        last = unordered(m);
-        if (i < a.k && i == lane) mine = e;
-#pragma unroll
-        for (int j = 0; j < PER; j++)
-            if (lane + 32 * j == e) key[j] = 0;
+        last = v;
+        if (i == lane) mine = e;
+        count = i + 1;
     }
     *chosen = mine;
-    return clear;
+    return count;
 }
 
-// The token's keys in binary64, and the choice from them.
+// The sum of the exponentials in binary64.
 template <int PER>
-__device__ __noinline__ int choose_exactly(const Route& a, const float* l, int lane, float top) {
-    uint64_t key[PER];
+__device__ __forceinline__ double exact_total(const Route& a, const Place& at, const float* l, float top) {
     double total = 0.0;
-    if (!a.sigmoid) {
-        for (int j = 0; j < PER; j++) {
-            const int e = lane + 32 * j;
-            if (e < a.E && l[e] > -INFINITY) total += exp((double)fminf(l[e], FLT_MAX) - (double)top);
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
-    }
 #pragma unroll
     for (int j = 0; j < PER; j++) {
-        const int e = lane + 32 * j;
+        const int e = at.expert(j);
+        if (at.there(j, a.E) && l[e] > -INFINITY) total += exp((double)fminf(l[e], FLT_MAX) - (double)top);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+    return total;
+}
+__device__ __forceinline__ double exact_key(const Route& a, const float* l, int e, float top, double total) {
+    const double v = fminf(l[e], FLT_MAX);
+    const double c = a.sigmoid ? 1.0 / (1.0 + exp(-v)) : exp(v - (double)top) / total;
+    return a.bias ? c + (double)a.bias[e] : c;
+}
+
+// The order of `count` candidates, one in a lane, by their keys in binary64 (one each, where all of a token's took 20 us).
+template <int PER>
+__device__ __noinline__ int order_exactly(const Route& a, const float* l, int lane, float top, int candidate, int count) {
+    const double total = a.sigmoid ? 1.0 : exact_total<PER>(a, place_of(a, lane), l, top);
+    const double mine = lane < count ? exact_key(a, l, candidate, top, total) : 0.0;
+    int rank = 0;
+    for (int t = 0; t < count; t++) {
+        const double other = __shfl_sync(0xffffffffu, mine, t);
+        const int e = __shfl_sync(0xffffffffu, candidate, t);
+        if (other > mine || (other == mine && e < candidate)) rank++;
+    }
+    int chosen = -1;
+    for (int j = 0; j < min(a.k, count); j++) {
+        const int from = __ffs(__ballot_sync(0xffffffffu, lane < count && rank == j)) - 1;
+        const int e = __shfl_sync(0xffffffffu, candidate, from);
+        if (lane == j) chosen = e;
+    }
+    return chosen;
+}
+
+// The choice from all of the token's keys in binary64: where the groups were in doubt.
+template <int PER>
+__device__ __noinline__ int choose_exactly(const Route& a, const float* l, int lane, float top) {
+    const Place at = place_of(a, lane);
+    uint64_t key[PER];
+    const double total = a.sigmoid ? 1.0 : exact_total<PER>(a, at, l, top);
+#pragma unroll
+    for (int j = 0; j < PER; j++) {
+        const int e = at.expert(j);
         key[j] = 0;
-        if (e < a.E && l[e] > -INFINITY) {
-            const double v = fminf(l[e], FLT_MAX);
-            double c = a.sigmoid ? 1.0 / (1.0 + exp(-v)) : exp(v - (double)top) / total;
-            if (a.bias) c += (double)a.bias[e];
+        if (at.there(j, a.E) && l[e] > -INFINITY) {
+            const double c = exact_key(a, l, e, top, total);
             if (c > -INFINITY) key[j] = ordered(c);
         }
     }
     int mine;
-    choose<PER, uint64_t, double>(a, key, lane, -1.0, 0.0, &mine);
+    bool doubt;
+    choose<PER, uint64_t, double>(a, at, key, lane, -1.0, 0.0, &mine, &doubt);
     return mine;
 }
 
+constexpr int kRouteThreads = 128;
+
 template <int PER>
-__global__ void __launch_bounds__(256) route_kernel(const __grid_constant__ Route a) {
+__global__ void __launch_bounds__(kRouteThreads) route_kernel(const __grid_constant__ Route a) {
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31;
     const int64_t t = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
     if (t >= a.T) return;  // whole warps leave together
     const float* l = a.logits + t * a.ld;
+    const Place at = place_of(a, lane);
     float v[PER];
     float top = -INFINITY;
 #pragma unroll
     for (int j = 0; j < PER; j++) {
-        const int e = lane + 32 * j;
-        float x = e < a.E && QMM_IN_BOUNDS(g_route_error, e, a.ld) ? l[e] : -INFINITY;
+        const int e = at.expert(j);
+        float x = at.there(j, a.E) && QMM_IN_BOUNDS(g_route_error, e, a.ld) ? l[e] : -INFINITY;
         x = x > -INFINITY ? fminf(x, FLT_MAX) : -INFINITY;  // NaN: closed
         v[j] = x;
         top = fmaxf(top, x);
@@ -207,17 +293,20 @@ __global__ void __launch_bounds__(256) route_kernel(const __grid_constant__ Rout
         float c = v[j];
         if (scored && c > -INFINITY) {
             c = score(c);
-            if (a.bias) c += a.bias[lane + 32 * j];
+            if (a.bias) c += a.bias[at.expert(j)];
         }
         key[j] = c > -INFINITY ? ordered(c) : 0u;
     }
     int e;
-    // Errors of two keys together (expf is within 2 units of 2^-23 relative): sigmoid, 2 (2^-22 s (1 - s) + 2^-23 s) and
-    // the bias's addition 2^-24 |key| each; softmax, scores up to the largest, 1 / total: the exponent's rounding (its
-    // size times the score at most 0.37 of the largest), the sum's 36 roundings, the quotient's.
-    const float near = !scored ? -1.0f : a.sigmoid ? 6e-7f : 8e-6f / total;
-    const bool sure = choose<PER, uint32_t, float>(a, key, lane, near, 1.2e-7f, &e);
-    if (!sure) e = choose_exactly<PER>(a, l, lane, top);
+    // Errors of two keys together (expf is within 2 units of 2^-23 relative): sigmoid, 2 (2^-22 s (1 - s) + 2^-23 s), at
+    // most 6 units of 2^-24, and the bias's addition 2^-24 |key| each (half of 1.2e-7; sums of two keys, as much again);
+    // softmax, scores up to the largest, 1 / total: the exponent's rounding (its size times the score at most 0.37 of the
+    // largest), the sum's 36 roundings, the quotient's.
+    const float near = !scored ? -1.0f : a.sigmoid ? 3.6e-7f : 8e-6f / total;
+    bool doubt;
+    const int count = choose<PER, uint32_t, float>(a, at, key, lane, near, 1.2e-7f, &e, &doubt);
+    if (doubt) e = count > 0 ? order_exactly<PER>(a, l, lane, top, e, count) : choose_exactly<PER>(a, l, lane, top);
+    else if (lane >= a.k) e = -1;
     float w = 0.0f;
     if (e >= 0) w = score(fminf(l[e], FLT_MAX));
     if (a.renorm) {
@@ -235,7 +324,7 @@ __global__ void __launch_bounds__(256) route_kernel(const __grid_constant__ Rout
 template <int PER>
 static qmm_status launch_route(const Route& a, cudaStream_t stream) {
     // few tokens: a warp per CTA, so that they spread over the SMs
-    const int warps = a.T <= 1024 ? 1 : 8;
+    const int warps = a.T <= 1024 ? 1 : kRouteThreads / 32;
     return launch_pdl(route_kernel<PER>, dim3((unsigned)((a.T + (int64_t)warps - 1) / warps)), warps * 32, 0, stream, a);
 }
 
@@ -261,12 +350,17 @@ qmm_status qmm_route(const qmm_route_spec* spec, const float* logits, int64_t ld
     a.T = (int)T, a.E = (int)E, a.k = s.k, a.groups = s.groups, a.each = (int)(E / s.groups), a.kept = s.groups_kept;
     a.top = s.group_top, a.sigmoid = s.score == QMM_ROUTE_SIGMOID, a.renorm = s.renorm != 0, a.scale = s.scale;
     cudaStream_t cs = (cudaStream_t)stream;
-    if (E <= 32) return launch_route<1>(a, cs);
-    if (E <= 64) return launch_route<2>(a, cs);
-    if (E <= 128) return launch_route<4>(a, cs);
-    if (E <= 256) return launch_route<8>(a, cs);
-    if (E <= 512) return launch_route<16>(a, cs);
-    return launch_route<32>(a, cs);
+    // lanes of a group, and the experts of a lane
+    a.lanes = 32;
+    while (a.lanes > 1 && a.lanes * a.groups > 32) a.lanes >>= 1;
+    const int per = s.groups > 32 ? 2 * a.each : (a.each + a.lanes - 1) / a.lanes;
+    if (per <= 1) return launch_route<1>(a, cs);
+    if (per <= 2) return launch_route<2>(a, cs);
+    if (per <= 4) return launch_route<4>(a, cs);
+    if (per <= 8) return launch_route<8>(a, cs);
+    if (per <= 16) return launch_route<16>(a, cs);
+    if (per <= 32) return launch_route<32>(a, cs);
+    return launch_route<64>(a, cs);
 }
 
 unsigned qmm_internal_route_error(int clear) {
