@@ -461,9 +461,9 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
                         const uint4 s = s4[2 * q + h];
-                        const uint64_t p0 = f2_mul(s2, f2_pack(s.x, s.y)), p1 = f2_mul(s2, f2_pack(s.z, s.w));
                         const uint32_t* u = v[q & 1] + 4 * h;
                         float* o = acc + 8 * q + 4 * h;
+                        const uint64_t p0 = f2_mul(s2, f2_pack(s.x, s.y)), p1 = f2_mul(s2, f2_pack(s.z, s.w));
                         o[0] = fmaf(__uint_as_float(u[0]), __uint_as_float((uint32_t)p0), o[0]);
                         o[1] = fmaf(__uint_as_float(u[1]), __uint_as_float((uint32_t)(p0 >> 32)), o[1]);
                         o[2] = fmaf(__uint_as_float(u[2]), __uint_as_float((uint32_t)p1), o[2]);
@@ -650,27 +650,45 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
                         const uint32_t ah = tmem + (uint32_t)A_COL0 + (m & 1) * 128;
                         const uint32_t op = sbase + L::OFF_OP + m % L::X_SLOTS * L::XSLOT;
                         if (leader) {
+                            // the accumulation's first MMA starts its sums
+                            bool add = L::KQ && h > 0;
+                            // the products with a lo come first: small sums lose less to truncation (half the error of
+                            // hi and lo in turn, at the same speed)
+                            if constexpr (L::WTERMS == 2) {
+                                uint32_t x = op >> 4;
+#pragma unroll
+                                for (int b = 0; b < L::BLOCKS; b++) {
+                                    if (!L::KQ && b >= mine) break;
+#pragma unroll
+                                    for (int k = 0; k < 2; k++) {
+                                        const uint32_t al = ah + L::BLOCK_COLS * b + 8 * k, xh = x + 16 * k;
+                                        mma_ts(d, al + 16, xh, 512, idesc, add);
+                                        add = true;
+                                        if constexpr (L::XTERMS == 2) mma_ts(d, al, xh + term, 512, idesc, true);
+                                    }
+                                    x += L::XTERMS * term;
+                                }
+                            }
+                            const uint64_t min = smem_desc(sbase + L::OFF_AMIN + ((c0 + c) & 1) * L::AMIN, 128, 256);
+                            const uint64_t sums = smem_desc(op + L::XSUMS, 128, 256);
+                            if (L::MIN && L::WTERMS == 2 && last) {
+                                mma_f16(d, min + (BM * 32 >> 4), sums, idesc, 1);
+                                mma_f16(d, min, sums + (rows * 32 >> 4), idesc, 1);
+                            }
                             uint32_t x = op >> 4;
 #pragma unroll
                             for (int b = 0; b < L::BLOCKS; b++) {
                                 if (!L::KQ && b >= mine) break;
 #pragma unroll
                                 for (int k = 0; k < 2; k++) {
-                                    const uint32_t al = ah + L::BLOCK_COLS * b + 8 * k, xh = x + 16 * k;
-                                    // the accumulation's first MMA starts its sums
-                                    const bool first = b == 0 && k == 0 && (!L::KQ || h == 0);
-                                    if constexpr (L::WTERMS == 2) mma_ts(d, al + 16, xh, 512, idesc, !first);
-                                    if constexpr (L::XTERMS == 2) mma_ts(d, al, xh + term, 512, idesc, true);
-                                    mma_ts(d, al, xh, 512, idesc, L::WTERMS == 2 || !first);
+                                    mma_ts(d, ah + L::BLOCK_COLS * b + 8 * k, x + 16 * k, 512, idesc, add);
+                                    add = true;
                                 }
                                 x += L::XTERMS * term;
                             }
                             if (L::MIN && last) {  // hi and lo of the minimums, 16 sums a row
-                                const uint64_t al = smem_desc(sbase + L::OFF_AMIN + ((c0 + c) & 1) * L::AMIN, 128, 256);
-                                const uint64_t xh = smem_desc(op + L::XSUMS, 128, 256);
-                                mma_f16(d, al + (BM * 32 >> 4), xh, idesc, 1);
-                                if constexpr (L::XTERMS == 2) mma_f16(d, al, xh + (rows * 32 >> 4), idesc, 1);
-                                mma_f16(d, al, xh, idesc, 1);
+                                if constexpr (L::WTERMS == 1) mma_f16(d, min + (BM * 32 >> 4), sums, idesc, 1);
+                                mma_f16(d, min, sums, idesc, 1);
                             }
                             mma_commit(bars.done(m));
                             if (L::KQ ? last : mine > 0) mma_commit(bars.acc_full(acc & 1));
