@@ -535,7 +535,7 @@ def _whole(name, t, dev, dtype, shape):
     """The address of a contiguous tensor of this type and shape (None for None)."""
     if t is None:
         return None
-    if t.dtype is not getattr(_torch, dtype) or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
         _refuse(name, t, dtype, shape, dev)
     return t.data_ptr()
 
@@ -553,9 +553,9 @@ def qmm_add_rmsnorm_quantize(act, x, r, w, eps, xq=None, sum=None, h=None, strea
     if x.dim() != 2:
         _refuse("x", x, "float32", ("M", "K"), dev)
     rows = M, K = x.shape
-    _call("qmm_add_rmsnorm_quantize", _type(act), _whole("x", x, dev, "float32", rows), _whole("r", r, dev, "float32", rows),
-          _whole("sum", sum, dev, "float32", rows), _whole("w", w, dev, "float32", (K,)), eps,
-          _whole("h", h, dev, "float32", rows), _whole("xq", xq, dev, "uint8", (M, qmm_row_bytes(act, K))), M, K,
+    _call("qmm_add_rmsnorm_quantize", _type(act), _whole("x", x, dev, _torch.float32, rows), _whole("r", r, dev, _torch.float32, rows),
+          _whole("sum", sum, dev, _torch.float32, rows), _whole("w", w, dev, _torch.float32, (K,)), eps,
+          _whole("h", h, dev, _torch.float32, rows), _whole("xq", xq, dev, _torch.uint8, (M, qmm_row_bytes(act, K))), M, K,
           _raw_stream(dev) if stream is None else stream_handle(stream))
 
 
@@ -573,8 +573,8 @@ def qmm_route(logits, ids, weights, score="softmax", bias=None, groups=1, groups
     k = ids.shape[1]
     spec = RouteSpec(ROUTE_SCORES[score], k, groups, groups_kept, group_top, 1 if renorm else 0, scale)
     _call("qmm_route", ctypes.addressof(spec), logits.data_ptr(), logits.stride(0) if T > 1 else E,
-          _whole("bias", bias, dev, "float32", (E,)), _whole("ids", ids, dev, "int32", (T, k)),
-          _whole("weights", weights, dev, "float32", (T, k)), T, E,
+          _whole("bias", bias, dev, _torch.float32, (E,)), _whole("ids", ids, dev, _torch.int32, (T, k)),
+          _whole("weights", weights, dev, _torch.float32, (T, k)), T, E,
           _raw_stream(dev) if stream is None else stream_handle(stream))
 
 
@@ -594,9 +594,9 @@ def qmm_experts_glu(wtype, Wg, Wu, xq, ids, h, scratch, scratch_bytes, gate="sil
     if size == 0 or row == 0 or row % size:
         raise ValueError("Wg: rows of %d bytes are no whole blocks of type %r" % (row, wtype))
     K = row // size * qmm_block_values(wt)
-    _call("qmm_experts_glu", wt, GLU_KINDS[gate], _whole("Wg", Wg, dev, "uint8", (E, N, row)),
-          _whole("Wu", Wu, dev, "uint8", matrix), _whole("xq", xq, dev, "uint8", (T, qmm_row_bytes(qmm_act_type(wt), K))),
-          _whole("ids", ids, dev, "int32", (T, k)), _whole("h", h, dev, "float32", (T, k, N)),
+    _call("qmm_experts_glu", wt, GLU_KINDS[gate], _whole("Wg", Wg, dev, _torch.uint8, (E, N, row)),
+          _whole("Wu", Wu, dev, _torch.uint8, matrix), _whole("xq", xq, dev, _torch.uint8, (T, qmm_row_bytes(qmm_act_type(wt), K))),
+          _whole("ids", ids, dev, _torch.int32, (T, k)), _whole("h", h, dev, _torch.float32, (T, k, N)),
           _workspace(scratch, scratch_bytes, dev), scratch_bytes, T, k, E, N, K,
           _raw_stream(dev) if stream is None else stream_handle(stream))
 
@@ -609,10 +609,10 @@ def qmm_experts_sum(wtype, W, h, ids, weights, y, scratch, scratch_bytes, residu
         _refuse("h, W", h if h.dim() != 3 else W, "float32, uint8", "of 3 dimensions", dev)
     T, k, K = h.shape
     E, N = W.shape[:2]
-    _call("qmm_experts_sum", wt, _whole("W", W, dev, "uint8", (E, N, qmm_row_bytes(wt, K))),
-          _whole("h", h, dev, "float32", (T, k, K)), _whole("ids", ids, dev, "int32", (T, k)),
-          _whole("weights", weights, dev, "float32", (T, k)), _whole("residual", residual, dev, "float32", (T, N)),
-          _whole("y", y, dev, "float32", (T, N)), _workspace(scratch, scratch_bytes, dev), scratch_bytes, T, k, E, N, K,
+    _call("qmm_experts_sum", wt, _whole("W", W, dev, _torch.uint8, (E, N, qmm_row_bytes(wt, K))),
+          _whole("h", h, dev, _torch.float32, (T, k, K)), _whole("ids", ids, dev, _torch.int32, (T, k)),
+          _whole("weights", weights, dev, _torch.float32, (T, k)), _whole("residual", residual, dev, _torch.float32, (T, N)),
+          _whole("y", y, dev, _torch.float32, (T, N)), _workspace(scratch, scratch_bytes, dev), scratch_bytes, T, k, E, N, K,
           _raw_stream(dev) if stream is None else stream_handle(stream))
 
 

@@ -1,4 +1,6 @@
 // experts.cu -- the entry points of the experts' products: checks, workspaces and the choice of the path.
+#include <math.h>
+
 #include "experts.h"
 #include "experts_mma.h"
 #include "tc_device.cuh"
@@ -297,9 +299,25 @@ static qmm_status on_tensor_cores(int wt, int kind, const ExpertShape& s, const 
     return expert_mma(wt, a, gate, l.tiles_most, stream);
 }
 
-// Which calls take the tensor cores.
-static bool many_rows(int wt, const ExpertShape& s) {
-    return s.T * s.k >= 32 && scratch_of(wt, s).tiles_most * ((s.N + 63) / 64) <= kMaxDim;
+// Which calls take the tensor cores: those for which they take less time, by what both paths were measured to cost (us).
+// The other path reads each choice's weights, 5.5 MB a us (half of what it reads several times comes from the L2), or
+// decodes them block by block where 32-value rows are not of 256s, 1.5; the tensor cores go over the tiles in waves of one
+// an SM, a chunk of 256 values in 1.6 (one-term weights) or 2.3.  Measured, other path / tensor cores: Q4_K, 64 experts of
+// 2048 -> 1024 twice, 128 choices 60 / 70, 256 101 / 84; Q8_0, 8 experts of 4096 -> 4096 twice, 16 choices 61 / 127, 32
+// 180 / 152; Q6_K, 64 experts of 1024 -> 2048, 128 choices 41 / 61, 256 111 / 73; Q5_1, 32 experts of 1408 -> 2048, 32
+// choices 41 / 50, 64 74 / 61.
+static bool many_rows(int wt, const ExpertShape& s, bool gate) {
+    DeviceInfo dev;
+    if (current_device(&dev) != QMM_OK) return false;
+    const double S = (double)(s.T * s.k), blocks = gate ? 64.0 : 128.0;
+    const int64_t most = scratch_of(wt, s).tiles_most * ((s.N + 63) / 64);
+    if (most > kMaxDim) return false;
+    const double bytes = S * (gate ? 2.0 : 1.0) * (double)s.N * (double)row_bytes_of(wt, s.K);
+    const double other = 6.0 + bytes / (act_type_of(wt) == QMM_Q8_0 && s.K % 256 ? 1.5e6 : 5.5e6);
+    const double tiles = (S / kTileRows + (S < (double)s.E ? S : (double)s.E)) * ceil((double)s.N / blocks);
+    const bool one_term = wt == QMM_Q4_K || wt == QMM_Q5_K || wt == QMM_Q2_K;
+    const double tensor = 12.0 + ceil(tiles / dev.sms) * ceil((double)s.K / 256.0) * (one_term ? 1.6 : 2.3);
+    return tensor < other;
 }
 
 // y[t][n] = residual[t][n] + sum_j weights[t][j] p[t][j][n] over the choices that are there, in their order.  Bound by
@@ -377,7 +395,7 @@ qmm_status qmm_experts_glu(int wtype, int kind, const void* Wg, const void* Wu, 
     if (!aligned16(Wg) || !aligned16(Wu) || !aligned16(xq) || !aligned4(ids) || !aligned16(h) || !aligned16(scratch))
         return QMM_E_ALIGN;
     if (scratch_bytes < scratch_of(wtype, s).bytes) return QMM_E_SCRATCH;
-    if (many_rows(wtype, s))
+    if (many_rows(wtype, s, true))
         return on_tensor_cores(wtype, kind, s, Wg, Wu, xq, nullptr, ids, h, (uint8_t*)scratch, (cudaStream_t)stream);
     return expert_vec_glu(wtype, kind, s, Wg, Wu, xq, ids, h, (cudaStream_t)stream);
 }
@@ -395,7 +413,7 @@ qmm_status qmm_experts_sum(int wtype, const void* W, const float* h, const int32
     if (scratch_bytes < scratch_of(wtype, s).bytes) return QMM_E_SCRATCH;
     cudaStream_t cs = (cudaStream_t)stream;
     float* p = reinterpret_cast<float*>((uint8_t*)scratch + scratch_of(wtype, s).products);
-    if (many_rows(wtype, s)) {
+    if (many_rows(wtype, s, false)) {
         const qmm_status all = on_tensor_cores(wtype, 0, s, W, nullptr, nullptr, h, ids, p, (uint8_t*)scratch, cs);
         return all != QMM_OK ? all : combine(s, p, ids, weights, residual, y, cs);
     }
