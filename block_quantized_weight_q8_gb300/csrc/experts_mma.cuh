@@ -515,8 +515,6 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
             for (int c = 0; c < nchunks; c++, gc++) {
                 const uint32_t s = gc % L::WST;
                 const int blocks = blocks_of(c);
-                // the first half of the chunk before, for which the MMAs of this one wait
-                if (pending && pending_halves == 2 && !(ok = fold(0))) break;
                 if (!(ok = warp_wait(bars.w_full(s), (gc / L::WST) & 1u, abort_flag))) break;
                 const SmemBytes w{smem + L::OFF_W + (s * BM + r) * L::PITCH};
                 const uint32_t o = (row + (uint32_t)(c * L::CHUNK)) & 15u;
@@ -529,12 +527,16 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
                 const uint32_t slot = lanes + (uint32_t)A_COL0 + (m & 1) * 128 + (2 * grp % L::BLOCKS) * L::BLOCK_COLS;
 #pragma unroll
                 for (int h = 0; h < 2; h++) {
-                    if (!L::KQ && 2 * grp + h >= blocks) break;
-                    uint32_t hi[16], lo[16];
-                    convert_block<WT>(w, o, 2 * grp + h, ws, hi, lo);
-                    tmem_st16(slot + L::BLOCK_COLS * h, hi);
-                    if constexpr (L::WTERMS == 2) tmem_st16(slot + L::BLOCK_COLS * h + 16, lo);
+                    if (L::KQ || 2 * grp + h < blocks) {
+                        uint32_t hi[16], lo[16];
+                        convert_block<WT>(w, o, 2 * grp + h, ws, hi, lo);
+                        tmem_st16(slot + L::BLOCK_COLS * h, hi);
+                        if constexpr (L::WTERMS == 2) tmem_st16(slot + L::BLOCK_COLS * h + 16, lo);
+                    }
+                    // in between, the first half of the chunk before: the MMAs of this one wait for it
+                    if (!L::KQ && h == 0 && ok && pending && pending_halves == 2) ok = fold(0);
                 }
+                if (!ok) break;
                 if constexpr (L::MIN) {
                     // the minimums go with the chunk's last item, by one of its groups in turn
                     if (grp == (L::ITEMS == 1 ? (int)(gc & 3) : 2 * (blocks > 4) + (int)(gc & 1))) {
