@@ -246,26 +246,39 @@ __device__ __forceinline__ uint32_t codes_of(const SmemBytes& w, uint32_t o, int
     }
 }
 
-// A K-quant block's sums are over its d, unless its minimums' scale is over 1000 times that (no weights have that): then
-// over a 1000th of the latter, so that minimums up to 63 times it stay f16.  The scales' rounding to f16 is then 2^-11 of
-// what is less than 2^-5 of the values.
-__device__ __forceinline__ WRow shared_scale(float d, float m) {
-    const bool usual = fabsf(m) <= 1000.0f * fabsf(d);
-    const float D = usual ? d : m * 1e-3f;
+// A K-quant block's sums are over its d, unless its minimums' scale is over 1000 times that (hardly any weights have that)
+// and not all minimums are zero: then over d times such a power of two that minimums up to 63 times their scale stay f16.
+// Scale times code is still exact where that power is at most 2^20; beyond, one minimum is over 2^20 times any of them.
+template <class None>
+__device__ __forceinline__ WRow shared_scale(float d, float m, None none) {
+    float D = d, value = 1.0f;
+    if (!(fabsf(m) <= 1000.0f * fabsf(d)) && !(isfinite(m) && none())) {
+        if (d == 0.0f) {
+            D = m, value = 0.0f;
+        } else {
+            const int p = ((__float_as_int(m) >> 23) & 255) - ((__float_as_int(d) >> 23) & 255) - 9;
+            const int up = p < 0 ? 0 : p > 60 ? 60 : p;
+            D = d * pow2(up), value = pow2(-up);
+        }
+    }
     const float inv = D != 0.0f ? __fdividef(1.0f, D) : 0.0f;  // 2 units of 2^-23, of what is 2^-22 in two terms
-    return {D, 0, usual ? 1.0f : d * inv, -(m * inv), make_uint4(0u, 0u, 0u, 0u)};
+    return {D, 0, value, -(m * inv), make_uint4(0u, 0u, 0u, 0u)};
 }
 
 template <int WT>
 __device__ __forceinline__ WRow row_scale(const SmemBytes& w, uint32_t o, int half, int blocks) {
     if constexpr (WT == QMM_Q4_K || WT == QMM_Q5_K) {
         const uint4 head = *reinterpret_cast<const uint4*>(w.base + o);
-        WRow r = shared_scale(h2f(head.x), h2f(head.x >> 16));
+        WRow r = shared_scale(h2f(head.x), h2f(head.x >> 16), [&] { return (head.z | (head.w & 0xF0F0F0F0u)) == 0u; });
         r.head = head;
         return r;
     } else if constexpr (WT == QMM_Q2_K) {
         const uint32_t dd = w.w32(o + 80);
-        return shared_scale(h2f(dd), h2f(dd >> 16));
+        return shared_scale(h2f(dd), h2f(dd >> 16), [&] {
+            uint32_t sc[4];
+            w.words_aligned<4>(o, sc);
+            return ((sc[0] | sc[1] | sc[2] | sc[3]) & 0xF0F0F0F0u) == 0u;
+        });
     } else if constexpr (WT == QMM_Q6_K) {
         return {h2f(w.u16(o + 208)), 0, 1.0f, 0.0f, make_uint4(0u, 0u, 0u, 0u)};
     } else {
