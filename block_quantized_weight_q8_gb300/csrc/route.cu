@@ -255,6 +255,15 @@ __device__ __noinline__ int choose_exactly(const Route& a, const float* l, int l
     return mine;
 }
 
+// Scores so small that f32 loses them, over their sum (0 where binary64 loses them too).
+__device__ __noinline__ float small_weight(bool sigmoid, bool real, float v, float top) {
+    const double s = !real ? 0.0 : sigmoid ? 1.0 / (1.0 + exp(-(double)v)) : exp((double)v - (double)top);
+    double sum = s;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    return sum > 0.0 ? (float)(s / sum) : 0.0f;
+}
+
 constexpr int kRouteThreads = 128;
 
 template <int PER>
@@ -313,7 +322,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const __grid_const
         float sum = w;
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        if (sum > 0.0f) w = w / sum;
+        w = sum > 1e-30f ? w / sum : small_weight(a.sigmoid, e >= 0, e >= 0 ? fminf(l[e], FLT_MAX) : 0.0f, top);
     }
     if (lane < a.k && QMM_IN_BOUNDS(g_route_error, t * a.k + lane, (int64_t)a.T * a.k)) {
         a.ids[t * a.k + lane] = e;
