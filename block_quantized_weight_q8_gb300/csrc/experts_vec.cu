@@ -222,8 +222,8 @@ static qmm_status plan_expert_vec(const DeviceInfo& dev, int64_t unit_count, int
     using F = Fmt<WT>;
     MatvecPlan p;
     int ends[kMaxGroup];
-    const int64_t rows_all = (int64_t)a->N * legs;
-    const qmm_status st = plan_matvec<WT>(&rows_all, 1, a->K, dev, false, false, &p, ends);
+    const int64_t one_row = 1;  // how rows are cut goes by the format and K
+    const qmm_status st = plan_matvec<WT>(&one_row, 1, a->K, dev, false, false, &p, ends);
     if (st != QMM_OK) return st;
     *su = p.su;
     a->lpr = p.lpr, a->pieces = p.pieces, a->piece_units = p.piece_units, a->item_segs = p.item_segs;

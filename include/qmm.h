@@ -48,8 +48,9 @@
  *             dependents early (griddepcontrol.launch_dependents); ordinary
  *             kernels, and this library's weight and activation quantizers,
  *             never release early, so a multiply right after them sees all of
- *             W.  The rotary and paged-cache kernels release early too, after
- *             their own wait; none of them writes weights.
+ *             W.  The rotary, paged-cache and mixture-of-experts kernels
+ *             release early too, and end after their own wait; none of them
+ *             writes weights.
  *   Errors.   Every call returns a qmm_status.  Arguments are checked on the
  *             host before anything is launched; a failed check launches
  *             nothing.  A launch failure returns QMM_E_CUDA.  No call aborts,
@@ -621,7 +622,10 @@ QMM_API qmm_status qmm_route(const qmm_route_spec* spec, const float* logits, in
  *        qmm_quantize_q8_0 / q8_K; h f32 [T][k][K] (without effect for a choice that is
  *        not there); weights f32 [T][k], NULL: 1; residual f32 [T][N], NULL: 0, may be y
  * Products agree with the block-wise definition (qmm_matvec) within 1e-5 of their row's
- * L2 norm, and are the same on every run.  k 1..64, E 1..1024, T * k <= 2^24, E * N <=
+ * L2 norm, and are the same on every run.  With many choices, values of 32-value formats
+ * and of Q8_0 rows are held to 2^-22 of the largest in their run of 256 (by eight scales),
+ * so that a choice's products may differ in their last bits between calls of few and of
+ * many choices.  k 1..64, E 1..1024, T * k <= 2^24, E * N <=
  * 2^31 - 1; N, K and the alignment (ids and weights: 4 bytes) as for qmm_matvec.
  * scratch: at least qmm_experts_scratch_bytes(wtype, T, k, E, N, K) bytes (0: a bad
  * argument), enough for either call of this shape, written before it is read; calls that

@@ -218,6 +218,39 @@ def test_rows_and_bytes_around_stay_as_they_are():
     assert (y[T:] == 7.0).all() and (scratch[n:] == 0xA5).all() and not (y[:T] == 7.0).all()
 
 
+@pytest.mark.parametrize("T", [2, 6000])
+def test_weights_beyond_32_bits_of_bytes(T):
+    """1024 experts of 4096 x 1024 Q8_0, 4.6 GB: the last expert's rows, by few and by many choices."""
+    E, N, K = 1024, 4096, 1024
+    W = torch.zeros(E, N, qmm.qmm_row_bytes("q8_0", K), dtype=torch.uint8, device="cuda")
+    last = weights_of("q8_0", 1, N, K, 3)
+    W[-1].copy_(dev(last[0]))
+    h = workloads.activations_f32(T, K, seed=4).reshape(T, 1, K)
+    ids = np.zeros((T, 1), np.int32)
+    ids[::2] = E - 1
+    y = torch.full((T, N), float("nan"), device="cuda")
+    scratch, n = scratch_of("q8_0", T, 1, E, N, K)
+    qmm.qmm_experts_sum("q8_0", W, dev(h), dev(ids), None, y, scratch, n)
+    got = host(y).astype(np.float64)
+    want, off = plain.summed("q8_0", last, h[:40:2], np.zeros((len(h[:40:2]), 1), np.int32), None, None, K)
+    assert (np.abs(got[:40:2] - want) <= off).all() and (got[1::2] == 0).all()
+
+
+def test_outputs_beyond_32_bits_of_bytes():
+    """300000 choices of 4096 outputs, 4.9 GB; the last tokens' are looked at."""
+    T, k, E, N, K = 150000, 2, 2, 4096, 256
+    Wg, Wu = weights_of("q4_K", E, N, K, 1), weights_of("q4_K", E, N, K, 2)
+    x = workloads.activations_f32(1000, K, seed=3)
+    xq = oracle.quantize("q8_K", x)
+    ids = picks(T, k, E, 4)
+    h = torch.empty(T, k, N, device="cuda")
+    scratch, n = scratch_of("q4_K", T, k, E, N, K)
+    qmm.qmm_experts_glu("q4_K", dev(Wg), dev(Wu), dev(np.tile(xq, (T // 1000, 1))), dev(ids), h, scratch, n)
+    for t in (0, T - 30):
+        want, off = plain.glu("q4_K", Wg, Wu, xq[t % 1000:t % 1000 + 30], ids[t:t + 30], "silu", K)
+        assert (np.abs(host(h[t:t + 30]) - want) <= off).all()
+
+
 @pytest.mark.parametrize("wtype,T", [("q4_K", 1), ("q4_K", 900), ("q8_0", 3), ("q5_1", 700)])
 def test_a_layer(wtype, T):
     """The added norm, a router's product, the choice, the gated and the summed products in a row on one stream, captured;
