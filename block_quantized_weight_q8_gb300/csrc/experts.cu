@@ -57,7 +57,7 @@ constexpr int kPlanThreads = 1024, kOperandThreads = 256;
 // Sorts the choices by their expert and cuts each expert's into tiles.  Counting and placing use shared-memory counters,
 // where there are few experts one addition for a warp's choices of one; the order within an expert varies from run to run,
 // and no result depends on it (a row's sums do not meet another row's).  One CTA; its loads are issued eight at a time
-// (one by one, each waiting for the counter of the one before, 16384 choices took 34 us).
+// (one by one, each waiting for the counter of the one before, 16384 choices took 34 us; so 13.5, 256 choices 4).
 constexpr int kFewExperts = 3;
 __device__ __forceinline__ int next_place(int* counter, int e, int lane, int E) {
     if (E > kFewExperts) return e >= 0 ? atomicAdd(&counter[e], 1) : 0;
@@ -133,7 +133,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
 // The tiles' activation operands, from 8-bit rows or from f32 rows (quantized by the activations' rule on the way), and,
 // for gated products, the zero rows of choices that are not there.  A warp makes a chunk of 8 rows at a time, lane 4 r + q
 // the values 8 q .. 8 q + 7 of each block of row r: its 16-byte stores lie side by side.  Bound by what it writes, 2 (Q8_K)
-// or 4 bytes a value.
+// or 4 bytes a value, which stays in the L2 (16384 rows of 2048 from 8-bit rows: 67 MB in 24 us), and for few rows by its
+// launch (256 rows of 2048: 11 us).
 template <int ACT, bool FROM_F32>
 __global__ void __launch_bounds__(kOperandThreads) operand_kernel(const __grid_constant__ Prepare a) {
     constexpr int TERMS = operand_terms(ACT);
@@ -322,7 +323,7 @@ static bool many_rows(int wt, const ExpertShape& s, bool gate) {
 }
 
 // y[t][n] = residual[t][n] + sum_j weights[t][j] p[t][j][n] over the choices that are there, in their order.  Bound by
-// memory: 4 (k + 2) bytes a value.  V values a thread: 4 where N is a multiple of it.
+// memory: 4 (k + 2) bytes a value (2048 tokens of 8 choices of 2048: 168 MB in 30 us, 5.5 TB/s).  V values a thread: 4 where N is a multiple of it.
 template <int V>
 __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ p, const int32_t* __restrict__ ids,
                                                       const float* __restrict__ weights, const float* residual, float* y,
