@@ -531,6 +531,24 @@ class RouteSpec(ctypes.Structure):
                 ("group_top", ctypes.c_int32), ("renorm", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
+_formats = {}
+
+
+def _format(t):
+    """(code, bytes of a block, its values, activation type's code) of a type."""
+    f = _formats.get(t)
+    if f is None:
+        c = _type(t)
+        f = _formats[t] = (c, qmm_block_bytes(c), qmm_block_values(c), qmm_act_type(c))
+    return f
+
+
+def _row(t, K):
+    """qmm_row_bytes without the call; 0 where K is no whole number of blocks."""
+    _, size, values, _ = _format(t)
+    return K // values * size if values and K % values == 0 else 0
+
+
 def _whole(name, t, dev, dtype, shape):
     """The address of a contiguous tensor of this type and shape (None for None)."""
     if t is None:
@@ -555,7 +573,7 @@ def qmm_add_rmsnorm_quantize(act, x, r, w, eps, xq=None, sum=None, h=None, strea
     rows = M, K = x.shape
     _call("qmm_add_rmsnorm_quantize", _type(act), _whole("x", x, dev, _torch.float32, rows), _whole("r", r, dev, _torch.float32, rows),
           _whole("sum", sum, dev, _torch.float32, rows), _whole("w", w, dev, _torch.float32, (K,)), eps,
-          _whole("h", h, dev, _torch.float32, rows), _whole("xq", xq, dev, _torch.uint8, (M, qmm_row_bytes(act, K))), M, K,
+          _whole("h", h, dev, _torch.float32, rows), _whole("xq", xq, dev, _torch.uint8, (M, _row(act, K))), M, K,
           _raw_stream(dev) if stream is None else stream_handle(stream))
 
 
@@ -585,17 +603,17 @@ def qmm_experts_scratch_bytes(wtype, T, k, E, N, K):
 def qmm_experts_glu(wtype, Wg, Wu, xq, ids, h, scratch, scratch_bytes, gate="silu", stream=None):
     """h[t][j] = gate(Wg[e] x_t) * (Wu[e] x_t), e = ids[t][j]: h f32 [T][k][N], Wg and Wu uint8 [E][N][row bytes], xq uint8
     [T][qmm_row_bytes(qmm_act_type(wtype), K)], ids int32 [T][k] (negative: no expert, zeros)."""
-    dev, wt = _device(), _type(wtype)
+    dev = _device()
+    wt, size, values, act = _format(wtype)
     if h.dim() != 3 or Wg.dim() != 3:
         _refuse("h, Wg", h if h.dim() != 3 else Wg, "float32, uint8", "of 3 dimensions", dev)
     T, k, N = h.shape
     matrix = E, _, row = Wg.shape
-    size = qmm_block_bytes(wt)
     if size == 0 or row == 0 or row % size:
         raise ValueError("Wg: rows of %d bytes are no whole blocks of type %r" % (row, wtype))
-    K = row // size * qmm_block_values(wt)
+    K = row // size * values
     _call("qmm_experts_glu", wt, GLU_KINDS[gate], _whole("Wg", Wg, dev, _torch.uint8, (E, N, row)),
-          _whole("Wu", Wu, dev, _torch.uint8, matrix), _whole("xq", xq, dev, _torch.uint8, (T, qmm_row_bytes(qmm_act_type(wt), K))),
+          _whole("Wu", Wu, dev, _torch.uint8, matrix), _whole("xq", xq, dev, _torch.uint8, (T, _row(act, K))),
           _whole("ids", ids, dev, _torch.int32, (T, k)), _whole("h", h, dev, _torch.float32, (T, k, N)),
           _workspace(scratch, scratch_bytes, dev), scratch_bytes, T, k, E, N, K,
           _raw_stream(dev) if stream is None else stream_handle(stream))
@@ -609,7 +627,7 @@ def qmm_experts_sum(wtype, W, h, ids, weights, y, scratch, scratch_bytes, residu
         _refuse("h, W", h if h.dim() != 3 else W, "float32, uint8", "of 3 dimensions", dev)
     T, k, K = h.shape
     E, N = W.shape[:2]
-    _call("qmm_experts_sum", wt, _whole("W", W, dev, _torch.uint8, (E, N, qmm_row_bytes(wt, K))),
+    _call("qmm_experts_sum", wt, _whole("W", W, dev, _torch.uint8, (E, N, _row(wt, K))),
           _whole("h", h, dev, _torch.float32, (T, k, K)), _whole("ids", ids, dev, _torch.int32, (T, k)),
           _whole("weights", weights, dev, _torch.float32, (T, k)), _whole("residual", residual, dev, _torch.float32, (T, N)),
           _whole("y", y, dev, _torch.float32, (T, N)), _workspace(scratch, scratch_bytes, dev), scratch_bytes, T, k, E, N, K,

@@ -98,13 +98,18 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) expert_vec_kernel(const __g
 
     // the activation rows, in the layout that the decoders read
     const int nthr = blockDim.x;
-    for (int leg = 0; leg < (GATED ? 1 : legs); leg++) {
-        if (leg_row[leg] < 0) continue;
-        uint8_t* aq = acts + (size_t)leg * a.act_stride;
-        float* ad = reinterpret_cast<float*>(aq + qbytes);
-        int* as = reinterpret_cast<int*>(ad + nd);
-        if constexpr (GATED) {
-            const uint8_t* row = a.xq + (uint64_t)(unit / a.k) * nd * (F::ACT == QMM_Q8_0 ? Q8_0_BB : Q8_K_BB);
+    auto act_of = [&](int leg, uint8_t*& aq, float*& ad, int*& as) {
+        aq = acts + (size_t)leg * a.act_stride;
+        ad = reinterpret_cast<float*>(aq + qbytes);
+        as = reinterpret_cast<int*>(ad + nd);
+    };
+    uint8_t* aq;
+    float* ad;
+    int* as;
+    if constexpr (GATED) {
+        const uint8_t* row = a.xq + (uint64_t)(unit / a.k) * nd * (F::ACT == QMM_Q8_0 ? Q8_0_BB : Q8_K_BB);
+        act_of(0, aq, ad, as);
+        if (leg_row[0] >= 0) {
             if constexpr (F::ACT == QMM_Q8_0) {
                 for (int b = tid; b < nd; b += nthr) {
                     const unsigned short* p = reinterpret_cast<const unsigned short*>(row + (size_t)b * 34);
@@ -116,20 +121,38 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) expert_vec_kernel(const __g
             } else {
                 unpack_q8_K_row_by(row, nd, ap, aq, ad, as, tid, nthr);
             }
-        } else {
-            const float4* x4 = reinterpret_cast<const float4*>(a.x + ((int64_t)unit * a.k + leg) * K);
-            if constexpr (F::ACT == QMM_Q8_0) {
-                for (int b = (tid + leg * nd) % nthr; b < nd; b += nthr) {  // the legs' blocks over all threads
-                    float4 v[8];
+        }
+    } else {
+        // the legs' blocks lie side by side over all threads (Q8_0) or warps, which read four before they make the first
+        const float4* x4 = reinterpret_cast<const float4*>(a.x + (int64_t)unit * a.k * K);
+        if constexpr (F::ACT == QMM_Q8_0) {
+            for (int i = tid; i < legs * nd; i += nthr) {
+                const int leg = i / nd, b = i - leg * nd;
+                if (leg_row[leg] < 0) continue;
+                float4 v[8];
 #pragma unroll
-                    for (int i = 0; i < 8; i++) v[i] = x4[(size_t)b * 8 + i];
-                    uint32_t w[8], dbits;
-                    quant_q8_0_block(v, &dbits, w);
-                    put_act_block<WT, SU>(w, dbits, b, nd, nsu, aq, ad, as);
+                for (int j = 0; j < 8; j++) v[j] = x4[(size_t)i * 8 + j];
+                uint32_t w[8], dbits;
+                quant_q8_0_block(v, &dbits, w);
+                act_of(leg, aq, ad, as);
+                put_act_block<WT, SU>(w, dbits, b, nd, nsu, aq, ad, as);
+            }
+        } else {
+            constexpr int U = 4;
+            for (int i0 = warp; i0 < legs * nd; i0 += U * nw) {
+                float4 v[U][2];
+#pragma unroll
+                for (int u = 0; u < U; u++) {
+                    const int i = i0 + u * nw;
+                    if (i < legs * nd && leg_row[i / nd] >= 0) v[u][0] = x4[i * 64 + 2 * lane], v[u][1] = x4[i * 64 + 2 * lane + 1];
                 }
-            } else {
-                for (int b = (warp + leg * nd) % nw; b < nd; b += nw)
-                    quant_q8_K_lane_put(x4[b * 64 + 2 * lane], x4[b * 64 + 2 * lane + 1], lane, b, ap, aq, ad, as, nullptr);
+#pragma unroll
+                for (int u = 0; u < U; u++) {
+                    const int i = i0 + u * nw, leg = i / nd;
+                    if (i >= legs * nd || leg_row[leg] < 0) continue;
+                    act_of(leg, aq, ad, as);
+                    quant_q8_K_lane_put(v[u][0], v[u][1], lane, i - leg * nd, ap, aq, ad, as, nullptr);
+                }
             }
         }
     }
@@ -152,9 +175,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) expert_vec_kernel(const __g
         const uint64_t a0 = (base + geo.off(s0)) & ~15ull;
         uint8_t* sbuf = slots + (size_t)slot * a.slot_bytes;
         const SmemBytes wv{sbuf};
-        uint8_t* aq = acts + (size_t)(GATED ? 0 : leg) * a.act_stride;
-        float* ad = reinterpret_cast<float*>(aq + qbytes);
-        int* as = reinterpret_cast<int*>(ad + nd);
+        act_of(GATED ? 0 : leg, aq, ad, as);
         const ActView act{aq, ad, as, ap};
         for (int ss = s0; ss < s1; ss += segs_per_pass) {
             const int seg = ss + ssub;
