@@ -5,8 +5,8 @@
 //   summed  y[t][n] = r[t][n] + sum_j w[t][j] (W[e_tj][n] . q(h[t][j]))   one leg for each choice j of token t
 //
 // Bound by the weights' bytes (each slot reads its experts' rows once) and, below some 20 MB, by the launch's fixed parts:
-// one token through 8 of 64 experts takes 9.8 us gated (Q4_K, 1024 x 2048 twice, 18.9 MB) and 9.3 summed (Q6_K, 2048 x
-// 1024, 13.8 MB), a call among others; 128 choices 60 us (5 TB/s).  The unit of work is a share of the output rows
+// one token through 8 of 64 experts takes 6.9 us gated (Q4_K, 1024 x 2048 twice, 18.9 MB) and 8.3 summed (Q6_K, 2048 x
+// 1024, 13.8 MB), replayed from a graph; 128 choices 60 us (5 TB/s).  The unit of work is a share of the output rows
 // of one slot (gated) or token (summed): the CTA streams that share's rows of every leg through its warps' rings of bulk
 // copies, with the decoders and the row geometry of the matvec, keeps each leg's sums in shared memory and joins the
 // legs at the end, in the order of the choices.  So the gate's activation and the weighted sum cost no launch and no

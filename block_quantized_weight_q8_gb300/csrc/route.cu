@@ -9,8 +9,8 @@
 // power of two, 32 where there is one group), lane l of it the group's experts l, l + L, ...; so all groups' worth comes of
 // one look at a lane's keys and log2 L exchanges.  A choice is a maximum over the lane's keys, one over the warp
 // (whole-number keys in the floats' order) and one of the index.  Bound by these instructions, two thousand a token:
-// 8192 tokens of 256 experts, 4 of 8 groups by two keys, 8 choices take 25 us with the issue slots 68% busy (with expert e
-// in lane e % 32 and the groups one after another: 43 us); a few tokens take one launch, 6.3 us.
+// 8192 tokens of 256 experts, 4 of 8 groups by two keys, 8 choices take 21.5 us (25 alone, the issue slots 68% busy) (with expert e
+// in lane e % 32 and the groups one after another: 43 us); a few tokens take 3.2 us.
 //
 // The choice is that of binary64.  Without a bias the scores' order is the logits' and keys are the logits themselves
 // (but where groups count by two keys).  Otherwise keys carry rounding errors, bounded below; where two keys that decide
@@ -266,8 +266,9 @@ __device__ __noinline__ float small_weight(bool sigmoid, bool real, float v, flo
 
 constexpr int kRouteThreads = 128;
 
+// 12 CTAs of 40 registers an SM where a lane has few keys (21.9 us without the bound, 21.5 with it).
 template <int PER>
-__global__ void __launch_bounds__(kRouteThreads) route_kernel(const __grid_constant__ Route a) {
+__global__ void __launch_bounds__(kRouteThreads, PER <= 8 ? 12 : 1) route_kernel(const __grid_constant__ Route a) {
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31;
