@@ -40,7 +40,9 @@ HEADLINE = "q8_0_matvec_12288x4096"
 L2_BYTES = 129 * 10**6
 PEAKS_FILE = os.path.join(ROOT, "MEASURED_PEAKS.json")
 PROFILE_FILE = os.path.join(ROOT, "profiles", "matvec_q8_0_12288x4096.txt")
-MATVEC_SOURCES = ["block_quantized_weight_q8_gb300/csrc/matvec.cu", "block_quantized_weight_q8_gb300/csrc/matvec_kernel.cuh", "block_quantized_weight_q8_gb300/csrc/qmm_device.cuh"]
+MATVEC_SOURCES = ["block_quantized_weight_q8_gb300/csrc/matvec.cu",
+                  "block_quantized_weight_q8_gb300/csrc/matvec_kernel.cuh",
+                  "block_quantized_weight_q8_gb300/csrc/qmm_device.cuh"]
 
 
 # ------------------------------------------------------------------ distributed helpers

@@ -11,7 +11,6 @@ ValueError for one of another type, shape, layout or device.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 from .buildlib import LIB, build  # noqa: F401
@@ -550,11 +549,6 @@ def _row(t, K):
     return K // values * size if values and K % values == 0 else 0
 
 
-@functools.lru_cache(64)
-def _route_spec(score, k, groups, groups_kept, group_top, renorm, scale):
-    return RouteSpec(ROUTE_SCORES[score], k, groups, groups_kept, group_top, 1 if renorm else 0, scale)
-
-
 def _whole(name, t, dev, dtype, shape):
     """The address of a contiguous tensor of this type and shape (None for None)."""
     if t is None:
@@ -595,7 +589,7 @@ def qmm_route(logits, ids, weights, score="softmax", bias=None, groups=1, groups
     if ids.dim() != 2:
         _refuse("ids", ids, "int32", (T, "k"), dev)
     k = ids.shape[1]
-    spec = _route_spec(score, k, groups, groups_kept, group_top, renorm, scale)
+    spec = RouteSpec(ROUTE_SCORES[score], k, groups, groups_kept, group_top, 1 if renorm else 0, scale)
     _call("qmm_route", ctypes.addressof(spec), logits.data_ptr(), logits.stride(0) if T > 1 else E,
           _whole("bias", bias, dev, _torch.float32, (E,)), _whole("ids", ids, dev, _torch.int32, (T, k)),
           _whole("weights", weights, dev, _torch.float32, (T, k)), T, E,
