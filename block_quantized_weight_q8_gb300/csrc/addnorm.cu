@@ -154,7 +154,8 @@ static qmm_status launch_act(const float* x, const float* r, float* sum, const f
     DeviceInfo dev;
     const qmm_status st = current_device(&dev);
     if (st != QMM_OK) return st;
-    if (units <= 32 && (units < H || M <= 2 * dev.sms)) return launch_rows<ACT, 1, true>(x, r, sum, w, eps, h, xq, M, K, (int)units, stream);
+    if (units <= 32 && (units < H || M <= 2 * dev.sms))
+        return launch_rows<ACT, 1, true>(x, r, sum, w, eps, h, xq, M, K, (int)units, stream);
     if (units <= 32 * H) return launch_rows<ACT, H, true>(x, r, sum, w, eps, h, xq, M, K, (int)((units + H - 1) / H), stream);
     return launch_rows<ACT, 1, false>(x, r, sum, w, eps, h, xq, M, K, 32, stream);
 }

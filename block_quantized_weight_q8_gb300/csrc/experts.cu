@@ -323,7 +323,8 @@ static bool many_rows(int wt, const ExpertShape& s, bool gate) {
 }
 
 // y[t][n] = residual[t][n] + sum_j weights[t][j] p[t][j][n] over the choices that are there, in their order.  Bound by
-// memory: 4 (k + 2) bytes a value (2048 tokens of 8 choices of 2048: 168 MB in 30 us, 5.5 TB/s).  V values a thread: 4 where N is a multiple of it.
+// memory: 4 (k + 2) bytes a value (2048 tokens of 8 choices of 2048: 168 MB in 30 us, 5.5 TB/s).  V values a thread: 4
+// where N is a multiple of it.
 template <int V>
 __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ p, const int32_t* __restrict__ ids,
                                                       const float* __restrict__ weights, const float* residual, float* y,

@@ -223,7 +223,8 @@ __device__ __forceinline__ uint32_t codes_of(const SmemBytes& w, uint32_t o, int
         const uint4 q0 = *reinterpret_cast<const uint4*>(w.base + b), q1 = *reinterpret_cast<const uint4*>(w.base + b + 16);
         const uint32_t q[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
 #pragma unroll
-        for (int i = 0; i < 8; i++) c[i] = WT == QMM_Q4_K ? q[i] & (kb & 1 ? 0xF0F0F0F0u : 0x0F0F0F0Fu) : (q[i] >> (4 * (kb & 1))) & 0x0F0F0F0Fu;
+        for (int i = 0; i < 8; i++)
+            c[i] = WT == QMM_Q4_K ? q[i] & (kb & 1 ? 0xF0F0F0F0u : 0x0F0F0F0Fu) : (q[i] >> (4 * (kb & 1))) & 0x0F0F0F0Fu;
         if constexpr (WT == QMM_Q5_K) {
             const uint4 h0 = *reinterpret_cast<const uint4*>(w.base + o + 16), h1 = *reinterpret_cast<const uint4*>(w.base + o + 32);
             const uint32_t h[8] = {h0.x, h0.y, h0.z, h0.w, h1.x, h1.y, h1.z, h1.w};
@@ -738,7 +739,8 @@ __global__ void __launch_bounds__(THREADS, 1) expert_mma_kernel(const __grid_con
                         if (h == 0) {
                             const uint32_t bar = bars.sx_full((int)(gc % SX_RING));
                             mbar_arrive_expect_tx(bar, rows * 4);
-                            bulk_g2s_nohint(sbase + L::OFF_SX + gc % SX_RING * (kTileRows * 4), sums + L::XTERMS * 32 * rows, rows * 4, bar);
+                            bulk_g2s_nohint(sbase + L::OFF_SX + gc % SX_RING * (kTileRows * 4),
+                                            sums + L::XTERMS * 32 * rows, rows * 4, bar);
                         }
                         const uint32_t dst = sbase + L::OFF_OP + m % L::X_SLOTS * L::XSLOT;
                         const uint32_t bytes = L::XTERMS * 64 * rows * (uint32_t)max(0, min(blocks - h * L::BLOCKS, L::BLOCKS));

@@ -115,7 +115,8 @@ __device__ __forceinline__ Key take_best(Key (&key)[PER], const Place& at, int* 
 // choice is sure; with *doubt more, up to where a key is surely smaller; 0 and *doubt where the groups are not sure, or
 // more than 32 keys.
 template <int PER, class Key, class Value>
-__device__ __forceinline__ int choose(const Route& a, const Place& at, Key (&key)[PER], int lane, Value near, Value rel, int* chosen, bool* doubt) {
+__device__ __forceinline__ int choose(const Route& a, const Place& at, Key (&key)[PER], int lane, Value near, Value rel,
+                                      int* chosen, bool* doubt) {
     constexpr int U = unrolled<PER, Key>();
     *doubt = false;
     if (a.groups > 1) {
