@@ -57,11 +57,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) expert_vec_kernel(const __g
         fence_mbar_init();
     }
     pdl_wait();  // the indexes and the rows come from earlier kernels
-    if (tid < legs) {
-        const int e = a.ids[(int64_t)unit * (GATED ? 1 : a.k) + (GATED ? 0 : tid)];
+    for (int j = tid; j < legs; j += blockDim.x) {  // long rows leave room for one warp, whose threads are fewer than the legs
+        const int e = a.ids[(int64_t)unit * (GATED ? 1 : a.k) + (GATED ? 0 : j)];
         const bool real = e >= 0 && e < a.E;
         if (e >= a.E) atomicOr(&g_matvec_error, kErrIndex);
-        leg_row[tid] = real ? (int64_t)e * N : -1;
+        leg_row[j] = real ? (int64_t)e * N : -1;
     }
     __syncthreads();
 
@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) expert_vec_kernel(const __g
         const int leg = it / litems, s0 = (it - leg * litems) * a.item_segs, s1 = min(s0 + a.item_segs, nseg);
         const uint8_t* W = GATED && leg ? a.W1 : a.W0;
         const int64_t row0 = leg_row[leg];
-        if (row0 < 0) {
+        if (row0 < 0 || !QMM_IN_BOUNDS(g_matvec_error, row0 + r_begin + rows - 1, (int64_t)a.E * N)) {
             mbar_arrive_expect_tx(smem_u32(&full[slot]), 0);
             return;
         }
