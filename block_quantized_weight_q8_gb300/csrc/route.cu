@@ -146,27 +146,35 @@ __device__ __forceinline__ int choose(const Route& a, const Place& at, Key (&key
             if (h == 1 && !at.second) worth[h] = 0;
         }
         if (at.lane_of != 0 || at.base < 0) worth[0] = 0;  // one lane speaks for its group
+        const Key all[2] = {worth[0], worth[1]};
         const int g = at.base < 0 ? 64 : at.base / at.per_group;
         uint64_t open = 0;
-        Value last = 0, last_size = 0;
-        for (int i = 0; i < a.kept + 1; i++) {
+        for (int i = 0; i < a.kept; i++) {
             const Key m = warp_max(max(worth[0], worth[1]));
             if (m == 0) break;
             const uint32_t mine = worth[0] == m ? (uint32_t)g : worth[1] == m ? (uint32_t)g + 32 : 0xFFFFFFFFu;
             const uint32_t win = __reduce_min_sync(0xffffffffu, mine);
-            const Value v = unordered(m);
-            const int from = a.groups > 32 ? win & 31 : win * at.L;
-            const Value sz = __shfl_sync(0xffffffffu, win < 32 || a.groups <= 32 ? size[0] : size[1], from);
-            // the first that stays closed against the last that is open
-            if (i == a.kept && near >= 0 && !(last - v > 2 * near + rel * (last_size + sz))) {
-                *doubt = true;
-                return 0;
-            }
-            last = v, last_size = sz;
-            if (i < a.kept) open |= 1ull << win;
+            open |= 1ull << win;
             if (mine == win) {
                 if (win == (uint32_t)g) worth[0] = 0;
                 else worth[1] = 0;
+            }
+        }
+        if (near >= 0) {
+            // Sure where the least that an open group can be worth is more than the most that a closed one can.  Every group
+            // counts, wherever it stands: two keys of opposite signs leave a worth that is small beside its error.
+            Key least = 0, most = 0;
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                if (all[h] == 0) continue;
+                const Value v = unordered(all[h]), off = near + (Value)1.5 * rel * size[h];
+                if (open >> (g + 32 * h) & 1) least = max(least, ordered(isfinite(v) ? off - v : (Value)INFINITY));
+                else most = max(most, ordered(isfinite(v) ? v + off : (Value)INFINITY));
+            }
+            least = warp_max(least), most = warp_max(most);
+            if (most != 0 && !(-unordered(least) > unordered(most))) {
+                *doubt = true;
+                return 0;
             }
         }
         const bool open0 = g < 64 && (open >> g) & 1, open1 = g < 32 && (open >> (g + 32)) & 1;
@@ -310,9 +318,10 @@ __global__ void __launch_bounds__(kRouteThreads, PER <= 8 ? 12 : 1) route_kernel
     }
     int e;
     // Errors of two keys together (expf is within 2 units of 2^-23 relative): sigmoid, 2 (2^-22 s (1 - s) + 2^-23 s), at
-    // most 6 units of 2^-24, and the bias's addition 2^-24 |key| each (half of 1.2e-7; sums of two keys, as much again);
-    // softmax, scores up to the largest, 1 / total: the exponent's rounding (its size times the score at most 0.37 of the
-    // largest), the sum's 36 roundings, the quotient's.
+    // most 6 units of 2^-24, and the bias's addition 2^-24 |key| each (half of 1.2e-7); softmax, scores up to the largest,
+    // 1 / total: the exponent's rounding (its size times the score at most 0.37 of the largest) and the quotient's, a few
+    // units of 2^-24, and, shared by all keys, the sum's at most 69 roundings (64 keys of a lane and the warp's five).  A
+    // group's worth of two keys has both their errors; its sum and the check's own addition round by 2^-24 of their sizes.
     const float near = !scored ? -1.0f : a.sigmoid ? 3.6e-7f : 8e-6f / total;
     bool doubt;
     const int count = choose<PER, uint32_t, float>(a, at, key, lane, near, 1.2e-7f, &e, &doubt);
