@@ -85,6 +85,7 @@ SIGNATURES = {
     "qmm_experts_scratch_bytes": ("tiiiii", ctypes.c_size_t),
     "qmm_experts_glu": ("ttppppppsiiiiiq", ctypes.c_int),
     "qmm_experts_sum": ("tppppppps" + "iiiiiq", ctypes.c_int),
+    "qmm_experts_path": ("ttiiiii", ctypes.c_int),
     "qmm_matmul_q4_K": ("pppiiiq", ctypes.c_int),
     "qmm_matmul_q6_K": ("pppiiiq", ctypes.c_int),
     "qmm_matmul_q5_K": ("pppiiiq", ctypes.c_int),
@@ -598,6 +599,15 @@ def qmm_route(logits, ids, weights, score="softmax", bias=None, groups=1, groups
 
 def qmm_experts_scratch_bytes(wtype, T, k, E, N, K):
     return int(load().qmm_experts_scratch_bytes(_type(wtype), int(T), int(k), int(E), int(N), int(K)))
+
+
+def qmm_experts_path(wtype, gated, T, k, E, N, K):
+    """0 where qmm_experts_glu (gated) or qmm_experts_sum streams each choice's weight rows at this shape, 1 where it goes by
+    the tensor cores."""
+    path = int(load().qmm_experts_path(_type(wtype), 1 if gated else 0, int(T), int(k), int(E), int(N), int(K)))
+    if path < 0:
+        raise ValueError("no experts' products of type %r and shape %s" % (wtype, (T, k, E, N, K)))
+    return path
 
 
 def qmm_experts_glu(wtype, Wg, Wu, xq, ids, h, scratch, scratch_bytes, gate="silu", stream=None):

@@ -387,6 +387,11 @@ size_t qmm_experts_scratch_bytes(int wtype, int64_t T, int64_t k, int64_t E, int
     return check_experts(wtype, s) == QMM_OK ? scratch_of(wtype, s).bytes : 0;
 }
 
+int qmm_experts_path(int wtype, int gated, int64_t T, int64_t k, int64_t E, int64_t N, int64_t K) {
+    const ExpertShape s{T, k, E, N, K};
+    return check_experts(wtype, s) != QMM_OK ? -1 : many_rows(wtype, s, gated != 0) ? 1 : 0;
+}
+
 qmm_status qmm_experts_glu(int wtype, int kind, const void* Wg, const void* Wu, const void* xq, const int32_t* ids, float* h,
                            void* scratch, size_t scratch_bytes, int64_t T, int64_t k, int64_t E, int64_t N, int64_t K,
                            qmm_stream_t stream) {

@@ -666,6 +666,11 @@ QMM_API qmm_status qmm_blocksums(int wtype, const void* W, const void* xq, int32
  * Returns QMM_E_CUDA if the launch fails. */
 QMM_API qmm_status qmm_test_wait_timeout(uint64_t limit_ns, qmm_stream_t stream);
 
+/* Which kernels qmm_experts_glu (gated != 0) or qmm_experts_sum takes for a shape on the
+ * current device: 0 where every choice streams its weight rows (few choices), 1 where
+ * rows sorted by expert meet them on the tensor cores (many); -1: a bad argument. */
+QMM_API int qmm_experts_path(int wtype, int gated, int64_t T, int64_t k, int64_t E, int64_t N, int64_t K);
+
 /* Reads (and with clear != 0 resets) the device error words that bounded waits
  * (QMM_E_TIMEOUT), qmm_get_rows (QMM_E_SHAPE for an id outside [0, N)), the experts'
  * calls (QMM_E_SHAPE for an id of E or more), the paged cache's calls (QMM_E_SHAPE for a position without a page) and, in a
