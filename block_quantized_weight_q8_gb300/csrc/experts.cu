@@ -49,6 +49,7 @@ struct Prepare {
     ExpertTile* tiles;
     uint8_t* operand;
     int S, k, E, N, K;
+    int spare;  // Q8_0 rows: act_spare of the weights
 };
 __device__ __forceinline__ __half2 half2_of(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
 __device__ __forceinline__ uint32_t bits_of(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
@@ -205,15 +206,15 @@ __global__ void __launch_bounds__(kOperandThreads) operand_kernel(const __grid_c
 #pragma unroll
             for (int b = 0; b < 8; b++) w[b] = real ? make_uint2(p[1 + 8 * b + 2 * kq], p[2 + 8 * b + 2 * kq]) : make_uint2(0u, 0u);
         }
-        uint32_t f = 0;  // Q8_0: the power of two that brings the largest scale below 2
+        uint32_t f = 0;  // Q8_0: the run's power of two
         float scale = d;
         if constexpr (ACT == QMM_Q8_0) {
             uint32_t top = 0;
 #pragma unroll
             for (int b = 0; b < 8; b++) top = max(top, dbits[b] & 0x7FFFu);
-            const int e = min(max((int)(top >> 10), 1), 30);
-            f = (uint32_t)__half_as_ushort(__float2half_rn(__int_as_float((15 - e + 127) << 23)));
-            scale = __int_as_float((e - 15 + 127) << 23);
+            const int shift = run_shift(top, a.spare);
+            f = (uint32_t)(shift + 15) << 10;
+            scale = __int_as_float((127 - shift) << 23);
         }
         if (!QMM_IN_BOUNDS(g_experts_error, (int64_t)t.at + 8 * g + row, (int64_t)a.S + 15 * min(a.S, a.E))) continue;
         uint8_t* const base = a.operand + ((int64_t)t.at * nchunks + (int64_t)c * rows) * operand_bytes(ACT);
@@ -290,6 +291,7 @@ static qmm_status on_tensor_cores(int wt, int kind, const ExpertShape& s, const 
     p.ids = ids, p.xq = (const uint8_t*)xq, p.x = x, p.h = gate ? out : nullptr;
     p.ntiles = reinterpret_cast<int32_t*>(scratch), p.order = reinterpret_cast<int32_t*>(scratch + l.order);
     p.tiles = reinterpret_cast<ExpertTile*>(scratch + l.tiles), p.operand = scratch + l.operand;
+    p.spare = act_spare(wt);
     p.S = (int)(s.T * s.k), p.k = (int)s.k, p.E = (int)s.E, p.N = (int)s.N, p.K = (int)s.K;
     const qmm_status st = prepare(act_type_of(wt), p, l.tiles_most, stream);
     if (st != QMM_OK) return st;

@@ -9,9 +9,10 @@
 //   Q4_K, Q5_K, Q2_K   scale times code, a whole number up to 1953 (exact), over the block's d; the minimums over d, in
 //                      two terms, times the activations' sums of 16 values (one more step of 16)
 //   Q6_K               scale times code, a whole number up to 4096, in two exact terms
-//   32-value blocks    the value over a power of two that the row's 256 share, in two terms, hi + lo (22 bits); the codes
-//                      of Q4_1 and Q5_1 are centered and the minimums multiply the sums, as above
-//   activations        Q8_K: the codes (exact); Q8_0: the values over a shared power of two, in two terms
+//   32-value blocks    the value over a power of two that the row's 256 share, in two terms, hi + lo, exact wherever the
+//                      scale is (run_shift in experts_mma.h); the codes of Q4_1 and Q5_1 are centered and the minimums
+//                      multiply the sums, as above
+//   activations        Q8_K: the codes (exact); Q8_0: the values over a shared power of two, in two terms, likewise
 // Products of two-term operands leave out lo lo.  Sums of steps are truncated to f32 by the tensor core; with at most 48
 // steps to a sum, those with a lo first, the errors measured are 0.04 to 0.45e-6 of the result.
 //
@@ -157,23 +158,15 @@ __device__ __forceinline__ void split2(float v, uint32_t* hi, uint32_t* lo) {
     *hi = h2_dup(h);
     *lo = h2_dup(f2h_bits(v - h2f(h)));
 }
-// The power of two that brings f16 magnitudes up to `bits` (sign cleared) below 2: its exponent field (at least the
-// smallest normal one, at most the largest), 2^(15 - e) as f32, and its inverse.
-__device__ __forceinline__ int exponent_of(uint32_t bits) {
-    const int e = (int)(bits >> 10);
-    return e < 1 ? 1 : e > 30 ? 30 : e;
-}
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
-__device__ __forceinline__ uint32_t pow2_half(int e) {  // -24 <= e <= 15
-    return e >= -14 ? (uint32_t)(e + 15) << 10 : 1u << (e + 24);
-}
+__device__ __forceinline__ uint32_t pow2_half(int e) { return (uint32_t)(e + 15) << 10; }  // -14 <= e <= 15
 
-// What the blocks of a row's chunk share: what their sums are multiplied by; the exponent field of the power of two
-// (32-value blocks), or what the scales and minimums are multiplied by over it (K-quants); the first 16 bytes of a Q4_K or
+// What the blocks of a row's chunk share: what their sums are multiplied by; the power that 32-value blocks are multiplied
+// by, or what the scales and minimums are multiplied by over it (K-quants); the first 16 bytes of a Q4_K or
 // Q5_K block.
 struct WRow {
     float scale;
-    int e;
+    int shift;
     float value, min;
     uint4 head;
 };
@@ -300,8 +293,8 @@ __device__ __forceinline__ WRow row_scale(const SmemBytes& w, uint32_t o, int ha
                 top = max(top, w.u16(b) & 0x7FFFu);
             }
         }
-        const int e = exponent_of(top);
-        return {pow2(e - 15), e, 0.0f, 0.0f, make_uint4(0u, 0u, 0u, 0u)};
+        const int shift = run_shift(top, weight_spare(WT));
+        return {pow2(-shift), shift, 0.0f, 0.0f, make_uint4(0u, 0u, 0u, 0u)};
     }
 }
 
@@ -330,7 +323,7 @@ __device__ __forceinline__ void convert_block(const SmemBytes& w, uint32_t o, in
         const uint32_t sc = w.u16(o + 192 + 2 * kb);
         d0 = h2_dup(f2h_bits((float)(int8_t)(sc & 0xFFu))), d1 = h2_dup(f2h_bits((float)(int8_t)(sc >> 8)));
     } else {
-        d0 = d1 = h2_mul(h2_dup(w.u16(o + Fmt<WT>::BB * kb)), h2_dup(pow2_half(15 - row.e)));
+        d0 = d1 = h2_mul(h2_dup(w.u16(o + Fmt<WT>::BB * kb)), h2_dup(pow2_half(row.shift)));
     }
     if constexpr (Lay<WT>::WTERMS == 1) {
         // scale (1024 + code) - 1024 scale: every part is an f16 and so is the result
@@ -357,7 +350,7 @@ template <int WT>
 __device__ __forceinline__ void convert_min(const SmemBytes& w, uint32_t o, int blocks, const WRow& row, uint32_t (&hi)[8],
                                             uint32_t (&lo)[8]) {
     if constexpr (WT == QMM_Q4_1 || WT == QMM_Q5_1) {
-        const float f = pow2(15 - row.e);
+        const float f = pow2(row.shift);
 #pragma unroll
         for (int b = 0; b < 8; b++) {
             const uint32_t dm = b < blocks ? w.w32(o + Fmt<WT>::BB * b) : 0u;

@@ -18,6 +18,19 @@ constexpr int kTileRows = 128;  // activation rows of a tile
 constexpr int operand_terms(int act) { return act == QMM_Q8_0 ? 2 : 1; }
 constexpr int operand_bytes(int act) { return operand_terms(act) * (512 + 32) + 4; }  // of a row's chunk
 
+// 32-value blocks (and Q8_0 rows) stand over a power of two that a run shares.  It brings the largest scale (or minimum) below
+// 2^(1 + spare), as far up as scale times code and, beside minimums, scale times the sum of 16 codes stay f16: so every f16
+// scale of a run is exact where the largest is below that, and else whatever is at least 2^-(14 + spare) of it.
+constexpr int weight_spare(int wt) {  // codes (Q4_1, Q5_1: centered, the minimum with them) up to 2^7, 2^3, 2^4
+    return wt == QMM_Q8_0 ? 7 : wt == QMM_Q4_0 || wt == QMM_Q4_1 ? 11 : 10;
+}
+constexpr int act_spare(int wt) { return wt == QMM_Q4_1 || wt == QMM_Q5_1 ? 4 : 7; }
+// the power that the run's values are multiplied by, from the largest scale's f16 bits (sign cleared); at least -11
+__host__ __device__ constexpr int run_shift(uint32_t bits, int spare) {
+    const int e = (int)(bits >> 10), s = 15 + spare - (e < 1 ? 1 : e > 30 ? 30 : e);
+    return s < 15 ? s : 15;  // f16 has no larger one, and every scale is over 2^-14 by then
+}
+
 struct ExpertTile {
     int32_t expert, first, count;  // rows order[first .. first + count) of one expert
     int32_t at;                    // where its operand begins, in rows
