@@ -244,9 +244,11 @@ __device__ __forceinline__ uint32_t codes_of(const SmemBytes& w, uint32_t o, int
     }
 }
 
-// A K-quant block's sums are over its d, unless its minimums' scale is over 1000 times that (hardly any weights have that)
-// and not all minimums are zero: then over d times such a power of two that minimums up to 63 times their scale stay f16.
-// Scale times code is still exact where that power is at most 2^20; beyond, one minimum is over 2^20 times any of them.
+// A K-quant block's sums are over its d, unless its minimums' scale m is over 1000 times that (hardly any weights have that)
+// and not all minimums are zero: then over d times such a power of two, 2^-10 to 2^-8 of m, that minimums up to 63 times
+// their scale stay f16.  Minimums, two f16, keep 2^-22 of themselves or 2^-25 of what the sums are over.  Scale times code
+// is exact where that power is at most 2^20, m at most 2^29 d; beyond, the scale (Q4_K: a 16th of it, times 16 code) is
+// rounded by up to 2^-25 of what the sums are over, and scale times code by up to 2^-25 m.
 template <class None>
 __device__ __forceinline__ WRow shared_scale(float d, float m, None none) {
     float D = d, value = 1.0f;

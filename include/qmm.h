@@ -623,12 +623,14 @@ QMM_API qmm_status qmm_route(const qmm_route_spec* spec, const float* logits, in
  *        not there); weights f32 [T][k], NULL: 1; residual f32 [T][N], NULL: 0, may be y
  * Products agree with the block-wise definition (qmm_matvec) within 1e-5 of their row's
  * L2 norm, and are the same on every run; between calls of few and of many choices a
- * choice's products may differ by as much.  With many choices (qmm_experts_path) this has
- * an exception: eight blocks of 32 values share a power of two, which keeps every scale
- * (Q4_1, Q5_1: and minimum) exactly where the largest of the eight, L, is below 256, Q8_0
- * rows beside Q4_1 and Q5_1 32; otherwise a scale below 2^-21 L (those rows: 2^-18 L) is
- * off by up to 2^-32 L (2^-29 L), which is over the bound only where what L scales meets
- * zeros.  k 1..64, E 1..1024, T * k <= 2^24, E * N <=
+ * choice's products may differ by as much.  With many choices (qmm_experts_path) two
+ * things are held to a share of what is larger beside them, which is over the bound only
+ * where that meets zeros.  Eight blocks of 32 values share a power of two: it keeps every
+ * scale (Q4_1, Q5_1: and minimum) exactly where the largest of the eight, L, is below 256,
+ * Q8_0 rows beside Q4_1 and Q5_1 32; otherwise a scale below 2^-21 L (those rows: 2^-18 L)
+ * is off by up to 2^-32 L (2^-29 L).  In a block of Q4_K, Q5_K or Q2_K with the scales d
+ * and m (of the minimums) a minimum is off by up to 2^-25 |d|, and a scale times code,
+ * where |m| > 2^29 |d|, by up to 2^-25 |m|.  k 1..64, E 1..1024, T * k <= 2^24, E * N <=
  * 2^31 - 1; N, K and the alignment (ids and weights: 4 bytes) as for qmm_matvec.
  * scratch: at least qmm_experts_scratch_bytes(wtype, T, k, E, N, K) bytes (0: a bad
  * argument), enough for either call of this shape, written before it is read; calls that
