@@ -574,10 +574,11 @@ QMM_API qmm_status qmm_kv_attend(const qmm_kv_pages* cache, const float* q, int6
  *   qmm_experts_sum(wd, Wd, h, ids, weights, x, x, scratch, bytes, T, k, E, K, F, stream);
  *
  * qmm_add_rmsnorm_quantize: y = x + r, one f32 rounding; h_i = (y_i s) w_i, s =
- * 1 / sqrt(ss / K + eps), ss = sum of y_i^2 summed to 2^-44 relative and rounded to
- * f32 once, every other step an f32 operation rounded once; xq the rows of h as
- * qmm_quantize_q8_0 / q8_K (act) gives them.  So sum, h and xq are those of a scalar
- * implementation with an exact sum of squares (where y^2 neither overflows f32 nor
+ * 1 / sqrt(ss / K + eps), ss = sum of y_i^2 summed to 2^-38 relative or better and
+ * rounded to f32 once, every other step an f32 operation rounded once; xq the rows of h
+ * as qmm_quantize_q8_0 / q8_K (act) gives them.  So sum, h and xq are those of a scalar
+ * implementation with an exact sum of squares, but where that sum lies within this of the
+ * middle between two floats (and where y^2 neither overflows f32 nor
  * falls below 2^-100).  x, r f32 [M][K]; w f32 [K]; sum f32 [M][K] receives y, NULL:
  * not kept; it may be x or r; h f32 [M][K] or xq may be NULL, not both.  Apart from sum
  * no output overlaps another argument.  K as for qmm_rmsnorm_quantize; every pointer
