@@ -526,6 +526,10 @@ ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
 GLU_KINDS = {"silu": 0, "gelu": 1}
 
 
+def _unknown(what, names, name):
+    raise ValueError("%s: one of %s is needed, got %r" % (what, ", ".join(sorted(names)), name))
+
+
 class RouteSpec(ctypes.Structure):
     """qmm_route_spec: how tokens choose their experts."""
     _fields_ = [("score", ctypes.c_int32), ("k", ctypes.c_int32), ("groups", ctypes.c_int32), ("groups_kept", ctypes.c_int32),
@@ -539,6 +543,8 @@ def _format(t):
     """(code, bytes of a block, its values, activation type's code) of a type."""
     f = _formats.get(t)
     if f is None:
+        if isinstance(t, str) and t not in TYPES:
+            _unknown("type", TYPES, t)
         c = _type(t)
         f = _formats[t] = (c, qmm_block_bytes(c), qmm_block_values(c), qmm_act_type(c))
     return f
@@ -568,11 +574,12 @@ def _workspace(t, size, dev):
 def qmm_add_rmsnorm_quantize(act, x, r, w, eps, xq=None, sum=None, h=None, stream=None):
     """sum = x + r, h = its RMSNorm with the weight w, xq = h quantized to act ("q8_0" or "q8_K"); x and r f32 [M][K], xq
     uint8 [M][qmm_row_bytes(act, K)]; sum (may be x or r) and one of h and xq may be None."""
+    at = _format(act)[0]
     dev = _device()
     if x.dim() != 2:
         _refuse("x", x, "float32", ("M", "K"), dev)
     rows = M, K = x.shape
-    _call("qmm_add_rmsnorm_quantize", _type(act), _whole("x", x, dev, _torch.float32, rows), _whole("r", r, dev, _torch.float32, rows),
+    _call("qmm_add_rmsnorm_quantize", at, _whole("x", x, dev, _torch.float32, rows), _whole("r", r, dev, _torch.float32, rows),
           _whole("sum", sum, dev, _torch.float32, rows), _whole("w", w, dev, _torch.float32, (K,)), eps,
           _whole("h", h, dev, _torch.float32, rows), _whole("xq", xq, dev, _torch.uint8, (M, _row(act, K))), M, K,
           _raw_stream(dev) if stream is None else stream_handle(stream))
@@ -582,6 +589,10 @@ def qmm_route(logits, ids, weights, score="softmax", bias=None, groups=1, groups
               stream=None):
     """ids and weights ([T][k], int32 and f32): the experts that each token's logits ([T][E] f32, rows any stride apart)
     choose, and what they weigh (see include/qmm.h)."""
+    if not isinstance(score, str) or score not in ROUTE_SCORES:
+        _unknown("score", ROUTE_SCORES, score)
+    if (groups | groups_kept | group_top) >> 31:  # the spec's fields have 32 bits, and none is negative
+        raise ValueError("groups, groups_kept, group_top: got %r, %r, %r" % (groups, groups_kept, group_top))
     dev = _device()
     if logits.dtype is not _torch.float32 or logits.get_device() != dev or logits.dim() != 2 or (
             logits.stride(1) != 1 and logits.shape[1] > 1):
@@ -598,13 +609,13 @@ def qmm_route(logits, ids, weights, score="softmax", bias=None, groups=1, groups
 
 
 def qmm_experts_scratch_bytes(wtype, T, k, E, N, K):
-    return int(load().qmm_experts_scratch_bytes(_type(wtype), int(T), int(k), int(E), int(N), int(K)))
+    return int(load().qmm_experts_scratch_bytes(_format(wtype)[0], int(T), int(k), int(E), int(N), int(K)))
 
 
 def qmm_experts_path(wtype, gated, T, k, E, N, K):
     """0 where qmm_experts_glu (gated) or qmm_experts_sum streams each choice's weight rows at this shape, 1 where it goes by
     the tensor cores."""
-    path = int(load().qmm_experts_path(_type(wtype), 1 if gated else 0, int(T), int(k), int(E), int(N), int(K)))
+    path = int(load().qmm_experts_path(_format(wtype)[0], 1 if gated else 0, int(T), int(k), int(E), int(N), int(K)))
     if path < 0:
         raise ValueError("no experts' products of type %r and shape %s" % (wtype, (T, k, E, N, K)))
     return path
@@ -613,8 +624,10 @@ def qmm_experts_path(wtype, gated, T, k, E, N, K):
 def qmm_experts_glu(wtype, Wg, Wu, xq, ids, h, scratch, scratch_bytes, gate="silu", stream=None):
     """h[t][j] = gate(Wg[e] x_t) * (Wu[e] x_t), e = ids[t][j]: h f32 [T][k][N], Wg and Wu uint8 [E][N][row bytes], xq uint8
     [T][qmm_row_bytes(qmm_act_type(wtype), K)], ids int32 [T][k] (negative: no expert, zeros)."""
-    dev = _device()
+    if not isinstance(gate, str) or gate not in GLU_KINDS:
+        _unknown("gate", GLU_KINDS, gate)
     wt, size, values, act = _format(wtype)
+    dev = _device()
     if h.dim() != 3 or Wg.dim() != 3:
         _refuse("h, Wg", h if h.dim() != 3 else Wg, "float32, uint8", "of 3 dimensions", dev)
     T, k, N = h.shape
@@ -632,7 +645,8 @@ def qmm_experts_glu(wtype, Wg, Wu, xq, ids, h, scratch, scratch_bytes, gate="sil
 def qmm_experts_sum(wtype, W, h, ids, weights, y, scratch, scratch_bytes, residual=None, stream=None):
     """y[t] = residual[t] + sum_j weights[t][j] (W[ids[t][j]] q(h[t][j])): y f32 [T][N], W uint8 [E][N][row bytes], h f32
     [T][k][K] (quantized on the way), ids int32 and weights f32 (or None: 1) [T][k]; residual f32 [T][N], may be y."""
-    dev, wt = _device(), _type(wtype)
+    wt = _format(wtype)[0]
+    dev = _device()
     if h.dim() != 3 or W.dim() != 3:
         _refuse("h, W", h if h.dim() != 3 else W, "float32, uint8", "of 3 dimensions", dev)
     T, k, K = h.shape
