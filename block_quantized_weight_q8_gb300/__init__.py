@@ -623,7 +623,7 @@ def qmm_experts_path(wtype, gated, T, k, E, N, K):
 
 def qmm_experts_glu(wtype, Wg, Wu, xq, ids, h, scratch, scratch_bytes, gate="silu", stream=None):
     """h[t][j] = gate(Wg[e] x_t) * (Wu[e] x_t), e = ids[t][j]: h f32 [T][k][N], Wg and Wu uint8 [E][N][row bytes], xq uint8
-    [T][qmm_row_bytes(qmm_act_type(wtype), K)], ids int32 [T][k] (negative: no expert, zeros)."""
+    [T][qmm_row_bytes(qmm_act_type(wtype), K)], ids int32 [T][k] (negative: no expert, zeros).  h overlaps no input."""
     if not isinstance(gate, str) or gate not in GLU_KINDS:
         _unknown("gate", GLU_KINDS, gate)
     wt, size, values, act = _format(wtype)
@@ -644,7 +644,8 @@ def qmm_experts_glu(wtype, Wg, Wu, xq, ids, h, scratch, scratch_bytes, gate="sil
 
 def qmm_experts_sum(wtype, W, h, ids, weights, y, scratch, scratch_bytes, residual=None, stream=None):
     """y[t] = residual[t] + sum_j weights[t][j] (W[ids[t][j]] q(h[t][j])): y f32 [T][N], W uint8 [E][N][row bytes], h f32
-    [T][k][K] (quantized on the way), ids int32 and weights f32 (or None: 1) [T][k]; residual f32 [T][N], may be y."""
+    [T][k][K] (quantized on the way), ids int32 and weights f32 (or None: 1) [T][k]; residual f32 [T][N], may be y, which
+    overlaps no other input."""
     wt = _format(wtype)[0]
     dev = _device()
     if h.dim() != 3 or W.dim() != 3:

@@ -578,8 +578,8 @@ QMM_API qmm_status qmm_kv_attend(const qmm_kv_pages* cache, const float* q, int6
  * rounded to f32 once, every other step an f32 operation rounded once; xq the rows of h
  * as qmm_quantize_q8_0 / q8_K (act) gives them.  So sum, h and xq are those of a scalar
  * implementation with an exact sum of squares, but where that sum lies within this of the
- * middle between two floats (and where y^2 neither overflows f32 nor
- * falls below 2^-100).  x, r f32 [M][K]; w f32 [K]; sum f32 [M][K] receives y, NULL:
+ * middle between two floats (and where y^2 neither overflows f32 nor falls below
+ * 2^-100).  x, r f32 [M][K]; w f32 [K]; sum f32 [M][K] receives y, NULL:
  * not kept; it may be x or r; h f32 [M][K] or xq may be NULL, not both.  Apart from sum
  * no output overlaps another argument.  K as for qmm_rmsnorm_quantize; every pointer
  * 16-byte aligned. */
@@ -598,9 +598,9 @@ QMM_API qmm_status qmm_add_rmsnorm_quantize(int act, const float* x, const float
  * than k open experts has ids -1 and weights 0 behind them.  +inf counts as the largest
  * f32.  softmax runs over all experts that are not closed by their logit.
  * logits f32 [T][E], ld values from one token to the next (at least E); bias f32 [E] or
- * NULL; ids int32 [T][k], weights f32 [T][k], all device, 4-byte aligned.  E 1..1024, k
- * 1..32 and at most groups_kept * E / groups, groups 1..64, dividing E; scale finite.
- * The spec is read by the call. */
+ * NULL; ids int32 [T][k], weights f32 [T][k], all device, 4-byte aligned, no output
+ * overlapping another argument.  E 1..1024, k 1..32 and at most groups_kept * E / groups,
+ * groups 1..64, dividing E; scale finite.  The spec is read by the call. */
 typedef enum { QMM_ROUTE_SOFTMAX = 0, QMM_ROUTE_SIGMOID = 1 } qmm_route_score;
 typedef struct {
     int32_t score;
@@ -626,13 +626,15 @@ QMM_API qmm_status qmm_route(const qmm_route_spec* spec, const float* logits, in
  * L2 norm, and are the same on every run; between calls of few and of many choices a
  * choice's products may differ by as much.  With many choices (qmm_experts_path) two
  * things are held to a share of what is larger beside them, which is over the bound only
- * where that meets zeros.  Eight blocks of 32 values share a power of two: it keeps every
+ * where that meets zeros or cancels.  Eight blocks of 32 values share a power of two: it keeps every
  * scale (Q4_1, Q5_1: and minimum) exactly where the largest of the eight, L, is below 256,
  * Q8_0 rows beside Q4_1 and Q5_1 32; otherwise a scale below 2^-21 L (those rows: 2^-18 L)
  * is off by up to 2^-32 L (2^-29 L).  In a block of Q4_K, Q5_K or Q2_K with the scales d
  * and m (of the minimums) a minimum is off by up to 2^-25 |d|, and a scale times code,
  * where |m| > 2^29 |d|, by up to 2^-25 |m|.  k 1..64, E 1..1024, T * k <= 2^24, E * N <=
  * 2^31 - 1; N, K and the alignment (ids and weights: 4 bytes) as for qmm_matvec.
+ * Apart from y on the residual no output (h of glu, y of sum, scratch) overlaps another
+ * argument: it is written while inputs are still read.
  * scratch: at least qmm_experts_scratch_bytes(wtype, T, k, E, N, K) bytes (0: a bad
  * argument), enough for either call of this shape, written before it is read; calls that
  * may overlap on the GPU take one each.  The launches depend on the shapes alone, so a
