@@ -309,7 +309,8 @@ static qmm_status on_tensor_cores(int wt, int kind, const ExpertShape& s, const 
 // 2048 -> 1024 twice, 128 choices 60 / 70, 256 101 / 84; Q8_0, 8 experts of 4096 -> 4096 twice, 16 choices 61 / 127, 32
 // 180 / 152; Q6_K, 64 experts of 1024 -> 2048, 128 choices 41 / 61, 256 111 / 73; Q5_1, 32 experts of 1408 -> 2048, 32
 // choices 41 / 50, 64 74 / 61.  Of 223 calls (all types, 4 to 16 experts, rows of 768 to 4096, 2 to 2048 choices) all but
-// two took at most 1.25 times the better path's time.
+// two took at most 1.25 times the better path's time.  The rule knows the number of choices, not how they fall to the
+// experts: it counts a partial tile for each of min(choices, experts).
 static bool many_rows(int wt, const ExpertShape& s, bool gate) {
     DeviceInfo dev;
     if (current_device(&dev) != QMM_OK) return false;

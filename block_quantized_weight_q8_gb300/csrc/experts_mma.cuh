@@ -13,8 +13,9 @@
 //                      scale is (run_shift in experts_mma.h); the codes of Q4_1 and Q5_1 are centered and the minimums
 //                      multiply the sums, as above
 //   activations        Q8_K: the codes (exact); Q8_0: the values over a shared power of two, in two terms, likewise
-// Products of two-term operands leave out lo lo.  Sums of steps are truncated to f32 by the tensor core; with at most 48
-// steps to a sum, those with a lo first, the errors measured are 0.04 to 0.45e-6 of the result.
+// Products of two-term operands leave out lo lo, up to 2^-22 of a product.  Sums of steps are truncated to f32 by the tensor
+// core; with 18 steps to a sum (Q4_K, Q5_K, Q2_K), 24 or, with minimums, 27 (32-value blocks) or 32 (Q6_K), those with a lo
+// first, the errors measured are 0.04 to 0.45e-6 of the result.
 //
 // A tile is 128 weight rows (gated: 64 rows of the gate's and of the up matrix, row by row, so that both sums of an
 // output lie in neighbouring lanes) by up to 128 rows of one expert; CTAs, one per SM, walk over the tiles, and a tile's
@@ -31,7 +32,7 @@
 // Weights are read once per 128 rows of their expert.  What bounds a tile is the converters' warps, their conversions and
 // as much again in waits, handovers and tensor-memory traffic, whatever the number of the tile's rows: 10 to 11 thousand
 // warp instructions a chunk.  Measured: 16384 rows over 64 experts of Q4_K, 1024 x 2048 twice (137 GFLOP), 265 us, 520
-// TFLOP/s, issue slots 72% busy, the tensor pipe 26%; over 64 of Q6_K, 2048 x 1024 (69 GFLOP), 213 us; 128 rows over 8 of
+// TFLOP/s, issue slots 72% busy, the tensor pipe 26%; over 64 of Q6_K, 2048 x 1024 (69 GFLOP), 213 us; 96 rows over 8 of
 // Q8_0, 4096 x 12288, 235 us; 256 rows over 32 of Q4_0, 1408 x 2048 twice, 97 us.  Not kept, as slower: adding two sums
 // with one packed fma (2 to 6%), every group of warps making a block of each item rather than two of one (12%).
 #pragma once

@@ -9,13 +9,14 @@
 // power of two, 32 where there is one group), lane l of it the group's experts l, l + L, ...; so all groups' worth comes of
 // one look at a lane's keys and log2 L exchanges.  A choice is a maximum over the lane's keys, one over the warp
 // (whole-number keys in the floats' order) and one of the index.  Bound by these instructions, two thousand a token:
-// 8192 tokens of 256 experts, 4 of 8 groups by two keys, 8 choices take 21.5 us (25 alone, the issue
-// slots 68% busy; with expert e in lane e % 32 and the groups one after another, 43); a few tokens take 3.2 us.
+// 8192 tokens of 256 experts, 4 of 8 groups by two keys, 8 choices take 20.4 us (25 from cold caches, the issue slots 67%
+// busy; with expert e in lane e % 32 and the groups one after another, 43); a few tokens take 3.2 us.
 //
 // The choice is that of binary64.  Without a bias the scores' order is the logits' and keys are the logits themselves
 // (but where groups count by two keys).  Otherwise keys carry rounding errors, bounded below; where two keys that decide
 // anything lie closer than both their errors (a few tokens in ten thousand), the warp orders the candidates by their keys
-// in binary64, or, where the groups are in doubt, chooses again from all of the token's.
+// in binary64, or, where the groups are in doubt, chooses again from all of the token's.  Weights are f32 scores over their
+// f32 sum, a few roundings each (6e-8 of the weight on the measured cases).
 #include <float.h>
 
 #include "experts.h"
