@@ -624,14 +624,16 @@ QMM_API qmm_status qmm_route(const qmm_route_spec* spec, const float* logits, in
  *        not there); weights f32 [T][k], NULL: 1; residual f32 [T][N], NULL: 0, may be y
  * Products agree with the block-wise definition (qmm_matvec) within 1e-5 of their row's
  * L2 norm, and are the same on every run; between calls of few and of many choices a
- * choice's products may differ by as much.  With many choices (qmm_experts_path) two
+ * choice's products may differ by as much.  With many choices (qmm_experts_path) three
  * things are held to a share of what is larger beside them, which is over the bound only
- * where that meets zeros or cancels.  Eight blocks of 32 values share a power of two: it keeps every
- * scale (Q4_1, Q5_1: and minimum) exactly where the largest of the eight, L, is below 256,
- * Q8_0 rows beside Q4_1 and Q5_1 32; otherwise a scale below 2^-21 L (those rows: 2^-18 L)
- * is off by up to 2^-32 L (2^-29 L).  In a block of Q4_K, Q5_K or Q2_K with the scales d
- * and m (of the minimums) a minimum is off by up to 2^-25 |d|, and a scale times code,
- * where |m| > 2^29 |d|, by up to 2^-25 |m|.  k 1..64, E 1..1024, T * k <= 2^24, E * N <=
+ * where that meets zeros or cancels.  Eight blocks of 32 values share a power of two: it
+ * keeps every scale (Q4_1, Q5_1: and minimum) exactly where the largest of the eight, L, is
+ * below 256, Q8_0 rows beside Q4_1 and Q5_1 32; otherwise a scale below 2^-21 L (those
+ * rows: 2^-18 L) is off by up to 2^-32 L (2^-29 L).  In a block of Q4_K, Q5_K or Q2_K with
+ * the scales d and m (of the minimums) a minimum is off by up to 2^-25 |d|, and a scale
+ * times code, where |m| > 2^29 |d|, by up to 2^-25 |m|.  A run's sum, whose parts are the
+ * codes' products and each minimum times a sum of 16 values, is off by up to 2^-18 of its
+ * parts' magnitudes.  k 1..64, E 1..1024, T * k <= 2^24, E * N <=
  * 2^31 - 1; N, K and the alignment (ids and weights: 4 bytes) as for qmm_matvec.
  * Apart from y on the residual no output (h of glu, y of sum, scratch) overlaps another
  * argument: it is written while inputs are still read.
