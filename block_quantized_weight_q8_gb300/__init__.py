@@ -591,7 +591,7 @@ def qmm_route(logits, ids, weights, score="softmax", bias=None, groups=1, groups
     choose, and what they weigh (see include/qmm.h)."""
     if not isinstance(score, str) or score not in ROUTE_SCORES:
         _unknown("score", ROUTE_SCORES, score)
-    if (groups | groups_kept | group_top) >> 31:  # the spec's fields have 32 bits, and none is negative
+    if (groups | groups_kept | group_top) >> 31 > 0:  # the spec's fields have 32 bits (negative ones are the library's to refuse)
         raise ValueError("groups, groups_kept, group_top: got %r, %r, %r" % (groups, groups_kept, group_top))
     dev = _device()
     if logits.dtype is not _torch.float32 or logits.get_device() != dev or logits.dim() != 2 or (
